@@ -497,11 +497,140 @@ svx_status svx_width_next(svx_width w, int32_t* q_out);
 /* Current estimate T_round_hat(q) / U_hat(q), or -1 without records. */
 svx_status svx_width_cost(svx_width w, int32_t q, double* cost_out);
 
+/* ---- a paged cache: the Draft's one-token step, and the tensors a round takes ---------------- */
+
+/* The pages of the paper hold none of the calls of this section: they are what a caller of the rounds needs
+ * beside them.  svx_qk_norm_rope turns a projection's output into the q and candidate K/V of a round;
+ * a Draft model, which proposes the candidates one token at a time, keeps its own K/V in pages:
+ * svx_paged_append fills it, svx_paged_decode attends to it, svx_paged_evict keeps it small.
+ *
+ * The calls allocate nothing, keep nothing between calls and return once their work is enqueued on `stream`
+ * (cudaStream_t, NULL = default stream) of the struct's device, so each may be captured into a CUDA graph.
+ * Two calls whose GPU work overlaps (two streams, two replayed graphs) need workspaces and outputs of their
+ * own; the status word may be shared.  Host arguments are checked (SVX_ERR_INVALID_ARG,
+ * SVX_ERR_UNSUPPORTED; message from svx_last_error(NULL)); lengths, slots and page ids live on the device, so the
+ * kernels check them: one outside its bounds is clamped or left out, nothing outside the buffers is read or
+ * written, the outputs that depend on it are unspecified, and the status word becomes non-zero (bits are only ever
+ * set; the caller reads and clears it).  Positions, scales and values are not checked. */
+
+/* Element types of q, K, V, O and the norms' weights. */
+#define SVX_BF16 0
+#define SVX_FP16 1
+
+/* Rotation of the first rot_dim dimensions of a head by its position: pair i turns by pos * inv_freq[i].
+ * turns[i] = inv_freq[i] / (2 pi) as a 64-bit fixed-point fraction of a turn, so that position * turns is
+ * the exact phase (mod one turn) however far the position.  Filled by svx_rope_init. */
+typedef struct {
+  uint64_t turns[64];
+  float scale;          /* factor on the rotated values (1 but for scaled-context variants) */
+  int32_t rot_dim;      /* even multiple of 8 up to head_dim; 0: no rotation */
+  int32_t neighbours;   /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1) */
+  int32_t pad;
+} svx_rope;
+
+/* inv_freq: host double[rot_dim / 2], finite, |inv_freq| < 2^20.  rot_dim: a multiple of 16, 0..128.
+ * Host-only. */
+svx_status svx_rope_init(svx_rope* rope, int32_t rot_dim, int32_t neighbours, const double* inv_freq, float scale);
+
+/* The heads of n_req requests x n_tok tokens as a projection leaves them, device memory.  Token (b, j) is
+ * row b * n_tok + j; its heads lie one after the other, n_heads * head_dim elements, at row * stride elements
+ * from the pointer (so q, k and v may be views of one fused output).  Pointers 16-byte aligned, strides
+ * multiples of 8 elements. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const void* q_norm;      /* [head_dim] weights, 16-byte aligned, or NULL: ones */
+  const void* k_norm;
+  const int32_t* pos;      /* [n_req][n_tok] positions (any int32) */
+  const int32_t* n_new;    /* [n_req]: only the first n_new[b] tokens of a request count, 0..n_tok; NULL: all */
+  int32_t* status;         /* device status word, or NULL (svx_paged_append uses the cache's) */
+  int32_t n_req, n_tok;    /* >= 1; n_req <= 256 */
+  int32_t n_q_heads, n_kv_heads, head_dim; /* head_dim 64 or 128 */
+  int32_t dtype;           /* SVX_BF16 or SVX_FP16 */
+  int32_t device;
+  float eps;               /* added to the mean square; < 0: no norms (q_norm and k_norm NULL) */
+} svx_heads;
+
+/* q and k heads: x_i * w_i / sqrt(mean(x^2) + eps), then the rotation; v heads: as they are.  All in fp32,
+ * rounded once.  q_out [n_req][n_q_heads][n_tok][head_dim] and k_out, v_out [n_req][n_tok][n_kv_heads][head_dim]
+ * are what svx_round_begin and svx_candidate_attn take (n_tok = n_query).  v and v_out may both be NULL.  Rows
+ * of tokens past n_new[b] are left as they were.  Outputs must not overlap inputs. */
+svx_status svx_qk_norm_rope(const svx_heads* in, const svx_rope* rope, void* q_out, void* k_out, void* v_out,
+                            void* stream);
+
+/* K and V pages and one table for all requests of a call.  k, v: device memory, element (page, slot, head, 0)
+ * at page * page_stride + slot * tok_stride + head * head_stride elements (strides multiples of 8, rows of
+ * head_dim contiguous, pointers 16-byte aligned): [page][slot][head][d] and [page][head][slot][d] alike.  Slot t
+ * of request b is slot t mod page_size of page table[b][t / page_size]; entries behind a request's length
+ * are not read.  max_pages * page_size < 2^31, n_pages < 2^31. */
+typedef struct {
+  void* k;
+  void* v;
+  const int32_t* table;  /* device [n_req][max_pages] */
+  int32_t* status;       /* device status word */
+  int64_t page_stride, tok_stride, head_stride;
+  int64_t n_pages;
+  int32_t page_size, max_pages;
+  int32_t n_kv_heads, head_dim; /* head_dim 64 or 128 */
+  int32_t dtype;
+  int32_t device;
+} svx_pages;
+
+/* svx_qk_norm_rope with K and V going into the cache: token j of request b becomes slot start[b] + j (device
+ * int32[n_req]).  acc (device float [n_req][n_kv_heads][max_pages * page_size], or NULL) is set to 0 and slot_pos
+ * (int32, the same shape, or NULL) to the token's position at the new slots.  Pages written must not be
+ * shared by two of the call's slots.  v is required. */
+svx_status svx_paged_append(const svx_heads* in, const svx_rope* rope, const svx_pages* cache, const int32_t* start,
+                            void* q_out, float* acc, int32_t* slot_pos, void* stream);
+
+/* Bytes of workspace that svx_paged_decode needs for these arguments.  Host-only but for the SM count. */
+svx_status svx_paged_decode_workspace(const svx_pages* cache, int32_t n_req, int32_t n_q_heads, int64_t max_len,
+                                      int32_t weights, int64_t* bytes);
+
+/* Attention of one new token per request over its cached slots [0, len[b]):
+ * O = softmax(q K^T scale) V, LSE = natural log of the softmax denominator; a row with no slot (or only scores of
+ * -inf) gets O = 0, LSE = -inf.  q, o [n_req][n_q_heads][head_dim] and lse [n_req][n_q_heads], device; query head
+ * h reads KV head h / (n_q_heads / n_kv_heads).  len: device int32[n_req], 0 <= len[b] <= max_len.  max_len:
+ * upper bound known on the host, 0 for max_pages * page_size; it sizes the launch and the workspace, so a
+ * captured call stays valid for all lengths up to it.  scale: 0 means 1/sqrt(head_dim).  K and V of the slots read
+ * must be finite; what lies behind a request's length is not used, whatever it holds.
+ * acc_in, acc_out (device float [n_req][n_kv_heads][max_pages * page_size], or both NULL): acc_out[t] =
+ * acc_in[t] + the sum over the KV head's query heads of slot t's softmax weight, t < len[b]; the rest is left as
+ * it was.  They may be one buffer.  workspace: device, 256-byte aligned; contents need no set-up. */
+svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, int32_t n_q_heads, const void* q, const int32_t* len,
+                            int64_t max_len, float scale, void* o, float* lse, const float* acc_in, float* acc_out,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that svx_paged_evict needs for these arguments.  Host-only. */
+svx_status svx_paged_evict_workspace(const svx_pages* cache, int32_t n_req, int64_t max_len, int32_t budget,
+                                     int64_t* bytes);
+
+/* Longest cache that svx_paged_evict takes. */
+#define SVX_EVICT_MAX_LEN 262144
+
+/* Eviction by accumulated attention weight.  Per request and KV head, of the slots [0, len[b]) keeps
+ * n = min(len[b], budget): first those at positions < sink or >= next_pos[b] - recent, then those with the largest
+ * acc_in; equal ones by the lower slot; NaN counts as -inf.  The kept slots >= n, in order, move into the
+ * evicted slots < n, in order: K and V rows inside the pages, and acc_in, pos_in into acc_out, pos_out, which get
+ * their first n entries written (the rest is left as it was).  Every other slot keeps its place, so slots are in no
+ * order of position; attention does not depend on it.  len_out[b] = n.  len, next_pos, len_out: device
+ * int32[n_req]; acc, pos: device [n_req][n_kv_heads][max_pages * page_size]; acc_out may be acc_in, pos_out pos_in and
+ * len_out len.  1 <= budget, sink, recent >= 0, sink + recent <= budget.  max_len: as svx_paged_decode, at most
+ * SVX_EVICT_MAX_LEN (0: the smaller of that and max_pages * page_size).  Pages below the lengths must belong to
+ * one request each: a page shared by two requests would be rewritten for both. */
+svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, const int32_t* len, int64_t max_len, int32_t budget,
+                           int32_t sink, int32_t recent, const int32_t* next_pos, const float* acc_in,
+                           const int32_t* pos_in, float* acc_out, int32_t* pos_out, int32_t* len_out, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
 /* Library version string. */
 const char* svx_version(void);
 
 /* sizeof of the ABI's structs, for bindings to check their layouts: svx_config, svx_part, svx_stats,
- * svx_window_summary, svx_plan_entry, svx_tier_state, svx_sched_config, svx_draft_instr, in this order.
+ * svx_window_summary, svx_plan_entry, svx_tier_state, svx_sched_config, svx_draft_instr, svx_rope, svx_heads,
+ * svx_pages, in this order.
  * Writes min(cap, count) entries to out and returns the count.  Host-only. */
 int32_t svx_abi_sizes(int64_t* out, int32_t cap);
 

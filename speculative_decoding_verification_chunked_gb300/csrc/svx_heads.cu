@@ -1,0 +1,392 @@
+// Norms of query and key heads with the position rotation, in one pass from a projection's output to a
+// round's tensors or a paged cache.
+//
+//   y_i = x_i w_i / sqrt(mean(x^2) + eps)
+//   (z_a, z_b) = s (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = pos * inv_freq   for each pair (a, b)
+//
+// All in fp32, rounded once at the end (a rounding between norm and rotation would be a second one).
+//
+// Phase.  t is needed mod 2 pi, and an fp32 product pos * inv_freq has lost it for far positions (2^17 * 2^-24 is
+// 8e-3 rad).  The host keeps inv_freq / 2 pi as a 64-bit fraction of a turn, so pos * turns mod 2^64 is
+// the fraction of a turn exactly, in three integer multiply-adds instead of FP64; its upper 32 bits, read as
+// signed half-turns, go to sincospif.
+//
+// Layout.  A head is d / 16 lanes; a lane holds 16 elements as two 16-byte vectors, chosen so that both members
+// of each rotated pair sit in one lane: vectors l and l + rot/16 of the rotated part, or two neighbouring vectors of the
+// rest.  So a rotation needs no shuffle, a norm three (d = 128).  A lane's eight angles are computed once and serve
+// all heads that its group of lanes walks (up to kMaxWalk of a token, loads of kBatch in flight).
+#include "svx_paged.h"
+
+namespace svx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;
+
+struct HeadsParams {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const void *q_norm, *k_norm;
+  const int32_t* pos;
+  const int32_t* n_new;
+  int* status;
+  void *q_out, *k_out, *v_out;  // k_out, v_out: dense; or NULL with a cache
+  const int32_t* start;         // cache: first slot of each request's tokens
+  float* acc;
+  int32_t* slot_pos;
+  PageView pages;
+  uint64_t turns[64];
+  int64_t tokens;               // n_req * n_tok
+  int64_t q_ext, k_ext, v_ext;  // elements of the inputs (checked build)
+  float eps, scale;
+  int32_t n_tok, n_q, n_kv;
+  int32_t heads;                // n_q + n_kv, + n_kv with v
+  int32_t walk;                 // heads that a group of lanes walks
+  int32_t groups;               // groups of lanes per token: ceil(heads / walk)
+  int32_t rot_dim, neighbours, norm, paged;
+};
+
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 up(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t down(float a, float b) {
+    __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&p);
+  }
+};
+template <>
+struct Pair<__half> {
+  static __device__ __forceinline__ float2 up(uint32_t u) { return __half22float2(*reinterpret_cast<__half2*>(&u)); }
+  static __device__ __forceinline__ uint32_t down(float a, float b) {
+    __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&p);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = Pair<T>::up(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float* f) {
+  return make_uint4(Pair<T>::down(f[0], f[1]), Pair<T>::down(f[2], f[3]), Pair<T>::down(f[4], f[5]),
+                    Pair<T>::down(f[6], f[7]));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__ HeadsParams P) {
+  constexpr int LANES = D / 16;  // lanes per head
+  grid_dependency_wait();
+  allow_dependents();
+  const int64_t id = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
+  const int lane = threadIdx.x % LANES;
+  int64_t token = id / P.groups;
+  const int group = static_cast<int>(id - token * P.groups);
+  bool live = token < P.tokens;
+  if (!live) token = 0;
+  const int b = static_cast<int>(token / P.n_tok);
+  const int j = static_cast<int>(token - static_cast<int64_t>(b) * P.n_tok);
+  const int nvec = P.rot_dim / 16;  // vectors in one half of the rotated part
+  const int v0 = lane < nvec ? lane : 2 * nvec + 2 * (lane - nvec);
+  const int v1 = lane < nvec ? lane + nvec : v0 + 1;
+  const bool turn = lane < nvec;
+
+  if (live && P.n_new) {
+    const int n = P.n_new[b];
+    if (n < 0 || n > P.n_tok) {
+      if (P.status && j == 0 && group == 0 && lane == 0) atomicOr(P.status, kErrInput);
+    }
+    live = j < n;
+  }
+  // where K and V of this token go: an element offset into the pages, or the dense row
+  int64_t kv_row = -1;
+  int32_t slot = 0;
+  const int32_t pos = P.pos[token];
+  if (P.paged) {
+    if (live) {
+      const int64_t s = static_cast<int64_t>(P.start[b]) + j;
+      if (s >= 0 && s < P.pages.cap) {
+        slot = static_cast<int32_t>(s);
+        const uint32_t pg = static_cast<uint32_t>(slot) / static_cast<uint32_t>(P.pages.page_size);
+        kv_row = slot_offset(P.pages, P.pages.table[static_cast<int64_t>(b) * P.pages.max_pages + pg],
+                             static_cast<uint32_t>(slot) - pg * P.pages.page_size);
+      }
+      if (kv_row < 0 && group == 0 && lane == 0) atomicOr(P.pages.status, kErrInput);
+    }
+  } else {
+    kv_row = token * P.n_kv * D;
+  }
+
+  // a lane's angles: pairs 8 lane .. 8 lane + 7 (halves), or 4 v0 .. and 4 v1 .. (neighbours)
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+    if (turn) {
+      const int f = P.neighbours ? (i < 4 ? 4 * v0 + i : 4 * v1 + i - 4) : 8 * lane + i;
+      const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[f];
+      // half-turns in [-1, 1): |error| <= 2^-25 of a half-turn from the conversion
+      const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
+      sincospif(half_turns, &sn[i], &cs[i]);
+      cs[i] *= P.scale;
+      sn[i] *= P.scale;
+    }
+  }
+
+  const int n_qk = P.n_q + P.n_kv;
+  const int64_t row_q = token * P.q_stride, row_k = token * P.k_stride, row_v = token * P.v_stride;
+  for (int i0 = 0; i0 < P.walk; i0 += kBatch) {
+    uint4 raw[kBatch][2];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = group + (i0 + u) * P.groups;
+      raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+      if (i0 + u < P.walk && live && h < P.heads) {
+        const T* src = h < P.n_q    ? static_cast<const T*>(P.q) + row_q + static_cast<int64_t>(h) * D
+                       : h < n_qk ? static_cast<const T*>(P.k) + row_k + static_cast<int64_t>(h - P.n_q) * D
+                                  : static_cast<const T*>(P.v) + row_v + static_cast<int64_t>(h - n_qk) * D;
+        if (in_bounds(src, D, static_cast<const T*>(h < P.n_q ? P.q : h < n_qk ? P.k : P.v),
+                      h < P.n_q ? P.q_ext : h < n_qk ? P.k_ext : P.v_ext, P.status, kSiteHeadsIn)) {
+          raw[u][0] = __ldg(reinterpret_cast<const uint4*>(src) + v0);
+          raw[u][1] = __ldg(reinterpret_cast<const uint4*>(src) + v1);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = group + (i0 + u) * P.groups;
+      if (i0 + u >= P.walk) break;  // the same for all lanes
+      const bool here = live && h < P.heads;
+      const bool is_v = h >= n_qk;
+      float x[16];
+      unpack<T>(raw[u][0], x);
+      unpack<T>(raw[u][1], x + 8);
+      if (P.norm) {  // all lanes of the warp take part in the shuffles
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (here && !is_v) {
+          const float r = rsqrtf(ss * (1.f / D) + P.eps);
+          const T* w = static_cast<const T*>(h < P.n_q ? P.q_norm : P.k_norm);
+          float g[16];
+          if (w) {
+            unpack<T>(__ldg(reinterpret_cast<const uint4*>(w) + v0), g);
+            unpack<T>(__ldg(reinterpret_cast<const uint4*>(w) + v1), g + 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) g[i] = 1.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = x[i] * r * g[i];
+        }
+      }
+      if (!here) continue;
+      uint4 out[2] = {raw[u][0], raw[u][1]};
+      if (!is_v) {
+        if (turn) {
+          if (P.neighbours) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = x[2 * i], c = x[2 * i + 1];
+              x[2 * i] = a * cs[i] - c * sn[i];
+              x[2 * i + 1] = c * cs[i] + a * sn[i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = x[i], c = x[8 + i];
+              x[i] = a * cs[i] - c * sn[i];
+              x[8 + i] = c * cs[i] + a * sn[i];
+            }
+          }
+        }
+        out[0] = pack<T>(x);
+        out[1] = pack<T>(x + 8);
+      }
+      T* dst;
+      if (h < P.n_q) {
+        dst = static_cast<T*>(P.q_out) + ((static_cast<int64_t>(b) * P.n_q + h) * P.n_tok + j) * D;
+        if (!in_bounds(dst, D, static_cast<T*>(P.q_out), P.tokens * P.n_q * D, P.status, kSiteHeadsOut)) continue;
+      } else {
+        if (kv_row < 0) continue;
+        const int hk = is_v ? h - n_qk : h - P.n_q;
+        if (P.paged) {
+          T* base = static_cast<T*>(is_v ? P.pages.v : P.pages.k);
+          dst = base + kv_row + static_cast<int64_t>(hk) * P.pages.head_stride;
+          if (!in_bounds(dst, D, base, P.pages.extent, P.status, kSitePool)) continue;
+          if (!is_v && lane == 0) {
+            const int64_t m = (static_cast<int64_t>(b) * P.n_kv + hk) * P.pages.cap + slot;
+            if (P.acc) P.acc[m] = 0.f;
+            if (P.slot_pos) P.slot_pos[m] = pos;
+          }
+        } else {
+          T* base = static_cast<T*>(is_v ? P.v_out : P.k_out);
+          dst = base + kv_row + static_cast<int64_t>(hk) * D;
+          if (!in_bounds(dst, D, base, P.tokens * P.n_kv * D, P.status, kSiteHeadsOut)) continue;
+        }
+      }
+      reinterpret_cast<uint4*>(dst)[v0] = out[0];
+      reinterpret_cast<uint4*>(dst)[v1] = out[1];
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch(HeadsParams& p, cudaStream_t stream, int sms) {
+  // Heads per group of lanes: one where tokens are few (latency: every head its own lanes), more once the
+  // grid fills the card anyway, so that a lane's eight sines and cosines serve several heads.
+  const int64_t lanes = p.tokens * p.heads * (D / 16);
+  const int64_t room = static_cast<int64_t>(sms) * 1024;
+  p.walk = lanes >= 8 * room ? 8 : lanes >= 4 * room ? 4 : lanes >= 2 * room ? 2 : 1;
+  p.groups = (p.heads + p.walk - 1) / p.walk;
+  const int64_t blocks = (p.tokens * p.groups * (D / 16) + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  return launch_pdl(heads_kernel<T, D>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, p);
+}
+
+struct Range {
+  const char* a;
+  const char* b;
+};
+bool overlap(const Range& x, const Range& y) { return x.a && y.a && x.a < y.b && y.a < x.b; }
+
+svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages* cache, const int32_t* start, void* q_out,
+                     void* k_out, void* v_out, float* acc, int32_t* slot_pos, void* stream) {
+  if (!in || !rope) return paged_fail(SVX_ERR_INVALID_ARG, "heads or rope is NULL");
+  if (in->n_req < 1 || in->n_req > kMaxReq) return paged_fail(SVX_ERR_INVALID_ARG, "n_req must be in [1, %d]", kMaxReq);
+  if (in->n_tok < 1) return paged_fail(SVX_ERR_INVALID_ARG, "n_tok must be >= 1");
+  if (in->head_dim != 64 && in->head_dim != 128) return paged_fail(SVX_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (in->dtype != SVX_BF16 && in->dtype != SVX_FP16)
+    return paged_fail(SVX_ERR_UNSUPPORTED, "dtype must be SVX_BF16 or SVX_FP16");
+  if (in->n_kv_heads < 1 || in->n_q_heads < in->n_kv_heads || in->n_q_heads % in->n_kv_heads || in->n_q_heads > 4096)
+    return paged_fail(SVX_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads, at most 4096");
+  if (rope->rot_dim < 0 || rope->rot_dim % 16 || rope->rot_dim > in->head_dim)
+    return paged_fail(SVX_ERR_INVALID_ARG, "rope: rot_dim must be a multiple of 16, at most head_dim");
+  const bool has_v = in->v != nullptr;
+  const int d = in->head_dim;
+  const int64_t q_row = static_cast<int64_t>(in->n_q_heads) * d, kv_row = static_cast<int64_t>(in->n_kv_heads) * d;
+  const int64_t tokens = static_cast<int64_t>(in->n_req) * in->n_tok;
+  const int64_t most = (int64_t{1} << 46) / tokens;
+  const int64_t str[3] = {in->q_stride, in->k_stride, in->v_stride}, row[3] = {q_row, kv_row, kv_row};
+  for (int i = 0; i < (has_v ? 3 : 2); ++i)
+    if (str[i] < row[i] || str[i] % 8 || str[i] > most)
+      return paged_fail(SVX_ERR_INVALID_ARG, "token strides must be multiples of 8 elements that hold all heads");
+  if (!in->q || !in->k || !q_out || !is_aligned(in->q, 16) || !is_aligned(in->k, 16) || !is_aligned(q_out, 16) ||
+      (has_v && !is_aligned(in->v, 16)))
+    return paged_fail(SVX_ERR_INVALID_ARG, "q, k, v and q_out must be 16-byte aligned device pointers");
+  if (!in->pos) return paged_fail(SVX_ERR_INVALID_ARG, "pos must be a device pointer");
+  if (!(in->eps >= 0.f) && !(in->eps < 0.f)) return paged_fail(SVX_ERR_INVALID_ARG, "eps is not a number");
+  if (in->eps < 0.f && (in->q_norm || in->k_norm))
+    return paged_fail(SVX_ERR_INVALID_ARG, "norm weights given with eps < 0 (no norms)");
+  if ((in->q_norm && !is_aligned(in->q_norm, 16)) || (in->k_norm && !is_aligned(in->k_norm, 16)))
+    return paged_fail(SVX_ERR_INVALID_ARG, "norm weights must be 16-byte aligned");
+
+  HeadsParams p = {};
+  if (cache) {
+    const svx_status st = paged_view(cache, in->n_req, &p.pages);
+    if (st != SVX_OK) return st;
+    if (cache->n_kv_heads != in->n_kv_heads || cache->head_dim != d || cache->dtype != in->dtype ||
+        cache->device != in->device)
+      return paged_fail(SVX_ERR_INVALID_ARG, "heads and cache differ in KV heads, head_dim, dtype or device");
+    if (!start || !has_v) return paged_fail(SVX_ERR_INVALID_ARG, "start and v are required");
+    p.paged = 1;
+    p.status = cache->status;
+  } else {
+    if (!k_out || !is_aligned(k_out, 16) || has_v != (v_out != nullptr) || (v_out && !is_aligned(v_out, 16)))
+      return paged_fail(SVX_ERR_INVALID_ARG, "k_out (and v_out with v) must be 16-byte aligned device pointers");
+  }
+  const int64_t es = 2;
+  auto range = [es](const void* a, int64_t elems) {
+    const char* c = static_cast<const char*>(a);
+    return Range{c, c + elems * es};
+  };
+  // the span of a strided input covers what lies between its rows: outputs there are taken for overlapping
+  // only if they meet a row of it, so rows are compared by span for dense inputs and refused alike for views
+  const Range ins[3] = {range(in->q, (tokens - 1) * str[0] + row[0]), range(in->k, (tokens - 1) * str[1] + row[1]),
+                        has_v ? range(in->v, (tokens - 1) * str[2] + row[2]) : Range{nullptr, nullptr}};
+  const Range outs[5] = {range(q_out, tokens * q_row),
+                         cache ? range(cache->k, p.pages.extent) : range(k_out, tokens * kv_row),
+                         cache ? range(cache->v, p.pages.extent) : v_out ? range(v_out, tokens * kv_row) : Range{nullptr, nullptr}};
+  for (const Range& i : ins)
+    for (int o = 0; o < 3; ++o)
+      if (overlap(i, outs[o])) return paged_fail(SVX_ERR_INVALID_ARG, "an output overlaps an input");
+  if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || (!cache && overlap(outs[1], outs[2])))
+    return paged_fail(SVX_ERR_INVALID_ARG, "two outputs overlap");
+
+  PagedDevice dev(in->device);
+  if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", in->device);
+  const void* ptrs[] = {in->q,   in->k,    in->v, in->q_norm, in->k_norm, in->pos, in->n_new, in->status,
+                        q_out,   k_out,    v_out, start,      acc,        slot_pos, cache ? cache->k : nullptr,
+                        cache ? cache->v : nullptr, cache ? cache->table : nullptr, cache ? cache->status : nullptr};
+  for (const void* x : ptrs)
+    if (x && !on_device(x, in->device)) return paged_fail(SVX_ERR_INVALID_ARG, "a pointer is not memory of device %d", in->device);
+
+  p.q = in->q;
+  p.k = in->k;
+  p.v = in->v;
+  p.q_stride = str[0];
+  p.k_stride = str[1];
+  p.v_stride = str[2];
+  p.q_norm = in->q_norm;
+  p.k_norm = in->k_norm;
+  p.pos = in->pos;
+  p.n_new = in->n_new;
+  if (!cache) p.status = in->status;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.start = start;
+  p.acc = acc;
+  p.slot_pos = slot_pos;
+  for (int i = 0; i < 64; ++i) p.turns[i] = rope->turns[i];
+  p.tokens = tokens;
+  p.q_ext = (tokens - 1) * str[0] + row[0];
+  p.k_ext = (tokens - 1) * str[1] + row[1];
+  p.v_ext = has_v ? (tokens - 1) * str[2] + row[2] : 0;
+  p.eps = in->eps;
+  p.scale = rope->scale;
+  p.n_tok = in->n_tok;
+  p.n_q = in->n_q_heads;
+  p.n_kv = in->n_kv_heads;
+  p.heads = in->n_q_heads + (has_v ? 2 : 1) * in->n_kv_heads;
+  p.rot_dim = rope->rot_dim;
+  p.neighbours = rope->neighbours;
+  p.norm = in->eps >= 0.f;
+  const int sms = sm_count(in->device);
+  if (sms <= 0) return paged_fail(SVX_ERR_CUDA, "cannot read the SM count");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (in->dtype == SVX_BF16)
+    e = d == 128 ? launch<__nv_bfloat16, 128>(p, s, sms) : launch<__nv_bfloat16, 64>(p, s, sms);
+  else
+    e = d == 128 ? launch<__half, 128>(p, s, sms) : launch<__half, 64>(p, s, sms);
+  if (e != cudaSuccess) return paged_fail(SVX_ERR_CUDA, "heads kernel launch failed: %s", cudaGetErrorString(e));
+  return SVX_OK;
+}
+
+}  // namespace
+}  // namespace svx
+
+extern "C" svx_status svx_qk_norm_rope(const svx_heads* in, const svx_rope* rope, void* q_out, void* k_out, void* v_out,
+                                       void* stream) {
+  return svx::run_heads(in, rope, nullptr, nullptr, q_out, k_out, v_out, nullptr, nullptr, stream);
+}
+
+extern "C" svx_status svx_paged_append(const svx_heads* in, const svx_rope* rope, const svx_pages* cache,
+                                       const int32_t* start, void* q_out, float* acc, int32_t* slot_pos, void* stream) {
+  if (!cache) return svx::paged_fail(SVX_ERR_INVALID_ARG, "cache is NULL");
+  return svx::run_heads(in, rope, cache, start, q_out, nullptr, nullptr, acc, slot_pos, stream);
+}

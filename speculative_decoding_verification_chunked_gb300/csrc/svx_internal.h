@@ -76,7 +76,7 @@ __device__ __forceinline__ bool in_bounds(const T* p, int64_t n, const T* base, 
     return true;
   } else {
     const bool ok = base != nullptr && n >= 0 && p >= base && p + n <= base + extent;
-    if (!ok) atomicOr(err, kErrBounds | (1 << (8 + site)));
+    if (!ok && err) atomicOr(err, kErrBounds | (1 << (8 + site)));
     return ok;
   }
 }

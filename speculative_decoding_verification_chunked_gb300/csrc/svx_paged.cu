@@ -1,0 +1,111 @@
+// Host side shared by the paged-cache entry points: argument checks, and the rotation's fixed-point phases.
+#include "svx_paged.h"
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+
+namespace svx {
+
+void set_thread_error(const char* msg);  // svx_runtime.cu: message for svx_last_error(NULL)
+
+svx_status paged_fail(svx_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  try {
+    set_thread_error(buf);
+  } catch (const std::bad_alloc&) {  // no memory for the message: the status still tells
+  }
+  return st;
+}
+
+bool on_device(const void* p, int device) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == device);
+}
+
+int sm_count(int device) {
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+svx_status paged_view(const svx_pages* c, int32_t n_req, PageView* out) {
+  if (!c) return paged_fail(SVX_ERR_INVALID_ARG, "cache is NULL");
+  if (n_req < 1 || n_req > kMaxReq) return paged_fail(SVX_ERR_INVALID_ARG, "n_req must be in [1, %d]", kMaxReq);
+  if (c->dtype != SVX_BF16 && c->dtype != SVX_FP16)
+    return paged_fail(SVX_ERR_UNSUPPORTED, "dtype must be SVX_BF16 or SVX_FP16");
+  if (c->head_dim != 64 && c->head_dim != 128) return paged_fail(SVX_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 4096)
+    return paged_fail(SVX_ERR_INVALID_ARG, "n_kv_heads must be in [1, 4096]");
+  if (c->page_size < 1 || c->max_pages < 1 ||
+      static_cast<int64_t>(c->page_size) * c->max_pages > 0x7fffffffLL)
+    return paged_fail(SVX_ERR_INVALID_ARG, "page_size and max_pages must be positive with a product below 2^31");
+  if (c->n_pages < 1 || c->n_pages > 0x7fffffffLL)
+    return paged_fail(SVX_ERR_INVALID_ARG, "n_pages must be in [1, 2^31)");
+  const int64_t s[3] = {c->page_stride, c->tok_stride, c->head_stride}, n[3] = {c->n_pages, c->page_size, c->n_kv_heads};
+  int64_t extent = c->head_dim;
+  for (int i = 0; i < 3; ++i) {
+    // (a stride over a dimension of one entry is never stepped over)
+    if (n[i] > 1 && (s[i] < c->head_dim || s[i] % 8 || s[i] > (int64_t{1} << 46) / n[i]))
+      return paged_fail(SVX_ERR_INVALID_ARG, "page, slot and head strides must be multiples of 8 elements, at least head_dim");
+    extent += (n[i] - 1) * s[i];
+  }
+  if (!c->k || !c->v || !is_aligned(c->k, 16) || !is_aligned(c->v, 16))
+    return paged_fail(SVX_ERR_INVALID_ARG, "k and v pages must be 16-byte aligned device pointers");
+  if (!c->table || !c->status || !is_aligned(c->table, 4) || !is_aligned(c->status, 4))
+    return paged_fail(SVX_ERR_INVALID_ARG, "table and status must be device pointers");
+  *out = PageView{c->k,
+                  c->v,
+                  c->table,
+                  c->status,
+                  s[0],
+                  s[1],
+                  s[2],
+                  extent,
+                  static_cast<int32_t>(c->n_pages),
+                  c->page_size,
+                  c->max_pages,
+                  c->n_kv_heads,
+                  n_req,
+                  c->page_size * c->max_pages};
+  return SVX_OK;
+}
+
+}  // namespace svx
+
+extern "C" svx_status svx_rope_init(svx_rope* rope, int32_t rot_dim, int32_t neighbours, const double* inv_freq,
+                                    float scale) {
+  using svx::paged_fail;
+  if (!rope) return paged_fail(SVX_ERR_INVALID_ARG, "rope is NULL");
+  if (rot_dim < 0 || rot_dim > 128 || rot_dim % 16)
+    return paged_fail(SVX_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [0, 128]");
+  if (rot_dim && !inv_freq) return paged_fail(SVX_ERR_INVALID_ARG, "inv_freq is NULL");
+  if (!std::isfinite(scale)) return paged_fail(SVX_ERR_INVALID_ARG, "scale must be finite");
+  svx_rope r = {};
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    if (!(std::fabs(inv_freq[i]) < 1048576.0))
+      return paged_fail(SVX_ERR_INVALID_ARG, "inv_freq[%d] must be finite, below 2^20 in magnitude", i);
+    // The fraction of a turn per position: whole turns drop out, since positions are whole numbers.
+    const double turns = inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    const double frac = turns - std::floor(turns);              // [0, 1)
+    const double scaled = std::ldexp(frac, 64);                 // exact: a power of two
+    r.turns[i] = scaled >= 18446744073709551616.0 ? 0u : static_cast<uint64_t>(scaled);
+  }
+  r.scale = scale;
+  r.rot_dim = rot_dim;
+  r.neighbours = neighbours ? 1 : 0;
+  *rope = r;
+  return SVX_OK;
+}

@@ -1,0 +1,80 @@
+// Internal interface of the paged-cache operators: head norms with rotation (svx_heads.cu), one-token
+// attention (svx_decode.cu) and eviction (svx_evict.cu).  Not part of the C ABI.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "svx.h"
+#include "svx_internal.h"
+
+namespace svx {
+
+// Status-word bit (beside kErrBounds of the checked build): a length, slot or page id read on the device
+// lies outside its bounds.  What it names was clamped or left out; nothing outside the buffers is touched.
+constexpr int kErrInput = 8;
+
+// Sites of the bounds-checked build, after those of svx_internal.h.
+enum PagedSite : int {
+  kSiteHeadsIn = 9,
+  kSiteHeadsOut = 10,
+  kSitePool = 11,      // K and V pages, any kernel
+  kSiteDecodeIn = 12,
+  kSiteDecodeOut = 13,
+  kSiteDecodeWs = 14,
+  kSiteEvictMeta = 15,
+  kSiteEvictWs = 16,
+};
+
+// K and V pages as the kernels see them: element (page, slot, head, 0) of either pool is at
+// page * page_stride + slot * tok_stride + head * head_stride elements.
+struct PageView {
+  void* k;
+  void* v;
+  const int32_t* table;  // [n_req][max_pages]
+  int* status;
+  int64_t page_stride, tok_stride, head_stride;
+  int64_t extent;        // elements from the first to one past the last (checked build)
+  int32_t n_pages, page_size, max_pages, n_kv_heads;
+  int32_t n_req;
+  int32_t cap;           // max_pages * page_size: slots of a request
+};
+
+// Page and offset of a request's slot, 0 <= slot < cap: the element offset of (slot, head 0), or -1 where
+// the table names no page of the pool.
+__device__ __forceinline__ int64_t slot_offset(const PageView& p, int32_t page_id, uint32_t in_page) {
+  if (static_cast<uint32_t>(page_id) >= static_cast<uint32_t>(p.n_pages)) return -1;
+  return static_cast<int64_t>(page_id) * p.page_stride + static_cast<int64_t>(in_page) * p.tok_stride;
+}
+
+// Host side, shared by the entry points (svx_paged.cu).
+svx_status paged_fail(svx_status st, const char* fmt, ...);
+// Checks a svx_pages and fills the view (with n_req rows in the table).  SVX_OK or the failure reported.
+svx_status paged_view(const svx_pages* c, int32_t n_req, PageView* out);
+// True for device (or managed) memory of `device`.
+bool on_device(const void* p, int device);
+inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int sm_count(int device);
+
+// Makes `device` current for the entry point's duration.
+struct PagedDevice {
+  int prev = -1;
+  bool ok = false;
+  explicit PagedDevice(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess) {
+      cudaGetLastError();
+      return;
+    }
+    ok = prev == dev || cudaSetDevice(dev) == cudaSuccess;
+    if (!ok) cudaGetLastError();
+    target = dev;
+  }
+  ~PagedDevice() {
+    if (ok && prev != target) cudaSetDevice(prev);
+  }
+  int target = -1;
+};
+
+}  // namespace svx

@@ -362,7 +362,9 @@ int32_t svx_abi_sizes(int64_t* out, int32_t cap) {
   const int64_t sz[] = {static_cast<int64_t>(sizeof(svx_config)),     static_cast<int64_t>(sizeof(svx_part)),
                         static_cast<int64_t>(sizeof(svx_stats)),      static_cast<int64_t>(sizeof(svx_window_summary)),
                         static_cast<int64_t>(sizeof(svx_plan_entry)), static_cast<int64_t>(sizeof(svx_tier_state)),
-                        static_cast<int64_t>(sizeof(svx_sched_config)), static_cast<int64_t>(sizeof(svx_draft_instr))};
+                        static_cast<int64_t>(sizeof(svx_sched_config)), static_cast<int64_t>(sizeof(svx_draft_instr)),
+                        static_cast<int64_t>(sizeof(svx_rope)),       static_cast<int64_t>(sizeof(svx_heads)),
+                        static_cast<int64_t>(sizeof(svx_pages))};
   const int32_t n = static_cast<int32_t>(sizeof(sz) / sizeof(sz[0]));
   for (int32_t i = 0; i < n && i < cap; ++i) out[i] = sz[i];
   return n;

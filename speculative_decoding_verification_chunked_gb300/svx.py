@@ -86,6 +86,28 @@ class PlanEntry(ctypes.Structure):
                 ("n_tok", ctypes.c_int32), ("tok_start", ctypes.c_int64)]
 
 
+class RopeTable(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64 * 64), ("scale", ctypes.c_float), ("rot_dim", ctypes.c_int32),
+                ("neighbours", ctypes.c_int32), ("pad", ctypes.c_int32)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("q_norm", ctypes.c_void_p),
+                ("k_norm", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("n_new", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("n_req", ctypes.c_int32), ("n_tok", ctypes.c_int32),
+                ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("device", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class Pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("tok_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("device", ctypes.c_int32)]
+
+
 # name -> (restype, argtypes); every symbol declared in include/svx.h
 _P = ctypes.c_void_p
 _SIGS = {
@@ -158,6 +180,19 @@ _SIGS = {
                                         ctypes.c_double, ctypes.c_double]),
     "svx_width_next": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32)]),
     "svx_width_cost": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_double)]),
+    "svx_rope_init": (ctypes.c_int, [ctypes.POINTER(RopeTable), ctypes.c_int32, ctypes.c_int32,
+                                     ctypes.POINTER(ctypes.c_double), ctypes.c_float]),
+    "svx_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(Heads), ctypes.POINTER(RopeTable), _P, _P, _P, _P]),
+    "svx_paged_append": (ctypes.c_int, [ctypes.POINTER(Heads), ctypes.POINTER(RopeTable), ctypes.POINTER(Pages), _P, _P,
+                                        _P, _P, _P]),
+    "svx_paged_decode_workspace": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
+                                                  ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
+    "svx_paged_decode": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_int64,
+                                        ctypes.c_float, _P, _P, _P, _P, _P, ctypes.c_int64, _P]),
+    "svx_paged_evict_workspace": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                                 ctypes.POINTER(ctypes.c_int64)]),
+    "svx_paged_evict": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32,
+                                       ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, _P]),
     "svx_version": (ctypes.c_char_p, []),
     "svx_abi_sizes": (ctypes.c_int32, [ctypes.POINTER(ctypes.c_int64), ctypes.c_int32]),
 }
@@ -182,7 +217,8 @@ def version() -> str:
     return lib.svx_version().decode()
 
 
-ABI_STRUCTS = ("Config", "Part", "Stats", "WindowStats", "PlanEntry", "TierState", "SchedConfig", "DraftInstr")
+ABI_STRUCTS = ("Config", "Part", "Stats", "WindowStats", "PlanEntry", "TierState", "SchedConfig", "DraftInstr",
+               "RopeTable", "Heads", "Pages")
 
 
 def abi_sizes() -> dict:
@@ -688,3 +724,258 @@ class Verifier:
                 arr[i] = Part(b, n, t0, base_k[b] + t0 * row_bytes, base_v[b] + t0 * row_bytes)
             self._check(lib.svx_push_chunk(self._h, arr, len(parts)))
         self.round_finish(o, lse, timeout_ms)
+
+
+# ------------------------------------------------------------ a paged cache
+
+
+BF16, FP16 = 0, 1
+EVICT_MAX_LEN = 262144
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _type_code(t, what: str) -> int:
+    torch = _torch()
+    code = {torch.bfloat16: BF16, torch.float16: FP16}.get(t.dtype)
+    if code is None:
+        raise SvxError(ERR_UNSUPPORTED, f"{what}: dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
+    return code
+
+
+def _dense(t, dtype, shape: tuple, device, what: str) -> Optional[int]:
+    """Address of a dense tensor of exactly this type and shape on this device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise SvxError(ERR_INVALID_ARG, f"{what}: {t.dtype} {list(t.shape)} on {t.device}, contiguous {t.is_contiguous()}; "
+                                        f"expected dense {dtype} {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _head_rows(t, n_req: int, n_tok: int, d: int, dtype, device, what: str):
+    """Address and token stride of heads [n_req][n_tok][heads][d], possibly a view of a fused projection."""
+    if t.dim() != 4 or t.shape[0] != n_req or t.shape[1] != n_tok or t.shape[3] != d or t.dtype != dtype or \
+            t.device != device:
+        raise SvxError(ERR_INVALID_ARG, f"{what}: {t.dtype} {list(t.shape)} on {t.device}, expected {dtype} "
+                                        f"[{n_req}, {n_tok}, heads, {d}] on {device}")
+    s0, s1, s2, s3 = t.stride()
+    heads = t.shape[2]
+    row = s1 if n_tok > 1 else s0 if n_req > 1 else heads * d
+    if s3 != 1 or (heads > 1 and s2 != d) or (n_tok > 1 and n_req > 1 and s0 != n_tok * s1):
+        raise SvxError(ERR_INVALID_ARG, f"{what}: strides {list(t.stride())}: a token's heads must be dense, and tokens "
+                                        "evenly spaced over the requests")
+    return t.data_ptr(), row
+
+
+def _launch_stream(device, stream) -> int:
+    """The given stream's handle, else the current stream of the tensors' device."""
+    return _torch().cuda.current_stream(device).cuda_stream if stream is None else _stream_handle(stream)
+
+
+def _workspace(workspace, need: int, device, stream):
+    """The caller's workspace, or one from the caching allocator that belongs to the call's stream."""
+    torch = _torch()
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous() or \
+                workspace.numel() * workspace.element_size() < need:
+            raise SvxError(ERR_INVALID_ARG, f"workspace: a dense tensor of at least {need} bytes on {device} is needed")
+        return workspace
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(s):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _static_error(st: int):
+    if st != OK:
+        raise SvxError(st, lib.svx_last_error(None).decode())
+
+
+class Rope:
+    """Rotation of heads by position (svx_rope_init): pair i of the first rot_dim dimensions turns by
+    position * inv_freq[i], by default theta^(-2 i / rot_dim).  neighbours: pairs (2i, 2i + 1) instead of
+    (i, i + rot_dim / 2).  scale: factor on the rotated values."""
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, inv_freq: Optional[Sequence[float]] = None,
+                 neighbours: bool = False, scale: float = 1.0):
+        if inv_freq is None:
+            inv_freq = [float(theta) ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+        if len(inv_freq) != rot_dim // 2:
+            raise SvxError(ERR_INVALID_ARG, f"inv_freq: {len(inv_freq)} entries, expected rot_dim / 2 = {rot_dim // 2}")
+        self.table = RopeTable()
+        f = (ctypes.c_double * max(1, len(inv_freq)))(*[float(x) for x in inv_freq])
+        _static_error(lib.svx_rope_init(ctypes.byref(self.table), rot_dim, int(bool(neighbours)), f, scale))
+
+
+def _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, status):
+    torch = _torch()
+    if q.dim() != 4 or k.dim() != 4:
+        raise SvxError(ERR_INVALID_ARG, "q, k and v: [requests][tokens][heads][head_dim] tensors are expected")
+    n_req, n_tok, hq, d = q.shape
+    dtype, device = q.dtype, q.device
+    code = _type_code(q, "q")
+    if device.type != "cuda":
+        raise SvxError(ERR_INVALID_ARG, f"q is on {device}, not on a CUDA device")
+    hkv = k.shape[2]
+    qp, qs = _head_rows(q, n_req, n_tok, d, dtype, device, "q")
+    kp, ks = _head_rows(k, n_req, n_tok, d, dtype, device, "k")
+    vp, vs = (None, 0) if v is None else _head_rows(v, n_req, n_tok, d, dtype, device, "v")
+    if v is not None and v.shape[2] != hkv:
+        raise SvxError(ERR_INVALID_ARG, f"v has {v.shape[2]} heads, k {hkv}")
+    if eps is not None and not eps >= 0.0:
+        raise SvxError(ERR_INVALID_ARG, "eps must be >= 0, or None for no norms")
+    h = Heads(qp, kp, vp, qs, ks, vs, _dense(q_norm, dtype, (d,), device, "q_norm"),
+              _dense(k_norm, dtype, (d,), device, "k_norm"), _dense(pos, torch.int32, (n_req, n_tok), device, "pos"),
+              _dense(n_new, torch.int32, (n_req,), device, "n_new"), status, n_req, n_tok, hq, hkv, d, code,
+              device.index, -1.0 if eps is None else eps)
+    return h, device, dtype
+
+
+def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None, k_norm=None,
+                 eps: Optional[float] = 1e-6, n_new=None, status=None, stream=None):
+    """svx_qk_norm_rope: normed and rotated heads in a round's layout.
+
+    q, k, v: device bf16 or fp16 [B][n][heads][d], views of a fused projection allowed (v and v_out may be None);
+    pos: int32 [B][n]; q_out [B][Hq][n][d], k_out, v_out [B][n][Hkv][d]: what Verifier.round_begin and
+    candidate_attn take.  eps None: no norms.  n_new: int32 [B], tokens of each request that count, or None.
+    status: int32 [1] that becomes non-zero if n_new leaves [0, n], or None.  stream: the current one by default.
+    """
+    torch = _torch()
+    sp = None if status is None else _dense(status, torch.int32, (1,), q.device, "status")
+    h, device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, sp)
+    b, n, hq, d = q.shape
+    hkv = h.n_kv_heads
+    _static_error(lib.svx_qk_norm_rope(
+        ctypes.byref(h), ctypes.byref(rope.table), _dense(q_out, dtype, (b, hq, n, d), device, "q_out"),
+        _dense(k_out, dtype, (b, n, hkv, d), device, "k_out"), _dense(v_out, dtype, (b, n, hkv, d), device, "v_out"),
+        _launch_stream(device, stream)))
+
+
+class PagedCache:
+    """K and V pages of one layer, for a model that takes its tokens one at a time (svx_paged_*).
+
+    k_pages, v_pages: device bf16 or fp16 [pages][page_size][Hkv][d], equally strided; any order of the first three
+    dimensions in memory, rows of d dense.  The tensors stay the caller's.  Page tables are int32 [B][max_pages]: slot t
+    of request b is slot t % page_size of page table[b][t // page_size].  Calls run on the current stream (or
+    ``stream``), allocate nothing but a workspace from torch's caching allocator (or take ``workspace``) and may be
+    captured into CUDA graphs.  Lengths, slots and page ids are read on the device; ``check()`` tells whether
+    one was out of bounds.
+    """
+
+    def __init__(self, k_pages, v_pages):
+        torch = _torch()
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() or \
+                k_pages.dtype != v_pages.dtype or k_pages.device != v_pages.device or k_pages.stride(3) != 1:
+            raise SvxError(ERR_INVALID_ARG, "k_pages and v_pages: equal [pages][page_size][Hkv][d] tensors with dense rows "
+                                            "are expected")
+        if k_pages.device.type != "cuda":
+            raise SvxError(ERR_INVALID_ARG, f"k_pages is on {k_pages.device}, not on a CUDA device")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.device, self.dtype = k_pages.device, k_pages.dtype
+        n_pages, self.page_size, self.n_kv_heads, self.head_dim = k_pages.shape
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._pages = Pages(k_pages.data_ptr(), v_pages.data_ptr(), None, self.status.data_ptr(), *k_pages.stride()[:3],
+                            n_pages, self.page_size, 0, self.n_kv_heads, self.head_dim, _type_code(k_pages, "k_pages"),
+                            self.device.index)
+        self._sizes = {}
+
+    def _with_table(self, table):
+        """The C struct for a call (a copy: calls from several threads do not share it)."""
+        if table.dim() != 2:
+            raise SvxError(ERR_INVALID_ARG, f"table: shape {list(table.shape)}, expected [requests][max_pages]")
+        p = Pages.from_buffer_copy(self._pages)
+        p.table = _dense(table, _torch().int32, tuple(table.shape), self.device, "table")
+        p.max_pages = table.shape[1]
+        return p
+
+    def _need(self, what: str, fn, pages, *args) -> int:
+        key = (what, pages.max_pages) + args
+        need = self._sizes.get(key)
+        if need is None:
+            n = ctypes.c_int64(0)
+            _static_error(fn(ctypes.byref(pages), *args, ctypes.byref(n)))
+            need = self._sizes[key] = n.value
+        return need
+
+    def check(self) -> bool:
+        """True if, since the last check, a call met a length, slot or page id out of its bounds (outputs that depend
+        on it are unspecified); clears the word.  Waits for the device."""
+        torch = _torch()
+        torch.cuda.synchronize(self.device)
+        bad = bool(self.status.item())
+        if bad:
+            self.status.zero_()
+            torch.cuda.synchronize(self.device)
+        return bad
+
+    def append(self, q, k, v, pos, rope: Rope, table, start, q_out, q_norm=None, k_norm=None,
+               eps: Optional[float] = 1e-6, n_new=None, acc=None, slot_pos=None, stream=None):
+        """svx_paged_append: norms and rotates the heads of n new tokens per request (as qk_norm_rope), puts K and V into
+        slots start[b] + j and q into q_out [B][Hq][n][d]; acc (fp32) becomes 0 and slot_pos (int32), both
+        [B][Hkv][max_pages * page_size], the token's position at the new slots."""
+        torch = _torch()
+        h, device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, None)
+        if device != self.device:
+            raise SvxError(ERR_INVALID_ARG, f"q is on {device}, the cache on {self.device}")
+        b, n, hq, d = q.shape
+        p = self._with_table(table)
+        if table.shape[0] != b:
+            raise SvxError(ERR_INVALID_ARG, f"table: {table.shape[0]} requests, q has {b}")
+        meta = (b, self.n_kv_heads, p.max_pages * self.page_size)
+        _static_error(lib.svx_paged_append(
+            ctypes.byref(h), ctypes.byref(rope.table), ctypes.byref(p), _dense(start, torch.int32, (b,), device, "start"),
+            _dense(q_out, dtype, (b, hq, n, d), device, "q_out"), _dense(acc, torch.float32, meta, device, "acc"),
+            _dense(slot_pos, torch.int32, meta, device, "slot_pos"), _launch_stream(device, stream)))
+
+    def decode(self, q, table, lens, o, lse, max_len: int = 0, scale: float = 0.0, acc_in=None, acc_out=None,
+               workspace=None, stream=None):
+        """svx_paged_decode: one new token per request attends to its cached slots [0, lens[b]).
+
+        q, o: [B][Hq][1][d]; lse: fp32 [B][Hq][1]; lens: int32 [B].  max_len: a bound on lens known on the host (0:
+        max_pages * page_size).  With acc_in and acc_out (fp32 [B][Hkv][max_pages * page_size], may be one tensor) the
+        slots' softmax weights, summed over a KV head's query heads, are added."""
+        torch = _torch()
+        if q.dim() != 4:
+            raise SvxError(ERR_INVALID_ARG, f"q: shape {list(q.shape)}, expected [requests][heads][1][head_dim]")
+        b, hq = q.shape[0], q.shape[1]
+        device, rows = self.device, (b, hq, 1, self.head_dim)
+        p = self._with_table(table)
+        if table.shape[0] != b:
+            raise SvxError(ERR_INVALID_ARG, f"table: {table.shape[0]} requests, q has {b}")
+        meta = (b, self.n_kv_heads, p.max_pages * self.page_size)
+        ws = _workspace(workspace, self._need("decode", lib.svx_paged_decode_workspace, p, b, hq, max_len,
+                                              int(acc_in is not None)), device, stream)
+        _static_error(lib.svx_paged_decode(
+            ctypes.byref(p), b, hq, _dense(q, self.dtype, rows, device, "q"),
+            _dense(lens, torch.int32, (b,), device, "lens"), max_len, scale, _dense(o, self.dtype, rows, device, "o"),
+            _dense(lse, torch.float32, (b, hq, 1), device, "lse"), _dense(acc_in, torch.float32, meta, device, "acc_in"),
+            _dense(acc_out, torch.float32, meta, device, "acc_out"), ws.data_ptr(), ws.numel() * ws.element_size(),
+            _launch_stream(device, stream)))
+
+    def evict(self, table, lens, budget: int, sink: int, recent: int, next_pos, acc_in, pos_in, acc_out, pos_out, len_out,
+              max_len: int = 0, workspace=None, stream=None):
+        """svx_paged_evict: per request and KV head keeps min(lens[b], budget) slots: positions < sink or >= next_pos[b] -
+        recent, then the largest acc_in (ties: the lower slot).  Kept slots behind the new length move into the
+        evicted ones before it, with their acc and position; len_out gets the new lengths.  acc (fp32), pos (int32):
+        [B][Hkv][max_pages * page_size]; lens, next_pos, len_out: int32 [B]; outputs may be their inputs."""
+        torch = _torch()
+        p = self._with_table(table)
+        b, device = table.shape[0], self.device
+        meta = (b, self.n_kv_heads, p.max_pages * self.page_size)
+        i32, f32 = torch.int32, torch.float32
+        for what, t in (("next_pos", next_pos), ("acc_in", acc_in), ("pos_in", pos_in), ("acc_out", acc_out),
+                        ("pos_out", pos_out), ("len_out", len_out), ("lens", lens)):
+            if t is None:
+                raise SvxError(ERR_INVALID_ARG, f"{what} is required")
+        ws = _workspace(workspace, self._need("evict", lib.svx_paged_evict_workspace, p, b, max_len, budget), device, stream)
+        _static_error(lib.svx_paged_evict(
+            ctypes.byref(p), b, _dense(lens, i32, (b,), device, "lens"), max_len, budget, sink, recent,
+            _dense(next_pos, i32, (b,), device, "next_pos"), _dense(acc_in, f32, meta, device, "acc_in"),
+            _dense(pos_in, i32, meta, device, "pos_in"), _dense(acc_out, f32, meta, device, "acc_out"),
+            _dense(pos_out, i32, meta, device, "pos_out"), _dense(len_out, i32, (b,), device, "len_out"), ws.data_ptr(),
+            ws.numel() * ws.element_size(), _launch_stream(device, stream)))
