@@ -8,9 +8,11 @@
 //
 // select_kernel: a cluster of CTAs per row holds the row's slots in registers as 32-bit keys whose unsigned order is
 // the order of preference (weights >= 0 or not, NaN as -inf, protected slots above all).  The n-th largest key is found
-// by bisection over the key's bits: a count per step, no histogram, so equal weights cost nothing extra and nothing
-// depends on the order of atomics.  Ties, holes and spares are numbered by ballots and one scan over the warps each.
-// move_kernel: a warp copies a row's K and V (512 bytes at d = 128) at a time, four rows in flight.
+// by histograms of 256 bins: first of the range that the keys span (which spreads them, where their top bits would
+// not), then of the bin that holds it, two or three passes as a rule.  The counts are sums of ones: no order of the
+// atomics changes a result.  Ties, holes and spares are numbered by ballots and one scan over the warps each.
+// move_kernel: a lane works out a move, then the warp brings up to 32 rows of K and V (512 bytes each at d = 128) into
+// shared memory with asynchronous copies and writes them out, so a warp has 16 KiB in flight without holding registers.
 // Floor: 8 bytes a slot read, 8 a kept slot written, 8 d bytes a moved slot.
 #include <cooperative_groups.h>
 
@@ -23,11 +25,11 @@ namespace cg = cooperative_groups;
 namespace svx {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 1024;
 constexpr int kMaxKeys = 32;    // per thread
 constexpr int kMaxCluster = 8;  // portable
-static_assert(kThreads * kMaxKeys * kMaxCluster == SVX_EVICT_MAX_LEN, "the longest row a cluster holds");
+constexpr int kSplitKeys = 8;
+static_assert(kMaxThreads * kMaxKeys * kMaxCluster == SVX_EVICT_MAX_LEN, "the longest row a cluster holds");
 
 struct EvictParams {
   PageView pages;
@@ -45,6 +47,7 @@ struct EvictParams {
   int32_t max_len, budget, sink, recent;
   int32_t most;     // moves a row can need
   int32_t cluster;
+  int32_t chunk;    // moves of a warp at a time, <= 32
 };
 
 // Unsigned order = float order; NaN as -inf, -0 as +0.
@@ -54,53 +57,49 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u ^ ((u & 0x80000000u) ? 0xffffffffu : 0x80000000u);
 }
 
-struct Counts {
-  int32_t warp[2][kWarps];
-  int32_t peer[2][kMaxCluster];
+constexpr int kBins = 256;
+constexpr int kPasses = 4;  // 8 bits of a 32-bit range each
+
+struct Shared {
+  int32_t hist[kPasses][kBins];  // a pass has its own, so that none is cleared while a peer may still read it
+  int32_t total[kBins];          // over the cluster
+  uint2 warp_range[32];
+  uint2 peer_range;
+  int32_t warp_protected[32];
+  int32_t peer_protected;
+  int2 warp_scan[2][32];
+  int2 peer_scan[2];
 };
 
-// Sum over the row's cluster of one value per warp (the same in all lanes); `turn` alternates between calls, so
-// that one barrier (two in a cluster) separates a call's writes from the last reads of the same buffer.
-__device__ __forceinline__ int cluster_sum(int v, Counts& s, int turn, int n_cta, int rank) {
+// Sums of the values of the warps before this one, in the order (CTA of the cluster, warp); `total` gets all.
+// `turn`: a buffer of its own for each use.  In a cluster, every look into a peer's shared memory follows a
+// cluster barrier, so the peer has started and has written what is read.
+template <int WARPS>
+__device__ __forceinline__ int2 cluster_scan(int2 v, Shared& s, int turn, int n_cta, int rank, int2* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) s.warp[turn][warp] = v;
+  if (lane == 0) s.warp_scan[turn][warp] = v;
   __syncthreads();
-  int sum = __reduce_add_sync(0xffffffffu, s.warp[turn][lane]);
+  const int2 x = lane < WARPS ? s.warp_scan[turn][lane] : make_int2(0, 0);
+  int2 before = make_int2(__reduce_add_sync(0xffffffffu, lane < warp ? x.x : 0),
+                          __reduce_add_sync(0xffffffffu, lane < warp ? x.y : 0));
+  int2 sum = make_int2(__reduce_add_sync(0xffffffffu, x.x), __reduce_add_sync(0xffffffffu, x.y));
   if (n_cta > 1) {
     cg::cluster_group cl = cg::this_cluster();
-    if (threadIdx.x < n_cta) *cl.map_shared_rank(&s.peer[turn][rank], threadIdx.x) = sum;
+    if (threadIdx.x == 0) s.peer_scan[turn] = sum;
     cl.sync();
-    sum = 0;
-    for (int i = 0; i < n_cta; ++i) sum += s.peer[turn][i];
-  }
-  return sum;
-}
-
-// Sum of the values of the warps before this one, in the order (CTA of the cluster, warp); `total` gets all.
-__device__ __forceinline__ int cluster_scan(int v, Counts& s, int turn, int n_cta, int rank, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) s.warp[turn][warp] = v;
-  __syncthreads();
-  const int x = s.warp[turn][lane];
-  int before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
-  int sum = __reduce_add_sync(0xffffffffu, x);
-  if (n_cta > 1) {
-    cg::cluster_group cl = cg::this_cluster();
-    if (threadIdx.x < n_cta) *cl.map_shared_rank(&s.peer[turn][rank], threadIdx.x) = sum;
-    cl.sync();
-    sum = 0;
-    for (int i = 0; i < n_cta; ++i) {
-      if (i < rank) before += s.peer[turn][i];
-      sum += s.peer[turn][i];
-    }
+    const int2 y = lane < n_cta ? *cl.map_shared_rank(&s.peer_scan[turn], lane) : make_int2(0, 0);
+    before.x += __reduce_add_sync(0xffffffffu, lane < rank ? y.x : 0);
+    before.y += __reduce_add_sync(0xffffffffu, lane < rank ? y.y : 0);
+    sum = make_int2(__reduce_add_sync(0xffffffffu, y.x), __reduce_add_sync(0xffffffffu, y.y));
   }
   *total = sum;
   return before;
 }
 
-template <int KEYS>
-__global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_constant__ EvictParams P) {
-  __shared__ Counts s;
+template <int KEYS, int THREADS>
+__global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ EvictParams P) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ Shared s;
   grid_dependency_wait();
   allow_dependents();
   const int n_cta = P.cluster, rank = static_cast<int>(blockIdx.x) % n_cta;
@@ -118,61 +117,154 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_consta
   const int first = (rank * kWarps + warp) * (32 * KEYS) + lane;  // this lane's slots: first + 32 i
   uint32_t key[KEYS];
   const int64_t recent_from = static_cast<int64_t>(P.next_pos[b]) - P.recent;
+  constexpr int LOADS = KEYS < 8 ? KEYS : 8;  // slots in flight at a time
 #pragma unroll
-  for (int i = 0; i < KEYS; ++i) {
-    const int t = first + 32 * i;
-    key[i] = 0;
-    if (t < L) {
-      const int32_t pos = P.pos_in[meta + t];
-      key[i] = pos < P.sink || pos >= recent_from ? 0xffffffffu : order_key(P.acc_in[meta + t]);
+  for (int i0 = 0; i0 < KEYS; i0 += LOADS) {
+    int32_t pos[LOADS];
+    float w[LOADS];
+#pragma unroll
+    for (int u = 0; u < LOADS; ++u) {
+      const int t = first + 32 * (i0 + u);
+      pos[u] = t < L ? P.pos_in[meta + t] : 0;
+      w[u] = t < L ? P.acc_in[meta + t] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < LOADS; ++u) {
+      const uint32_t k = pos[u] < P.sink || pos[u] >= recent_from ? 0xffffffffu : order_key(w[u]);
+      key[i0 + u] = first + 32 * (i0 + u) < L ? k : 0u;
     }
   }
-  // the n-th largest key: the largest `cut` with at least n keys >= cut
-  int turn = 0;
+  // Keep the keys > cut, and of those equal to it the first `need`.
   uint32_t cut = 0;
-  int above = 0;  // keys > cut, if not exact
-  bool exact = L <= P.budget;
-  if (n_cta > 1) cg::this_cluster().sync();  // every CTA runs before another writes to its shared memory
-  if (!exact) {
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t tryc = cut | (1u << bit);
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < KEYS; ++i) c += key[i] >= tryc;
-      c = cluster_sum(__reduce_add_sync(0xffffffffu, c), s, turn, n_cta, rank);
-      turn ^= 1;
-      if (c >= n) {
-        cut = tryc;
-        exact = c == n;
-        if (exact) break;
-      } else {
-        above = c;
-      }
-    }
-  } else {
-    cut = 1;  // every slot's key
-  }
-  uint32_t keep = 0;  // bit i: slot first + 32 i is kept
-  if (exact) {
-#pragma unroll
-    for (int i = 0; i < KEYS; ++i) keep |= static_cast<uint32_t>(key[i] >= cut) << i;
-  } else {
-    // after the last bit the trials that followed the last failing one all held, so that one was cut + 1 and
-    // `above` counts the keys > cut (none failed: cut is the largest key, above 0)
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < KEYS; ++i) mine += __popc(__ballot_sync(0xffffffffu, key[i] == cut));
-    int ties;
-    int at = cluster_scan(mine, s, turn, n_cta, rank, &ties);
-    turn ^= 1;
-    const int need = n - above;
+  int need = 0;
+  if (L > P.budget) {
+    // range of the keys that are not protected, and how many are
+    uint32_t lo = 0xffffffffu, hi = 0;
+    int prot = 0;
 #pragma unroll
     for (int i = 0; i < KEYS; ++i) {
-      const bool tie = key[i] == cut;
-      const uint32_t m = __ballot_sync(0xffffffffu, tie);
-      const int mine_at = at + __popc(m & ((1u << lane) - 1u));
-      at += __popc(m);
-      keep |= static_cast<uint32_t>(key[i] > cut || (tie && mine_at < need)) << i;
+      prot += key[i] == 0xffffffffu;
+      if (key[i] != 0 && key[i] != 0xffffffffu) {
+        lo = min(lo, key[i]);
+        hi = max(hi, key[i]);
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    prot = __reduce_add_sync(0xffffffffu, prot);
+    for (int i = threadIdx.x; i < kPasses * kBins; i += THREADS) (&s.hist[0][0])[i] = 0;
+    if (lane == 0) {
+      s.warp_range[warp] = make_uint2(lo, hi);
+      s.warp_protected[warp] = prot;
+    }
+    __syncthreads();
+    uint2 r = lane < kWarps ? s.warp_range[lane] : make_uint2(0xffffffffu, 0u);
+    int q = lane < kWarps ? s.warp_protected[lane] : 0;
+    if (n_cta > 1) {
+      r = make_uint2(__reduce_min_sync(0xffffffffu, r.x), __reduce_max_sync(0xffffffffu, r.y));
+      q = __reduce_add_sync(0xffffffffu, q);
+      cg::cluster_group cl = cg::this_cluster();
+      if (threadIdx.x == 0) {
+        s.peer_range = r;
+        s.peer_protected = q;
+      }
+      cl.sync();
+      r = lane < n_cta ? *cl.map_shared_rank(&s.peer_range, lane) : make_uint2(0xffffffffu, 0u);
+      q = lane < n_cta ? *cl.map_shared_rank(&s.peer_protected, lane) : 0;
+    }
+    lo = __reduce_min_sync(0xffffffffu, r.x);
+    hi = __reduce_max_sync(0xffffffffu, r.y);
+    need = n - __reduce_add_sync(0xffffffffu, q);
+    if (need <= 0) {  // only among the protected: the first n of them
+      cut = 0xffffffffu;
+      need = n;
+    } else {
+      // up to 256 equal bins, a power of two wide, of [lo, hi], then of the bin in which the need-th largest lies, until
+      // all of a bin is kept or it holds one value.  (As L > n, some key is not protected: lo <= hi.)
+      int bits = 32 - __clz(hi - lo);  // keys in question are less than 2^bits above lo
+      for (int pass = 0;; ++pass) {
+        const int shift = max(bits - 8, 0);
+        const uint32_t n_bins = 1u << min(bits, 8);
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) {
+          const uint32_t d = (key[i] - lo) >> shift;
+          if (key[i] != 0xffffffffu && key[i] >= lo && d < n_bins) atomicAdd(&s.hist[pass][d], 1);
+        }
+        __syncthreads();
+        const int32_t* bins = s.hist[pass];
+        if (n_cta > 1) {
+          cg::cluster_group cl = cg::this_cluster();
+          cl.sync();
+          for (int i = threadIdx.x; i < kBins; i += THREADS) {
+            int32_t sum = 0;
+            for (int c = 0; c < n_cta; ++c) sum += *cl.map_shared_rank(&s.hist[pass][i], c);
+            s.total[i] = sum;
+          }
+          __syncthreads();
+          bins = s.total;
+        }
+        // every warp alike: lane l has bins 8 l .. 8 l + 7; keys above a bin = suffix sums
+        int c[8], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          c[i] = bins[lane * 8 + i];
+          mine += c[i];
+        }
+        int above = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_down_sync(0xffffffffu, above, o);
+          if (lane + o < 32) above += y;
+        }
+        above -= mine;  // keys in the bins of higher lanes
+        int bin = -1, held = 0, left = 0;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+          if (bin < 0 && above < need && above + c[i] >= need) {
+            bin = lane * 8 + i;
+            held = c[i];
+            left = need - above;
+          }
+          above += c[i];
+        }
+        const int who = __ffs(__ballot_sync(0xffffffffu, bin >= 0)) - 1;  // one lane: the counts reach need
+        bin = __shfl_sync(0xffffffffu, bin, who);
+        held = __shfl_sync(0xffffffffu, held, who);
+        need = __shfl_sync(0xffffffffu, left, who);
+        lo += static_cast<uint32_t>(bin) << shift;
+        if (held == need) {  // the whole bin is kept: the cut lies below it
+          cut = lo - 1;
+          need = 0;
+          break;
+        }
+        if (shift == 0) {
+          cut = lo;
+          break;
+        }
+        bits = shift;
+      }
+    }
+  }
+  uint32_t keep = 0;  // bit i: slot first + 32 i is kept
+  int2 all;
+  {
+    int at = 0;
+    if (need > 0) {  // the same in all threads of the row
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) mine += __popc(__ballot_sync(0xffffffffu, key[i] == cut));
+      at = cluster_scan<kWarps>(make_int2(mine, 0), s, 0, n_cta, rank, &all).x;
+    }
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) {
+      bool k = key[i] > cut;
+      if (need > 0) {
+        const bool tie = key[i] == cut;
+        const uint32_t m = __ballot_sync(0xffffffffu, tie);
+        k = k || (tie && at + __popc(m & ((1u << lane) - 1u)) < need);
+        at += __popc(m);
+      }
+      keep |= static_cast<uint32_t>(k) << i;
     }
   }
   // holes and spares, numbered in order of slot
@@ -184,12 +276,9 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_consta
     nh += __popc(__ballot_sync(0xffffffffu, t < n && !k));
     ns += __popc(__ballot_sync(0xffffffffu, t >= n && k));
   }
-  int all_h, all_s;
-  int ah = cluster_scan(nh, s, turn, n_cta, rank, &all_h);
-  turn ^= 1;
-  int as = cluster_scan(ns, s, turn, n_cta, rank, &all_s);
-  turn ^= 1;
-  if (threadIdx.x == 0 && rank == 0) P.moves[row] = min(min(all_h, all_s), P.most);
+  const int2 start = cluster_scan<kWarps>(make_int2(nh, ns), s, 1, n_cta, rank, &all);
+  int ah = start.x, as = start.y;
+  if (threadIdx.x == 0 && rank == 0) P.moves[row] = min(min(all.x, all.y), P.most);
   int32_t* holes = P.holes + static_cast<int64_t>(row) * P.most;
   int32_t* spares = P.spares + static_cast<int64_t>(row) * P.most;
   const bool copy_acc = P.acc_out != P.acc_in, copy_pos = P.pos_out != P.pos_in;
@@ -210,16 +299,15 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_consta
       if (copy_pos) P.pos_out[meta + t] = P.pos_in[meta + t];
     }
   }
-  if (n_cta > 1) cg::this_cluster().sync();  // no CTA leaves while another may still write to its shared memory
+  if (n_cta > 1) cg::this_cluster().sync();  // no CTA leaves while another may still read its shared memory
 }
 
-constexpr int kMoveWarps = 8;
-constexpr int kMoveBatch = 4;
+constexpr int kMoveWarps = 2;
 
 template <int D>
 __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const __grid_constant__ EvictParams P) {
-  using T = uint16_t;                    // rows move as bits, whatever the type
-  constexpr int PIECES = D / 8;          // 16-byte pieces of a row
+  using T = uint16_t;                      // rows move as bits, whatever the type
+  constexpr int PIECES = D / 8;            // 16-byte pieces of a row
   constexpr int SIDE = 32 / (2 * PIECES);  // moves of a warp at a time: K on one half of the lanes, V on the other
   grid_dependency_wait();
   allow_dependents();
@@ -232,54 +320,54 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const __grid_cons
   const int64_t meta = static_cast<int64_t>(row) * P.pages.cap;
   const int32_t* table = P.pages.table + static_cast<int64_t>(b) * P.pages.max_pages;
   const bool is_v = lane >= 16;
-  uint4* pool = static_cast<uint4*>(is_v ? P.pages.v : P.pages.k);
   const int piece = lane % PIECES, side = (lane % 16) / PIECES;
-  const int step = gridDim.x * kMoveWarps * SIDE * kMoveBatch;
-  for (int i0 = (blockIdx.x * kMoveWarps + warp) * SIDE * kMoveBatch; i0 < M; i0 += step) {
-    int64_t to[kMoveBatch];
-    uint4 v[kMoveBatch];
-    int32_t hole[kMoveBatch], spare[kMoveBatch];
-#pragma unroll
-    for (int u = 0; u < kMoveBatch; ++u) {
-      const int i = i0 + u * SIDE + side;
-      hole[u] = spare[u] = -1;
-      if (i < M) {
-        hole[u] = holes[i];
-        spare[u] = spares[i];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kMoveBatch; ++u) {
-      to[u] = -1;
-      if (hole[u] < 0) continue;
+  T* pool = static_cast<T*>(is_v ? P.pages.v : P.pages.k);
+  __shared__ uint4 buf[kMoveWarps][32 / SIDE][32];
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&buf[warp][0][lane]));
+  const int step = gridDim.x * kMoveWarps * P.chunk;
+  for (int i0 = (blockIdx.x * kMoveWarps + warp) * P.chunk; i0 < M; i0 += step) {
+    // one lane works out one move: where from, where to; and moves the slot's weight and position
+    int64_t from = -1, to = -1;
+    if (lane < P.chunk && i0 + lane < M) {
+      const int hole = holes[i0 + lane], spare = spares[i0 + lane];
       const uint32_t ps = P.pages.page_size;
-      const uint32_t pt = static_cast<uint32_t>(hole[u]) / ps, pf = static_cast<uint32_t>(spare[u]) / ps;
-      const int64_t ot = slot_offset(P.pages, table[pt], hole[u] - pt * ps);
-      const int64_t of = slot_offset(P.pages, table[pf], spare[u] - pf * ps);
-      if (ot < 0 || of < 0) {
+      const uint32_t pt = static_cast<uint32_t>(hole) / ps, pf = static_cast<uint32_t>(spare) / ps;
+      const int32_t page_to = table[pt], page_from = table[pf];
+      const float w = P.acc_in[meta + spare];
+      const int32_t pos = P.pos_in[meta + spare];
+      to = slot_offset(P.pages, page_to, hole - pt * ps);
+      from = slot_offset(P.pages, page_from, spare - pf * ps);
+      if (to < 0 || from < 0) {
         atomicOr(P.pages.status, kErrInput);
-        continue;
+        to = from = -1;
+      } else {
+        const int64_t head = static_cast<int64_t>(h) * P.pages.head_stride;
+        to += head;
+        from += head;
+        if (!in_bounds(pool + from, D, pool, P.pages.extent, P.pages.status, kSitePool) ||
+            !in_bounds(pool + to, D, pool, P.pages.extent, P.pages.status, kSitePool))
+          to = from = -1;
       }
-      const int64_t from = of + static_cast<int64_t>(h) * P.pages.head_stride;
-      to[u] = ot + static_cast<int64_t>(h) * P.pages.head_stride;
-      const T* base = reinterpret_cast<const T*>(pool);
-      if (!in_bounds(base + from, D, base, P.pages.extent, P.pages.status, kSitePool) ||
-          !in_bounds(base + to[u], D, base, P.pages.extent, P.pages.status, kSitePool)) {
-        to[u] = -1;
-        continue;
-      }
-      v[u] = pool[from / 8 + piece];
+      P.acc_out[meta + hole] = w;
+      P.pos_out[meta + hole] = pos;
     }
-#pragma unroll
-    for (int u = 0; u < kMoveBatch; ++u)
-      if (to[u] >= 0) pool[to[u] / 8 + piece] = v[u];
-    if (piece == 0) {
-#pragma unroll
-      for (int u = 0; u < kMoveBatch; ++u)
-        if (hole[u] >= 0) {
-          if (is_v) P.pos_out[meta + hole[u]] = P.pos_in[meta + spare[u]];
-          else P.acc_out[meta + hole[u]] = P.acc_in[meta + spare[u]];
-        }
+    // the rows come in together, 16 bytes a lane and copy, and leave together
+    const int n = min(P.chunk, M - i0);
+#pragma unroll 4
+    for (int c = 0; c < n; c += SIDE) {
+      const int m = c + side;
+      const int64_t f = __shfl_sync(0xffffffffu, from, m & 31);
+      if (m < n && f >= 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + (c / SIDE) * 512u),
+                     "l"(reinterpret_cast<const uint4*>(pool + f) + piece)
+                     : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // a lane reads back what it copied itself
+#pragma unroll 4
+    for (int c = 0; c < n; c += SIDE) {
+      const int m = c + side;
+      const int64_t t = __shfl_sync(0xffffffffu, to, m & 31);
+      if (m < n && t >= 0) reinterpret_cast<uint4*>(pool + t)[piece] = buf[warp][c / SIDE][lane];
     }
   }
 }
@@ -309,11 +397,11 @@ svx_status sizes(const svx_pages* c, int32_t n_req, int64_t max_len, int32_t bud
   return SVX_OK;
 }
 
-template <int KEYS>
+template <int KEYS, int THREADS>
 cudaError_t launch_select(const EvictParams& p, int rows, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows) * p.cluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -324,7 +412,38 @@ cudaError_t launch_select(const EvictParams& p, int rows, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<KEYS>, p);
+  return cudaLaunchKernelEx(&cfg, select_kernel<KEYS, THREADS>, p);
+}
+
+// Threads and CTAs of a row: up to kSmallRow slots 256 threads (a barrier of 8 warps), above 1024; a cluster of CTAs
+// where one does not hold the row, or where there are SMs for it and it shortens a thread's part.
+constexpr int kSmallRow = 256 * 16;
+cudaError_t launch_selects(EvictParams& p, int rows, int sms, cudaStream_t s) {
+  const int threads = p.max_len <= kSmallRow ? 256 : 1024;
+  p.cluster = 1;
+  auto keys = [&](int c) { return (p.max_len + c * threads - 1) / (c * threads); };
+  while (p.cluster < kMaxCluster &&
+         (keys(p.cluster) > kMaxKeys || (keys(p.cluster) > kSplitKeys && rows * p.cluster * 2 <= sms)))
+    p.cluster *= 2;
+  const int per = keys(p.cluster);
+  if (threads == 256)
+    return per <= 4 ? launch_select<4, 256>(p, rows, s) : per <= 8 ? launch_select<8, 256>(p, rows, s)
+                                                                    : launch_select<16, 256>(p, rows, s);
+  return per <= 4    ? launch_select<4, 1024>(p, rows, s)
+         : per <= 8  ? launch_select<8, 1024>(p, rows, s)
+         : per <= 16 ? launch_select<16, 1024>(p, rows, s)
+                     : launch_select<32, 1024>(p, rows, s);
+}
+
+cudaError_t launch_moves(EvictParams& p, int head_dim, int rows, int sms, cudaStream_t s) {
+  // moves of a warp: as many as it looks up at a time, fewer where that leaves SMs without a warp
+  p.chunk = 32;
+  while (p.chunk > 8 && static_cast<int64_t>(rows) * p.most < static_cast<int64_t>(p.chunk) * sms * kMoveWarps) p.chunk /= 2;
+  const int per_cta = kMoveWarps * p.chunk;
+  const int want = (p.most + per_cta - 1) / per_cta, room = std::max(1, 16 * sms / rows);
+  const dim3 grid(static_cast<unsigned>(std::max(1, std::min(want, room))), static_cast<unsigned>(rows));
+  return head_dim == 128 ? launch_pdl(move_kernel<128>, grid, dim3(kMoveWarps * 32), 0, s, p)
+                         : launch_pdl(move_kernel<64>, grid, dim3(kMoveWarps * 32), 0, s, p);
 }
 
 }  // namespace
@@ -396,24 +515,9 @@ extern "C" svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, con
   p.recent = recent;
   p.most = z.most;
   const int rows = n_req * p.pages.n_kv_heads;
-  p.cluster = 1;
-  while (p.cluster * svx::kThreads * svx::kMaxKeys < z.max_len) p.cluster *= 2;
-  const int per = (z.max_len + p.cluster * svx::kThreads - 1) / (p.cluster * svx::kThreads);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = per <= 2    ? svx::launch_select<2>(p, rows, s)
-                  : per <= 4  ? svx::launch_select<4>(p, rows, s)
-                  : per <= 8  ? svx::launch_select<8>(p, rows, s)
-                  : per <= 16 ? svx::launch_select<16>(p, rows, s)
-                              : svx::launch_select<32>(p, rows, s);
-  if (e == cudaSuccess) {
-    // enough CTAs for a row's most moves, no more than about eight per SM over all rows
-    const int side = cache->head_dim == 128 ? 1 : 2;
-    const int per_cta = svx::kMoveWarps * svx::kMoveBatch * side;
-    const int want = (z.most + per_cta - 1) / per_cta, room = std::max(1, 8 * sms / rows);
-    const dim3 grid(static_cast<unsigned>(std::max(1, std::min(want, room))), static_cast<unsigned>(rows));
-    e = cache->head_dim == 128 ? svx::launch_pdl(svx::move_kernel<128>, grid, dim3(svx::kMoveWarps * 32), 0, s, p)
-                               : svx::launch_pdl(svx::move_kernel<64>, grid, dim3(svx::kMoveWarps * 32), 0, s, p);
-  }
+  cudaError_t e = svx::launch_selects(p, rows, sms, s);
+  if (e == cudaSuccess) e = svx::launch_moves(p, cache->head_dim, rows, sms, s);
   if (e != cudaSuccess) return paged_fail(SVX_ERR_CUDA, "evict kernel launch failed: %s", cudaGetErrorString(e));
   return SVX_OK;
 }

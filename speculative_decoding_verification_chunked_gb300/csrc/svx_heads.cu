@@ -13,15 +13,19 @@
 //
 // Layout.  A head is d / 16 lanes; a lane holds 16 elements as two 16-byte vectors, chosen so that both members
 // of each rotated pair sit in one lane: vectors l and l + rot/16 of the rotated part, or two neighbouring vectors of the
-// rest.  So a rotation needs no shuffle, a norm three (d = 128).  A lane's eight angles are computed once and serve
-// all heads that its group of lanes walks (up to kMaxWalk of a token, loads of kBatch in flight).
+// rest.  So a rotation needs no shuffle, a norm three (d = 128).  A warp takes 4 (d = 128) or 8 tokens and walks up to
+// kMaxWalk heads of one kind (q, k or v) of them; a lane's eight angles and its weights become 32 factors once for the
+// whole walk, which leaves three operations an element besides the sum of squares.
 #include "svx_paged.h"
 
 namespace svx {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBatch = 4;
+constexpr int kThreads = 128;
+constexpr int kCtas = 4;  // per SM
+constexpr int kMaxWalk = 8;
+constexpr double kFill = 0.5;
+constexpr int kBig = 4;
 
 struct HeadsParams {
   const void *q, *k, *v;
@@ -40,9 +44,9 @@ struct HeadsParams {
   int64_t q_ext, k_ext, v_ext;  // elements of the inputs (checked build)
   float eps, scale;
   int32_t n_tok, n_q, n_kv;
-  int32_t heads;                // n_q + n_kv, + n_kv with v
-  int32_t walk;                 // heads that a group of lanes walks
-  int32_t groups;               // groups of lanes per token: ceil(heads / walk)
+  int32_t walk;                 // heads that a warp walks
+  int32_t q_parts, kv_parts;    // warps per block of tokens for the heads of q, of k (and of v)
+  int32_t parts;                // all of them
   int32_t rot_dim, neighbours, norm, paged;
 };
 
@@ -83,178 +87,207 @@ __device__ __forceinline__ uint4 pack(const float* f) {
                     Pair<T>::down(f[6], f[7]));
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__ HeadsParams P) {
-  constexpr int LANES = D / 16;  // lanes per head
+template <typename T, int D, int kBatch>
+__global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_constant__ HeadsParams P) {
+  constexpr int LANES = D / 16;       // lanes per head
+  constexpr int TOKENS = 32 / LANES;  // tokens of a warp
   grid_dependency_wait();
   allow_dependents();
-  const int64_t id = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
+  const int64_t gw = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t block = gw / P.parts;
+  const int part = static_cast<int>(gw - block * P.parts);  // which heads: the same for the whole warp
   const int lane = threadIdx.x % LANES;
-  int64_t token = id / P.groups;
-  const int group = static_cast<int>(id - token * P.groups);
+  int64_t token = block * TOKENS + (threadIdx.x & 31) / LANES;
   bool live = token < P.tokens;
   if (!live) token = 0;
   const int b = static_cast<int>(token / P.n_tok);
   const int j = static_cast<int>(token - static_cast<int64_t>(b) * P.n_tok);
-  const int nvec = P.rot_dim / 16;  // vectors in one half of the rotated part
-  const int v0 = lane < nvec ? lane : 2 * nvec + 2 * (lane - nvec);
-  const int v1 = lane < nvec ? lane + nvec : v0 + 1;
-  const bool turn = lane < nvec;
-
   if (live && P.n_new) {
     const int n = P.n_new[b];
-    if (n < 0 || n > P.n_tok) {
-      if (P.status && j == 0 && group == 0 && lane == 0) atomicOr(P.status, kErrInput);
-    }
+    if (P.status && (n < 0 || n > P.n_tok) && j == 0 && part == 0 && lane == 0) atomicOr(P.status, kErrInput);
     live = j < n;
   }
-  // where K and V of this token go: an element offset into the pages, or the dense row
-  int64_t kv_row = -1;
+  // the part's heads: of q, of k or of v
+  const bool is_q = part < P.q_parts, is_v = part >= P.q_parts + P.kv_parts;
+  const int h0 = (is_q ? part : part - P.q_parts - (is_v ? P.kv_parts : 0)) * P.walk;
+  const int count = min(P.walk, (is_q ? P.n_q : P.n_kv) - h0);
+  const T* in = static_cast<const T*>(is_q ? P.q : is_v ? P.v : P.k);
+  const int64_t in_ext = is_q ? P.q_ext : is_v ? P.v_ext : P.k_ext;
+  const T* src = in + token * (is_q ? P.q_stride : is_v ? P.v_stride : P.k_stride) + static_cast<int64_t>(h0) * D;
+
+  // this lane's vectors
+  const int nvec = P.rot_dim / 16;  // vectors in one half of the rotated part
+  const bool turn = lane < nvec;
+  const int v0 = turn ? lane : 2 * nvec + 2 * (lane - nvec);
+  const int v1 = turn ? lane + nvec : v0 + 1;
+  auto load = [&](int i, uint4 (&raw)[2]) {
+    raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+    if (live && i < count && in_bounds(src + i * D, D, in, in_ext, P.status, kSiteHeadsIn)) {
+      raw[0] = __ldg(reinterpret_cast<const uint4*>(src + i * D) + v0);
+      raw[1] = __ldg(reinterpret_cast<const uint4*>(src + i * D) + v1);
+    }
+  };
+  uint4 next[kBatch][2];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) load(u, next[u]);
+
+  // where the heads go: dst + i * step
+  T* out = nullptr;
+  int64_t at = -1, step = D, out_ext = 0;
   int32_t slot = 0;
   const int32_t pos = P.pos[token];
-  if (P.paged) {
-    if (live) {
-      const int64_t s = static_cast<int64_t>(P.start[b]) + j;
-      if (s >= 0 && s < P.pages.cap) {
-        slot = static_cast<int32_t>(s);
-        const uint32_t pg = static_cast<uint32_t>(slot) / static_cast<uint32_t>(P.pages.page_size);
-        kv_row = slot_offset(P.pages, P.pages.table[static_cast<int64_t>(b) * P.pages.max_pages + pg],
-                             static_cast<uint32_t>(slot) - pg * P.pages.page_size);
-      }
-      if (kv_row < 0 && group == 0 && lane == 0) atomicOr(P.pages.status, kErrInput);
+  if (is_q) {
+    out = static_cast<T*>(P.q_out);
+    step = static_cast<int64_t>(P.n_tok) * D;
+    at = ((static_cast<int64_t>(b) * P.n_q + h0) * P.n_tok + j) * D;
+    out_ext = P.tokens * P.n_q * D;
+  } else if (!P.paged) {
+    out = static_cast<T*>(is_v ? P.v_out : P.k_out);
+    at = (token * P.n_kv + h0) * D;
+    out_ext = P.tokens * P.n_kv * D;
+  } else if (live) {
+    out = static_cast<T*>(is_v ? P.pages.v : P.pages.k);
+    step = P.pages.head_stride;
+    out_ext = P.pages.extent;
+    const int64_t s = static_cast<int64_t>(P.start[b]) + j;
+    if (s >= 0 && s < P.pages.cap) {
+      slot = static_cast<int32_t>(s);
+      const uint32_t pg = static_cast<uint32_t>(slot) / static_cast<uint32_t>(P.pages.page_size);
+      at = slot_offset(P.pages, P.pages.table[static_cast<int64_t>(b) * P.pages.max_pages + pg],
+                       static_cast<uint32_t>(slot) - pg * P.pages.page_size);
     }
-  } else {
-    kv_row = token * P.n_kv * D;
-  }
-
-  // a lane's angles: pairs 8 lane .. 8 lane + 7 (halves), or 4 v0 .. and 4 v1 .. (neighbours)
-  float cs[8], sn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-    if (turn) {
-      const int f = P.neighbours ? (i < 4 ? 4 * v0 + i : 4 * v1 + i - 4) : 8 * lane + i;
-      const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[f];
-      // half-turns in [-1, 1): |error| <= 2^-25 of a half-turn from the conversion
-      const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
-      sincospif(half_turns, &sn[i], &cs[i]);
-      cs[i] *= P.scale;
-      sn[i] *= P.scale;
+    if (at < 0) {
+      if (lane == 0) atomicOr(P.pages.status, kErrInput);
+    } else {
+      at += h0 * step;
     }
   }
+  if (at < 0) live = false;
 
-  const int n_qk = P.n_q + P.n_kv;
-  const int64_t row_q = token * P.q_stride, row_k = token * P.k_stride, row_v = token * P.v_stride;
-  for (int i0 = 0; i0 < P.walk; i0 += kBatch) {
-    uint4 raw[kBatch][2];
+  if (is_v) {
+    for (int i0 = 0; i0 < P.walk; i0 += kBatch) {
+      uint4 raw[kBatch][2];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int h = group + (i0 + u) * P.groups;
-      raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
-      if (i0 + u < P.walk && live && h < P.heads) {
-        const T* src = h < P.n_q    ? static_cast<const T*>(P.q) + row_q + static_cast<int64_t>(h) * D
-                       : h < n_qk ? static_cast<const T*>(P.k) + row_k + static_cast<int64_t>(h - P.n_q) * D
-                                  : static_cast<const T*>(P.v) + row_v + static_cast<int64_t>(h - n_qk) * D;
-        if (in_bounds(src, D, static_cast<const T*>(h < P.n_q ? P.q : h < n_qk ? P.k : P.v),
-                      h < P.n_q ? P.q_ext : h < n_qk ? P.k_ext : P.v_ext, P.status, kSiteHeadsIn)) {
-          raw[u][0] = __ldg(reinterpret_cast<const uint4*>(src) + v0);
-          raw[u][1] = __ldg(reinterpret_cast<const uint4*>(src) + v1);
+      for (int u = 0; u < kBatch; ++u) raw[u][0] = next[u][0], raw[u][1] = next[u][1];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) load(i0 + kBatch + u, next[u]);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        T* dst = out + at + (i0 + u) * step;
+        if (live && i0 + u < count && in_bounds(dst, D, out, out_ext, P.status, kSitePool)) {
+          reinterpret_cast<uint4*>(dst)[v0] = raw[u][0];
+          reinterpret_cast<uint4*>(dst)[v1] = raw[u][1];
         }
       }
     }
+    return;
+  }
+
+  // a lane's factors, weights included: z_a = r (x_a fa - x_b fb), z_b = r (x_b ga + x_a gb)
+  // pairs 8 lane .. 8 lane + 7 (halves), or 4 v0 .. and 4 v1 .. (neighbours)
+  float fa[8], fb[8], ga[8], gb[8];
+  {
+    float w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = 1.f;
+    if (const T* wp = static_cast<const T*>(is_q ? P.q_norm : P.k_norm)) {
+      unpack<T>(__ldg(reinterpret_cast<const uint4*>(wp) + v0), w);
+      unpack<T>(__ldg(reinterpret_cast<const uint4*>(wp) + v1), w + 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float wa = P.neighbours && turn ? w[2 * i] : w[i], wb = P.neighbours && turn ? w[2 * i + 1] : w[8 + i];
+      fa[i] = wa;
+      ga[i] = wb;
+      fb[i] = gb[i] = 0.f;
+      if (turn) {
+        const int f = P.neighbours ? (i < 4 ? 4 * v0 + i : 4 * v1 + i - 4) : 8 * lane + i;
+        const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[f];
+        // half-turns in [-1, 1): |error| <= 2^-25 of a half-turn from the conversion
+        const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
+        float sn, cs;
+        sincospif(half_turns, &sn, &cs);
+        sn *= P.scale;
+        cs *= P.scale;
+        fa[i] = wa * cs;
+        fb[i] = wb * sn;
+        ga[i] = wb * cs;
+        gb[i] = wa * sn;
+      }
+    }
+  }
+
+  for (int i0 = 0; i0 < P.walk; i0 += kBatch) {
+    uint4 raw[kBatch][2];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) raw[u][0] = next[u][0], raw[u][1] = next[u][1];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) load(i0 + kBatch + u, next[u]);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int h = group + (i0 + u) * P.groups;
-      if (i0 + u >= P.walk) break;  // the same for all lanes
-      const bool here = live && h < P.heads;
-      const bool is_v = h >= n_qk;
       float x[16];
       unpack<T>(raw[u][0], x);
       unpack<T>(raw[u][1], x + 8);
+      float r = 1.f;
       if (P.norm) {  // all lanes of the warp take part in the shuffles
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (here && !is_v) {
-          const float r = rsqrtf(ss * (1.f / D) + P.eps);
-          const T* w = static_cast<const T*>(h < P.n_q ? P.q_norm : P.k_norm);
-          float g[16];
-          if (w) {
-            unpack<T>(__ldg(reinterpret_cast<const uint4*>(w) + v0), g);
-            unpack<T>(__ldg(reinterpret_cast<const uint4*>(w) + v1), g + 8);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = 1.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = x[i] * r * g[i];
-        }
+        r = rsqrtf(fmaf(ss, 1.f / D, P.eps));
       }
-      if (!here) continue;
-      uint4 out[2] = {raw[u][0], raw[u][1]};
-      if (!is_v) {
-        if (turn) {
-          if (P.neighbours) {
+      if (!turn) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a = x[2 * i], c = x[2 * i + 1];
-              x[2 * i] = a * cs[i] - c * sn[i];
-              x[2 * i + 1] = c * cs[i] + a * sn[i];
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a = x[i], c = x[8 + i];
-              x[i] = a * cs[i] - c * sn[i];
-              x[8 + i] = c * cs[i] + a * sn[i];
-            }
-          }
+        for (int i = 0; i < 8; ++i) {
+          x[i] = x[i] * r * fa[i];
+          x[8 + i] = x[8 + i] * r * ga[i];
         }
-        out[0] = pack<T>(x);
-        out[1] = pack<T>(x + 8);
-      }
-      T* dst;
-      if (h < P.n_q) {
-        dst = static_cast<T*>(P.q_out) + ((static_cast<int64_t>(b) * P.n_q + h) * P.n_tok + j) * D;
-        if (!in_bounds(dst, D, static_cast<T*>(P.q_out), P.tokens * P.n_q * D, P.status, kSiteHeadsOut)) continue;
+      } else if (P.neighbours) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = x[2 * i], c = x[2 * i + 1];
+          x[2 * i] = (a * fa[i] - c * fb[i]) * r;
+          x[2 * i + 1] = (c * ga[i] + a * gb[i]) * r;
+        }
       } else {
-        if (kv_row < 0) continue;
-        const int hk = is_v ? h - n_qk : h - P.n_q;
-        if (P.paged) {
-          T* base = static_cast<T*>(is_v ? P.pages.v : P.pages.k);
-          dst = base + kv_row + static_cast<int64_t>(hk) * P.pages.head_stride;
-          if (!in_bounds(dst, D, base, P.pages.extent, P.status, kSitePool)) continue;
-          if (!is_v && lane == 0) {
-            const int64_t m = (static_cast<int64_t>(b) * P.n_kv + hk) * P.pages.cap + slot;
-            if (P.acc) P.acc[m] = 0.f;
-            if (P.slot_pos) P.slot_pos[m] = pos;
-          }
-        } else {
-          T* base = static_cast<T*>(is_v ? P.v_out : P.k_out);
-          dst = base + kv_row + static_cast<int64_t>(hk) * D;
-          if (!in_bounds(dst, D, base, P.tokens * P.n_kv * D, P.status, kSiteHeadsOut)) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = x[i], c = x[8 + i];
+          x[i] = (a * fa[i] - c * fb[i]) * r;
+          x[8 + i] = (c * ga[i] + a * gb[i]) * r;
         }
       }
-      reinterpret_cast<uint4*>(dst)[v0] = out[0];
-      reinterpret_cast<uint4*>(dst)[v1] = out[1];
+      T* dst = out + at + (i0 + u) * step;
+      if (!live || i0 + u >= count || !in_bounds(dst, D, out, out_ext, P.status, kSiteHeadsOut)) continue;
+      reinterpret_cast<uint4*>(dst)[v0] = pack<T>(x);
+      reinterpret_cast<uint4*>(dst)[v1] = pack<T>(x + 8);
+      if (P.paged && !is_q && lane == 0) {
+        const int64_t m = (static_cast<int64_t>(b) * P.n_kv + h0 + i0 + u) * P.pages.cap + slot;
+        if (P.acc) P.acc[m] = 0.f;
+        if (P.slot_pos) P.slot_pos[m] = pos;
+      }
     }
   }
 }
 
 template <typename T, int D>
 cudaError_t launch(HeadsParams& p, cudaStream_t stream, int sms) {
-  // Heads per group of lanes: one where tokens are few (latency: every head its own lanes), more once the
-  // grid fills the card anyway, so that a lane's eight sines and cosines serve several heads.
-  const int64_t lanes = p.tokens * p.heads * (D / 16);
-  const int64_t room = static_cast<int64_t>(sms) * 1024;
-  p.walk = lanes >= 8 * room ? 8 : lanes >= 4 * room ? 4 : lanes >= 2 * room ? 2 : 1;
-  p.groups = (p.heads + p.walk - 1) / p.walk;
-  const int64_t blocks = (p.tokens * p.groups * (D / 16) + kThreads - 1) / kThreads;
+  // Heads that a warp walks (its tokens' heads of one kind): one where tokens are few (latency: every head its own
+  // warp), more once the grid fills the card anyway, so that a lane's eight sines and cosines serve several heads.
+  const int64_t blocks_of_tokens = (p.tokens * (D / 16) + 31) / 32;
+  const int64_t room = static_cast<int64_t>(sms) * 32;  // warps
+  const int64_t warps = blocks_of_tokens * (p.n_q + p.n_kv);
+  p.walk = 1;
+  while (p.walk < kMaxWalk && warps >= kFill * room * p.walk) p.walk *= 2;
+  p.q_parts = (p.n_q + p.walk - 1) / p.walk;
+  p.kv_parts = (p.n_kv + p.walk - 1) / p.walk;
+  p.parts = p.q_parts + (p.v ? 2 : 1) * p.kv_parts;
+  const int64_t blocks = (blocks_of_tokens * p.parts + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(heads_kernel<T, D>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, p);
+  // heads loaded ahead of the ones at work
+  auto kernel = p.walk >= kBig ? heads_kernel<T, D, kBig> : heads_kernel<T, D, 1>;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, p);
 }
 
 struct Range {
@@ -361,7 +394,6 @@ svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages*
   p.n_tok = in->n_tok;
   p.n_q = in->n_q_heads;
   p.n_kv = in->n_kv_heads;
-  p.heads = in->n_q_heads + (has_v ? 2 : 1) * in->n_kv_heads;
   p.rot_dim = rope->rot_dim;
   p.neighbours = rope->neighbours;
   p.norm = in->eps >= 0.f;
