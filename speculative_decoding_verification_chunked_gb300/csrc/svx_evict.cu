@@ -28,7 +28,7 @@ namespace {
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxKeys = 32;    // per thread
 constexpr int kMaxCluster = 8;  // portable
-constexpr int kSplitKeys = 8;
+constexpr int kSplitKeys = 16;
 static_assert(kMaxThreads * kMaxKeys * kMaxCluster == SVX_EVICT_MAX_LEN, "the longest row a cluster holds");
 
 struct EvictParams {
@@ -62,7 +62,7 @@ constexpr int kPasses = 4;  // 8 bits of a 32-bit range each
 
 struct Shared {
   int32_t hist[kPasses][kBins];  // a pass has its own, so that none is cleared while a peer may still read it
-  int32_t total[kBins];          // over the cluster
+  int3 found[kPasses];           // bin, its keys, how many of them are kept
   uint2 warp_range[32];
   uint2 peer_range;
   int32_t warp_protected[32];
@@ -70,6 +70,17 @@ struct Shared {
   int2 warp_scan[2][32];
   int2 peer_scan[2];
 };
+
+// Sum of the lower lanes' values.
+__device__ __forceinline__ int warp_before(int v, int lane) {
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x - v;
+}
 
 // Sums of the values of the warps before this one, in the order (CTA of the cluster, warp); `total` gets all.
 // `turn`: a buffer of its own for each use.  In a cluster, every look into a peer's shared memory follows a
@@ -181,57 +192,44 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     } else {
       // up to 256 equal bins, a power of two wide, of [lo, hi], then of the bin in which the need-th largest lies, until
       // all of a bin is kept or it holds one value.  (As L > n, some key is not protected: lo <= hi.)
-      int bits = 32 - __clz(hi - lo);  // keys in question are less than 2^bits above lo
+      uint32_t span = hi - lo;  // the keys in question: lo .. lo + span
       for (int pass = 0;; ++pass) {
-        const int shift = max(bits - 8, 0);
-        const uint32_t n_bins = 1u << min(bits, 8);
+        const int shift = max(24 - __clz(span), 0);
 #pragma unroll
         for (int i = 0; i < KEYS; ++i) {
-          const uint32_t d = (key[i] - lo) >> shift;
-          if (key[i] != 0xffffffffu && key[i] >= lo && d < n_bins) atomicAdd(&s.hist[pass][d], 1);
+          const uint32_t d = key[i] - lo;  // keys below lo wrap to more than span
+          if (d <= span) atomicAdd(&s.hist[pass][d >> shift], 1);
         }
         __syncthreads();
-        const int32_t* bins = s.hist[pass];
-        if (n_cta > 1) {
-          cg::cluster_group cl = cg::this_cluster();
-          cl.sync();
-          for (int i = threadIdx.x; i < kBins; i += THREADS) {
-            int32_t sum = 0;
-            for (int c = 0; c < n_cta; ++c) sum += *cl.map_shared_rank(&s.hist[pass][i], c);
-            s.total[i] = sum;
+        if (n_cta > 1) cg::this_cluster().sync();
+        if (warp == 0) {  // lane l has bins 8 l .. 8 l + 7; keys above a bin = suffix sums
+          int c[8] = {};
+          for (int peer = 0; peer < n_cta; ++peer) {
+            const int32_t* bins = n_cta > 1 ? cg::this_cluster().map_shared_rank(s.hist[pass], peer) : s.hist[pass];
+            const int4 x = reinterpret_cast<const int4*>(bins)[2 * lane], y = reinterpret_cast<const int4*>(bins)[2 * lane + 1];
+            c[0] += x.x, c[1] += x.y, c[2] += x.z, c[3] += x.w, c[4] += y.x, c[5] += y.y, c[6] += y.z, c[7] += y.w;
           }
-          __syncthreads();
-          bins = s.total;
-        }
-        // every warp alike: lane l has bins 8 l .. 8 l + 7; keys above a bin = suffix sums
-        int c[8], mine = 0;
+          int above = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          c[i] = bins[lane * 8 + i];
-          mine += c[i];
-        }
-        int above = mine;
+          for (int i = 0; i < 8; ++i) above += c[i];
+          const int mine = above;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_down_sync(0xffffffffu, above, o);
-          if (lane + o < 32) above += y;
-        }
-        above -= mine;  // keys in the bins of higher lanes
-        int bin = -1, held = 0, left = 0;
-#pragma unroll
-        for (int i = 7; i >= 0; --i) {
-          if (bin < 0 && above < need && above + c[i] >= need) {
-            bin = lane * 8 + i;
-            held = c[i];
-            left = need - above;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_down_sync(0xffffffffu, above, o);
+            if (lane + o < 32) above += y;
           }
-          above += c[i];
+          above -= mine;  // keys in the bins of higher lanes
+#pragma unroll
+          for (int i = 7; i >= 0; --i) {
+            // one bin of one lane, as the counts reach need
+            if (above < need && above + c[i] >= need) s.found[pass] = make_int3(lane * 8 + i, c[i], need - above);
+            above += c[i];
+          }
         }
-        const int who = __ffs(__ballot_sync(0xffffffffu, bin >= 0)) - 1;  // one lane: the counts reach need
-        bin = __shfl_sync(0xffffffffu, bin, who);
-        held = __shfl_sync(0xffffffffu, held, who);
-        need = __shfl_sync(0xffffffffu, left, who);
-        lo += static_cast<uint32_t>(bin) << shift;
+        __syncthreads();
+        const int held = s.found[pass].y;
+        need = s.found[pass].z;
+        lo += static_cast<uint32_t>(s.found[pass].x) << shift;
         if (held == need) {  // the whole bin is kept: the cut lies below it
           cut = lo - 1;
           need = 0;
@@ -241,62 +239,75 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
           cut = lo;
           break;
         }
-        bits = shift;
+        span = min((1u << shift) - 1u, hi - lo);  // (protected keys lie above hi, and the wrap behind them)
       }
     }
   }
-  uint32_t keep = 0;  // bit i: slot first + 32 i is kept
-  int2 all;
-  {
-    int at = 0;
-    if (need > 0) {  // the same in all threads of the row
-      int mine = 0;
-#pragma unroll
-      for (int i = 0; i < KEYS; ++i) mine += __popc(__ballot_sync(0xffffffffu, key[i] == cut));
-      at = cluster_scan<kWarps>(make_int2(mine, 0), s, 0, n_cta, rank, &all).x;
-    }
-#pragma unroll
-    for (int i = 0; i < KEYS; ++i) {
-      bool k = key[i] > cut;
-      if (need > 0) {
-        const bool tie = key[i] == cut;
-        const uint32_t m = __ballot_sync(0xffffffffu, tie);
-        k = k || (tie && at + __popc(m & ((1u << lane) - 1u)) < need);
-        at += __popc(m);
-      }
-      keep |= static_cast<uint32_t>(k) << i;
-    }
-  }
-  // holes and spares, numbered in order of slot
-  int nh = 0, ns = 0;
+  // From here lane i speaks for the 32 slots base .. base + 31, of which lane j held the j-th in key[i]: bit j of its
+  // words.  So ties, holes and spares are counted once a word, and one scan over the lanes numbers them.
+  const int base = first - lane + 32 * lane;
+  uint32_t keep = 0, tie = 0;
 #pragma unroll
   for (int i = 0; i < KEYS; ++i) {
-    const int t = first + 32 * i;
-    const bool k = (keep >> i) & 1u;
-    nh += __popc(__ballot_sync(0xffffffffu, t < n && !k));
-    ns += __popc(__ballot_sync(0xffffffffu, t >= n && k));
+    const uint32_t m = __ballot_sync(0xffffffffu, key[i] > cut);
+    if (lane == i) keep = m;
   }
-  const int2 start = cluster_scan<kWarps>(make_int2(nh, ns), s, 1, n_cta, rank, &all);
-  int ah = start.x, as = start.y;
+  int2 all;
+  if (need > 0) {  // the same in all threads of the row
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) {
+      const uint32_t m = __ballot_sync(0xffffffffu, key[i] == cut);
+      if (lane == i) tie = m;
+    }
+    const int mine = __popc(tie);
+    int at = warp_before(mine, lane);
+    at += cluster_scan<kWarps>(make_int2(__shfl_sync(0xffffffffu, at + mine, 31), 0), s, 0, n_cta, rank, &all).x;
+    // the first need - at of them
+    for (int left = need - at; __popc(tie) > max(left, 0);) tie &= ~(0x80000000u >> __clz(tie));
+    keep |= tie;
+  }
+  const int in_front = min(max(n - base, 0), 32);
+  const uint32_t front = in_front == 32 ? 0xffffffffu : (1u << in_front) - 1u;  // slots < n
+  uint32_t hole = lane < KEYS ? front & ~keep : 0u, spare = keep & ~front;
+  int ah = warp_before(__popc(hole), lane), as = warp_before(__popc(spare), lane);
+  const int2 warp_all = make_int2(__shfl_sync(0xffffffffu, ah + __popc(hole), 31), __shfl_sync(0xffffffffu, as + __popc(spare), 31));
+  const int2 start = cluster_scan<kWarps>(warp_all, s, 1, n_cta, rank, &all);
+  ah += start.x;
+  as += start.y;
   if (threadIdx.x == 0 && rank == 0) P.moves[row] = min(min(all.x, all.y), P.most);
   int32_t* holes = P.holes + static_cast<int64_t>(row) * P.most;
   int32_t* spares = P.spares + static_cast<int64_t>(row) * P.most;
-  const bool copy_acc = P.acc_out != P.acc_in, copy_pos = P.pos_out != P.pos_in;
   const uint32_t before = (1u << lane) - 1u;
 #pragma unroll
   for (int i = 0; i < KEYS; ++i) {
-    const int t = first + 32 * i;
-    const bool k = (keep >> i) & 1u;
-    const bool hole = t < n && !k, spare = t >= n && k;
-    const uint32_t mh = __ballot_sync(0xffffffffu, hole), ms = __ballot_sync(0xffffffffu, spare);
-    const int ih = ah + __popc(mh & before), is = as + __popc(ms & before);
-    ah += __popc(mh);
-    as += __popc(ms);
-    if (hole && ih < P.most) holes[ih] = t;
-    if (spare && is < P.most) spares[is] = t;
-    if (t < n && k) {
-      if (copy_acc) P.acc_out[meta + t] = P.acc_in[meta + t];
-      if (copy_pos) P.pos_out[meta + t] = P.pos_in[meta + t];
+    const uint32_t mh = __shfl_sync(0xffffffffu, hole, i), ms = __shfl_sync(0xffffffffu, spare, i);
+    const int ih = __shfl_sync(0xffffffffu, ah, i) + __popc(mh & before), is = __shfl_sync(0xffffffffu, as, i) + __popc(ms & before);
+    if ((mh >> lane & 1u) && ih < P.most) holes[ih] = first + 32 * i;
+    if ((ms >> lane & 1u) && is < P.most) spares[is] = first + 32 * i;
+  }
+  // weights and positions of the slots that stay where they are
+  const bool copy_acc = P.acc_out != P.acc_in, copy_pos = P.pos_out != P.pos_in;
+  if (copy_acc || copy_pos) {
+    keep &= front;
+#pragma unroll
+    for (int i0 = 0; i0 < KEYS; i0 += LOADS) {
+      if (first - lane + 32 * i0 >= n) break;  // the same for the warp
+      float w[LOADS];
+      int32_t pos[LOADS];
+      uint32_t stays = 0;
+#pragma unroll
+      for (int u = 0; u < LOADS; ++u) {  // together, ahead of the stores
+        const int64_t t = meta + first + 32 * (i0 + u);
+        stays |= (__shfl_sync(0xffffffffu, keep, i0 + u) >> lane & 1u) << u;
+        if (copy_acc && (stays >> u & 1u)) w[u] = P.acc_in[t];
+        if (copy_pos && (stays >> u & 1u)) pos[u] = P.pos_in[t];
+      }
+#pragma unroll
+      for (int u = 0; u < LOADS; ++u) {
+        const int64_t t = meta + first + 32 * (i0 + u);
+        if (copy_acc && (stays >> u & 1u)) P.acc_out[t] = w[u];
+        if (copy_pos && (stays >> u & 1u)) P.pos_out[t] = pos[u];
+      }
     }
   }
   if (n_cta > 1) cg::this_cluster().sync();  // no CTA leaves while another may still read its shared memory
