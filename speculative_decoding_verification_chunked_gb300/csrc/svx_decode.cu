@@ -25,6 +25,7 @@
 #include "svx_paged.h"
 
 #include <algorithm>
+#include <atomic>
 
 namespace svx {
 namespace {
@@ -621,12 +622,13 @@ constexpr int kMinChunks = 2 * kWarps;
 template <typename T, int D, bool WIDE, bool SCORES>
 cudaError_t launch_attend(const DecodeParams& p, int device, cudaStream_t s) {
   constexpr int bytes = Smem<D>::BYTES;
-  // set on each device's first use; setting it again is harmless
-  static bool done[64];
-  if (device >= 64 || !done[device]) {
-    const cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, D, WIDE, SCORES>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // set on each device's first use; setting it twice is harmless
+  static std::atomic<bool> done[64];
+  if (device >= 64 || !done[device].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(attend_kernel<T, D, WIDE, SCORES>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    if (device < 64) done[device] = true;
+    if (device < 64) done[device].store(true, std::memory_order_release);
   }
   return launch_pdl(attend_kernel<T, D, WIDE, SCORES>, dim3(p.ctas), dim3(kWarps * 32), bytes, s, p);
 }
@@ -682,7 +684,7 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", cache->device);
   const void* ptrs[] = {cache->k, cache->v, cache->table, cache->status, q, len, o, lse, acc_in, acc_out, workspace};
   for (const void* x : ptrs)
-    if (x && !svx::on_device(x, cache->device))
+    if (x && !(cache->flags & SVX_POINTERS_CHECKED) && !svx::on_device(x, cache->device))
       return paged_fail(SVX_ERR_INVALID_ARG, "a pointer is not memory of device %d", cache->device);
 
   char* ws = static_cast<char*>(workspace);

@@ -503,7 +503,7 @@ extern "C" svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, con
   const void* ptrs[] = {cache->k, cache->v, cache->table, cache->status, len,     next_pos, acc_in,
                         pos_in,   acc_out,  pos_out,      len_out,       workspace};
   for (const void* x : ptrs)
-    if (!svx::on_device(x, cache->device))
+    if (!(cache->flags & SVX_POINTERS_CHECKED) && !svx::on_device(x, cache->device))
       return paged_fail(SVX_ERR_INVALID_ARG, "a pointer is not memory of device %d", cache->device);
   const int sms = svx::sm_count(cache->device);
   if (sms <= 0) return paged_fail(SVX_ERR_CUDA, "cannot read the SM count");

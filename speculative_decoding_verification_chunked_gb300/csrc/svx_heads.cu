@@ -365,7 +365,8 @@ svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages*
                         q_out,   k_out,    v_out, start,      acc,        slot_pos, cache ? cache->k : nullptr,
                         cache ? cache->v : nullptr, cache ? cache->table : nullptr, cache ? cache->status : nullptr};
   for (const void* x : ptrs)
-    if (x && !on_device(x, in->device)) return paged_fail(SVX_ERR_INVALID_ARG, "a pointer is not memory of device %d", in->device);
+    if (x && !(in->flags & SVX_POINTERS_CHECKED) && !on_device(x, in->device))
+      return paged_fail(SVX_ERR_INVALID_ARG, "a pointer is not memory of device %d", in->device);
 
   p.q = in->q;
   p.k = in->k;

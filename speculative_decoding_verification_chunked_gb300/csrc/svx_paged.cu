@@ -1,6 +1,7 @@
 // Host side shared by the paged-cache entry points: argument checks, and the rotation's fixed-point phases.
 #include "svx_paged.h"
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -33,11 +34,17 @@ bool on_device(const void* p, int device) {
 }
 
 int sm_count(int device) {
+  static std::atomic<int> known[64];  // a property of the device: asked once
+  if (device >= 0 && device < 64) {
+    const int n = known[device].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+  }
   int n = 0;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
+  if (device >= 0 && device < 64) known[device].store(n, std::memory_order_relaxed);
   return n;
 }
 

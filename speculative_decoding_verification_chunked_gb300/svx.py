@@ -97,7 +97,8 @@ class Heads(ctypes.Structure):
                 ("k_norm", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("n_new", ctypes.c_void_p),
                 ("status", ctypes.c_void_p), ("n_req", ctypes.c_int32), ("n_tok", ctypes.c_int32),
                 ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("device", ctypes.c_int32), ("eps", ctypes.c_float)]
+                ("dtype", ctypes.c_int32), ("device", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("flags", ctypes.c_uint32), ("pad", ctypes.c_int32)]
 
 
 class Pages(ctypes.Structure):
@@ -105,7 +106,7 @@ class Pages(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("tok_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("device", ctypes.c_int32)]
+                ("device", ctypes.c_int32), ("flags", ctypes.c_uint32), ("pad", ctypes.c_int32)]
 
 
 # name -> (restype, argtypes); every symbol declared in include/svx.h
@@ -731,64 +732,79 @@ class Verifier:
 
 BF16, FP16 = 0, 1
 EVICT_MAX_LEN = 262144
+POINTERS_CHECKED = 1  # the binding checks every tensor's device itself
+
+_torch_module = None
 
 
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _type_code(t, what: str) -> int:
     torch = _torch()
-    code = {torch.bfloat16: BF16, torch.float16: FP16}.get(t.dtype)
-    if code is None:
-        raise SvxError(ERR_UNSUPPORTED, f"{what}: dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
-    return code
+    if t.dtype is torch.bfloat16:
+        return BF16
+    if t.dtype is torch.float16:
+        return FP16
+    raise SvxError(ERR_UNSUPPORTED, f"{what}: dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
 
 
-def _dense(t, dtype, shape: tuple, device, what: str) -> Optional[int]:
-    """Address of a dense tensor of exactly this type and shape on this device (None stays None)."""
+def _dense(t, dtype, shape: tuple, device: int, what: str) -> Optional[int]:
+    """Address of a dense tensor of exactly this type and shape on this CUDA device (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise SvxError(ERR_INVALID_ARG, f"{what}: {t.dtype} {list(t.shape)} on {t.device}, contiguous {t.is_contiguous()}; "
-                                        f"expected dense {dtype} {list(shape)} on {device}")
+                                        f"expected dense {dtype} {list(shape)} on cuda:{device}")
     return t.data_ptr()
 
 
-def _head_rows(t, n_req: int, n_tok: int, d: int, dtype, device, what: str):
-    """Address and token stride of heads [n_req][n_tok][heads][d], possibly a view of a fused projection."""
-    if t.dim() != 4 or t.shape[0] != n_req or t.shape[1] != n_tok or t.shape[3] != d or t.dtype != dtype or \
-            t.device != device:
+def _head_rows(t, n_req: int, n_tok: int, d: int, dtype, device: int, what: str):
+    """Address, token stride and count of heads [n_req][n_tok][heads][d], possibly a view of a fused projection."""
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != n_req or shape[1] != n_tok or shape[3] != d or t.dtype is not dtype or \
+            t.get_device() != device:
         raise SvxError(ERR_INVALID_ARG, f"{what}: {t.dtype} {list(t.shape)} on {t.device}, expected {dtype} "
-                                        f"[{n_req}, {n_tok}, heads, {d}] on {device}")
+                                        f"[{n_req}, {n_tok}, heads, {d}] on cuda:{device}")
     s0, s1, s2, s3 = t.stride()
-    heads = t.shape[2]
+    heads = shape[2]
     row = s1 if n_tok > 1 else s0 if n_req > 1 else heads * d
     if s3 != 1 or (heads > 1 and s2 != d) or (n_tok > 1 and n_req > 1 and s0 != n_tok * s1):
         raise SvxError(ERR_INVALID_ARG, f"{what}: strides {list(t.stride())}: a token's heads must be dense, and tokens "
                                         "evenly spaced over the requests")
-    return t.data_ptr(), row
+    return t.data_ptr(), row, heads
 
 
-def _launch_stream(device, stream) -> int:
+def _launch_stream(device: int, stream) -> int:
     """The given stream's handle, else the current stream of the tensors' device."""
-    return _torch().cuda.current_stream(device).cuda_stream if stream is None else _stream_handle(stream)
+    if stream is not None:
+        return _stream_handle(stream)
+    torch = _torch()
+    try:  # what current_stream() reads, without making a Stream object of it (0.1 us in place of 2)
+        return torch._C._cuda_getCurrentRawStream(device)
+    except AttributeError:
+        return torch.cuda.current_stream(device).cuda_stream
 
 
-def _workspace(workspace, need: int, device, stream):
+def _workspace(workspace, need: int, device: int, stream):
     """The caller's workspace, or one from the caching allocator that belongs to the call's stream."""
     torch = _torch()
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous() or \
+        if workspace.get_device() != device or not workspace.is_contiguous() or \
                 workspace.numel() * workspace.element_size() < need:
-            raise SvxError(ERR_INVALID_ARG, f"workspace: a dense tensor of at least {need} bytes on {device} is needed")
+            raise SvxError(ERR_INVALID_ARG, f"workspace: a dense tensor of at least {need} bytes on cuda:{device} is needed")
         return workspace
+    dev = torch.device("cuda", device)
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
     with torch.cuda.stream(s):
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=dev)
 
 
 def _static_error(st: int):
@@ -813,27 +829,30 @@ class Rope:
 
 
 def _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, status):
+    """The C struct of a call's heads, and [requests, tokens, q heads, KV heads, head_dim], device and type."""
     torch = _torch()
-    if q.dim() != 4 or k.dim() != 4:
-        raise SvxError(ERR_INVALID_ARG, "q, k and v: [requests][tokens][heads][head_dim] tensors are expected")
+    if q.dim() != 4:
+        raise SvxError(ERR_INVALID_ARG, f"q: shape {list(q.shape)}, expected [requests, tokens, heads, head_dim]")
     n_req, n_tok, hq, d = q.shape
-    dtype, device = q.dtype, q.device
+    dtype, device = q.dtype, q.get_device()
     code = _type_code(q, "q")
-    if device.type != "cuda":
-        raise SvxError(ERR_INVALID_ARG, f"q is on {device}, not on a CUDA device")
-    hkv = k.shape[2]
-    qp, qs = _head_rows(q, n_req, n_tok, d, dtype, device, "q")
-    kp, ks = _head_rows(k, n_req, n_tok, d, dtype, device, "k")
-    vp, vs = (None, 0) if v is None else _head_rows(v, n_req, n_tok, d, dtype, device, "v")
-    if v is not None and v.shape[2] != hkv:
-        raise SvxError(ERR_INVALID_ARG, f"v has {v.shape[2]} heads, k {hkv}")
+    if device < 0:
+        raise SvxError(ERR_INVALID_ARG, f"q is on {q.device}, not on a CUDA device")
+    qp, qs, _ = _head_rows(q, n_req, n_tok, d, dtype, device, "q")
+    kp, ks, hkv = _head_rows(k, n_req, n_tok, d, dtype, device, "k")
+    vp, vs, hv = (None, 0, hkv) if v is None else _head_rows(v, n_req, n_tok, d, dtype, device, "v")
+    if hv != hkv:
+        raise SvxError(ERR_INVALID_ARG, f"v has {hv} heads, k {hkv}")
     if eps is not None and not eps >= 0.0:
         raise SvxError(ERR_INVALID_ARG, "eps must be >= 0, or None for no norms")
+    if pos is None:
+        raise SvxError(ERR_INVALID_ARG, "pos is required")
+    i32 = torch.int32
     h = Heads(qp, kp, vp, qs, ks, vs, _dense(q_norm, dtype, (d,), device, "q_norm"),
-              _dense(k_norm, dtype, (d,), device, "k_norm"), _dense(pos, torch.int32, (n_req, n_tok), device, "pos"),
-              _dense(n_new, torch.int32, (n_req,), device, "n_new"), status, n_req, n_tok, hq, hkv, d, code,
-              device.index, -1.0 if eps is None else eps)
-    return h, device, dtype
+              _dense(k_norm, dtype, (d,), device, "k_norm"), _dense(pos, i32, (n_req, n_tok), device, "pos"),
+              _dense(n_new, i32, (n_req,), device, "n_new"), status, n_req, n_tok, hq, hkv, d, code, device,
+              -1.0 if eps is None else eps, POINTERS_CHECKED, 0)
+    return h, (n_req, n_tok, hq, hkv, d), device, dtype
 
 
 def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None, k_norm=None,
@@ -845,11 +864,8 @@ def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None
     candidate_attn take.  eps None: no norms.  n_new: int32 [B], tokens of each request that count, or None.
     status: int32 [1] that becomes non-zero if n_new leaves [0, n], or None.  stream: the current one by default.
     """
-    torch = _torch()
-    sp = None if status is None else _dense(status, torch.int32, (1,), q.device, "status")
-    h, device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, sp)
-    b, n, hq, d = q.shape
-    hkv = h.n_kv_heads
+    sp = None if status is None else _dense(status, _torch().int32, (1,), q.get_device(), "status")
+    h, (b, n, hq, hkv, d), device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, sp)
     _static_error(lib.svx_qk_norm_rope(
         ctypes.byref(h), ctypes.byref(rope.table), _dense(q_out, dtype, (b, hq, n, d), device, "q_out"),
         _dense(k_out, dtype, (b, n, hkv, d), device, "k_out"), _dense(v_out, dtype, (b, n, hkv, d), device, "v_out"),
@@ -876,21 +892,22 @@ class PagedCache:
         if k_pages.device.type != "cuda":
             raise SvxError(ERR_INVALID_ARG, f"k_pages is on {k_pages.device}, not on a CUDA device")
         self.k_pages, self.v_pages = k_pages, v_pages
-        self.device, self.dtype = k_pages.device, k_pages.dtype
+        self.device, self.dtype = k_pages.get_device(), k_pages.dtype
         n_pages, self.page_size, self.n_kv_heads, self.head_dim = k_pages.shape
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
         self._pages = Pages(k_pages.data_ptr(), v_pages.data_ptr(), None, self.status.data_ptr(), *k_pages.stride()[:3],
                             n_pages, self.page_size, 0, self.n_kv_heads, self.head_dim, _type_code(k_pages, "k_pages"),
-                            self.device.index)
+                            self.device, POINTERS_CHECKED, 0)
         self._sizes = {}
 
-    def _with_table(self, table):
+    def _with_table(self, table, n_req: Optional[int]):
         """The C struct for a call (a copy: calls from several threads do not share it)."""
-        if table.dim() != 2:
-            raise SvxError(ERR_INVALID_ARG, f"table: shape {list(table.shape)}, expected [requests][max_pages]")
+        shape = table.shape
+        if len(shape) != 2 or (n_req is not None and shape[0] != n_req):
+            raise SvxError(ERR_INVALID_ARG, f"table: shape {list(shape)}, expected [{n_req or 'requests'}, max_pages]")
         p = Pages.from_buffer_copy(self._pages)
-        p.table = _dense(table, _torch().int32, tuple(table.shape), self.device, "table")
-        p.max_pages = table.shape[1]
+        p.table = _dense(table, _torch().int32, shape, self.device, "table")
+        p.max_pages = shape[1]
         return p
 
     def _need(self, what: str, fn, pages, *args) -> int:
@@ -919,13 +936,10 @@ class PagedCache:
         slots start[b] + j and q into q_out [B][Hq][n][d]; acc (fp32) becomes 0 and slot_pos (int32), both
         [B][Hkv][max_pages * page_size], the token's position at the new slots."""
         torch = _torch()
-        h, device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, None)
+        h, (b, n, hq, _, d), device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, None)
         if device != self.device:
-            raise SvxError(ERR_INVALID_ARG, f"q is on {device}, the cache on {self.device}")
-        b, n, hq, d = q.shape
-        p = self._with_table(table)
-        if table.shape[0] != b:
-            raise SvxError(ERR_INVALID_ARG, f"table: {table.shape[0]} requests, q has {b}")
+            raise SvxError(ERR_INVALID_ARG, f"q is on cuda:{device}, the cache on cuda:{self.device}")
+        p = self._with_table(table, b)
         meta = (b, self.n_kv_heads, p.max_pages * self.page_size)
         _static_error(lib.svx_paged_append(
             ctypes.byref(h), ctypes.byref(rope.table), ctypes.byref(p), _dense(start, torch.int32, (b,), device, "start"),
@@ -944,9 +958,7 @@ class PagedCache:
             raise SvxError(ERR_INVALID_ARG, f"q: shape {list(q.shape)}, expected [requests][heads][1][head_dim]")
         b, hq = q.shape[0], q.shape[1]
         device, rows = self.device, (b, hq, 1, self.head_dim)
-        p = self._with_table(table)
-        if table.shape[0] != b:
-            raise SvxError(ERR_INVALID_ARG, f"table: {table.shape[0]} requests, q has {b}")
+        p = self._with_table(table, b)
         meta = (b, self.n_kv_heads, p.max_pages * self.page_size)
         ws = _workspace(workspace, self._need("decode", lib.svx_paged_decode_workspace, p, b, hq, max_len,
                                               int(acc_in is not None)), device, stream)
@@ -964,7 +976,7 @@ class PagedCache:
         evicted ones before it, with their acc and position; len_out gets the new lengths.  acc (fp32), pos (int32):
         [B][Hkv][max_pages * page_size]; lens, next_pos, len_out: int32 [B]; outputs may be their inputs."""
         torch = _torch()
-        p = self._with_table(table)
+        p = self._with_table(table, None)
         b, device = table.shape[0], self.device
         meta = (b, self.n_kv_heads, p.max_pages * self.page_size)
         i32, f32 = torch.int32, torch.float32
