@@ -6,15 +6,17 @@
 // the bytes of K and V are the floor, and the kernel's task is to keep enough of them in flight.
 //
 // Work.  The slots of every (request, KV head, block of 16 query heads) - an item - are cut into chunks of
-// 4 KiB of K; all items' chunks form one flat range, which is cut evenly over the CTAs ("stream-K"), so a
-// ragged batch loads every SM alike, and one long request uses all of them.  The lengths are read on the device.
-// An item that lies in one CTA is finished there; a piece of an item leaves (m, l, O) in the CTA's slot 0 (the item
-// began before the CTA's range) or 1 (it goes on behind it), and join_kernel merges the pieces.
-//
-// A warp is its own pipeline: chunk i of a CTA's range belongs to warp i mod 8, which brings its chunks in with 16-byte
-// cp.async (rows found through the page table, the next entry fetched a chunk ahead), kStages deep, with no
-// barrier shared with the other warps.  8 warps x 2 chunks in flight are 128 KiB an SM.  The warps' states meet in
-// shared memory at the end of an item's part only, while their next chunks are already on the way.
+// 4 KiB of K; all items' chunks form one flat range, which is cut evenly over the CTAs and again over a CTA's warps
+// ("stream-K"), so a ragged batch loads every warp alike, and one long request uses all of them.  The lengths are read on
+// the device.  A warp is its own pipeline: it brings its chunks in with 16-byte cp.async (rows found through the page
+// table, the next entry fetched a chunk ahead), kStages deep, through the ends of items and with no barrier shared with
+// the other warps.  8 warps x 2 chunks in flight are 128 KiB an SM.
+// An item that lies in one warp is finished there.  Of the others a warp keeps the piece that ends in its range in global
+// memory (lead) and the one that goes on behind it in its emptied stages (tail); when all warps of the CTA are done
+// they merge the pieces that belong together, finish the items that lie in the CTA, and leave (m, l, O) of the others in the
+// CTA's slot 0 (the item began before the CTA's range) or 1 (it goes on behind it), which join_kernel merges.
+// (Warps that shared an item's chunks in turn and merged at its end took 70 us where this takes %RAGGED%, 16 ragged requests:
+// every item stopped the whole CTA.)
 //
 // Products: mma.sync m16n8k16, query heads on M.  They cost a few percent of the time (32 a chunk), so the
 // tensor memory path, which wants 64 rows or more on M and a second trip through it, gains nothing here.  With up to 8
@@ -47,6 +49,8 @@ struct DecodeParams {
   const float* acc_in;
   float* acc_out;
   float* part_o;    // [ctas][2][16][D]
+  float* lead;      // [ctas][8 warps][16][D], then (m, l) [ctas][8][16]
+  float2* lead_ml;
   float2* part_ml;  // [ctas][2][16]
   float2* row_ml;   // [n_req * n_q]: final (m, l), for the weights
   float* scores;    // [n_req * n_q][score_stride], log2 units
@@ -58,20 +62,16 @@ struct DecodeParams {
   int32_t ctas;                // of the attention kernel
 };
 
-// The flat range of chunks, as every kernel of the call computes it from the lengths: first[b] is the first
-// chunk of request b's items (KV head, block of query heads), first[kMaxReq] their number.
+// The flat range of chunks, as every kernel of the call computes it from the lengths.
 struct Plan {
-  int64_t first[kMaxReq + 1];
-  int64_t warp_sum[kWarps];
-  uint8_t pad[kMaxReq];  // slots by which a request's length falls short of whole chunks
-  // chunks of one of request b's items, and its length
-  __device__ __forceinline__ int chunks(int b, int items) const {
-    return static_cast<int>((first[b + 1] - first[b]) / items);
-  }
+  int32_t first[kMaxReq + 1];  // first chunk of each request's items; their number (below 2^31: checked on the host)
+  int32_t warp_sum[kWarps];
+  int32_t n[kMaxReq];          // chunks of one of a request's items
+  int32_t len[kMaxReq];        // its length, within bounds
 };
 
 template <int CT>
-__device__ __forceinline__ int64_t build_plan(const DecodeParams& P, Plan& s, bool report) {
+__device__ __forceinline__ int build_plan(const DecodeParams& P, Plan& s, bool report) {
   // one request per thread (kMaxReq = threads of a block), prefix sum over the block
   static_assert(kMaxReq == kWarps * 32, "one thread per request");
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -82,20 +82,21 @@ __device__ __forceinline__ int64_t build_plan(const DecodeParams& P, Plan& s, bo
     if (report && n != raw) atomicOr(P.pages.status, kErrInput);
   }
   const int chunks = (n + CT - 1) / CT;
-  s.pad[t] = static_cast<uint8_t>(chunks * CT - n);
-  const int64_t mine = static_cast<int64_t>(P.pages.n_kv_heads) * P.blocks * chunks;
-  int64_t x = mine;
+  s.n[t] = chunks;
+  s.len[t] = n;
+  const int mine = P.pages.n_kv_heads * P.blocks * chunks;
+  int x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) s.warp_sum[warp] = x;
   __syncthreads();
-  int64_t base = 0, total = 0;
+  int base = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const int64_t v = s.warp_sum[w];
+    const int v = s.warp_sum[w];
     if (w < warp) base += v;
     total += v;
   }
@@ -105,11 +106,27 @@ __device__ __forceinline__ int64_t build_plan(const DecodeParams& P, Plan& s, bo
   return total;
 }
 
-// CTAs that share T chunks, and their ranges [c T / n, (c + 1) T / n).
-__device__ __forceinline__ int64_t used_ctas(const DecodeParams& P, int64_t T) {
-  const int64_t n = (T + P.min_chunks - 1) / P.min_chunks;
-  return n < P.ctas ? n : P.ctas;
-}
+// The T chunks over the CTAs: the first `used` ones share them, CTA c has [begin(c), begin(c + 1)) = [floor(c T / used), ..),
+// in 32 bits with T = q used + r.
+struct Split {
+  uint32_t used, q, r, total;
+  __device__ __forceinline__ Split(const DecodeParams& P, int T) {
+    total = T;
+    used = (total + P.min_chunks - 1) / P.min_chunks;
+    if (used > static_cast<uint32_t>(P.ctas)) used = P.ctas;
+    q = used ? total / used : 0;
+    r = total - q * used;
+  }
+  __device__ __forceinline__ int begin(uint32_t c) const { return static_cast<int>(c * q + c * r / used); }  // c, r <= 256
+  // the CTA that holds chunk x
+  __device__ __forceinline__ int of(int x) const {
+    int c = min(static_cast<int>(static_cast<float>(x) * (static_cast<float>(used) / static_cast<float>(total))),
+                static_cast<int>(used) - 1);
+    while (c + 1 < static_cast<int>(used) && begin(c + 1) <= x) ++c;
+    while (c > 0 && begin(c) > x) --c;
+    return c;
+  }
+};
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -156,6 +173,10 @@ struct Mma<__nv_bfloat16> {
     __nv_bfloat162 l = __floats2bfloat162_rn(x - __low2float(h), y - __high2float(h));
     lo = *reinterpret_cast<uint32_t*>(&l);
   }
+  static __device__ __forceinline__ uint32_t down2(float x, float y) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<uint32_t*>(&a);
+  }
   static __device__ __forceinline__ uint2 down4(float4 v) {
     __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
     return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
@@ -179,39 +200,64 @@ struct Mma<__half> {
     __half2 l = __floats2half2_rn(x - __low2float(h), y - __high2float(h));
     lo = *reinterpret_cast<uint32_t*>(&l);
   }
+  static __device__ __forceinline__ uint32_t down2(float x, float y) {
+    __half2 a = __floats2half2_rn(x, y);
+    return *reinterpret_cast<uint32_t*>(&a);
+  }
   static __device__ __forceinline__ uint2 down4(float4 v) {
     __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
     return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
   }
 };
 
+// A piece of an item that a warp does not finish itself.
+struct Piece {
+  int32_t first, end;  // the item's chunks; first < 0: there is no such piece
+  int32_t b, h, blk;
+};
+
 template <int D>
 struct Smem {
-  static constexpr int OFF_O = kWarps * kStages * 2 * kChunkBytes;  // [8 warps][8 rows][D] partial outputs
-  static constexpr int OFF_ML = OFF_O + kWarps * 8 * D * 4;         // [8 warps][8 rows] (m, l)
-  static constexpr int BYTES = OFF_ML + kWarps * 8 * 8;
+  static constexpr int RING = kStages * 2 * kChunkBytes;  // a warp's stages; at the end its tail [16 rows][D], then (m, l)
+  static constexpr int OFF_PIECE = kWarps * RING;         // [leads, tails][8 warps]
+  static constexpr int BYTES = OFF_PIECE + kWarps * 2 * static_cast<int>(sizeof(Piece));
+  static_assert(kRowsMax * D * 4 + kRowsMax * 8 <= RING, "a tail fits the stages");
   // a row's float4 columns are permuted by the row, so that the fragments' stores spread over the banks
-  static __device__ __forceinline__ int at(int w, int r, int d) { return (w * 8 + r) * D + ((d >> 2 ^ r) << 2) + (d & 3); }
+  static __device__ __forceinline__ int at(int r, int d) { return r * D + ((d >> 2 ^ (r & 7)) << 2) + (d & 3); }
 };
 
 // A place in the flat range: the item it lies in.
 struct Cursor {
-  int64_t first, end;  // the item's chunks
+  int first, end;  // the item's chunks
   int b, h, blk;       // request, KV head, block of query heads
   int len;
 };
 
-template <int CT>
-__device__ __forceinline__ void seek(Cursor& c, const DecodeParams& P, const Plan& s, int64_t x) {
-  // moves on to the item that holds x (x >= c.first); requests without chunks are passed over
-  while (x >= s.first[c.b + 1]) ++c.b;
-  const int n = s.chunks(c.b, P.pages.n_kv_heads * P.blocks);
-  c.len = n * CT - s.pad[c.b];
-  const int i = static_cast<int>((x - s.first[c.b]) / n);
-  c.first = s.first[c.b] + static_cast<int64_t>(i) * n;
+// Moves on to the item that holds x (all lanes of a warp alike).
+__device__ __forceinline__ void seek(Cursor& c, const DecodeParams& P, const Plan& s, int x) {
+  if (x >= s.first[c.b + 1]) {  // another request: as many lie before it as end at x or before
+    c.b = 0;
+    for (int i = 0; i < P.pages.n_req; i += 32) {
+      const int r = i + (threadIdx.x & 31);
+      c.b += __popc(__ballot_sync(0xffffffffu, r < P.pages.n_req && s.first[r + 1] <= x));
+    }
+  }
+  const int n = s.n[c.b];
+  const int i = static_cast<int>(static_cast<uint32_t>(x - s.first[c.b]) / static_cast<uint32_t>(n));
+  c.len = s.len[c.b];
+  c.first = s.first[c.b] + i * n;
   c.end = c.first + n;
-  c.h = i / P.blocks;
+  c.h = P.blocks == 1 ? i : i / P.blocks;
   c.blk = i - c.h * P.blocks;
+}
+
+// O and LSE of a row from its merged state.
+template <typename T, int D>
+__device__ __forceinline__ void write_row(const DecodeParams& P, int64_t row, int d4, float M, float L, float4 o) {
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  o = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(static_cast<T*>(P.o) + row * D + d4) = Mma<T>::down4(o);
+  if (d4 == 0) P.lse[row] = L == 0.f ? kNegInf : (M + log2f(L)) * kLn2;
 }
 
 template <typename T, int D, bool WIDE, bool SCORES>
@@ -229,7 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
 
   grid_dependency_wait();
   allow_dependents();
-  const int64_t T_all = build_plan<CT>(P, plan, blockIdx.x == 0);
+  const int T_all = build_plan<CT>(P, plan, blockIdx.x == 0);
 
   // requests without slots: O = 0, LSE = -inf
   for (int b = blockIdx.x; b < P.pages.n_req; b += gridDim.x) {
@@ -238,40 +284,49 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
     for (int i = tid; i < P.n_q * D / 2; i += blockDim.x) ob[i] = 0u;
     for (int i = tid; i < P.n_q; i += blockDim.x) P.lse[static_cast<int64_t>(b) * P.n_q + i] = kNegInf;
   }
-  const int64_t used = used_ctas(P, T_all);
-  if (static_cast<int64_t>(blockIdx.x) >= used) return;
-  const int64_t x0 = cta_tile_begin(blockIdx.x, used, T_all), x1 = cta_tile_begin(blockIdx.x + 1, used, T_all);
+  const Split split(P, T_all);
+  if (blockIdx.x >= split.used) return;
+  const int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
+  const int w0 = x0 + static_cast<int>(static_cast<int64_t>(x1 - x0) * warp / kWarps);
+  const int w1 = x0 + static_cast<int>(static_cast<int64_t>(x1 - x0) * (warp + 1) / kWarps);
 
-  const uint32_t stage0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (kStages * 2 * kChunkBytes);
-  float* s_o = reinterpret_cast<float*>(smem + S::OFF_O);
-  float2* s_ml = reinterpret_cast<float2*>(smem + S::OFF_ML);
+  const uint32_t stage0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::RING;
+  Piece* pieces = reinterpret_cast<Piece*>(smem + S::OFF_PIECE);
+  if (lane < 2) pieces[lane * kWarps + warp].first = -1;
+  __syncwarp();
 
-  // ---- this warp's loads: chunk lx next; its rows' pages are looked up one chunk ahead
+  // ---- this warp's loads.  look() fetches the page of each row of the next chunk, load() copies the rows
   const int my_row = lane % CT;  // the row of a chunk whose place this lane works out
   Cursor lc{0, 0, 0, 0, 0, 0};
-  int64_t lx = x0 + warp;
-  int look_page = -1, look_in = 0;
-  bool look_live = false;
-  auto look = [&]() {
-    look_live = false;
-    if (lx < x1) {
-      if (lx >= lc.end) seek<CT>(lc, P, plan, lx);
-      const int t = static_cast<int>(lx - lc.first) * CT + my_row;
-      if (t < lc.len) {
-        const uint32_t pg = static_cast<uint32_t>(t) / static_cast<uint32_t>(P.pages.page_size);
-        look_in = t - pg * P.pages.page_size;
-        look_page = __ldg(P.pages.table + static_cast<int64_t>(lc.b) * P.pages.max_pages + pg);
-        look_live = true;
-      }
-    }
+  int lx = w0;
+  struct Look {
+    int64_t head;  // element offset of the KV head
+    int32_t page, in_page;
+    bool chunk, row;  // there is a chunk (the same in all lanes), and this lane's row of it
   };
-  auto load = [&](int stage) {
-    if (lx < x1) {
+  auto look = [&]() {
+    Look k{0, -1, 0, lx < w1, false};
+    if (k.chunk) {
+      if (lx >= lc.end) seek(lc, P, plan, lx);
+      const int t = (lx - lc.first) * CT + my_row;
+      k.row = t < lc.len;
+      if (k.row) {
+        const uint32_t pg = page_of(P.pages, static_cast<uint32_t>(t));
+        k.in_page = t - pg * P.pages.page_size;
+        k.page = __ldg(P.pages.table + static_cast<int64_t>(lc.b) * P.pages.max_pages + pg);
+      }
+      k.head = static_cast<int64_t>(lc.h) * P.pages.head_stride;
+      ++lx;
+    }
+    return k;
+  };
+  auto load = [&](int stage, const Look& k) {
+    if (k.chunk) {
       int64_t off = -1;
-      if (look_live) {
-        off = slot_offset(P.pages, look_page, look_in);
+      if (k.row) {
+        off = slot_offset(P.pages, k.page, k.in_page);
         if (off < 0) atomicOr(P.pages.status, kErrInput);
-        else off += static_cast<int64_t>(lc.h) * P.pages.head_stride;
+        else off += k.head;
         if (off >= 0 && !in_bounds(static_cast<const T*>(P.pages.k) + off, D, static_cast<const T*>(P.pages.k),
                                    P.pages.extent, P.pages.status, kSitePool))
           off = -1;
@@ -288,41 +343,48 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
         cp16(at, static_cast<const T*>(P.pages.k) + e, bytes);
         cp16(at + kChunkBytes, static_cast<const T*>(P.pages.v) + e, bytes);
       }
-      lx += kWarps;
     }
     cp_commit();
   };
-  look();
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    load(i);
-    look();
-  }
-
-  // ---- the parts of items in this CTA's range
   const int g = lane >> 2, c2 = (lane & 3) * 2;
-  int stage = 0;
-  int64_t cx = x0 + warp;  // this warp's next chunk
   Cursor cc{0, 0, 0, 0, 0, 0};
-  for (int64_t seg = x0; seg < x1; seg = cc.end) {
-    seek<CT>(cc, P, plan, seg);
-    const int64_t seg_end = cc.end < x1 ? cc.end : x1;
+  // q fragments of an item: rows g and (WIDE) g + 8
+  uint32_t qa[KS][WIDE ? 4 : 2];
+  auto load_q = [&]() {
     const int rows = min(P.group - cc.blk * kRowsMax, kRowsMax);
-    const int64_t row0 = static_cast<int64_t>(cc.b) * P.n_q + cc.h * P.group + cc.blk * kRowsMax;
-    // q fragments: rows g and (WIDE) g + 8
-    uint32_t qa[KS][WIDE ? 4 : 2];
-    {
-      const T* q0 = static_cast<const T*>(P.q) + (row0 + g) * D + c2;
+    const T* q0 = static_cast<const T*>(P.q) +
+                  (static_cast<int64_t>(cc.b) * P.n_q + cc.h * P.group + cc.blk * kRowsMax + g) * D + c2;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        qa[k][0] = g < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16)) : 0u;
-        qa[k][1] = g < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16 + 8)) : 0u;
-        if constexpr (WIDE) {
-          qa[k][2] = g + 8 < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * D + k * 16)) : 0u;
-          qa[k][3] = g + 8 < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * D + k * 16 + 8)) : 0u;
-        }
+    for (int k = 0; k < KS; ++k) {
+      qa[k][0] = g < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16)) : 0u;
+      qa[k][1] = g < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16 + 8)) : 0u;
+      if constexpr (WIDE) {
+        qa[k][2] = g + 8 < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * D + k * 16)) : 0u;
+        qa[k][3] = g + 8 < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 8 * D + k * 16 + 8)) : 0u;
       }
     }
+  };
+  // the first chunks' pages and the first q are fetched together
+  Look ahead[kStages];
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) ahead[i] = look();
+  if (w0 < w1) {
+    seek(cc, P, plan, w0);
+    load_q();
+  }
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load(i, ahead[i]);
+  Look next = ahead[kStages - 1];
+
+  // ---- the parts of items in this warp's range
+  int stage = 0;
+  int cx = w0;  // the next chunk
+  while (cx < w1) {
+    const Cursor it = cc;
+    const int seg_end = min(it.end, w1);
+    const bool whole = it.first == cx && it.end <= w1;
+    const int rows = min(P.group - it.blk * kRowsMax, kRowsMax);
+    const int64_t row0 = static_cast<int64_t>(it.b) * P.n_q + it.h * P.group + it.blk * kRowsMax;
     constexpr int H = WIDE ? 2 : 1;
     float m[H], l[H], acc[NO][4];
 #pragma unroll
@@ -333,11 +395,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < NO; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
-    for (; cx < seg_end; cx += kWarps) {
+    for (; cx < seg_end; ++cx) {
       cp_wait<kStages - 2>();
       __syncwarp();  // every lane's copies of this chunk are here, and every lane is done with the last one
-      load(stage == 0 ? kStages - 1 : stage - 1);
-      look();
+      load(stage == 0 ? kStages - 1 : stage - 1, next);
+      next = look();
       const uint32_t kb = stage0 + stage * (2 * kChunkBytes), vb = kb + kChunkBytes;
       stage = stage == kStages - 1 ? 0 : stage + 1;
 
@@ -362,8 +424,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
           }
         }
       }
-      const int t0 = static_cast<int>(cx - cc.first) * CT;
-      const int left = cc.len - t0;
+      const int t0 = (cx - it.first) * CT;
+      const int left = it.len - t0;
       float top[H];
 #pragma unroll
       for (int h = 0; h < H; ++h) top[h] = kNegInf;
@@ -446,151 +508,255 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
       }
     }
 
-    // ---- the warps' states meet, 8 query heads at a time
+    // ---- the end of the item, or of the warp's range
+    if (seg_end < w1) {  // the next item's q is on its way meanwhile
+      seek(cc, P, plan, seg_end);
+      load_q();
+    }
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     }
-    const bool whole = cc.first >= x0 && cc.end <= x1;
-    const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (cc.first >= x0 ? 1 : 0)) * kRowsMax;
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      if (h * 8 >= rows) break;  // the same for all threads
-      if ((lane & 3) == 0) s_ml[warp * 8 + g] = make_float2(m[h], l[h]);
+    if constexpr (!WIDE) {
 #pragma unroll
       for (int i = 0; i < NO; ++i) {
-        float2 v = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
-        if constexpr (!WIDE) {
-          v.x += acc[i][2];
-          v.y += acc[i][3];
-        }
-        *reinterpret_cast<float2*>(s_o + S::at(warp, g, i * 8 + c2)) = v;
+        acc[i][0] += acc[i][2];
+        acc[i][1] += acc[i][3];
       }
-      __syncthreads();
-      const int n_here = min(rows - h * 8, 8);
-      for (int i = tid; i < n_here * (D / 4); i += kWarps * 32) {
-        const int r = i / (D / 4), d4 = (i - r * (D / 4)) * 4;
-        float M = kNegInf;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * 8 + r].x);
-        const float base = M == kNegInf ? 0.f : M;
-        float L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 ml = s_ml[w * 8 + r];
-          const float f = ex2(ml.x - base);
-          const float4 v = *reinterpret_cast<const float4*>(s_o + S::at(w, r, d4));
-          L = fmaf(ml.y, f, L);
-          o.x = fmaf(v.x, f, o.x);
-          o.y = fmaf(v.y, f, o.y);
-          o.z = fmaf(v.z, f, o.z);
-          o.w = fmaf(v.w, f, o.w);
-        }
-        const int64_t row = row0 + h * 8 + r;
-        if (whole) {
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-          if (L == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-          *reinterpret_cast<uint2*>(static_cast<T*>(P.o) + row * D + d4) = Mma<T>::down4(o);
-          if (d4 == 0) {
-            P.lse[row] = L == 0.f ? kNegInf : (M + log2f(L)) * kLn2;
-            if constexpr (SCORES) P.row_ml[row] = make_float2(M, L);
-          }
-        } else {
-          *reinterpret_cast<float4*>(P.part_o + (slot + h * 8 + r) * D + d4) = o;
-          if (d4 == 0) P.part_ml[slot + h * 8 + r] = make_float2(M, L);
-        }
-      }
-      __syncthreads();
     }
+    if (whole) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        if (g + 8 * h >= rows) continue;
+        const int64_t row = row0 + g + 8 * h;
+        const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(P.o) + row * D + c2);
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+          dst[i * 4] = l[h] == 0.f ? 0u : Mma<T>::down2(acc[i][2 * h] * inv, acc[i][2 * h + 1] * inv);
+        if ((lane & 3) == 0) {
+          P.lse[row] = l[h] == 0.f ? kNegInf : (m[h] + log2f(l[h])) * kLn2;
+          if constexpr (SCORES) P.row_ml[row] = make_float2(m[h], l[h]);
+        }
+      }
+      continue;
+    }
+    const bool tail = seg_end == w1;
+    float* po;
+    float2* pml;
+    if (tail) {  // every chunk has been read: the stages are free
+      cp_wait<0>();
+      __syncwarp();
+      po = reinterpret_cast<float*>(smem + warp * S::RING);
+      pml = reinterpret_cast<float2*>(po + kRowsMax * D);
+    } else {
+      po = P.lead + (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRowsMax * D;
+      pml = P.lead_ml + (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRowsMax;
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      if (g + 8 * h >= rows) continue;
+      if ((lane & 3) == 0) pml[g + 8 * h] = make_float2(m[h], l[h]);
+#pragma unroll
+      for (int i = 0; i < NO; ++i)
+        *reinterpret_cast<float2*>(po + S::at(g + 8 * h, i * 8 + c2)) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+    }
+    if (lane == 0) pieces[tail ? kWarps + warp : warp] = Piece{it.first, it.end, it.b, it.h, it.blk};
   }
   cp_wait<0>();
+  __syncthreads();
+
+  // ---- the items that have pieces here: lane p < 16 looks at piece p (leads, then tails) and names its item, if no
+  // lower one has.  An item has tails in any number of warps and a lead in one at most.
+  uint32_t named;
+  {
+    const int f = lane < 2 * kWarps ? pieces[lane].first : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, f);  // by all lanes
+    named = __ballot_sync(0xffffffffu, f >= 0 && (same & ((1u << lane) - 1u)) == 0);
+  }
+  const int per_item = min(P.group, kRowsMax) * (D / 4);
+  for (int i = tid; i < __popc(named) * per_item; i += kWarps * 32) {
+    const int nth = i / per_item, e = i - nth * per_item;
+    const int r = e / (D / 4), d4 = (e - r * (D / 4)) * 4;
+    uint32_t which = named;
+    for (int k = 0; k < nth; ++k) which &= which - 1u;
+    const Piece it = pieces[__ffs(which) - 1];
+    if (r >= P.group - it.blk * kRowsMax) continue;
+    int lead = -1;
+    float2 ml[kWarps + 1];
+    float M = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (pieces[w].first == it.first) lead = w;
+      ml[w] = make_float2(kNegInf, 0.f);
+      if (pieces[kWarps + w].first == it.first)
+        ml[w] = reinterpret_cast<const float2*>(smem + w * S::RING + kRowsMax * D * 4)[r];
+      M = fmaxf(M, ml[w].x);
+    }
+    const int64_t at_lead = (static_cast<int64_t>(blockIdx.x) * kWarps + lead) * kRowsMax;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    ml[kWarps] = make_float2(kNegInf, 0.f);
+    if (lead >= 0) {
+      ml[kWarps] = P.lead_ml[at_lead + r];
+      o = *reinterpret_cast<const float4*>(P.lead + at_lead * D + S::at(r, d4));
+    }
+    M = fmaxf(M, ml[kWarps].x);
+    const float base = M == kNegInf ? 0.f : M;
+    float f = ex2(ml[kWarps].x - base);
+    float L = ml[kWarps].y * f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (pieces[kWarps + w].first != it.first) continue;
+      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * S::RING) + S::at(r, d4));
+      f = ex2(ml[w].x - base);
+      L = fmaf(ml[w].y, f, L);
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+    if (it.first >= x0 && it.end <= x1) {
+      const int64_t row = static_cast<int64_t>(it.b) * P.n_q + it.h * P.group + it.blk * kRowsMax + r;
+      write_row<T, D>(P, row, d4, M, L, o);
+      if (SCORES && d4 == 0) P.row_ml[row] = make_float2(M, L);
+    } else {
+      const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (it.first >= x0 ? 1 : 0)) * kRowsMax + r;
+      *reinterpret_cast<float4*>(P.part_o + slot * D + d4) = o;
+      if (d4 == 0) P.part_ml[slot] = make_float2(M, L);
+    }
+  }
 }
 
-// Merges the pieces of the items that more than one CTA worked on: one CTA per item.
-template <typename T, int D>
+// Merges the pieces of the items that more than one CTA worked on, and adds the weights.  CTA (x, y): KV head x of all
+// requests' heads; block of query heads y, and slots [2048 y, 2048 (y + 1)):
+// acc_out[t] = acc_in[t] + sum over the KV head's query heads of 2^(s_t - m) / l, from the stored scores.
+constexpr int kMaxCtas = 256;
+constexpr int kWeightSlots = 2048;
+
+template <typename T, int D, bool SCORES>
 __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant__ DecodeParams P) {
   constexpr int CT = kChunkBytes / (2 * D);
   __shared__ Plan plan;
+  __shared__ float s_f[kMaxCtas * kRowsMax];  // a piece's factor for each row
+  __shared__ float2 s_ml[kRowsMax];
+  __shared__ float4 s_o[kWarps * 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // The lengths are not the attention kernel's work, and that kernel has waited for whoever wrote them before it let this
+  // one start: the plan need not wait for it.
+  const int T_all = build_plan<CT>(P, plan, false);
   grid_dependency_wait();
   allow_dependents();
-  const int per = P.pages.n_kv_heads * P.blocks;
-  const int b = blockIdx.x / per, i = blockIdx.x - b * per;
-  const int64_t T_all = build_plan<CT>(P, plan, false);
-  const int n = plan.chunks(b, per);
-  if (n == 0) return;
-  const int64_t used = used_ctas(P, T_all);
-  const int64_t first = plan.first[b] + static_cast<int64_t>(i) * n;
-  const int64_t c0 = cta_of_tile(first, used, T_all), c1 = cta_of_tile(first + n - 1, used, T_all);
-  if (c0 == c1) return;
-  const int h = i / P.blocks, blk = i - h * P.blocks;
-  const int rows = min(P.group - blk * kRowsMax, kRowsMax);
-  const int64_t row0 = static_cast<int64_t>(b) * P.n_q + h * P.group + blk * kRowsMax;
-  const bool at_start = cta_tile_begin(c0, used, T_all) <= first;  // the item begins inside c0's range
-  for (int x = threadIdx.x; x < rows * (D / 4); x += kWarps * 32) {
-    const int r = x / (D / 4), d4 = (x - r * (D / 4)) * 4;
-    float M = kNegInf, L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t c = c0; c <= c1; ++c) {
-      const int64_t s = (c * 2 + (c == c0 && at_start ? 1 : 0)) * kRowsMax + r;
-      const float2 ml = P.part_ml[s];
-      const float4 v = *reinterpret_cast<const float4*>(P.part_o + s * D + d4);
-      const float t = fmaxf(M, ml.x);
-      const float base = t == kNegInf ? 0.f : t;
-      const float fa = ex2(M - base), fb = ex2(ml.x - base);
-      L = L * fa + ml.y * fb;
-      o.x = o.x * fa + v.x * fb;
-      o.y = o.y * fa + v.y * fb;
-      o.z = o.z * fa + v.z * fb;
-      o.w = o.w * fa + v.w * fb;
-      M = t;
-    }
-    const int64_t row = row0 + r;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    o = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(static_cast<T*>(P.o) + row * D + d4) = Mma<T>::down4(o);
-    if (d4 == 0) {
-      P.lse[row] = L == 0.f ? kNegInf : (M + log2f(L)) * kLn2;
-      if (P.row_ml) P.row_ml[row] = make_float2(M, L);
-    }
-  }
-}
-
-// acc_out[t] = acc_in[t] + sum over a KV head's query heads of 2^(s_t - m) / l, from the stored scores.
-__global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ DecodeParams P) {
-  grid_dependency_wait();
-  allow_dependents();
-  const int bh = blockIdx.y, b = bh / P.pages.n_kv_heads, h = bh - b * P.pages.n_kv_heads;
-  const int len = min(max(P.len[b], 0), P.max_len);
-  const int t0 = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (t0 >= len) return;
-  const int64_t row0 = static_cast<int64_t>(b) * P.n_q + static_cast<int64_t>(h) * P.group;
-  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int g = 0; g < P.group; ++g) {
-    const float2 ml = P.row_ml[row0 + g];
-    if (ml.y == 0.f) continue;  // only scores of -inf: no weight
-    const float inv = 1.f / ml.y;
-    const float4 s = *reinterpret_cast<const float4*>(P.scores + (row0 + g) * P.score_stride + t0);
-    w.x = fmaf(ex2(s.x - ml.x), inv, w.x);
-    w.y = fmaf(ex2(s.y - ml.x), inv, w.y);
-    w.z = fmaf(ex2(s.z - ml.x), inv, w.z);
-    w.w = fmaf(ex2(s.w - ml.x), inv, w.w);
-  }
-  const int64_t a = static_cast<int64_t>(bh) * P.pages.cap + t0;
-  const float v[4] = {w.x, w.y, w.z, w.w};
+  const int b = blockIdx.x / P.pages.n_kv_heads, h = blockIdx.x - b * P.pages.n_kv_heads;
+  const int n = plan.n[b], len = plan.len[b];
+  const int t_first = blockIdx.y * kWeightSlots + tid * 4;  // this thread's slots: 4 here and 4 behind 1024 more
+  const bool weigh = SCORES && static_cast<int>(blockIdx.y) * kWeightSlots < len;
+  if (n == 0 || (!weigh && static_cast<int>(blockIdx.y) >= P.blocks)) return;
+  const Split split(P, T_all);
+  float4 w[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int blk = 0; blk < P.blocks; ++blk) {
+    const bool merge = static_cast<int>(blockIdx.y) == blk;
+    if (!merge && !weigh) continue;
+    const int first = plan.first[b] + (h * P.blocks + blk) * n;
+    const int c0 = split.of(first), c1 = split.of(first + n - 1);
+    const int pieces = c1 - c0 + 1;
+    if (pieces == 1 && !weigh) continue;
+    const int rows = min(P.group - blk * kRowsMax, kRowsMax);
+    const int64_t row0 = static_cast<int64_t>(b) * P.n_q + h * P.group + blk * kRowsMax;
+    // piece c lies in slot 0 of its CTA, but the first in slot 1 if the item begins in that CTA's range
+    const int64_t slot0 = static_cast<int64_t>(c0 * 2 + (split.begin(c0) <= first ? 1 : 0)) * kRowsMax;
+    auto slot = [&](int c) { return c == 0 ? slot0 : static_cast<int64_t>(c0 + c) * 2 * kRowsMax; };
+    for (int r = warp; r < rows; r += kWarps) {
+      if (pieces == 1) {
+        if (lane == 0) s_ml[r] = P.row_ml[row0 + r];
+        continue;
+      }
+      float M = kNegInf, L = 0.f;
+      for (int c = lane; c < pieces; c += 32) M = fmaxf(M, P.part_ml[slot(c) + r].x);
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (t0 + e < len) P.acc_out[a + e] = P.acc_in[a + e] + v[e];
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float base = M == kNegInf ? 0.f : M;
+      for (int c = lane; c < pieces; c += 32) {
+        const float2 ml = P.part_ml[slot(c) + r];
+        const float f = ex2(ml.x - base);
+        s_f[c * kRowsMax + r] = f;
+        L = fmaf(ml.y, f, L);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (lane == 0) s_ml[r] = make_float2(M, L);
+    }
+    __syncthreads();
+    if (merge && pieces > 1) {
+      // several threads share an output where there are more of them than outputs
+      const int outs = rows * (D / 4), share = max(kWarps * 32 / outs, 1);
+      for (int i0 = 0; i0 < outs; i0 += kWarps * 32) {
+        const int i = share > 1 ? tid % outs : i0 + tid, part = share > 1 ? tid / outs : 0;
+        const int r = i / (D / 4), d4 = (i - r * (D / 4)) * 4;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < outs && part < share) {
+#pragma unroll 4
+          for (int c = part; c < pieces; c += share) {
+            const float f = s_f[c * kRowsMax + r];
+            const float4 v = *reinterpret_cast<const float4*>(P.part_o + (slot(c) + r) * D + d4);
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z);
+            o.w = fmaf(v.w, f, o.w);
+          }
+        }
+        if (share > 1) {
+          s_o[tid] = o;
+          __syncthreads();
+          if (part == 0)
+            for (int p = 1; p < share; ++p) {
+              const float4 v = s_o[p * outs + i];
+              o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+            }
+        }
+        if (i < outs && part == 0) write_row<T, D>(P, row0 + r, d4, s_ml[r].x, s_ml[r].y, o);
+      }
+    }
+    if (weigh) {
+      for (int r = 0; r < rows; ++r) {
+        const float2 ml = s_ml[r];
+        if (ml.y == 0.f) continue;  // only scores of -inf: no weight
+        const float inv = 1.f / ml.y;
+        const float* src = P.scores + (row0 + r) * P.score_stride + t_first;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (t_first + u * 1024 >= len) continue;
+          const float4 s = *reinterpret_cast<const float4*>(src + u * 1024);
+          w[u].x = fmaf(ex2(s.x - ml.x), inv, w[u].x);
+          w[u].y = fmaf(ex2(s.y - ml.x), inv, w[u].y);
+          w[u].z = fmaf(ex2(s.z - ml.x), inv, w[u].z);
+          w[u].w = fmaf(ex2(s.w - ml.x), inv, w[u].w);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (!weigh) return;
+  const int64_t a = static_cast<int64_t>(blockIdx.x) * P.pages.cap + t_first;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t_first + u * 1024 + e < len) P.acc_out[a + u * 1024 + e] = P.acc_in[a + u * 1024 + e] + v[e];
+  }
 }
 
 // ------------------------------------------------------------------ host
 
+constexpr int kMinChunks = 2 * kWarps;
+
 struct Sizes {
   int32_t max_len, blocks, ctas;
+  bool one;  // one CTA does it all, whatever the lengths
   int64_t score_stride;
-  size_t part_o, part_ml, row_ml, scores, total;
+  size_t part_o, part_ml, lead, lead_ml, row_ml, scores, total;
 };
 
 svx_status sizes(const svx_pages* c, int32_t n_req, int32_t n_q, int64_t max_len, bool weights, Sizes* z) {
@@ -606,18 +772,23 @@ svx_status sizes(const svx_pages* c, int32_t n_req, int32_t n_q, int64_t max_len
   z->max_len = static_cast<int32_t>(max_len);
   z->blocks = (group + kRowsMax - 1) / kRowsMax;
   const int64_t chunks = static_cast<int64_t>(n_req) * c->n_kv_heads * z->blocks * ((max_len + ct - 1) / ct);
-  z->ctas = static_cast<int32_t>(std::min<int64_t>(sms, std::max<int64_t>(chunks, 1)));
+  if (chunks > 0x7fffffff)
+    return paged_fail(SVX_ERR_UNSUPPORTED, "n_req * heads * max_len is too large (%lld chunks of %d slots, at most 2^31 - 1)",
+                      static_cast<long long>(chunks), ct);
+  z->one = chunks <= kMinChunks;
+  z->ctas = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kMaxCtas), std::max<int64_t>((chunks + kMinChunks - 1) / kMinChunks, 1)));
   z->score_stride = (max_len + ct - 1) / ct * ct;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   z->part_o = 0;
   z->part_ml = z->part_o + up(static_cast<size_t>(z->ctas) * 2 * kRowsMax * c->head_dim * 4);
-  z->row_ml = z->part_ml + up(static_cast<size_t>(z->ctas) * 2 * kRowsMax * 8);
+  z->lead = z->part_ml + up(static_cast<size_t>(z->ctas) * 2 * kRowsMax * 8);
+  z->lead_ml = z->lead + up(static_cast<size_t>(z->ctas) * kWarps * kRowsMax * c->head_dim * 4);
+  z->row_ml = z->lead_ml + up(static_cast<size_t>(z->ctas) * kWarps * kRowsMax * 8);
   z->scores = z->row_ml + (weights ? up(static_cast<size_t>(n_req) * n_q * 8) : 0);
   z->total = z->scores + (weights ? up(static_cast<size_t>(n_req) * n_q * z->score_stride * 4) : 0);
   return SVX_OK;
 }
 
-constexpr int kMinChunks = 2 * kWarps;
 
 template <typename T, int D, bool WIDE, bool SCORES>
 cudaError_t launch_attend(const DecodeParams& p, int device, cudaStream_t s) {
@@ -634,15 +805,16 @@ cudaError_t launch_attend(const DecodeParams& p, int device, cudaStream_t s) {
 }
 
 template <typename T, int D>
-cudaError_t launch_all(const DecodeParams& p, int device, cudaStream_t s) {
+cudaError_t launch_all(const DecodeParams& p, bool one, int device, cudaStream_t s) {
   const bool wide = p.group > 8, scores = p.scores != nullptr;
-  cudaError_t e = wide ? (scores ? launch_attend<T, D, true, true>(p, device, s) : launch_attend<T, D, true, false>(p, device, s))
-                       : (scores ? launch_attend<T, D, false, true>(p, device, s) : launch_attend<T, D, false, false>(p, device, s));
-  if (e != cudaSuccess) return e;
-  const int64_t items = static_cast<int64_t>(p.pages.n_req) * p.pages.n_kv_heads * p.blocks;
-  e = launch_pdl(join_kernel<T, D>, dim3(static_cast<unsigned>(items)), dim3(kWarps * 32), 0, s, p);
-  if (e != cudaSuccess || !scores) return e;
-  return launch_pdl(weights_kernel, dim3((p.max_len + 1023) / 1024, p.pages.n_req * p.pages.n_kv_heads), dim3(256), 0, s, p);
+  const cudaError_t e =
+      wide ? (scores ? launch_attend<T, D, true, true>(p, device, s) : launch_attend<T, D, true, false>(p, device, s))
+           : (scores ? launch_attend<T, D, false, true>(p, device, s) : launch_attend<T, D, false, false>(p, device, s));
+  if (e != cudaSuccess || (one && !scores)) return e;  // (one CTA leaves no pieces)
+  const int slots = scores ? (p.max_len + kWeightSlots - 1) / kWeightSlots : 1;
+  const dim3 grid(p.pages.n_req * p.pages.n_kv_heads, std::max(p.blocks, slots));
+  return scores ? launch_pdl(join_kernel<T, D, true>, grid, dim3(kWarps * 32), 0, s, p)
+                : launch_pdl(join_kernel<T, D, false>, grid, dim3(kWarps * 32), 0, s, p);
 }
 
 }  // namespace
@@ -696,6 +868,8 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   p.acc_out = acc_out;
   p.part_o = reinterpret_cast<float*>(ws + z.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + z.part_ml);
+  p.lead = reinterpret_cast<float*>(ws + z.lead);
+  p.lead_ml = reinterpret_cast<float2*>(ws + z.lead_ml);
   p.row_ml = acc_in ? reinterpret_cast<float2*>(ws + z.row_ml) : nullptr;
   p.scores = acc_in ? reinterpret_cast<float*>(ws + z.scores) : nullptr;
   p.score_stride = z.score_stride;
@@ -710,11 +884,11 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (cache->dtype == SVX_BF16)
-    e = cache->head_dim == 128 ? svx::launch_all<__nv_bfloat16, 128>(p, cache->device, s)
-                               : svx::launch_all<__nv_bfloat16, 64>(p, cache->device, s);
+    e = cache->head_dim == 128 ? svx::launch_all<__nv_bfloat16, 128>(p, z.one, cache->device, s)
+                               : svx::launch_all<__nv_bfloat16, 64>(p, z.one, cache->device, s);
   else
-    e = cache->head_dim == 128 ? svx::launch_all<__half, 128>(p, cache->device, s)
-                               : svx::launch_all<__half, 64>(p, cache->device, s);
+    e = cache->head_dim == 128 ? svx::launch_all<__half, 128>(p, z.one, cache->device, s)
+                               : svx::launch_all<__half, 64>(p, z.one, cache->device, s);
   if (e != cudaSuccess) return paged_fail(SVX_ERR_CUDA, "decode kernel launch failed: %s", cudaGetErrorString(e));
   return SVX_OK;
 }

@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const __grid_cons
     if (lane < P.chunk && i0 + lane < M) {
       const int hole = holes[i0 + lane], spare = spares[i0 + lane];
       const uint32_t ps = P.pages.page_size;
-      const uint32_t pt = static_cast<uint32_t>(hole) / ps, pf = static_cast<uint32_t>(spare) / ps;
+      const uint32_t pt = page_of(P.pages, static_cast<uint32_t>(hole)), pf = page_of(P.pages, static_cast<uint32_t>(spare));
       const int32_t page_to = table[pt], page_from = table[pf];
       const float w = P.acc_in[meta + spare];
       const int32_t pos = P.pos_in[meta + spare];

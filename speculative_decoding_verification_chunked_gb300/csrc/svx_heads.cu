@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
     const int64_t s = static_cast<int64_t>(P.start[b]) + j;
     if (s >= 0 && s < P.pages.cap) {
       slot = static_cast<int32_t>(s);
-      const uint32_t pg = static_cast<uint32_t>(slot) / static_cast<uint32_t>(P.pages.page_size);
+      const uint32_t pg = page_of(P.pages, static_cast<uint32_t>(slot));
       at = slot_offset(P.pages, P.pages.table[static_cast<int64_t>(b) * P.pages.max_pages + pg],
                        static_cast<uint32_t>(slot) - pg * P.pages.page_size);
     }

@@ -86,7 +86,14 @@ svx_status paged_view(const svx_pages* c, int32_t n_req, PageView* out) {
                   c->max_pages,
                   c->n_kv_heads,
                   n_req,
-                  c->page_size * c->max_pages};
+                  c->page_size * c->max_pages,
+                  0,
+                  0};
+  // round-up multiplication: with 2^l >= page_size, mul = floor(2^32 (2^l - page_size) / page_size) + 1
+  uint32_t l = 0;
+  while ((int64_t{1} << l) < c->page_size) ++l;
+  out->div_shift = l;
+  out->div_mul = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << l) - c->page_size)) / c->page_size + 1);
   return SVX_OK;
 }
 

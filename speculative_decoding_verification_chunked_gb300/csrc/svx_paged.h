@@ -40,7 +40,13 @@ struct PageView {
   int32_t n_pages, page_size, max_pages, n_kv_heads;
   int32_t n_req;
   int32_t cap;           // max_pages * page_size: slots of a request
+  uint32_t div_mul, div_shift;  // t / page_size = (t + mulhi(t, div_mul)) >> div_shift for t < 2^31
 };
+
+// Page of a request's slot (an index into its row of the table).
+__device__ __forceinline__ uint32_t page_of(const PageView& p, uint32_t t) {
+  return (t + __umulhi(t, p.div_mul)) >> p.div_shift;
+}
 
 // Page and offset of a request's slot, 0 <= slot < cap: the element offset of (slot, head 0), or -1 where
 // the table names no page of the pool.
