@@ -644,20 +644,18 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
   __shared__ float4 s_o[kWarps * 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The lengths are not the attention kernel's work, and that kernel has waited for whoever wrote them before it let this
-  // one start: the plan need not wait for it.
+  // one start: the plan, and where the pieces lie, need not wait for it.
   const int T_all = build_plan<CT>(P, plan, false);
-  grid_dependency_wait();
-  allow_dependents();
   const int b = blockIdx.x / P.pages.n_kv_heads, h = blockIdx.x - b * P.pages.n_kv_heads;
   const int n = plan.n[b], len = plan.len[b];
   const int t_first = blockIdx.y * kWeightSlots + tid * 4;  // this thread's slots: 4 here and 4 behind 1024 more
   const bool weigh = SCORES && static_cast<int>(blockIdx.y) * kWeightSlots < len;
-  if (n == 0 || (!weigh && static_cast<int>(blockIdx.y) >= P.blocks)) return;
+  const bool idle = n == 0 || (!weigh && static_cast<int>(blockIdx.y) >= P.blocks);
   const Split split(P, T_all);
   float4 w[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int blk = 0; blk < P.blocks; ++blk) {
+  bool waited = false;
+  for (int blk = weigh ? 0 : blockIdx.y; !idle && blk < (weigh ? P.blocks : static_cast<int>(blockIdx.y) + 1); ++blk) {
     const bool merge = static_cast<int>(blockIdx.y) == blk;
-    if (!merge && !weigh) continue;
     const int first = plan.first[b] + (h * P.blocks + blk) * n;
     const int c0 = split.of(first), c1 = split.of(first + n - 1);
     const int pieces = c1 - c0 + 1;
@@ -667,18 +665,39 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
     // piece c lies in slot 0 of its CTA, but the first in slot 1 if the item begins in that CTA's range
     const int64_t slot0 = static_cast<int64_t>(c0 * 2 + (split.begin(c0) <= first ? 1 : 0)) * kRowsMax;
     auto slot = [&](int c) { return c == 0 ? slot0 : static_cast<int64_t>(c0 + c) * 2 * kRowsMax; };
+    // the outputs over the threads: several share one where there are more of them than outputs
+    const int outs = rows * (D / 4), share = max(kWarps * 32 / outs, 1);
+    const int part = share > 1 ? tid / outs : 0;
+    int i = share > 1 ? tid - part * outs : tid;
+    auto piece_o = [&](int c) {
+      return __ldcg(reinterpret_cast<const float4*>(P.part_o + (slot(c) + i / (D / 4)) * D + (i % (D / 4)) * 4));
+    };
+    if (!waited) {
+      grid_dependency_wait();
+      allow_dependents();
+      waited = true;
+    }
+    // this thread's first pieces are fetched along with the states
+    constexpr int kAhead = 4;
+    float4 v[kAhead];
+    const bool mine = merge && pieces > 1 && i < outs && part < share;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (mine && part + u * share < pieces) v[u] = piece_o(part + u * share);
     for (int r = warp; r < rows; r += kWarps) {
       if (pieces == 1) {
         if (lane == 0) s_ml[r] = P.row_ml[row0 + r];
         continue;
       }
-      float M = kNegInf, L = 0.f;
-      for (int c = lane; c < pieces; c += 32) M = fmaxf(M, P.part_ml[slot(c) + r].x);
+      float2 ml = lane < pieces ? __ldcg(&P.part_ml[slot(lane) + r]) : make_float2(kNegInf, 0.f);
+      float M = ml.x;
+      for (int c = lane + 32; c < pieces; c += 32) M = fmaxf(M, __ldcg(&P.part_ml[slot(c) + r]).x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       const float base = M == kNegInf ? 0.f : M;
+      float L = 0.f;
       for (int c = lane; c < pieces; c += 32) {
-        const float2 ml = P.part_ml[slot(c) + r];
+        if (c != lane) ml = __ldcg(&P.part_ml[slot(c) + r]);
         const float f = ex2(ml.x - base);
         s_f[c * kRowsMax + r] = f;
         L = fmaf(ml.y, f, L);
@@ -689,55 +708,77 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
     }
     __syncthreads();
     if (merge && pieces > 1) {
-      // several threads share an output where there are more of them than outputs
-      const int outs = rows * (D / 4), share = max(kWarps * 32 / outs, 1);
-      for (int i0 = 0; i0 < outs; i0 += kWarps * 32) {
-        const int i = share > 1 ? tid % outs : i0 + tid, part = share > 1 ? tid / outs : 0;
-        const int r = i / (D / 4), d4 = (i - r * (D / 4)) * 4;
+      for (bool again = false;; again = true) {  // (once, unless there are more outputs than threads)
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < outs && part < share) {
-#pragma unroll 4
-          for (int c = part; c < pieces; c += share) {
+          const int r = i / (D / 4);
+          auto add = [&](const float4& x, int c) {
             const float f = s_f[c * kRowsMax + r];
-            const float4 v = *reinterpret_cast<const float4*>(P.part_o + (slot(c) + r) * D + d4);
-            o.x = fmaf(v.x, f, o.x);
-            o.y = fmaf(v.y, f, o.y);
-            o.z = fmaf(v.z, f, o.z);
-            o.w = fmaf(v.w, f, o.w);
+            o.x = fmaf(x.x, f, o.x);
+            o.y = fmaf(x.y, f, o.y);
+            o.z = fmaf(x.z, f, o.z);
+            o.w = fmaf(x.w, f, o.w);
+          };
+          int c = part;
+          if (!again) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u, c += share)
+              if (c < pieces) add(v[u], c);
           }
+#pragma unroll 4
+          for (; c < pieces; c += share) add(piece_o(c), c);
         }
         if (share > 1) {
           s_o[tid] = o;
           __syncthreads();
           if (part == 0)
             for (int p = 1; p < share; ++p) {
-              const float4 v = s_o[p * outs + i];
-              o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+              const float4 x = s_o[p * outs + i];
+              o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
             }
         }
-        if (i < outs && part == 0) write_row<T, D>(P, row0 + r, d4, s_ml[r].x, s_ml[r].y, o);
+        if (i < outs && part == 0) {
+          const int r = i / (D / 4);
+          write_row<T, D>(P, row0 + r, (i - r * (D / 4)) * 4, s_ml[r].x, s_ml[r].y, o);
+        }
+        if (share > 1 || i + kWarps * 32 - tid >= outs) break;  // the same for all threads
+        i += kWarps * 32;
       }
     }
     if (weigh) {
-      for (int r = 0; r < rows; ++r) {
-        const float2 ml = s_ml[r];
-        if (ml.y == 0.f) continue;  // only scores of -inf: no weight
-        const float inv = 1.f / ml.y;
-        const float* src = P.scores + (row0 + r) * P.score_stride + t_first;
+      constexpr int kRowsAtOnce = 4;
+      for (int r0 = 0; r0 < rows; r0 += kRowsAtOnce) {
+        float4 sc[kRowsAtOnce][2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (t_first + u * 1024 >= len) continue;
-          const float4 s = *reinterpret_cast<const float4*>(src + u * 1024);
-          w[u].x = fmaf(ex2(s.x - ml.x), inv, w[u].x);
-          w[u].y = fmaf(ex2(s.y - ml.x), inv, w[u].y);
-          w[u].z = fmaf(ex2(s.z - ml.x), inv, w[u].z);
-          w[u].w = fmaf(ex2(s.w - ml.x), inv, w[u].w);
+        for (int q = 0; q < kRowsAtOnce; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            sc[q][u] = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+            if (r0 + q < rows && t_first + u * 1024 < len)
+              sc[q][u] = __ldcg(reinterpret_cast<const float4*>(P.scores + (row0 + r0 + q) * P.score_stride + t_first + u * 1024));
+          }
+#pragma unroll
+        for (int q = 0; q < kRowsAtOnce; ++q) {
+          const float2 ml = r0 + q < rows ? s_ml[r0 + q] : make_float2(0.f, 0.f);
+          if (ml.y == 0.f) continue;  // only scores of -inf: no weight
+          const float inv = 1.f / ml.y;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            w[u].x = fmaf(ex2(sc[q][u].x - ml.x), inv, w[u].x);
+            w[u].y = fmaf(ex2(sc[q][u].y - ml.x), inv, w[u].y);
+            w[u].z = fmaf(ex2(sc[q][u].z - ml.x), inv, w[u].z);
+            w[u].w = fmaf(ex2(sc[q][u].w - ml.x), inv, w[u].w);
+          }
         }
       }
     }
     __syncthreads();
   }
-  if (!weigh) return;
+  if (!waited) {  // every CTA waits: the next kernel relies on this one's end for all that came before
+    grid_dependency_wait();
+    allow_dependents();
+  }
+  if (idle || !weigh) return;
   const int64_t a = static_cast<int64_t>(blockIdx.x) * P.pages.cap + t_first;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
