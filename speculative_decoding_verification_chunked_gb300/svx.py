@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -109,6 +110,11 @@ class Pages(ctypes.Structure):
                 ("device", ctypes.c_int32), ("flags", ctypes.c_uint32), ("pad", ctypes.c_int32)]
 
 
+# svx_heads and svx_pages as bytes, in the order of the fields above: a quarter of the time of filling the structures
+_HEADS = struct.Struct("@3P3q5P7ifIi")
+_PAGES = struct.Struct("@4P4q6iIi")
+assert (_HEADS.size, _PAGES.size) == (ctypes.sizeof(Heads), ctypes.sizeof(Pages))
+
 # name -> (restype, argtypes); every symbol declared in include/svx.h
 _P = ctypes.c_void_p
 _SIGS = {
@@ -183,16 +189,16 @@ _SIGS = {
     "svx_width_cost": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_double)]),
     "svx_rope_init": (ctypes.c_int, [ctypes.POINTER(RopeTable), ctypes.c_int32, ctypes.c_int32,
                                      ctypes.POINTER(ctypes.c_double), ctypes.c_float]),
-    "svx_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(Heads), ctypes.POINTER(RopeTable), _P, _P, _P, _P]),
-    "svx_paged_append": (ctypes.c_int, [ctypes.POINTER(Heads), ctypes.POINTER(RopeTable), ctypes.POINTER(Pages), _P, _P,
-                                        _P, _P, _P]),
-    "svx_paged_decode_workspace": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
+    # (svx_heads and svx_pages go in as packed bytes: _HEADS, _PAGES)
+    "svx_qk_norm_rope": (ctypes.c_int, [_P, _P, _P, _P, _P, _P]),
+    "svx_paged_append": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
+    "svx_paged_decode_workspace": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
                                                   ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
-    "svx_paged_decode": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_int64,
+    "svx_paged_decode": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_int64,
                                         ctypes.c_float, _P, _P, _P, _P, _P, ctypes.c_int64, _P]),
-    "svx_paged_evict_workspace": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+    "svx_paged_evict_workspace": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
                                                  ctypes.POINTER(ctypes.c_int64)]),
-    "svx_paged_evict": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32,
+    "svx_paged_evict": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32,
                                        ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, _P]),
     "svx_version": (ctypes.c_char_p, []),
     "svx_abi_sizes": (ctypes.c_int32, [ctypes.POINTER(ctypes.c_int64), ctypes.c_int32]),
@@ -754,30 +760,31 @@ def _type_code(t, what: str) -> int:
     raise SvxError(ERR_UNSUPPORTED, f"{what}: dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
 
 
-def _dense(t, dtype, shape: tuple, device: int, what: str) -> Optional[int]:
-    """Address of a dense tensor of exactly this type and shape on this CUDA device (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        raise SvxError(ERR_INVALID_ARG, f"{what}: {t.dtype} {list(t.shape)} on {t.device}, contiguous {t.is_contiguous()}; "
-                                        f"expected dense {dtype} {list(shape)} on cuda:{device}")
+def _dense(t, dtype, shape: tuple, device: int, what: str) -> int:
+    """Address of a dense tensor of exactly this type and shape on this CUDA device."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        got = "None" if t is None else f"{t.dtype} {list(t.shape)} on {t.device}, contiguous {t.is_contiguous()}"
+        raise SvxError(ERR_INVALID_ARG, f"{what}: {got}; expected dense {dtype} {list(shape)} on cuda:{device}")
     return t.data_ptr()
+
+
+def _optional(t, dtype, shape: tuple, device: int, what: str) -> int:
+    return 0 if t is None else _dense(t, dtype, shape, device, what)
 
 
 def _head_rows(t, n_req: int, n_tok: int, d: int, dtype, device: int, what: str):
     """Address, token stride and count of heads [n_req][n_tok][heads][d], possibly a view of a fused projection."""
-    shape = t.shape
-    if len(shape) != 4 or shape[0] != n_req or shape[1] != n_tok or shape[3] != d or t.dtype is not dtype or \
-            t.get_device() != device:
-        raise SvxError(ERR_INVALID_ARG, f"{what}: {t.dtype} {list(t.shape)} on {t.device}, expected {dtype} "
-                                        f"[{n_req}, {n_tok}, heads, {d}] on cuda:{device}")
-    s0, s1, s2, s3 = t.stride()
-    heads = shape[2]
-    row = s1 if n_tok > 1 else s0 if n_req > 1 else heads * d
-    if s3 != 1 or (heads > 1 and s2 != d) or (n_tok > 1 and n_req > 1 and s0 != n_tok * s1):
-        raise SvxError(ERR_INVALID_ARG, f"{what}: strides {list(t.stride())}: a token's heads must be dense, and tokens "
-                                        "evenly spaced over the requests")
-    return t.data_ptr(), row, heads
+    if t is not None and t.dtype is dtype and t.get_device() == device and t.dim() == 4:
+        b, n, heads, dim = t.shape
+        if b == n_req and n == n_tok and dim == d:
+            s0, s1, s2, s3 = t.stride()
+            row = s1 if n_tok > 1 else s0 if n_req > 1 else heads * d
+            if s3 != 1 or (heads > 1 and s2 != d) or (n_tok > 1 and n_req > 1 and s0 != n_tok * s1):
+                raise SvxError(ERR_INVALID_ARG, f"{what}: strides {list(t.stride())}: a token's heads must be dense, and "
+                                                "tokens evenly spaced over the requests")
+            return t.data_ptr(), row, heads
+    got = "None" if t is None else f"{t.dtype} {list(t.shape)} on {t.device}"
+    raise SvxError(ERR_INVALID_ARG, f"{what}: {got}, expected {dtype} [{n_req}, {n_tok}, heads, {d}] on cuda:{device}")
 
 
 def _launch_stream(device: int, stream) -> int:
@@ -799,9 +806,9 @@ def _workspace(workspace, need: int, device: int, stream):
                 workspace.numel() * workspace.element_size() < need:
             raise SvxError(ERR_INVALID_ARG, f"workspace: a dense tensor of at least {need} bytes on cuda:{device} is needed")
         return workspace
-    dev = torch.device("cuda", device)
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    dev = torch.device("cuda", device)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
     with torch.cuda.stream(s):
         return torch.empty(need, dtype=torch.uint8, device=dev)
@@ -826,6 +833,7 @@ class Rope:
         self.table = RopeTable()
         f = (ctypes.c_double * max(1, len(inv_freq)))(*[float(x) for x in inv_freq])
         _static_error(lib.svx_rope_init(ctypes.byref(self.table), rot_dim, int(bool(neighbours)), f, scale))
+        self.address = ctypes.addressof(self.table)
 
 
 def _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, status):
@@ -840,18 +848,16 @@ def _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, status):
         raise SvxError(ERR_INVALID_ARG, f"q is on {q.device}, not on a CUDA device")
     qp, qs, _ = _head_rows(q, n_req, n_tok, d, dtype, device, "q")
     kp, ks, hkv = _head_rows(k, n_req, n_tok, d, dtype, device, "k")
-    vp, vs, hv = (None, 0, hkv) if v is None else _head_rows(v, n_req, n_tok, d, dtype, device, "v")
+    vp, vs, hv = (0, 0, hkv) if v is None else _head_rows(v, n_req, n_tok, d, dtype, device, "v")
     if hv != hkv:
         raise SvxError(ERR_INVALID_ARG, f"v has {hv} heads, k {hkv}")
     if eps is not None and not eps >= 0.0:
         raise SvxError(ERR_INVALID_ARG, "eps must be >= 0, or None for no norms")
-    if pos is None:
-        raise SvxError(ERR_INVALID_ARG, "pos is required")
     i32 = torch.int32
-    h = Heads(qp, kp, vp, qs, ks, vs, _dense(q_norm, dtype, (d,), device, "q_norm"),
-              _dense(k_norm, dtype, (d,), device, "k_norm"), _dense(pos, i32, (n_req, n_tok), device, "pos"),
-              _dense(n_new, i32, (n_req,), device, "n_new"), status, n_req, n_tok, hq, hkv, d, code, device,
-              -1.0 if eps is None else eps, POINTERS_CHECKED, 0)
+    h = _HEADS.pack(qp, kp, vp, qs, ks, vs, _optional(q_norm, dtype, (d,), device, "q_norm"),
+                    _optional(k_norm, dtype, (d,), device, "k_norm"), _dense(pos, i32, (n_req, n_tok), device, "pos"),
+                    _optional(n_new, i32, (n_req,), device, "n_new"), status, n_req, n_tok, hq, hkv, d, code, device,
+                    -1.0 if eps is None else eps, POINTERS_CHECKED, 0)
     return h, (n_req, n_tok, hq, hkv, d), device, dtype
 
 
@@ -864,11 +870,11 @@ def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None
     candidate_attn take.  eps None: no norms.  n_new: int32 [B], tokens of each request that count, or None.
     status: int32 [1] that becomes non-zero if n_new leaves [0, n], or None.  stream: the current one by default.
     """
-    sp = None if status is None else _dense(status, _torch().int32, (1,), q.get_device(), "status")
+    sp = _optional(status, _torch().int32, (1,), q.get_device(), "status")
     h, (b, n, hq, hkv, d), device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, sp)
     _static_error(lib.svx_qk_norm_rope(
-        ctypes.byref(h), ctypes.byref(rope.table), _dense(q_out, dtype, (b, hq, n, d), device, "q_out"),
-        _dense(k_out, dtype, (b, n, hkv, d), device, "k_out"), _dense(v_out, dtype, (b, n, hkv, d), device, "v_out"),
+        h, rope.address, _dense(q_out, dtype, (b, hq, n, d), device, "q_out"),
+        _dense(k_out, dtype, (b, n, hkv, d), device, "k_out"), _optional(v_out, dtype, (b, n, hkv, d), device, "v_out"),
         _launch_stream(device, stream)))
 
 
@@ -895,28 +901,28 @@ class PagedCache:
         self.device, self.dtype = k_pages.get_device(), k_pages.dtype
         n_pages, self.page_size, self.n_kv_heads, self.head_dim = k_pages.shape
         self.status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
-        self._pages = Pages(k_pages.data_ptr(), v_pages.data_ptr(), None, self.status.data_ptr(), *k_pages.stride()[:3],
-                            n_pages, self.page_size, 0, self.n_kv_heads, self.head_dim, _type_code(k_pages, "k_pages"),
-                            self.device, POINTERS_CHECKED, 0)
+        # the C struct's fields before and after the table and its width
+        self._front = (k_pages.data_ptr(), v_pages.data_ptr())
+        self._middle = (self.status.data_ptr(), *k_pages.stride()[:3], n_pages, self.page_size)
+        self._back = (self.n_kv_heads, self.head_dim, _type_code(k_pages, "k_pages"), self.device, POINTERS_CHECKED, 0)
         self._sizes = {}
 
     def _with_table(self, table, n_req: Optional[int]):
-        """The C struct for a call (a copy: calls from several threads do not share it)."""
+        """The C struct for a call, the number of requests and the table's width."""
         shape = table.shape
         if len(shape) != 2 or (n_req is not None and shape[0] != n_req):
             raise SvxError(ERR_INVALID_ARG, f"table: shape {list(shape)}, expected [{n_req or 'requests'}, max_pages]")
-        p = Pages.from_buffer_copy(self._pages)
-        p.table = _dense(table, _torch().int32, shape, self.device, "table")
-        p.max_pages = shape[1]
-        return p
+        at = _dense(table, _torch().int32, shape, self.device, "table")
+        n_req, wide = shape
+        return _PAGES.pack(*self._front, at, *self._middle, wide, *self._back), n_req, wide
 
     def _need(self, what: str, fn, pages, *args) -> int:
-        key = (what, pages.max_pages) + args
-        need = self._sizes.get(key)
+        """Bytes of workspace (a function of sizes alone)."""
+        need = self._sizes.get((what,) + args)
         if need is None:
             n = ctypes.c_int64(0)
-            _static_error(fn(ctypes.byref(pages), *args, ctypes.byref(n)))
-            need = self._sizes[key] = n.value
+            _static_error(fn(pages, *args[1:], ctypes.byref(n)))
+            need = self._sizes[(what,) + args] = n.value
         return need
 
     def check(self) -> bool:
@@ -936,15 +942,17 @@ class PagedCache:
         slots start[b] + j and q into q_out [B][Hq][n][d]; acc (fp32) becomes 0 and slot_pos (int32), both
         [B][Hkv][max_pages * page_size], the token's position at the new slots."""
         torch = _torch()
-        h, (b, n, hq, _, d), device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, None)
+        if v is None:
+            raise SvxError(ERR_INVALID_ARG, "v is required")
+        h, (b, n, hq, _, d), device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, 0)
         if device != self.device:
             raise SvxError(ERR_INVALID_ARG, f"q is on cuda:{device}, the cache on cuda:{self.device}")
-        p = self._with_table(table, b)
-        meta = (b, self.n_kv_heads, p.max_pages * self.page_size)
+        p, _, wide = self._with_table(table, b)
+        meta = (b, self.n_kv_heads, wide * self.page_size)
         _static_error(lib.svx_paged_append(
-            ctypes.byref(h), ctypes.byref(rope.table), ctypes.byref(p), _dense(start, torch.int32, (b,), device, "start"),
-            _dense(q_out, dtype, (b, hq, n, d), device, "q_out"), _dense(acc, torch.float32, meta, device, "acc"),
-            _dense(slot_pos, torch.int32, meta, device, "slot_pos"), _launch_stream(device, stream)))
+            h, rope.address, p, _dense(start, torch.int32, (b,), device, "start"),
+            _dense(q_out, dtype, (b, hq, n, d), device, "q_out"), _optional(acc, torch.float32, meta, device, "acc"),
+            _optional(slot_pos, torch.int32, meta, device, "slot_pos"), _launch_stream(device, stream)))
 
     def decode(self, q, table, lens, o, lse, max_len: int = 0, scale: float = 0.0, acc_in=None, acc_out=None,
                workspace=None, stream=None):
@@ -958,15 +966,15 @@ class PagedCache:
             raise SvxError(ERR_INVALID_ARG, f"q: shape {list(q.shape)}, expected [requests][heads][1][head_dim]")
         b, hq = q.shape[0], q.shape[1]
         device, rows = self.device, (b, hq, 1, self.head_dim)
-        p = self._with_table(table, b)
-        meta = (b, self.n_kv_heads, p.max_pages * self.page_size)
-        ws = _workspace(workspace, self._need("decode", lib.svx_paged_decode_workspace, p, b, hq, max_len,
+        p, _, wide = self._with_table(table, b)
+        meta = (b, self.n_kv_heads, wide * self.page_size)
+        ws = _workspace(workspace, self._need("decode", lib.svx_paged_decode_workspace, p, wide, b, hq, max_len,
                                               int(acc_in is not None)), device, stream)
         _static_error(lib.svx_paged_decode(
-            ctypes.byref(p), b, hq, _dense(q, self.dtype, rows, device, "q"),
+            p, b, hq, _dense(q, self.dtype, rows, device, "q"),
             _dense(lens, torch.int32, (b,), device, "lens"), max_len, scale, _dense(o, self.dtype, rows, device, "o"),
-            _dense(lse, torch.float32, (b, hq, 1), device, "lse"), _dense(acc_in, torch.float32, meta, device, "acc_in"),
-            _dense(acc_out, torch.float32, meta, device, "acc_out"), ws.data_ptr(), ws.numel() * ws.element_size(),
+            _dense(lse, torch.float32, (b, hq, 1), device, "lse"), _optional(acc_in, torch.float32, meta, device, "acc_in"),
+            _optional(acc_out, torch.float32, meta, device, "acc_out"), ws.data_ptr(), ws.numel() * ws.element_size(),
             _launch_stream(device, stream)))
 
     def evict(self, table, lens, budget: int, sink: int, recent: int, next_pos, acc_in, pos_in, acc_out, pos_out, len_out,
@@ -976,17 +984,13 @@ class PagedCache:
         evicted ones before it, with their acc and position; len_out gets the new lengths.  acc (fp32), pos (int32):
         [B][Hkv][max_pages * page_size]; lens, next_pos, len_out: int32 [B]; outputs may be their inputs."""
         torch = _torch()
-        p = self._with_table(table, None)
-        b, device = table.shape[0], self.device
-        meta = (b, self.n_kv_heads, p.max_pages * self.page_size)
+        p, b, wide = self._with_table(table, None)
+        device, meta = self.device, (b, self.n_kv_heads, wide * self.page_size)
         i32, f32 = torch.int32, torch.float32
-        for what, t in (("next_pos", next_pos), ("acc_in", acc_in), ("pos_in", pos_in), ("acc_out", acc_out),
-                        ("pos_out", pos_out), ("len_out", len_out), ("lens", lens)):
-            if t is None:
-                raise SvxError(ERR_INVALID_ARG, f"{what} is required")
-        ws = _workspace(workspace, self._need("evict", lib.svx_paged_evict_workspace, p, b, max_len, budget), device, stream)
+        ws = _workspace(workspace, self._need("evict", lib.svx_paged_evict_workspace, p, wide, b, max_len, budget), device,
+                        stream)
         _static_error(lib.svx_paged_evict(
-            ctypes.byref(p), b, _dense(lens, i32, (b,), device, "lens"), max_len, budget, sink, recent,
+            p, b, _dense(lens, i32, (b,), device, "lens"), max_len, budget, sink, recent,
             _dense(next_pos, i32, (b,), device, "next_pos"), _dense(acc_in, f32, meta, device, "acc_in"),
             _dense(pos_in, i32, meta, device, "pos_in"), _dense(acc_out, f32, meta, device, "acc_out"),
             _dense(pos_out, i32, meta, device, "pos_out"), _dense(len_out, i32, (b,), device, "len_out"), ws.data_ptr(),
