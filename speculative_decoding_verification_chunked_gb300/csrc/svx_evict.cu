@@ -29,6 +29,8 @@ constexpr int kMaxThreads = 1024;
 constexpr int kMaxKeys = 32;    // per thread
 constexpr int kMaxCluster = 8;  // portable
 constexpr int kSplitKeys = 16;
+constexpr int kSmallThreads = 256;
+constexpr int kFewMoves = 8;  // of a warp
 static_assert(kMaxThreads * kMaxKeys * kMaxCluster == SVX_EVICT_MAX_LEN, "the longest row a cluster holds");
 
 struct EvictParams {
@@ -48,6 +50,8 @@ struct EvictParams {
   int32_t most;     // moves a row can need
   int32_t cluster;
   int32_t chunk;    // moves of a warp at a time, <= 32
+  int32_t fused;    // select_kernel makes the moves too
+  int32_t head_dim;
 };
 
 // Unsigned order = float order; NaN as -inf, -0 as +0.
@@ -105,6 +109,29 @@ __device__ __forceinline__ int2 cluster_scan(int2 v, Shared& s, int turn, int n_
   }
   *total = sum;
   return before;
+}
+
+// One move: where a row of the request's head comes from and where it goes (element offsets; -1: left out).
+struct Move {
+  int64_t from, to;
+};
+template <typename T, int D>
+__device__ __forceinline__ Move look_up(const EvictParams& P, const int32_t* table, int h, const T* pool, int hole, int spare) {
+  const uint32_t ps = P.pages.page_size;
+  const uint32_t pt = page_of(P.pages, static_cast<uint32_t>(hole)), pf = page_of(P.pages, static_cast<uint32_t>(spare));
+  const int32_t page_to = table[pt], page_from = table[pf];
+  Move m{slot_offset(P.pages, page_from, spare - pf * ps), slot_offset(P.pages, page_to, hole - pt * ps)};
+  if (m.to < 0 || m.from < 0) {
+    atomicOr(P.pages.status, kErrInput);
+    return Move{-1, -1};
+  }
+  const int64_t head = static_cast<int64_t>(h) * P.pages.head_stride;
+  m.to += head;
+  m.from += head;
+  if (!in_bounds(pool + m.from, D, pool, P.pages.extent, P.pages.status, kSitePool) ||
+      !in_bounds(pool + m.to, D, pool, P.pages.extent, P.pages.status, kSitePool))
+    return Move{-1, -1};
+  return m;
 }
 
 template <int KEYS, int THREADS>
@@ -281,9 +308,14 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
 #pragma unroll
   for (int i = 0; i < KEYS; ++i) {
     const uint32_t mh = __shfl_sync(0xffffffffu, hole, i), ms = __shfl_sync(0xffffffffu, spare, i);
-    const int ih = __shfl_sync(0xffffffffu, ah, i) + __popc(mh & before), is = __shfl_sync(0xffffffffu, as, i) + __popc(ms & before);
-    if ((mh >> lane & 1u) && ih < P.most) holes[ih] = first + 32 * i;
-    if ((ms >> lane & 1u) && is < P.most) spares[is] = first + 32 * i;
+    if (mh) {  // the same in all lanes
+      const int ih = __shfl_sync(0xffffffffu, ah, i) + __popc(mh & before);
+      if ((mh >> lane & 1u) && ih < P.most) holes[ih] = first + 32 * i;
+    }
+    if (ms) {
+      const int is = __shfl_sync(0xffffffffu, as, i) + __popc(ms & before);
+      if ((ms >> lane & 1u) && is < P.most) spares[is] = first + 32 * i;
+    }
   }
   // weights and positions of the slots that stay where they are
   const bool copy_acc = P.acc_out != P.acc_in, copy_pos = P.pos_out != P.pos_in;
@@ -311,6 +343,45 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     }
   }
   if (n_cta > 1) cg::this_cluster().sync();  // no CTA leaves while another may still read its shared memory
+  if constexpr (THREADS != kSmallThreads) return;
+  if (!P.fused) return;
+  // Few moves, one small CTA to the row: they are made here, without another kernel.
+  if (threadIdx.x == 0 && row == b * P.pages.n_kv_heads) P.len_out[b] = n;
+  __syncthreads();  // holes and spares are written
+  const int M = min(min(all.x, all.y), P.most);
+  const int32_t* table = P.pages.table + static_cast<int64_t>(b) * P.pages.max_pages;
+  const int h = row - b * P.pages.n_kv_heads;
+  using T = uint16_t;
+  T *pk = static_cast<T*>(P.pages.k), *pv = static_cast<T*>(P.pages.v);
+  // A lane looks up a move, eight to a warp; then d / 8 lanes copy a row of K and as many its row of V.
+  constexpr int kFew = 8;
+  const int pieces = P.head_dim / 8, side = 16 / pieces;  // side: moves of a warp at a time
+  const int piece = lane % pieces, mine = (lane % 16) / pieces;
+  T* pool = lane >= 16 ? pv : pk;
+  for (int i0 = warp * kFew; i0 < M; i0 += kWarps * kFew) {
+    Move m{-1, -1};
+    if (lane < kFew && i0 + lane < M) {
+      const int hole = holes[i0 + lane], spare = spares[i0 + lane];
+      const float w = P.acc_in[meta + spare];
+      const int32_t pos = P.pos_in[meta + spare];
+      m = P.head_dim == 128 ? look_up<T, 128>(P, table, h, pk, hole, spare) : look_up<T, 64>(P, table, h, pk, hole, spare);
+      P.acc_out[meta + hole] = w;
+      P.pos_out[meta + hole] = pos;
+    }
+    int64_t to[kFew];
+    uint4 v[kFew];
+#pragma unroll
+    for (int u = 0; u < kFew; ++u) {
+      const int k = u * side + mine;  // (with two at a time, four turns do)
+      const int64_t from = __shfl_sync(0xffffffffu, m.from, k & 7);
+      to[u] = __shfl_sync(0xffffffffu, m.to, k & 7);
+      if (k >= kFew) to[u] = -1;
+      if (to[u] >= 0) v[u] = reinterpret_cast<const uint4*>(pool + from)[piece];
+    }
+#pragma unroll
+    for (int u = 0; u < kFew; ++u)
+      if (to[u] >= 0) reinterpret_cast<uint4*>(pool + to[u])[piece] = v[u];
+  }
 }
 
 constexpr int kMoveWarps = 2;
@@ -341,24 +412,11 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const __grid_cons
     int64_t from = -1, to = -1;
     if (lane < P.chunk && i0 + lane < M) {
       const int hole = holes[i0 + lane], spare = spares[i0 + lane];
-      const uint32_t ps = P.pages.page_size;
-      const uint32_t pt = page_of(P.pages, static_cast<uint32_t>(hole)), pf = page_of(P.pages, static_cast<uint32_t>(spare));
-      const int32_t page_to = table[pt], page_from = table[pf];
       const float w = P.acc_in[meta + spare];
       const int32_t pos = P.pos_in[meta + spare];
-      to = slot_offset(P.pages, page_to, hole - pt * ps);
-      from = slot_offset(P.pages, page_from, spare - pf * ps);
-      if (to < 0 || from < 0) {
-        atomicOr(P.pages.status, kErrInput);
-        to = from = -1;
-      } else {
-        const int64_t head = static_cast<int64_t>(h) * P.pages.head_stride;
-        to += head;
-        from += head;
-        if (!in_bounds(pool + from, D, pool, P.pages.extent, P.pages.status, kSitePool) ||
-            !in_bounds(pool + to, D, pool, P.pages.extent, P.pages.status, kSitePool))
-          to = from = -1;
-      }
+      const Move move = look_up<T, D>(P, table, h, pool, hole, spare);
+      from = move.from;
+      to = move.to;
       P.acc_out[meta + hole] = w;
       P.pos_out[meta + hole] = pos;
     }
@@ -430,12 +488,17 @@ cudaError_t launch_select(const EvictParams& p, int rows, cudaStream_t s) {
 // where one does not hold the row, or where there are SMs for it and it shortens a thread's part.
 constexpr int kSmallRow = 256 * 16;
 cudaError_t launch_selects(EvictParams& p, int rows, int sms, cudaStream_t s) {
-  const int threads = p.max_len <= kSmallRow ? 256 : 1024;
+  const int threads = p.max_len <= kSmallRow ? kSmallThreads : kMaxThreads;
   p.cluster = 1;
   auto keys = [&](int c) { return (p.max_len + c * threads - 1) / (c * threads); };
   while (p.cluster < kMaxCluster &&
          (keys(p.cluster) > kMaxKeys || (keys(p.cluster) > kSplitKeys && rows * p.cluster * 2 <= sms)))
     p.cluster *= 2;
+  // Moves in the same kernel where a small CTA has one turn of its warps of them, which saves a launch and a trip through
+  // memory: 64 rows of 2112 slots to 2048 take 9.2 us so and 9.6 us in two kernels, 256 rows of 1040 to 1024 7.2 and 8.0 us;
+  // with four turns it is 14.4 and 11.8 us.  Not where the new lengths go over the old, which other heads' CTAs may
+  // still have to read.
+  p.fused = threads == kSmallThreads && p.cluster == 1 && p.most <= kFewMoves * (threads / 32) && p.len_out != p.len;
   const int per = keys(p.cluster);
   if (threads == 256)
     return per <= 4 ? launch_select<4, 256>(p, rows, s) : per <= 8 ? launch_select<8, 256>(p, rows, s)
@@ -525,10 +588,11 @@ extern "C" svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, con
   p.sink = sink;
   p.recent = recent;
   p.most = z.most;
+  p.head_dim = cache->head_dim;
   const int rows = n_req * p.pages.n_kv_heads;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = svx::launch_selects(p, rows, sms, s);
-  if (e == cudaSuccess) e = svx::launch_moves(p, cache->head_dim, rows, sms, s);
+  if (e == cudaSuccess && !p.fused) e = svx::launch_moves(p, cache->head_dim, rows, sms, s);
   if (e != cudaSuccess) return paged_fail(SVX_ERR_CUDA, "evict kernel launch failed: %s", cudaGetErrorString(e));
   return SVX_OK;
 }
