@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kStages = 3;
+constexpr uint32_t kMinChunks = 2 * kWarps;  // a CTA takes at least so many chunks, if there are
 constexpr int kChunkBytes = 4096;  // of K (and as much of V)
 constexpr int kRowsMax = 16;       // query heads of an item
 constexpr float kTau = 8.0f;       // p stays below 2^8
@@ -58,7 +59,6 @@ struct DecodeParams {
   float scale;      // softmax scale * log2(e)
   int32_t max_len;
   int32_t n_q, group, blocks;  // blocks of 16 query heads per KV head
-  int32_t min_chunks;          // a CTA takes at least this many (if there are)
   int32_t ctas;                // of the attention kernel
 };
 
@@ -110,14 +110,18 @@ __device__ __forceinline__ int build_plan(const DecodeParams& P, Plan& s, bool r
 // in 32 bits with T = q used + r.
 struct Split {
   uint32_t used, q, r, total;
+  float per_used;
   __device__ __forceinline__ Split(const DecodeParams& P, int T) {
     total = T;
-    used = (total + P.min_chunks - 1) / P.min_chunks;
-    if (used > static_cast<uint32_t>(P.ctas)) used = P.ctas;
+    used = min((total + kMinChunks - 1) / kMinChunks, static_cast<uint32_t>(P.ctas));
     q = used ? total / used : 0;
     r = total - q * used;
+    per_used = __frcp_rn(static_cast<float>(used));
   }
-  __device__ __forceinline__ int begin(uint32_t c) const { return static_cast<int>(c * q + c * r / used); }  // c, r <= 256
+  // c r <= 2^16, and its quotient by used <= 256 is whole or at least 1/256 off: the float product is within 2^-14 of it
+  __device__ __forceinline__ int begin(uint32_t c) const {
+    return static_cast<int>(c * q) + __float2int_rd(fmaf(static_cast<float>(c * r), per_used, 0.001f));
+  }
   // the CTA that holds chunk x
   __device__ __forceinline__ int of(int x) const {
     int c = min(static_cast<int>(static_cast<float>(x) * (static_cast<float>(used) / static_cast<float>(total))),
@@ -260,6 +264,17 @@ __device__ __forceinline__ void write_row(const DecodeParams& P, int64_t row, in
   if (d4 == 0) P.lse[row] = L == 0.f ? kNegInf : (M + log2f(L)) * kLn2;
 }
 
+// Requests without slots: O = 0, LSE = -inf.
+template <typename T, int D>
+__device__ __forceinline__ void write_empty(const DecodeParams& P, const Plan& plan) {
+  for (int b = blockIdx.x; b < P.pages.n_req; b += gridDim.x) {
+    if (plan.first[b + 1] > plan.first[b]) continue;
+    uint32_t* ob = reinterpret_cast<uint32_t*>(static_cast<T*>(P.o) + static_cast<int64_t>(b) * P.n_q * D);
+    for (int i = threadIdx.x; i < P.n_q * D / 2; i += blockDim.x) ob[i] = 0u;
+    for (int i = threadIdx.x; i < P.n_q; i += blockDim.x) P.lse[static_cast<int64_t>(b) * P.n_q + i] = kNegInf;
+  }
+}
+
 template <typename T, int D, bool WIDE, bool SCORES>
 __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_constant__ DecodeParams P) {
   constexpr int CT = kChunkBytes / (2 * D);  // slots of a chunk: 16 (d = 128) or 32 (d = 64)
@@ -277,15 +292,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
   allow_dependents();
   const int T_all = build_plan<CT>(P, plan, blockIdx.x == 0);
 
-  // requests without slots: O = 0, LSE = -inf
-  for (int b = blockIdx.x; b < P.pages.n_req; b += gridDim.x) {
-    if (plan.first[b + 1] > plan.first[b]) continue;
-    uint32_t* ob = reinterpret_cast<uint32_t*>(static_cast<T*>(P.o) + static_cast<int64_t>(b) * P.n_q * D);
-    for (int i = tid; i < P.n_q * D / 2; i += blockDim.x) ob[i] = 0u;
-    for (int i = tid; i < P.n_q; i += blockDim.x) P.lse[static_cast<int64_t>(b) * P.n_q + i] = kNegInf;
-  }
   const Split split(P, T_all);
-  if (blockIdx.x >= split.used) return;
+  if (blockIdx.x >= split.used) {
+    write_empty<T, D>(P, plan);
+    return;
+  }
   const int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
   const int w0 = x0 + static_cast<int>(static_cast<int64_t>(x1 - x0) * warp / kWarps);
   const int w1 = x0 + static_cast<int>(static_cast<int64_t>(x1 - x0) * (warp + 1) / kWarps);
@@ -627,6 +638,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
       if (d4 == 0) P.part_ml[slot] = make_float2(M, L);
     }
   }
+  write_empty<T, D>(P, plan);
 }
 
 // Merges the pieces of the items that more than one CTA worked on, and adds the weights.  CTA (x, y): KV head x of all
@@ -634,6 +646,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
 // acc_out[t] = acc_in[t] + sum over the KV head's query heads of 2^(s_t - m) / l, from the stored scores.
 constexpr int kMaxCtas = 256;
 constexpr int kWeightSlots = 2048;
+constexpr int kQuads = kWeightSlots / (4 * kWarps * 32);  // of slots, to a thread
 
 template <typename T, int D, bool SCORES>
 __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant__ DecodeParams P) {
@@ -648,11 +661,14 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
   const int T_all = build_plan<CT>(P, plan, false);
   const int b = blockIdx.x / P.pages.n_kv_heads, h = blockIdx.x - b * P.pages.n_kv_heads;
   const int n = plan.n[b], len = plan.len[b];
-  const int t_first = blockIdx.y * kWeightSlots + tid * 4;  // this thread's slots: 4 here and 4 behind 1024 more
+  const int t_first = blockIdx.y * kWeightSlots + tid * 4;  // this thread's slots: 4 here and 4 behind each 1024 more
   const bool weigh = SCORES && static_cast<int>(blockIdx.y) * kWeightSlots < len;
   const bool idle = n == 0 || (!weigh && static_cast<int>(blockIdx.y) >= P.blocks);
   const Split split(P, T_all);
-  float4 w[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  float4 w[kQuads], before[kQuads];  // the weights, and acc_in
+#pragma unroll
+  for (int u = 0; u < kQuads; ++u) w[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int64_t at_acc = static_cast<int64_t>(blockIdx.x) * P.pages.cap + t_first;
   bool waited = false;
   for (int blk = weigh ? 0 : blockIdx.y; !idle && blk < (weigh ? P.blocks : static_cast<int>(blockIdx.y) + 1); ++blk) {
     const bool merge = static_cast<int>(blockIdx.y) == blk;
@@ -676,6 +692,14 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
       grid_dependency_wait();
       allow_dependents();
       waited = true;
+      if (weigh) {
+#pragma unroll
+        for (int u = 0; u < kQuads; ++u) {
+          const int left = len - t_first - u * 1024;
+          const float* a = P.acc_in + at_acc + u * 1024;
+          before[u] = make_float4(left > 0 ? a[0] : 0.f, left > 1 ? a[1] : 0.f, left > 2 ? a[2] : 0.f, left > 3 ? a[3] : 0.f);
+        }
+      }
     }
     // this thread's first pieces are fetched along with the states
     constexpr int kAhead = 4;
@@ -748,11 +772,11 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
     if (weigh) {
       constexpr int kRowsAtOnce = 4;
       for (int r0 = 0; r0 < rows; r0 += kRowsAtOnce) {
-        float4 sc[kRowsAtOnce][2];
+        float4 sc[kRowsAtOnce][kQuads];
 #pragma unroll
         for (int q = 0; q < kRowsAtOnce; ++q)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < kQuads; ++u) {
             sc[q][u] = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
             if (r0 + q < rows && t_first + u * 1024 < len)
               sc[q][u] = __ldcg(reinterpret_cast<const float4*>(P.scores + (row0 + r0 + q) * P.score_stride + t_first + u * 1024));
@@ -763,7 +787,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
           if (ml.y == 0.f) continue;  // only scores of -inf: no weight
           const float inv = 1.f / ml.y;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < kQuads; ++u) {
             w[u].x = fmaf(ex2(sc[q][u].x - ml.x), inv, w[u].x);
             w[u].y = fmaf(ex2(sc[q][u].y - ml.x), inv, w[u].y);
             w[u].z = fmaf(ex2(sc[q][u].z - ml.x), inv, w[u].z);
@@ -779,19 +803,17 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
     allow_dependents();
   }
   if (idle || !weigh) return;
-  const int64_t a = static_cast<int64_t>(blockIdx.x) * P.pages.cap + t_first;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const float v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+  for (int u = 0; u < kQuads; ++u) {
+    const float v[4] = {before[u].x + w[u].x, before[u].y + w[u].y, before[u].z + w[u].z, before[u].w + w[u].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (t_first + u * 1024 + e < len) P.acc_out[a + u * 1024 + e] = P.acc_in[a + u * 1024 + e] + v[e];
+      if (t_first + u * 1024 + e < len) P.acc_out[at_acc + u * 1024 + e] = v[e];
   }
 }
 
 // ------------------------------------------------------------------ host
 
-constexpr int kMinChunks = 2 * kWarps;
 
 struct Sizes {
   int32_t max_len, blocks, ctas;
@@ -920,7 +942,6 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   p.n_q = n_q_heads;
   p.group = n_q_heads / cache->n_kv_heads;
   p.blocks = z.blocks;
-  p.min_chunks = svx::kMinChunks;
   p.ctas = z.ctas;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
