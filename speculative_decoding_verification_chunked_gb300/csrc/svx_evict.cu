@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
         if (n_cta > 1) cg::this_cluster().sync();
         if (warp == 0) {  // lane l has bins 8 l .. 8 l + 7; keys above a bin = suffix sums
           int c[8] = {};
+#pragma unroll 2
           for (int peer = 0; peer < n_cta; ++peer) {
             const int32_t* bins = n_cta > 1 ? cg::this_cluster().map_shared_rank(s.hist[pass], peer) : s.hist[pass];
             const int4 x = reinterpret_cast<const int4*>(bins)[2 * lane], y = reinterpret_cast<const int4*>(bins)[2 * lane + 1];
@@ -295,6 +296,30 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
   }
   const int in_front = min(max(n - base, 0), 32);
   const uint32_t front = in_front == 32 ? 0xffffffffu : (1u << in_front) - 1u;  // slots < n
+  // weights and positions of the slots that stay where they are
+  const bool copy_acc = P.acc_out != P.acc_in, copy_pos = P.pos_out != P.pos_in;
+  if (copy_acc || copy_pos) {
+#pragma unroll
+    for (int i0 = 0; i0 < KEYS; i0 += LOADS) {
+      if (first - lane + 32 * i0 >= n) break;  // the same for the warp
+      float w[LOADS];
+      int32_t pos[LOADS];
+      uint32_t stays = 0;
+#pragma unroll
+      for (int u = 0; u < LOADS; ++u) {  // together, ahead of the stores
+        const int64_t t = meta + first + 32 * (i0 + u);
+        stays |= (__shfl_sync(0xffffffffu, keep & front, i0 + u) >> lane & 1u) << u;
+        if (copy_acc && (stays >> u & 1u)) w[u] = P.acc_in[t];
+        if (copy_pos && (stays >> u & 1u)) pos[u] = P.pos_in[t];
+      }
+#pragma unroll
+      for (int u = 0; u < LOADS; ++u) {
+        const int64_t t = meta + first + 32 * (i0 + u);
+        if (copy_acc && (stays >> u & 1u)) P.acc_out[t] = w[u];
+        if (copy_pos && (stays >> u & 1u)) P.pos_out[t] = pos[u];
+      }
+    }
+  }
   uint32_t hole = lane < KEYS ? front & ~keep : 0u, spare = keep & ~front;
   int ah = warp_before(__popc(hole), lane), as = warp_before(__popc(spare), lane);
   const int2 warp_all = make_int2(__shfl_sync(0xffffffffu, ah + __popc(hole), 31), __shfl_sync(0xffffffffu, as + __popc(spare), 31));
@@ -315,31 +340,6 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     if (ms) {
       const int is = __shfl_sync(0xffffffffu, as, i) + __popc(ms & before);
       if ((ms >> lane & 1u) && is < P.most) spares[is] = first + 32 * i;
-    }
-  }
-  // weights and positions of the slots that stay where they are
-  const bool copy_acc = P.acc_out != P.acc_in, copy_pos = P.pos_out != P.pos_in;
-  if (copy_acc || copy_pos) {
-    keep &= front;
-#pragma unroll
-    for (int i0 = 0; i0 < KEYS; i0 += LOADS) {
-      if (first - lane + 32 * i0 >= n) break;  // the same for the warp
-      float w[LOADS];
-      int32_t pos[LOADS];
-      uint32_t stays = 0;
-#pragma unroll
-      for (int u = 0; u < LOADS; ++u) {  // together, ahead of the stores
-        const int64_t t = meta + first + 32 * (i0 + u);
-        stays |= (__shfl_sync(0xffffffffu, keep, i0 + u) >> lane & 1u) << u;
-        if (copy_acc && (stays >> u & 1u)) w[u] = P.acc_in[t];
-        if (copy_pos && (stays >> u & 1u)) pos[u] = P.pos_in[t];
-      }
-#pragma unroll
-      for (int u = 0; u < LOADS; ++u) {
-        const int64_t t = meta + first + 32 * (i0 + u);
-        if (copy_acc && (stays >> u & 1u)) P.acc_out[t] = w[u];
-        if (copy_pos && (stays >> u & 1u)) P.pos_out[t] = pos[u];
-      }
     }
   }
   if (n_cta > 1) cg::this_cluster().sync();  // no CTA leaves while another may still read its shared memory

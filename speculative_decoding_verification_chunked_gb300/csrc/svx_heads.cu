@@ -21,11 +21,11 @@
 namespace svx {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kCtas = 4;  // per SM
+constexpr int kThreads = 64;
+constexpr int kCtas = 12;  // per SM
 constexpr int kMaxWalk = 8;
 constexpr double kFill = 0.5;
-constexpr int kBig = 4;
+constexpr int kGroup = 4;  // heads whose copies are waited for together
 
 struct HeadsParams {
   const void *q, *k, *v;
@@ -87,7 +87,8 @@ __device__ __forceinline__ uint4 pack(const float* f) {
                     Pair<T>::down(f[6], f[7]));
 }
 
-template <typename T, int D, int kBatch>
+// RING: a walk of up to kMaxWalk heads, all of them on their way at once in shared memory; else one head, in registers.
+template <typename T, int D, bool RING>
 __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_constant__ HeadsParams P) {
   constexpr int LANES = D / 16;       // lanes per head
   constexpr int TOKENS = 32 / LANES;  // tokens of a warp
@@ -120,16 +121,43 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
   const bool turn = lane < nvec;
   const int v0 = turn ? lane : 2 * nvec + 2 * (lane - nvec);
   const int v1 = turn ? lane + nvec : v0 + 1;
-  auto load = [&](int i, uint4 (&raw)[2]) {
-    raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
-    if (live && i < count && in_bounds(src + i * D, D, in, in_ext, P.status, kSiteHeadsIn)) {
-      raw[0] = __ldg(reinterpret_cast<const uint4*>(src + i * D) + v0);
-      raw[1] = __ldg(reinterpret_cast<const uint4*>(src + i * D) + v1);
+  // Every lane copies what it reads itself, so no lane waits for another.
+  extern __shared__ uint4 ring[];
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+                        (threadIdx.x / 32 * (kMaxWalk * 64) + (threadIdx.x & 31)) * 16u;
+  uint4 only[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if constexpr (RING) {
+#pragma unroll
+    for (int i = 0; i < kMaxWalk; ++i) {
+      if (live && i < count && in_bounds(src + i * D, D, in, in_ext, P.status, kSiteHeadsIn)) {
+        const uint4* from = reinterpret_cast<const uint4*>(src + i * D);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + i * 1024u), "l"(from + v0) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + i * 1024u + 512u), "l"(from + v1) : "memory");
+      }
+      if (i % kGroup == kGroup - 1) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  } else if (live && in_bounds(src, D, in, in_ext, P.status, kSiteHeadsIn)) {
+    only[0] = __ldg(reinterpret_cast<const uint4*>(src) + v0);
+    only[1] = __ldg(reinterpret_cast<const uint4*>(src) + v1);
+  }
+  // the walk's i-th head of this lane, once its group of copies has come in
+  auto fetch = [&](int i, uint4 (&raw)[2]) {
+    if constexpr (RING) {
+      const uint4* at = ring + (threadIdx.x / 32 * (kMaxWalk * 64) + (threadIdx.x & 31)) + i * 64;
+      raw[0] = at[0];
+      raw[1] = at[32];
+    } else {
+      raw[0] = only[0];
+      raw[1] = only[1];
     }
   };
-  uint4 next[kBatch][2];
-#pragma unroll
-  for (int u = 0; u < kBatch; ++u) load(u, next[u]);
+  auto arrive = [&](int group) {  // group by group
+    if constexpr (RING) {
+      if (group == 0) asm volatile("cp.async.wait_group %0;" ::"n"(kMaxWalk / kGroup - 1) : "memory");
+      else if (group == 1) asm volatile("cp.async.wait_group %0;" ::"n"(kMaxWalk / kGroup > 1 ? kMaxWalk / kGroup - 2 : 0) : "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+  };
 
   // where the heads go: dst + i * step
   T* out = nullptr;
@@ -164,20 +192,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
   }
   if (at < 0) live = false;
 
+  const int walk = RING ? count : 1;
   if (is_v) {
-    for (int i0 = 0; i0 < P.walk; i0 += kBatch) {
-      uint4 raw[kBatch][2];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) raw[u][0] = next[u][0], raw[u][1] = next[u][1];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) load(i0 + kBatch + u, next[u]);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        T* dst = out + at + (i0 + u) * step;
-        if (live && i0 + u < count && in_bounds(dst, D, out, out_ext, P.status, kSitePool)) {
-          reinterpret_cast<uint4*>(dst)[v0] = raw[u][0];
-          reinterpret_cast<uint4*>(dst)[v1] = raw[u][1];
-        }
+    for (int i = 0; i < walk; ++i) {
+      if (i % kGroup == 0) arrive(i / kGroup);
+      uint4 raw[2];
+      fetch(i, raw);
+      T* dst = out + at + i * step;
+      if (live && in_bounds(dst, D, out, out_ext, P.status, kSitePool)) {
+        reinterpret_cast<uint4*>(dst)[v0] = raw[0];
+        reinterpret_cast<uint4*>(dst)[v1] = raw[1];
       }
     }
     return;
@@ -217,56 +241,51 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
     }
   }
 
-  for (int i0 = 0; i0 < P.walk; i0 += kBatch) {
-    uint4 raw[kBatch][2];
+  for (int i = 0; i < walk; ++i) {  // the same number of turns for all lanes
+    if (i % kGroup == 0) arrive(i / kGroup);
+    uint4 raw[2];
+    fetch(i, raw);
+    float x[16];
+    unpack<T>(raw[0], x);
+    unpack<T>(raw[1], x + 8);
+    float r = 1.f;
+    if (P.norm) {
+      float ss = 0.f;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) raw[u][0] = next[u][0], raw[u][1] = next[u][1];
+      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) load(i0 + kBatch + u, next[u]);
+      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      r = rsqrtf(fmaf(ss, 1.f / D, P.eps));
+    }
+    if (!turn) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      float x[16];
-      unpack<T>(raw[u][0], x);
-      unpack<T>(raw[u][1], x + 8);
-      float r = 1.f;
-      if (P.norm) {  // all lanes of the warp take part in the shuffles
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        r = rsqrtf(fmaf(ss, 1.f / D, P.eps));
+      for (int e = 0; e < 8; ++e) {
+        x[e] = x[e] * r * fa[e];
+        x[8 + e] = x[8 + e] * r * ga[e];
       }
-      if (!turn) {
+    } else if (P.neighbours) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = x[i] * r * fa[i];
-          x[8 + i] = x[8 + i] * r * ga[i];
-        }
-      } else if (P.neighbours) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = x[2 * i], c = x[2 * i + 1];
-          x[2 * i] = (a * fa[i] - c * fb[i]) * r;
-          x[2 * i + 1] = (c * ga[i] + a * gb[i]) * r;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = x[i], c = x[8 + i];
-          x[i] = (a * fa[i] - c * fb[i]) * r;
-          x[8 + i] = (c * ga[i] + a * gb[i]) * r;
-        }
+      for (int e = 0; e < 8; ++e) {
+        const float a = x[2 * e], c = x[2 * e + 1];
+        x[2 * e] = (a * fa[e] - c * fb[e]) * r;
+        x[2 * e + 1] = (c * ga[e] + a * gb[e]) * r;
       }
-      T* dst = out + at + (i0 + u) * step;
-      if (!live || i0 + u >= count || !in_bounds(dst, D, out, out_ext, P.status, kSiteHeadsOut)) continue;
-      reinterpret_cast<uint4*>(dst)[v0] = pack<T>(x);
-      reinterpret_cast<uint4*>(dst)[v1] = pack<T>(x + 8);
-      if (P.paged && !is_q && lane == 0) {
-        const int64_t m = (static_cast<int64_t>(b) * P.n_kv + h0 + i0 + u) * P.pages.cap + slot;
-        if (P.acc) P.acc[m] = 0.f;
-        if (P.slot_pos) P.slot_pos[m] = pos;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = x[e], c = x[8 + e];
+        x[e] = (a * fa[e] - c * fb[e]) * r;
+        x[8 + e] = (c * ga[e] + a * gb[e]) * r;
       }
+    }
+    T* dst = out + at + i * step;
+    if (!live || !in_bounds(dst, D, out, out_ext, P.status, kSiteHeadsOut)) continue;
+    reinterpret_cast<uint4*>(dst)[v0] = pack<T>(x);
+    reinterpret_cast<uint4*>(dst)[v1] = pack<T>(x + 8);
+    if (P.paged && !is_q && lane == 0) {
+      const int64_t m = (static_cast<int64_t>(b) * P.n_kv + h0 + i) * P.pages.cap + slot;
+      if (P.acc) P.acc[m] = 0.f;
+      if (P.slot_pos) P.slot_pos[m] = pos;
     }
   }
 }
@@ -285,9 +304,9 @@ cudaError_t launch(HeadsParams& p, cudaStream_t stream, int sms) {
   p.parts = p.q_parts + (p.v ? 2 : 1) * p.kv_parts;
   const int64_t blocks = (blocks_of_tokens * p.parts + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  // heads loaded ahead of the ones at work
-  auto kernel = p.walk >= kBig ? heads_kernel<T, D, kBig> : heads_kernel<T, D, 1>;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, p);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  return p.walk > 1 ? launch_pdl(heads_kernel<T, D, true>, grid, dim3(kThreads), kThreads / 32 * kMaxWalk * 1024, stream, p)
+                    : launch_pdl(heads_kernel<T, D, false>, grid, dim3(kThreads), 0, stream, p);
 }
 
 struct Range {
