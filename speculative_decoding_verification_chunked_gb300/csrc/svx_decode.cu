@@ -132,8 +132,10 @@ struct Split {
   }
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes),
+               "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -306,6 +308,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
   if (lane < 2) pieces[lane * kWarps + warp].first = -1;
   __syncwarp();
 
+  // K and V are read once: they leave L2 before the scores and pieces, which the join reads back
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   // ---- this warp's loads.  look() fetches the page of each row of the next chunk, load() copies the rows
   const int my_row = lane % CT;  // the row of a chunk whose place this lane works out
   Cursor lc{0, 0, 0, 0, 0, 0};
@@ -351,8 +356,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
         const int bytes = ro >= 0 ? 16 : 0;  // 0: the 16 bytes become zero
         const int64_t e = (ro >= 0 ? ro : 0) + piece * 8;
         const uint32_t at = dst + r * (2 * D) + ((piece ^ (r & 7)) << 4);
-        cp16(at, static_cast<const T*>(P.pages.k) + e, bytes);
-        cp16(at + kChunkBytes, static_cast<const T*>(P.pages.v) + e, bytes);
+        cp16(at, static_cast<const T*>(P.pages.k) + e, bytes, policy);
+        cp16(at + kChunkBytes, static_cast<const T*>(P.pages.v) + e, bytes, policy);
       }
     }
     cp_commit();

@@ -514,7 +514,7 @@ cudaError_t launch_moves(EvictParams& p, int head_dim, int rows, int sms, cudaSt
   p.chunk = 32;
   while (p.chunk > 8 && static_cast<int64_t>(rows) * p.most < static_cast<int64_t>(p.chunk) * sms * kMoveWarps) p.chunk /= 2;
   const int per_cta = kMoveWarps * p.chunk;
-  const int want = (p.most + per_cta - 1) / per_cta, room = std::max(1, 16 * sms / rows);
+  const int want = (p.most + per_cta - 1) / per_cta, room = std::max(1, 40 * sms / rows);
   const dim3 grid(static_cast<unsigned>(std::max(1, std::min(want, room))), static_cast<unsigned>(rows));
   return head_dim == 128 ? launch_pdl(move_kernel<128>, grid, dim3(kMoveWarps * 32), 0, s, p)
                          : launch_pdl(move_kernel<64>, grid, dim3(kMoveWarps * 32), 0, s, p);
