@@ -505,7 +505,8 @@ svx_status svx_width_cost(svx_width w, int32_t q, double* cost_out);
  * svx_paged_append fills it, svx_paged_decode attends to it, svx_paged_evict keeps it small.
  *
  * The calls allocate nothing, keep nothing between calls and return once their work is enqueued on `stream`
- * (cudaStream_t, NULL = default stream) of the struct's device, so each may be captured into a CUDA graph.
+ * (cudaStream_t, NULL = default stream) of the struct's device, so each may be captured into a CUDA graph (after one eager
+ * call: kernel set-up happens on first use).
  * Two calls whose GPU work overlaps (two streams, two replayed graphs) need workspaces and outputs of their
  * own; the status word may be shared.  Host arguments are checked (SVX_ERR_INVALID_ARG,
  * SVX_ERR_UNSUPPORTED; message from svx_last_error(NULL)); lengths, slots and page ids live on the device, so the
@@ -606,7 +607,7 @@ svx_status svx_paged_decode_workspace(const svx_pages* cache, int32_t n_req, int
  * must be finite; what lies behind a request's length is not used, whatever it holds.
  * acc_in, acc_out (device float [n_req][n_kv_heads][max_pages * page_size], or both NULL): acc_out[t] =
  * acc_in[t] + the sum over the KV head's query heads of slot t's softmax weight, t < len[b]; the rest is left as
- * it was.  They may be one buffer.  workspace: device, 256-byte aligned; contents need no set-up. */
+ * it was.  They may be one buffer.  With weights max_len is at most 134,215,680.  workspace: device, 256-byte aligned; contents need no set-up. */
 svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, int32_t n_q_heads, const void* q, const int32_t* len,
                             int64_t max_len, float scale, void* o, float* lse, const float* acc_in, float* acc_out,
                             void* workspace, int64_t workspace_bytes, void* stream);

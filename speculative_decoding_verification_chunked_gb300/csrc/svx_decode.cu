@@ -15,8 +15,11 @@
 // memory (lead) and the one that goes on behind it in its emptied stages (tail); when all warps of the CTA are done
 // they merge the pieces that belong together, finish the items that lie in the CTA, and leave (m, l, O) of the others in the
 // CTA's slot 0 (the item began before the CTA's range) or 1 (it goes on behind it), which join_kernel merges.
-// (Warps that shared an item's chunks in turn and merged at its end took 70 us where this takes %RAGGED%, 16 ragged requests:
-// every item stopped the whole CTA.)
+// (Where the warps of a CTA shared an item's chunks in turn and merged at its end, every item stopped the CTA: 16 requests
+// of 1 to 8192 slots, 8 KV heads, took 70 us and take 48 us so; 64 of 100 to 1000 slots 58 and 31 us.)
+// What bounds it: the copy rate.  8 x 32768 slots (8 KV heads, d = 128, 1.07 GB) 159 us = 6750 GB/s, 99.5% of the
+// measured copy rate; 1 x 131072 slots 86 us = 6260 GB/s; below some 200 MB the fixed cost shows, about 5 us until the
+// first chunk is in (lengths, split, page table, chunk: four trips to memory in a row) and 5 us of joining.
 //
 // Products: mma.sync m16n8k16, query heads on M.  They cost a few percent of the time (32 a chunk), so the
 // tensor memory path, which wants 64 rows or more on M and a second trip through it, gains nothing here.  With up to 8
@@ -49,9 +52,9 @@ struct DecodeParams {
   float* lse;
   const float* acc_in;
   float* acc_out;
+  float* lead;      // [ctas][8 warps][16][D]
+  float2* lead_ml;  // [ctas][8 warps][16]
   float* part_o;    // [ctas][2][16][D]
-  float* lead;      // [ctas][8 warps][16][D], then (m, l) [ctas][8][16]
-  float2* lead_ml;
   float2* part_ml;  // [ctas][2][16]
   float2* row_ml;   // [n_req * n_q]: final (m, l), for the weights
   float* scores;    // [n_req * n_q][score_stride], log2 units
@@ -81,7 +84,7 @@ __device__ __forceinline__ int build_plan(const DecodeParams& P, Plan& s, bool r
     n = min(max(raw, 0), P.max_len);
     if (report && n != raw) atomicOr(P.pages.status, kErrInput);
   }
-  const int chunks = (n + CT - 1) / CT;
+  const int chunks = static_cast<int>((static_cast<uint32_t>(n) + (CT - 1)) / CT);
   s.n[t] = chunks;
   s.len[t] = n;
   const int mine = P.pages.n_kv_heads * P.blocks * chunks;
@@ -308,7 +311,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
   if (lane < 2) pieces[lane * kWarps + warp].first = -1;
   __syncwarp();
 
-  // K and V are read once: they leave L2 before the scores and pieces, which the join reads back
+  // K and V are read once: they leave L2 before the scores and pieces, which the join reads back (131072 slots with
+  // weights 93 us, with the usual policy 98; 16 ragged requests 48 and 51; the largest batch 159 and 157)
   uint64_t policy;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   // ---- this warp's loads.  look() fetches the page of each row of the next chunk, load() copies the rows
@@ -819,6 +823,8 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
 
 // ------------------------------------------------------------------ host
 
+constexpr int64_t kMaxGridY = 65535;
+
 
 struct Sizes {
   int32_t max_len, blocks, ctas;
@@ -840,6 +846,9 @@ svx_status sizes(const svx_pages* c, int32_t n_req, int32_t n_q, int64_t max_len
   z->max_len = static_cast<int32_t>(max_len);
   z->blocks = (group + kRowsMax - 1) / kRowsMax;
   const int64_t chunks = static_cast<int64_t>(n_req) * c->n_kv_heads * z->blocks * ((max_len + ct - 1) / ct);
+  if (weights && max_len > kMaxGridY * kWeightSlots)
+    return paged_fail(SVX_ERR_UNSUPPORTED, "max_len must be at most %lld with weights",
+                      static_cast<long long>(kMaxGridY * kWeightSlots));
   if (chunks > 0x7fffffff)
     return paged_fail(SVX_ERR_UNSUPPORTED, "n_req * heads * max_len is too large (%lld chunks of %d slots, at most 2^31 - 1)",
                       static_cast<long long>(chunks), ct);
@@ -912,6 +921,11 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   if (st != SVX_OK) return st;
   if ((acc_in == nullptr) != (acc_out == nullptr))
     return paged_fail(SVX_ERR_INVALID_ARG, "give both acc_in and acc_out, or neither");
+  if (acc_in && acc_in != acc_out) {
+    const size_t n = static_cast<size_t>(n_req) * p.pages.n_kv_heads * p.pages.cap * 4;
+    const char *a = reinterpret_cast<const char*>(acc_in), *b = reinterpret_cast<const char*>(acc_out);
+    if (a < b + n && b < a + n) return paged_fail(SVX_ERR_INVALID_ARG, "acc_out must be acc_in or not overlap it");
+  }
   if (!q || !o || !lse || !len || !svx::is_aligned(q, 16) || !svx::is_aligned(o, 16) || !svx::is_aligned(lse, 4))
     return paged_fail(SVX_ERR_INVALID_ARG, "q, len, o and lse must be device pointers, q and o 16-byte aligned");
   if (!(scale >= 0.f) || scale > 3.0e38f) return paged_fail(SVX_ERR_INVALID_ARG, "scale must be positive and finite, or 0");

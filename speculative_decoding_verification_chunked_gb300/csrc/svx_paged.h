@@ -16,16 +16,11 @@ namespace svx {
 // lies outside its bounds.  What it names was clamped or left out; nothing outside the buffers is touched.
 constexpr int kErrInput = 8;
 
-// Sites of the bounds-checked build, after those of svx_internal.h.
+// Sites of the bounds-checked build, after those of svx_internal.h: rows of heads, and rows of K and V pages.
 enum PagedSite : int {
   kSiteHeadsIn = 9,
   kSiteHeadsOut = 10,
-  kSitePool = 11,      // K and V pages, any kernel
-  kSiteDecodeIn = 12,
-  kSiteDecodeOut = 13,
-  kSiteDecodeWs = 14,
-  kSiteEvictMeta = 15,
-  kSiteEvictWs = 16,
+  kSitePool = 11,
 };
 
 // K and V pages as the kernels see them: element (page, slot, head, 0) of either pool is at

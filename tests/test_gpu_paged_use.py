@@ -417,3 +417,30 @@ def test_heads_rows_do_not_depend_on_the_batch(svx):
     q, qs, k, ks, _ = heads_reference(case, qkv, pos, wq, wk, inv)
     near(big[0], q, qs, torch.bfloat16)
     assert unit(torch.bfloat16) == 2.0 ** -8
+
+
+@pytest.mark.parametrize("layout", ["head", "pair"])
+def test_evict_in_other_layouts(svx, layout):
+    """Heads outside the slots, and K and V side by side in one tensor: rows move, nothing between them does."""
+    g = torch.Generator().manual_seed(20)
+    page, hkv, d, n, budget = 24, 3, 64, 500, 200
+    table, total = make_table(g, [n, n], page)
+    kp, vp = make_pool(g, total, page, hkv, d, torch.float16, layout) if layout == "pair" else \
+        tuple(make_pool(g, total, page, hkv, d, torch.float16, layout) for _ in range(2))
+    k0, v0 = kp.cpu().clone(), vp.cpu().clone()
+    room = table.shape[1] * page
+    acc = torch.rand((2, hkv, room), generator=g)
+    pos = torch.arange(room, dtype=torch.int32).expand(2, hkv, room).contiguous()
+    cache = svx.PagedCache(kp, vp)
+    a, p, lo = acc.cuda(), pos.cuda(), i32([0, 0])
+    cache.evict(table.cuda(), i32([n, n]), budget, 3, 20, i32([n, n]), a, p, a, p, lo)
+    assert not cache.check() and lo.tolist() == [budget, budget]
+    for b in range(2):
+        for h in range(hkv):
+            order = evict64(acc[b, h].numpy(), pos[b, h].numpy(), n, n, budget, 3, 20)
+            assert torch.equal(p[b, h, :budget].cpu(), pos[b, h][order])
+            for t, f in enumerate(order):
+                if t != f:
+                    k0[int(table[b, t // page]), t % page, h] = k0[int(table[b, f // page]), f % page, h]
+                    v0[int(table[b, t // page]), t % page, h] = v0[int(table[b, f // page]), f % page, h]
+    assert torch.equal(kp.cpu(), k0) and torch.equal(vp.cpu(), v0)
