@@ -4,7 +4,8 @@ accesses against the buffers its launch describes and reports a stray one throug
 the device error word instead of making it).
 
 Each translation unit is compiled by its own nvcc process (all in parallel), then
-linked into one shared library next to this file.
+linked into one shared library next to this file.  The binding's native part,
+``svx_torch.so`` (a Python extension against this machine's PyTorch), is compiled beside them.
 """
 from __future__ import annotations
 
@@ -20,6 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsvx.so")
 LIB_CHECKED = os.path.join(PKG, "libsvx_checked.so")
+LIB_TORCH = os.path.join(PKG, "svx_torch.so")
 
 SOURCES = ["svx_kernels.cu", "svx_tc_kernel.cu", "svx_runtime.cu", "svx_static.cu", "svx_tier.cu", "svx_sched.cu", "svx_width.cu",
            "svx_paged.cu", "svx_heads.cu", "svx_decode.cu", "svx_evict.cu"]
@@ -34,6 +36,21 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libsvx.so")
+
+
+def torch_command(out: str) -> list:
+    """The compiler call that makes svx_torch.so."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    lib = os.path.join(home, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[x for d in includes for x in ("-isystem" if d != INCLUDE else "-I", d)], os.path.join(CSRC, "svx_torch.cpp"), "-o", out,
+            "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def build(verbose: bool = False, extra_flags: tuple = (), checked: bool = True) -> str:
@@ -52,6 +69,10 @@ def build(verbose: bool = False, extra_flags: tuple = (), checked: bool = True) 
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
             objs.setdefault(lib, []).append(obj)
+    cmd = torch_command(LIB_TORCH + ".tmp")
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    procs.append(("svx_torch.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -60,7 +81,8 @@ def build(verbose: bool = False, extra_flags: tuple = (), checked: bool = True) 
         elif verbose and out.strip():
             print(out, file=sys.stderr)
     if failed:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+        raise RuntimeError("compilation failed:\n" + "\n".join(failed))
+    os.replace(LIB_TORCH + ".tmp", LIB_TORCH)
     for _sub, lib, _flags in variants:
         tmp = lib + ".tmp"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs[lib]]

@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -110,11 +109,6 @@ class Pages(ctypes.Structure):
                 ("device", ctypes.c_int32), ("flags", ctypes.c_uint32), ("pad", ctypes.c_int32)]
 
 
-# svx_heads and svx_pages as bytes, in the order of the fields above: a quarter of the time of filling the structures
-_HEADS = struct.Struct("@3P3q5P7ifIi")
-_PAGES = struct.Struct("@4P4q6iIi")
-assert (_HEADS.size, _PAGES.size) == (ctypes.sizeof(Heads), ctypes.sizeof(Pages))
-
 # name -> (restype, argtypes); every symbol declared in include/svx.h
 _P = ctypes.c_void_p
 _SIGS = {
@@ -189,16 +183,16 @@ _SIGS = {
     "svx_width_cost": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_double)]),
     "svx_rope_init": (ctypes.c_int, [ctypes.POINTER(RopeTable), ctypes.c_int32, ctypes.c_int32,
                                      ctypes.POINTER(ctypes.c_double), ctypes.c_float]),
-    # (svx_heads and svx_pages go in as packed bytes: _HEADS, _PAGES)
-    "svx_qk_norm_rope": (ctypes.c_int, [_P, _P, _P, _P, _P, _P]),
-    "svx_paged_append": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
-    "svx_paged_decode_workspace": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
+    "svx_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(Heads), ctypes.POINTER(RopeTable), _P, _P, _P, _P]),
+    "svx_paged_append": (ctypes.c_int, [ctypes.POINTER(Heads), ctypes.POINTER(RopeTable), ctypes.POINTER(Pages), _P, _P,
+                                        _P, _P, _P]),
+    "svx_paged_decode_workspace": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
                                                   ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
-    "svx_paged_decode": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_int64,
+    "svx_paged_decode": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_int64,
                                         ctypes.c_float, _P, _P, _P, _P, _P, ctypes.c_int64, _P]),
-    "svx_paged_evict_workspace": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+    "svx_paged_evict_workspace": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
                                                  ctypes.POINTER(ctypes.c_int64)]),
-    "svx_paged_evict": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32,
+    "svx_paged_evict": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32,
                                        ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, _P]),
     "svx_version": (ctypes.c_char_p, []),
     "svx_abi_sizes": (ctypes.c_int32, [ctypes.POINTER(ctypes.c_int64), ctypes.c_int32]),
@@ -736,87 +730,37 @@ class Verifier:
 # ------------------------------------------------------------ a paged cache
 
 
-BF16, FP16 = 0, 1
 EVICT_MAX_LEN = 262144
-POINTERS_CHECKED = 1  # the binding checks every tensor's device itself
-
-_torch_module = None
+_native_module = None
 
 
-def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
+def _native():
+    """svx_torch.so: the calls of this section, checking torch tensors in native code (in place of ctypes, since they are made
+    once a layer and token).  Loaded on first use, with PyTorch."""
+    global _native_module
+    if _native_module is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries first)
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "svx_torch.so")
+        if not os.path.exists(path):
+            raise ImportError(f"native binding not built: {path} is missing (run __graft_entry__.build())")
+        spec = importlib.util.spec_from_file_location("svx_torch", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.set_up(SvxError, *[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "svx_qk_norm_rope", "svx_paged_append", "svx_paged_decode_workspace", "svx_paged_decode",
+            "svx_paged_evict_workspace", "svx_paged_evict", "svx_last_error")])
+        _native_module = mod
+    return _native_module
 
 
-def _type_code(t, what: str) -> int:
-    torch = _torch()
-    if t.dtype is torch.bfloat16:
-        return BF16
-    if t.dtype is torch.float16:
-        return FP16
-    raise SvxError(ERR_UNSUPPORTED, f"{what}: dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
-
-
-def _dense(t, dtype, shape: tuple, device: int, what: str) -> int:
-    """Address of a dense tensor of exactly this type and shape on this CUDA device."""
-    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        got = "None" if t is None else f"{t.dtype} {list(t.shape)} on {t.device}, contiguous {t.is_contiguous()}"
-        raise SvxError(ERR_INVALID_ARG, f"{what}: {got}; expected dense {dtype} {list(shape)} on cuda:{device}")
-    return t.data_ptr()
-
-
-def _optional(t, dtype, shape: tuple, device: int, what: str) -> int:
-    return 0 if t is None else _dense(t, dtype, shape, device, what)
-
-
-def _head_rows(t, n_req: int, n_tok: int, d: int, dtype, device: int, what: str):
-    """Address, token stride and count of heads [n_req][n_tok][heads][d], possibly a view of a fused projection."""
-    if t is not None and t.dtype is dtype and t.get_device() == device and t.dim() == 4:
-        b, n, heads, dim = t.shape
-        if b == n_req and n == n_tok and dim == d:
-            s0, s1, s2, s3 = t.stride()
-            row = s1 if n_tok > 1 else s0 if n_req > 1 else heads * d
-            if s3 != 1 or (heads > 1 and s2 != d) or (n_tok > 1 and n_req > 1 and s0 != n_tok * s1):
-                raise SvxError(ERR_INVALID_ARG, f"{what}: strides {list(t.stride())}: a token's heads must be dense, and "
-                                                "tokens evenly spaced over the requests")
-            return t.data_ptr(), row, heads
-    got = "None" if t is None else f"{t.dtype} {list(t.shape)} on {t.device}"
-    raise SvxError(ERR_INVALID_ARG, f"{what}: {got}, expected {dtype} [{n_req}, {n_tok}, heads, {d}] on cuda:{device}")
-
-
-def _launch_stream(device: int, stream) -> int:
-    """The given stream's handle, else the current stream of the tensors' device."""
-    if stream is not None:
-        return _stream_handle(stream)
-    torch = _torch()
-    try:  # what current_stream() reads, without making a Stream object of it (0.1 us in place of 2)
-        return torch._C._cuda_getCurrentRawStream(device)
-    except AttributeError:
-        return torch.cuda.current_stream(device).cuda_stream
-
-
-def _workspace(workspace, need: int, device: int, stream):
-    """The caller's workspace, or one from the caching allocator that belongs to the call's stream."""
-    torch = _torch()
-    if workspace is not None:
-        if workspace.get_device() != device or not workspace.is_contiguous() or \
-                workspace.numel() * workspace.element_size() < need:
-            raise SvxError(ERR_INVALID_ARG, f"workspace: a dense tensor of at least {need} bytes on cuda:{device} is needed")
-        return workspace
-    if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    dev = torch.device("cuda", device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(s):
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-
-
-def _static_error(st: int):
-    if st != OK:
-        raise SvxError(st, lib.svx_last_error(None).decode())
+def _on_stream(stream, device: int):
+    """A context in which ``stream`` (a torch stream or a raw handle) is the current one."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=torch.device("cuda", device))
+    return torch.cuda.stream(stream)
 
 
 class Rope:
@@ -832,33 +776,10 @@ class Rope:
             raise SvxError(ERR_INVALID_ARG, f"inv_freq: {len(inv_freq)} entries, expected rot_dim / 2 = {rot_dim // 2}")
         self.table = RopeTable()
         f = (ctypes.c_double * max(1, len(inv_freq)))(*[float(x) for x in inv_freq])
-        _static_error(lib.svx_rope_init(ctypes.byref(self.table), rot_dim, int(bool(neighbours)), f, scale))
+        st = lib.svx_rope_init(ctypes.byref(self.table), rot_dim, int(bool(neighbours)), f, scale)
+        if st != OK:
+            raise SvxError(st, lib.svx_last_error(None).decode())
         self.address = ctypes.addressof(self.table)
-
-
-def _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, status):
-    """The C struct of a call's heads, and [requests, tokens, q heads, KV heads, head_dim], device and type."""
-    torch = _torch()
-    if q.dim() != 4:
-        raise SvxError(ERR_INVALID_ARG, f"q: shape {list(q.shape)}, expected [requests, tokens, heads, head_dim]")
-    n_req, n_tok, hq, d = q.shape
-    dtype, device = q.dtype, q.get_device()
-    code = _type_code(q, "q")
-    if device < 0:
-        raise SvxError(ERR_INVALID_ARG, f"q is on {q.device}, not on a CUDA device")
-    qp, qs, _ = _head_rows(q, n_req, n_tok, d, dtype, device, "q")
-    kp, ks, hkv = _head_rows(k, n_req, n_tok, d, dtype, device, "k")
-    vp, vs, hv = (0, 0, hkv) if v is None else _head_rows(v, n_req, n_tok, d, dtype, device, "v")
-    if hv != hkv:
-        raise SvxError(ERR_INVALID_ARG, f"v has {hv} heads, k {hkv}")
-    if eps is not None and not eps >= 0.0:
-        raise SvxError(ERR_INVALID_ARG, "eps must be >= 0, or None for no norms")
-    i32 = torch.int32
-    h = _HEADS.pack(qp, kp, vp, qs, ks, vs, _optional(q_norm, dtype, (d,), device, "q_norm"),
-                    _optional(k_norm, dtype, (d,), device, "k_norm"), _dense(pos, i32, (n_req, n_tok), device, "pos"),
-                    _optional(n_new, i32, (n_req,), device, "n_new"), status, n_req, n_tok, hq, hkv, d, code, device,
-                    -1.0 if eps is None else eps, POINTERS_CHECKED, 0)
-    return h, (n_req, n_tok, hq, hkv, d), device, dtype
 
 
 def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None, k_norm=None,
@@ -870,12 +791,10 @@ def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None
     candidate_attn take.  eps None: no norms.  n_new: int32 [B], tokens of each request that count, or None.
     status: int32 [1] that becomes non-zero if n_new leaves [0, n], or None.  stream: the current one by default.
     """
-    sp = _optional(status, _torch().int32, (1,), q.get_device(), "status")
-    h, (b, n, hq, hkv, d), device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, sp)
-    _static_error(lib.svx_qk_norm_rope(
-        h, rope.address, _dense(q_out, dtype, (b, hq, n, d), device, "q_out"),
-        _dense(k_out, dtype, (b, n, hkv, d), device, "k_out"), _optional(v_out, dtype, (b, n, hkv, d), device, "v_out"),
-        _launch_stream(device, stream)))
+    if stream is not None:
+        with _on_stream(stream, q.get_device()):
+            return qk_norm_rope(q, k, v, pos, rope, q_out, k_out, v_out, q_norm, k_norm, eps, n_new, status)
+    (_native_module or _native()).qk_norm_rope(q, k, v, pos, rope.address, q_out, k_out, v_out, q_norm, k_norm, eps, n_new, status)
 
 
 class PagedCache:
@@ -885,50 +804,23 @@ class PagedCache:
     dimensions in memory, rows of d dense.  The tensors stay the caller's.  Page tables are int32 [B][max_pages]: slot t
     of request b is slot t % page_size of page table[b][t // page_size].  Calls run on the current stream (or
     ``stream``), allocate nothing but a workspace from torch's caching allocator (or take ``workspace``) and may be
-    captured into CUDA graphs.  Lengths, slots and page ids are read on the device; ``check()`` tells whether
-    one was out of bounds.
+    captured into CUDA graphs, after one eager call.  Lengths, slots and page ids are read on the device; ``check()`` tells
+    whether one was out of bounds.
     """
 
     def __init__(self, k_pages, v_pages):
-        torch = _torch()
-        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() or \
-                k_pages.dtype != v_pages.dtype or k_pages.device != v_pages.device or k_pages.stride(3) != 1:
-            raise SvxError(ERR_INVALID_ARG, "k_pages and v_pages: equal [pages][page_size][Hkv][d] tensors with dense rows "
-                                            "are expected")
+        import torch
         if k_pages.device.type != "cuda":
             raise SvxError(ERR_INVALID_ARG, f"k_pages is on {k_pages.device}, not on a CUDA device")
-        self.k_pages, self.v_pages = k_pages, v_pages
-        self.device, self.dtype = k_pages.get_device(), k_pages.dtype
-        n_pages, self.page_size, self.n_kv_heads, self.head_dim = k_pages.shape
+        self.k_pages, self.v_pages, self.device = k_pages, v_pages, k_pages.get_device()
         self.status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
-        # the C struct's fields before and after the table and its width
-        self._front = (k_pages.data_ptr(), v_pages.data_ptr())
-        self._middle = (self.status.data_ptr(), *k_pages.stride()[:3], n_pages, self.page_size)
-        self._back = (self.n_kv_heads, self.head_dim, _type_code(k_pages, "k_pages"), self.device, POINTERS_CHECKED, 0)
-        self._sizes = {}
-
-    def _with_table(self, table, n_req: Optional[int]):
-        """The C struct for a call, the number of requests and the table's width."""
-        shape = table.shape
-        if len(shape) != 2 or (n_req is not None and shape[0] != n_req):
-            raise SvxError(ERR_INVALID_ARG, f"table: shape {list(shape)}, expected [{n_req or 'requests'}, max_pages]")
-        at = _dense(table, _torch().int32, shape, self.device, "table")
-        n_req, wide = shape
-        return _PAGES.pack(*self._front, at, *self._middle, wide, *self._back), n_req, wide
-
-    def _need(self, what: str, fn, pages, *args) -> int:
-        """Bytes of workspace (a function of sizes alone)."""
-        need = self._sizes.get((what,) + args)
-        if need is None:
-            n = ctypes.c_int64(0)
-            _static_error(fn(pages, *args[1:], ctypes.byref(n)))
-            need = self._sizes[(what,) + args] = n.value
-        return need
+        self._native = _native()
+        self._pages = self._native.pages(k_pages, v_pages, self.status)
 
     def check(self) -> bool:
         """True if, since the last check, a call met a length, slot or page id out of its bounds (outputs that depend
         on it are unspecified); clears the word.  Waits for the device."""
-        torch = _torch()
+        import torch
         torch.cuda.synchronize(self.device)
         bad = bool(self.status.item())
         if bad:
@@ -941,18 +833,10 @@ class PagedCache:
         """svx_paged_append: norms and rotates the heads of n new tokens per request (as qk_norm_rope), puts K and V into
         slots start[b] + j and q into q_out [B][Hq][n][d]; acc (fp32) becomes 0 and slot_pos (int32), both
         [B][Hkv][max_pages * page_size], the token's position at the new slots."""
-        torch = _torch()
-        if v is None:
-            raise SvxError(ERR_INVALID_ARG, "v is required")
-        h, (b, n, hq, _, d), device, dtype = _heads_args(q, k, v, pos, q_norm, k_norm, eps, n_new, 0)
-        if device != self.device:
-            raise SvxError(ERR_INVALID_ARG, f"q is on cuda:{device}, the cache on cuda:{self.device}")
-        p, _, wide = self._with_table(table, b)
-        meta = (b, self.n_kv_heads, wide * self.page_size)
-        _static_error(lib.svx_paged_append(
-            h, rope.address, p, _dense(start, torch.int32, (b,), device, "start"),
-            _dense(q_out, dtype, (b, hq, n, d), device, "q_out"), _optional(acc, torch.float32, meta, device, "acc"),
-            _optional(slot_pos, torch.int32, meta, device, "slot_pos"), _launch_stream(device, stream)))
+        if stream is not None:
+            with _on_stream(stream, self.device):
+                return self.append(q, k, v, pos, rope, table, start, q_out, q_norm, k_norm, eps, n_new, acc, slot_pos)
+        self._native.append(self._pages, q, k, v, pos, rope.address, table, start, q_out, q_norm, k_norm, eps, n_new, acc, slot_pos)
 
     def decode(self, q, table, lens, o, lse, max_len: int = 0, scale: float = 0.0, acc_in=None, acc_out=None,
                workspace=None, stream=None):
@@ -961,21 +845,10 @@ class PagedCache:
         q, o: [B][Hq][1][d]; lse: fp32 [B][Hq][1]; lens: int32 [B].  max_len: a bound on lens known on the host (0:
         max_pages * page_size).  With acc_in and acc_out (fp32 [B][Hkv][max_pages * page_size], may be one tensor) the
         slots' softmax weights, summed over a KV head's query heads, are added."""
-        torch = _torch()
-        if q.dim() != 4:
-            raise SvxError(ERR_INVALID_ARG, f"q: shape {list(q.shape)}, expected [requests][heads][1][head_dim]")
-        b, hq = q.shape[0], q.shape[1]
-        device, rows = self.device, (b, hq, 1, self.head_dim)
-        p, _, wide = self._with_table(table, b)
-        meta = (b, self.n_kv_heads, wide * self.page_size)
-        ws = _workspace(workspace, self._need("decode", lib.svx_paged_decode_workspace, p, wide, b, hq, max_len,
-                                              int(acc_in is not None)), device, stream)
-        _static_error(lib.svx_paged_decode(
-            p, b, hq, _dense(q, self.dtype, rows, device, "q"),
-            _dense(lens, torch.int32, (b,), device, "lens"), max_len, scale, _dense(o, self.dtype, rows, device, "o"),
-            _dense(lse, torch.float32, (b, hq, 1), device, "lse"), _optional(acc_in, torch.float32, meta, device, "acc_in"),
-            _optional(acc_out, torch.float32, meta, device, "acc_out"), ws.data_ptr(), ws.numel() * ws.element_size(),
-            _launch_stream(device, stream)))
+        if stream is not None:
+            with _on_stream(stream, self.device):
+                return self.decode(q, table, lens, o, lse, max_len, scale, acc_in, acc_out, workspace)
+        self._native.decode(self._pages, q, table, lens, o, lse, max_len, scale, acc_in, acc_out, workspace)
 
     def evict(self, table, lens, budget: int, sink: int, recent: int, next_pos, acc_in, pos_in, acc_out, pos_out, len_out,
               max_len: int = 0, workspace=None, stream=None):
@@ -983,15 +856,9 @@ class PagedCache:
         recent, then the largest acc_in (ties: the lower slot).  Kept slots behind the new length move into the
         evicted ones before it, with their acc and position; len_out gets the new lengths.  acc (fp32), pos (int32):
         [B][Hkv][max_pages * page_size]; lens, next_pos, len_out: int32 [B]; outputs may be their inputs."""
-        torch = _torch()
-        p, b, wide = self._with_table(table, None)
-        device, meta = self.device, (b, self.n_kv_heads, wide * self.page_size)
-        i32, f32 = torch.int32, torch.float32
-        ws = _workspace(workspace, self._need("evict", lib.svx_paged_evict_workspace, p, wide, b, max_len, budget), device,
-                        stream)
-        _static_error(lib.svx_paged_evict(
-            p, b, _dense(lens, i32, (b,), device, "lens"), max_len, budget, sink, recent,
-            _dense(next_pos, i32, (b,), device, "next_pos"), _dense(acc_in, f32, meta, device, "acc_in"),
-            _dense(pos_in, i32, meta, device, "pos_in"), _dense(acc_out, f32, meta, device, "acc_out"),
-            _dense(pos_out, i32, meta, device, "pos_out"), _dense(len_out, i32, (b,), device, "len_out"), ws.data_ptr(),
-            ws.numel() * ws.element_size(), _launch_stream(device, stream)))
+        if stream is not None:
+            with _on_stream(stream, self.device):
+                return self.evict(table, lens, budget, sink, recent, next_pos, acc_in, pos_in, acc_out, pos_out, len_out, max_len,
+                                  workspace)
+        self._native.evict(self._pages, table, lens, budget, sink, recent, next_pos, acc_in, pos_in, acc_out, pos_out, len_out,
+                           max_len, workspace)

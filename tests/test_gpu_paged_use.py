@@ -335,9 +335,9 @@ def test_refusals_of_tensors_on_the_device(svx):
         args.update(kw)
         with pytest.raises((svx.SvxError, AttributeError)):
             c.decode(**args)
-    n = svx.ctypes.c_int64(0)
-    p, _, _ = c._with_table(table, 1)
-    assert svx.lib.svx_paged_decode_workspace(p, 1, 4, 0, 0, svx.ctypes.byref(n)) == svx.OK
+    n, p = svx.ctypes.c_int64(0), svx.Pages.from_buffer_copy(c._pages)
+    p.table, p.max_pages = table.data_ptr(), 2
+    assert svx.lib.svx_paged_decode_workspace(svx.ctypes.byref(p), 1, 4, 0, 0, svx.ctypes.byref(n)) == svx.OK
     ws = z(n.value + 256, t=torch.uint8)
     c.decode(q, table, lens, o, lse, workspace=ws)
     with pytest.raises(svx.SvxError):  # a workspace off its alignment
@@ -379,12 +379,15 @@ def test_refusals_of_tensors_on_the_device(svx):
         svx.qk_norm_rope(y[:, :, :4], y[:, :, 4:6], None, p2, rope, qo, ko)
     # C ABI: a host address where device memory is wanted is refused, unless the caller vouches for it
     host = np.zeros(64, dtype=np.int32)
-    args = svx._PAGES.unpack(p)
-    raw = svx._PAGES.pack(*args[:-2], 0, 0)
-    for pages, want in ((raw, svx.ERR_INVALID_ARG),):
-        st = svx.lib.svx_paged_decode(pages, 1, 4, q.data_ptr(), host.ctypes.data, 0, 0.0, o.data_ptr(), lse.data_ptr(), None, None,
-                                      ws.data_ptr(), ws.numel(), None)
-        assert st == want
+    p.flags = 0
+    st = svx.lib.svx_paged_decode(svx.ctypes.byref(p), 1, 4, q.data_ptr(), host.ctypes.data, 0, 0.0, o.data_ptr(), lse.data_ptr(), None,
+                                  None, ws.data_ptr(), ws.numel(), None)
+    assert st == svx.ERR_INVALID_ARG
+    assert svx.lib.svx_paged_decode(svx.ctypes.byref(p), 1, 4, q.data_ptr(), lens.data_ptr(), 0, 0.0, o.data_ptr(), lse.data_ptr(), None,
+                                    None, ws.data_ptr(), ws.numel(), None) == svx.OK
+    for bad in ((1, 2), (None,) * 11, (c._pages,) * 11):  # the native calls themselves: counts and kinds of arguments
+        with pytest.raises((TypeError, svx.SvxError)):
+            c._native.decode(*bad)
     assert not c.check()
 
 

@@ -11,7 +11,7 @@ import pytest
 @pytest.fixture(scope="module")
 def svx():
     from speculative_decoding_verification_chunked_gb300 import build
-    if not (os.path.exists(build.LIB) and os.path.exists(build.LIB_CHECKED)):
+    if not all(os.path.exists(x) for x in (build.LIB, build.LIB_CHECKED, build.LIB_TORCH)):
         build.build()
     from speculative_decoding_verification_chunked_gb300 import svx as mod
     return mod
@@ -81,7 +81,7 @@ def test_bad_pages_are_refused_by_every_call(svx, bad):
     assert svx.lib.svx_paged_evict(p, 2, LEN, 0, 8, 0, 0, NEXT, ACC, POS, ACC2, POS2, LEN2, WS, 1 << 40, None) in refused
     h = heads(svx, k=KOUT, v=VOUT)
     if "head_dim" not in bad and "dtype" not in bad:
-        assert svx.lib.svx_paged_append(ctypes.byref(h), svx.Rope(128).address, p, LEN, O, None, None, None) in refused
+        assert svx.lib.svx_paged_append(ctypes.byref(h), ctypes.byref(svx.Rope(128).table), p, LEN, O, None, None, None) in refused
     assert svx.lib.svx_last_error(None)
 
 
@@ -128,25 +128,25 @@ def test_evict_refusals_and_workspace(svx):
 def test_heads_refusals(svx):
     rope = svx.Rope(128)
 
-    def dense(q_out=O, k_out=KOUT, v_out=VOUT, r=rope.address, **kw):
+    def dense(q_out=O, k_out=KOUT, v_out=VOUT, r=ctypes.byref(rope.table), **kw):
         return svx.lib.svx_qk_norm_rope(ctypes.byref(heads(svx, **kw)), r, q_out, k_out, v_out, None)
     bad = [dict(n_req=0), dict(n_req=257), dict(n_tok=0), dict(head_dim=80), dict(dtype=7), dict(n_kv_heads=0), dict(n_kv_heads=3),
            dict(n_q_heads=8192, n_kv_heads=1, q_stride=1 << 20), dict(q_stride=504), dict(k_stride=128), dict(v_stride=1028), dict(q_stride=1 << 60),
            dict(q=None), dict(k=None), dict(q=Q + 8), dict(v=V + 4), dict(q_out=None), dict(k_out=None), dict(k_out=KOUT + 8),
            dict(v_out=None), dict(v=None), dict(pos=None), dict(eps=float("nan")), dict(eps=-1.0, q_norm=LSE),
            dict(q_norm=LSE + 8), dict(k_norm=LSE + 2), dict(r=None),
-           dict(r=svx.Rope(128).address, head_dim=64),                                  # rotation wider than the head
+           dict(r=ctypes.byref(rope.table), head_dim=64),                                  # rotation wider than the head
            dict(q_out=Q), dict(k_out=Q + 1024), dict(v_out=V), dict(q_out=KOUT), dict(v_out=KOUT + 512)]  # overlaps
     for kw in bad:
         assert dense(**kw) in (svx.ERR_INVALID_ARG, svx.ERR_UNSUPPORTED), kw
     p = pages(svx, k=KOUT, v=VOUT)
 
     def append(start=LEN, q_out=O, cache=p, **kw):
-        return svx.lib.svx_paged_append(ctypes.byref(heads(svx, **kw)), rope.address, ctypes.byref(cache), start, q_out, None, None, None)
+        return svx.lib.svx_paged_append(ctypes.byref(heads(svx, **kw)), ctypes.byref(rope.table), ctypes.byref(cache), start, q_out, None, None, None)
     for kw in (dict(start=None), dict(v=None), dict(n_kv_heads=1), dict(dtype=1), dict(device=1), dict(q_out=KOUT),
                dict(k=KOUT + 1024), dict(cache=pages(svx, k=KOUT, v=VOUT, head_dim=64))):
         assert append(**kw) == svx.ERR_INVALID_ARG, kw
-    assert svx.lib.svx_paged_append(ctypes.byref(heads(svx)), rope.address, None, LEN, O, None, None, None) == svx.ERR_INVALID_ARG
+    assert svx.lib.svx_paged_append(ctypes.byref(heads(svx)), ctypes.byref(rope.table), None, LEN, O, None, None, None) == svx.ERR_INVALID_ARG
 
 
 def test_binding_refuses_tensors_off_the_gpu(svx):
