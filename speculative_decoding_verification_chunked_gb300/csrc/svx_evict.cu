@@ -33,7 +33,7 @@ constexpr int kMaxKeys = 32;    // per thread
 constexpr int kMaxCluster = 8;  // portable
 constexpr int kSplitKeys = 16;  // a thread's keys above which a row takes more CTAs, where SMs are free: a barrier of the
                                 // cluster costs 0.45 us a pass (8 rows of 8192 slots: 8 keys in 2 CTAs 17.6 us, 16 in 1 15.8)
-constexpr int kSmallThreads = 256;
+constexpr int kFewThreads = 512;  // up to so many, a CTA makes its row's moves too, if they are few
 constexpr int kFewMoves = 8;  // of a warp
 static_assert(kMaxThreads * kMaxKeys * kMaxCluster == SVX_EVICT_MAX_LEN, "the longest row a cluster holds");
 
@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
   const int first = (rank * kWarps + warp) * (32 * KEYS) + lane;  // this lane's slots: first + 32 i
   uint32_t key[KEYS];
   const int64_t recent_from = static_cast<int64_t>(P.next_pos[b]) - P.recent;
-  constexpr int LOADS = KEYS < 8 ? KEYS : 8;  // slots in flight at a time
+  constexpr int LOADS = KEYS <= 10 ? KEYS : KEYS == 12 ? 6 : 8;  // slots in flight at a time
+  static_assert(KEYS % LOADS == 0, "whole turns");
 #pragma unroll
   for (int i0 = 0; i0 < KEYS; i0 += LOADS) {
     int32_t pos[LOADS];
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     }
   }
   if (n_cta > 1) cg::this_cluster().sync();  // no CTA leaves while another may still read its shared memory
-  if constexpr (THREADS != kSmallThreads) return;
+  if constexpr (THREADS > kFewThreads) return;
   if (!P.fused) return;
   // Few moves, one small CTA to the row: they are made here, without another kernel.
   if (threadIdx.x == 0 && row == b * P.pages.n_kv_heads) P.len_out[b] = n;
@@ -488,29 +489,34 @@ cudaError_t launch_select(const EvictParams& p, int rows, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, select_kernel<KEYS, THREADS>, p);
 }
 
-// Threads and CTAs of a row: up to kSmallRow slots 256 threads (a barrier of 8 warps), above 1024; a cluster of CTAs
-// where one does not hold the row, or where there are SMs for it and it shortens a thread's part.
-constexpr int kSmallRow = 256 * 16;
+// Threads and CTAs of a row: few warps where few slots need them, since every histogram pass waits for all; a cluster of
+// CTAs where one does not hold the row, or where there are SMs for it and it shortens a thread's part.  (64 rows of 2112
+// slots: 256 threads 7.9 us, 512 8.5; of 4096: 512 threads 8.9 us, 256 9.9.)
+constexpr int kSmallRow = 256 * 10, kMiddleRow = 512 * 16;
 cudaError_t launch_selects(EvictParams& p, int rows, int sms, cudaStream_t s) {
-  const int threads = p.max_len <= kSmallRow ? kSmallThreads : kMaxThreads;
+  const int threads = p.max_len <= kSmallRow ? 256 : p.max_len <= kMiddleRow ? kFewThreads : kMaxThreads;
   p.cluster = 1;
   auto keys = [&](int c) { return (p.max_len + c * threads - 1) / (c * threads); };
   while (p.cluster < kMaxCluster &&
          (keys(p.cluster) > kMaxKeys || (keys(p.cluster) > kSplitKeys && rows * p.cluster * 2 <= sms)))
     p.cluster *= 2;
   // Moves in the same kernel where a small CTA has one turn of its warps of them, which saves a launch and a trip through
-  // memory: 64 rows of 2112 slots to 2048 take 9.2 us so and 9.6 us in two kernels, 256 rows of 1040 to 1024 7.2 and 8.0 us;
+  // memory: 64 rows of 2112 slots to 2048 took 9.2 us so and 9.6 us in two kernels, 256 rows of 1040 to 1024 7.2 and 8.0 us;
   // with four turns it is 14.4 and 11.8 us.  Not where the new lengths go over the old, which other heads' CTAs may
   // still have to read.
-  p.fused = threads == kSmallThreads && p.cluster == 1 && p.most <= kFewMoves * (threads / 32) && p.len_out != p.len;
+  p.fused = threads <= kFewThreads && p.cluster == 1 && p.most <= kFewMoves * (threads / 32) && p.len_out != p.len;
   const int per = keys(p.cluster);
   if (threads == 256)
-    return per <= 4 ? launch_select<4, 256>(p, rows, s) : per <= 8 ? launch_select<8, 256>(p, rows, s)
-                                                                    : launch_select<16, 256>(p, rows, s);
-  return per <= 4    ? launch_select<4, 1024>(p, rows, s)
-         : per <= 8  ? launch_select<8, 1024>(p, rows, s)
-         : per <= 16 ? launch_select<16, 1024>(p, rows, s)
-                     : launch_select<32, 1024>(p, rows, s);
+    return per <= 4   ? launch_select<4, 256>(p, rows, s)
+           : per <= 8 ? launch_select<8, 256>(p, rows, s)
+                      : launch_select<10, 256>(p, rows, s);
+  if (threads == kFewThreads)
+    return per <= 8    ? launch_select<8, kFewThreads>(p, rows, s)
+           : per <= 12 ? launch_select<12, kFewThreads>(p, rows, s)
+                       : launch_select<16, kFewThreads>(p, rows, s);
+  return per <= 12   ? launch_select<12, kMaxThreads>(p, rows, s)
+         : per <= 16 ? launch_select<16, kMaxThreads>(p, rows, s)
+                     : launch_select<32, kMaxThreads>(p, rows, s);
 }
 
 cudaError_t launch_moves(EvictParams& p, int head_dim, int rows, int sms, cudaStream_t s) {
