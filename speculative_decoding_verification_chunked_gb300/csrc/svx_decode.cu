@@ -384,17 +384,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
       }
     }
   };
-  // the first chunks' pages and the first q are fetched together
-  Look ahead[kStages];
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) ahead[i] = look();
+  // pages are looked up two chunks ahead; the first two chunks' and the first q are fetched together
+  Look next = look(), after = look();
   if (w0 < w1) {
     seek(cc, P, plan, w0);
     load_q();
   }
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) load(i, ahead[i]);
-  Look next = ahead[kStages - 1];
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) {
+    load(i, next);
+    next = after;
+    after = look();
+  }
 
   // ---- the parts of items in this warp's range
   int stage = 0;
@@ -419,7 +420,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
       cp_wait<kStages - 2>();
       __syncwarp();  // every lane's copies of this chunk are here, and every lane is done with the last one
       load(stage == 0 ? kStages - 1 : stage - 1, next);
-      next = look();
+      next = after;
+      after = look();
       const uint32_t kb = stage0 + stage * (2 * kChunkBytes), vb = kb + kChunkBytes;
       stage = stage == kStages - 1 ? 0 : stage + 1;
 
