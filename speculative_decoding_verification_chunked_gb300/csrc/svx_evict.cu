@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
           need = 0;
           break;
         }
-        if (shift == 0) {
+        if (shift == 0 || pass == kPasses - 1) {  // (the last pass has shift 0)
           cut = lo;
           break;
         }
@@ -569,6 +569,8 @@ extern "C" svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, con
   };
   if (meets(acc_in, acc_out, meta) || meets(pos_in, pos_out, meta) || meets(len, len_out, static_cast<size_t>(n_req) * 4))
     return paged_fail(SVX_ERR_INVALID_ARG, "acc_out, pos_out and len_out must be their inputs or not overlap them");
+  if (next_pos == len_out || meets(next_pos, len_out, static_cast<size_t>(n_req) * 4))
+    return paged_fail(SVX_ERR_INVALID_ARG, "len_out must not overlap next_pos");
   if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(z.total))
     return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", z.total);
   svx::PagedDevice dev(cache->device);

@@ -91,7 +91,7 @@ def test_decode_refusals(svx):
     def call(n_req=2, hq=4, q=Q, ln=LEN, max_len=0, scale=0.0, o=O, lse=LSE, a=None, b=None, ws=WS, size=1 << 40):
         return svx.lib.svx_paged_decode(p, n_req, hq, q, ln, max_len, scale, o, lse, a, b, ws, size, None)
     for kw in (dict(n_req=0), dict(n_req=257), dict(q=None), dict(ln=None), dict(o=None), dict(lse=None), dict(q=Q + 8),
-               dict(o=O + 4), dict(lse=LSE + 2), dict(a=ACC), dict(b=ACC), dict(scale=-1.0), dict(scale=float("nan")),
+               dict(o=O + 4), dict(lse=LSE + 2), dict(a=ACC), dict(b=ACC), dict(a=ACC, b=ACC + 64), dict(scale=-1.0), dict(scale=float("nan")),
                dict(scale=float("inf"))):
         assert call(**kw) in (svx.ERR_INVALID_ARG, svx.ERR_UNSUPPORTED), kw
     for kw in (dict(hq=3), dict(hq=0), dict(hq=8192), dict(max_len=-1), dict(max_len=65)):
@@ -113,7 +113,7 @@ def test_evict_refusals_and_workspace(svx):
     for kw in (dict(n_req=0), dict(ln=None), dict(nxt=None), dict(a=None), dict(q=None), dict(a2=None), dict(q2=None), dict(l2=None),
                dict(budget=0), dict(budget=-3), dict(sink=-1), dict(recent=-1), dict(sink=7, recent=2), dict(max_len=65),
                dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1, budget=2 ** 31 - 1), dict(max_len=-1), dict(ws=None), dict(ws=WS + 16), dict(size=16),
-               dict(a2=ACC + 4), dict(q2=POS - 8), dict(l2=LEN + 4)):
+               dict(a2=ACC + 4), dict(q2=POS - 8), dict(l2=LEN + 4), dict(l2=NEXT), dict(l2=NEXT + 4)):
         assert call(**kw) == svx.ERR_INVALID_ARG, kw
     n = ctypes.c_int64(0)
     for max_len, budget in ((0, 8), (64, 64), (10, 64), (64, 1)):
