@@ -8,8 +8,8 @@
 //
 // Phase.  t is needed mod 2 pi, and an fp32 product pos * inv_freq has lost it for far positions (2^17 * 2^-24 is
 // 8e-3 rad).  The host keeps inv_freq / 2 pi as a 64-bit fraction of a turn, so pos * turns mod 2^64 is
-// the fraction of a turn exactly, in three integer multiply-adds instead of FP64; its upper 32 bits, read as
-// signed half-turns, go to sincospif.
+// the fraction of a turn exactly, in three integer multiply-adds instead of FP64; its upper 32 bits give an angle in
+// [-pi, pi), rounded to fp32 (2^-22), on which the fast sine and cosine hold 2^-21 (sincospif: 40 instructions more an angle).
 //
 // Layout.  A head is d / 16 lanes; a lane holds 16 elements as two 16-byte vectors, chosen so that both members
 // of each rotated pair sit in one lane: vectors l and l + rot/16 of the rotated part, or two neighbouring vectors of the
@@ -17,9 +17,10 @@
 // kMaxWalk heads of one kind (q, k or v) of them; a lane's eight angles and its weights become 32 factors once for the
 // whole walk, which leaves three operations an element besides the sum of squares.  The walk's heads are all brought in at
 // once, into shared memory, so the loads need no registers and do not wait for the sines.
-// What bounds it: the copy rate.  32768 tokens of 32 + 8 + 8 heads, d = 128 (806 MB moved): 120 us = 6720 GB/s, 99% of the
-// measured copy rate (138 us with four heads held ahead in registers, 210 us with angles and weights applied head by head);
-// one token 3.5 us, the latency of a launch and three trips to memory.
+// What bounds it: the copy rate.  32768 tokens of 32 + 8 + 8 heads, d = 128 (806 MB moved): 119 us = 6790 GB/s, the
+// measured copy rate (138 us with four heads held ahead in registers, 210 us with angles and weights applied head by head).
+// With few heads to a token the angles and a warp's start show: 106272 tokens of 4 + 2 + 2 heads, d = 64 (220 MB) 43 us
+// (48 with sincospif and 64-bit divisions).  One token: 3.2 us, the latency of a launch and three trips to memory.
 #include "svx_paged.h"
 
 namespace svx {
@@ -49,7 +50,7 @@ struct HeadsParams {
   int32_t n_tok, n_q, n_kv;
   int32_t walk;                 // heads that a warp walks
   int32_t q_parts, kv_parts;    // warps per block of tokens for the heads of q, of k (and of v)
-  int32_t parts;                // all of them
+  uint32_t parts;               // all of them
   int32_t rot_dim, neighbours, norm, paged;
 };
 
@@ -97,15 +98,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
   constexpr int TOKENS = 32 / LANES;  // tokens of a warp
   grid_dependency_wait();
   allow_dependents();
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t block = gw / P.parts;
+  const uint32_t gw = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t block = gw / P.parts;
   const int part = static_cast<int>(gw - block * P.parts);  // which heads: the same for the whole warp
   const int lane = threadIdx.x % LANES;
-  int64_t token = block * TOKENS + (threadIdx.x & 31) / LANES;
-  bool live = token < P.tokens;
-  if (!live) token = 0;
-  const int b = static_cast<int>(token / P.n_tok);
-  const int j = static_cast<int>(token - static_cast<int64_t>(b) * P.n_tok);
+  uint32_t token32 = block * TOKENS + (threadIdx.x & 31) / LANES;
+  bool live = token32 < static_cast<uint32_t>(P.tokens);
+  if (!live) token32 = 0;
+  const int b = static_cast<int>(token32 / static_cast<uint32_t>(P.n_tok));
+  const int j = static_cast<int>(token32) - b * P.n_tok;
+  const int64_t token = token32;
   if (live && P.n_new) {
     const int n = P.n_new[b];
     if (P.status && (n < 0 || n > P.n_tok) && j == 0 && part == 0 && lane == 0) atomicOr(P.status, kErrInput);
@@ -230,12 +232,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
       if (turn) {
         const int f = P.neighbours ? (i < 4 ? 4 * v0 + i : 4 * v1 + i - 4) : 8 * lane + i;
         const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[f];
-        // half-turns in [-1, 1): |error| <= 2^-25 of a half-turn from the conversion
-        const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
-        float sn, cs;
-        sincospif(half_turns, &sn, &cs);
-        sn *= P.scale;
-        cs *= P.scale;
+        // radians in [-pi, pi), where the fast sine and cosine are within 2^-21; the 16-bit outputs step by 2^-11 and more
+        const float angle = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 1.4629180792671596e-9f;  // pi / 2^31
+        const float sn = __sinf(angle) * P.scale, cs = __cosf(angle) * P.scale;
         fa[i] = wa * cs;
         fb[i] = wb * sn;
         ga[i] = wb * cs;
@@ -297,7 +296,7 @@ template <typename T, int D>
 cudaError_t launch(HeadsParams& p, cudaStream_t stream, int sms) {
   // Heads that a warp walks (its tokens' heads of one kind): one where tokens are few (latency: every head its own
   // warp), more once the grid half fills the card anyway, so that a lane's eight sines and cosines serve several heads.
-  // (2331 tokens of 18 heads, d = 64: 7.8 us with four, 8.2 with two; 128 tokens of 48: 3.5 us with one.)
+  // (d = 64: 2331 tokens of 15 heads 6.7 us with four, 6.1 with two; 20436 tokens of 6 9.7 us with eight, 11.2 with four.)
   const int64_t blocks_of_tokens = (p.tokens * (D / 16) + 31) / 32;
   const int64_t room = static_cast<int64_t>(sms) * 32;  // warps
   const int64_t warps = blocks_of_tokens * (p.n_q + p.n_kv);
@@ -335,6 +334,7 @@ svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages*
   const int d = in->head_dim;
   const int64_t q_row = static_cast<int64_t>(in->n_q_heads) * d, kv_row = static_cast<int64_t>(in->n_kv_heads) * d;
   const int64_t tokens = static_cast<int64_t>(in->n_req) * in->n_tok;
+  if (tokens > 0x7fffffff) return paged_fail(SVX_ERR_UNSUPPORTED, "n_req * n_tok must be below 2^31");
   const int64_t most = (int64_t{1} << 46) / tokens;
   const int64_t str[3] = {in->q_stride, in->k_stride, in->v_stride}, row[3] = {q_row, kv_row, kv_row};
   for (int i = 0; i < (has_v ? 3 : 2); ++i)

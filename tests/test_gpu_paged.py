@@ -2,8 +2,8 @@
 
 Error bounds, derived before any run.  u = torch.finfo(type).eps / 2 is a rounding to the output type.
   heads   fp32 throughout, one rounding.  The norm's sum of d squares, its square root and three products stay under
-          2^-19 relative; the phase is exact to 2^-25 of a half-turn and sine and cosine to 2^-22, so a
-          rotated value is off by at most (|y_a| + |y_b|) 2^-19 before its rounding: |z| u + (|y_a| + |y_b|) 2^-18.
+          2^-19 relative; the angle is exact to 2^-22 and sine and cosine to 2^-21, together under 2^-20, so a
+          rotated value is off by at most (|y_a| + |y_b|) (2^-19 + 2^-20) before its rounding: |z| u + (|y_a| + |y_b|) 2^-18.
   decode  a score (natural units) is off by at most 2^-19 S, S = scale max sum |q_i k_i| (8 tensor-core steps, each
           within 2^-22 of the running size); p keeps 16 bits in two pieces (2^-16 relative, the exponential
           2^-21); sums of n terms within n 2^-24.  So O is off by |O| u + c sum w|v| with
