@@ -62,6 +62,7 @@ struct DecodeParams {
   float scale;      // softmax scale * log2(e)
   int32_t max_len;
   int32_t n_q, group, blocks;  // blocks of 16 query heads per KV head
+  int32_t whole;               // no item is split over CTAs: there is nothing to join
   int32_t ctas;                // of the attention kernel
 };
 
@@ -260,6 +261,14 @@ __device__ __forceinline__ void seek(Cursor& c, const DecodeParams& P, const Pla
   c.blk = i - c.h * P.blocks;
 }
 
+// The first chunk at x or behind it that begins an item.
+__device__ __forceinline__ int item_start(const DecodeParams& P, const Plan& s, int x, int total) {
+  if (x >= total) return total;
+  Cursor c{0, 0, 0, 0, 0, 0};
+  seek(c, P, s, x);
+  return c.first == x ? x : c.end;
+}
+
 // O and LSE of a row from its merged state.
 template <typename T, int D>
 __device__ __forceinline__ void write_row(const DecodeParams& P, int64_t row, int d4, float M, float L, float4 o) {
@@ -302,7 +311,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
     write_empty<T, D>(P, plan);
     return;
   }
-  const int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
+  int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
+  if (P.whole) {  // the items that begin in the range, whole
+    x0 = item_start(P, plan, x0, T_all);
+    x1 = item_start(P, plan, x1, T_all);
+  }
   const int w0 = x0 + static_cast<int>(static_cast<int64_t>(x1 - x0) * warp / kWarps);
   const int w1 = x0 + static_cast<int>(static_cast<int64_t>(x1 - x0) * (warp + 1) / kWarps);
 
@@ -826,11 +839,12 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
 // ------------------------------------------------------------------ host
 
 constexpr int64_t kMaxGridY = 65535;
+constexpr int64_t kWholeItem = 32;  // chunks
 
 
 struct Sizes {
   int32_t max_len, blocks, ctas;
-  bool one;  // one CTA does it all, whatever the lengths
+  bool whole;  // no item is split over CTAs, whatever the lengths
   int64_t score_stride;
   size_t part_o, part_ml, lead, lead_ml, row_ml, scores, total;
 };
@@ -854,7 +868,11 @@ svx_status sizes(const svx_pages* c, int32_t n_req, int32_t n_q, int64_t max_len
   if (chunks > 0x7fffffff)
     return paged_fail(SVX_ERR_UNSUPPORTED, "n_req * heads * max_len is too large (%lld chunks of %d slots, at most 2^31 - 1)",
                       static_cast<long long>(chunks), ct);
-  z->one = chunks <= kMinChunks;
+  // Whole items to the CTAs where they are few and short: the longest takes a CTA kWholeItem / 8 chunks a warp, and the join's
+  // launch and wait go.  Split and whole: one KV head of 64, 512 slots, 6.2 and 5.9 us; 8 KV heads of 128, 8 requests of 1 to 512
+  // slots 9.4 and 8.7, 8 of 512 slots 8.3 and 8.5; 2 of 1024 slots (64 chunks, and so split) 8.0 and 11.7.
+  const int64_t per_item = (max_len + ct - 1) / ct;
+  z->whole = !weights && per_item <= kWholeItem && chunks <= sms * per_item;
   z->ctas = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kMaxCtas), std::max<int64_t>((chunks + kMinChunks - 1) / kMinChunks, 1)));
   z->score_stride = (max_len + ct - 1) / ct * ct;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -884,12 +902,12 @@ cudaError_t launch_attend(const DecodeParams& p, int device, cudaStream_t s) {
 }
 
 template <typename T, int D>
-cudaError_t launch_all(const DecodeParams& p, bool one, int device, cudaStream_t s) {
+cudaError_t launch_all(const DecodeParams& p, int device, cudaStream_t s) {
   const bool wide = p.group > 8, scores = p.scores != nullptr;
   const cudaError_t e =
       wide ? (scores ? launch_attend<T, D, true, true>(p, device, s) : launch_attend<T, D, true, false>(p, device, s))
            : (scores ? launch_attend<T, D, false, true>(p, device, s) : launch_attend<T, D, false, false>(p, device, s));
-  if (e != cudaSuccess || (one && !scores)) return e;  // (one CTA leaves no pieces)
+  if (e != cudaSuccess || p.whole) return e;
   const int slots = scores ? (p.max_len + kWeightSlots - 1) / kWeightSlots : 1;
   const dim3 grid(p.pages.n_req * p.pages.n_kv_heads, std::max(p.blocks, slots));
   return scores ? launch_pdl(join_kernel<T, D, true>, grid, dim3(kWarps * 32), 0, s, p)
@@ -963,15 +981,16 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   p.n_q = n_q_heads;
   p.group = n_q_heads / cache->n_kv_heads;
   p.blocks = z.blocks;
+  p.whole = z.whole;
   p.ctas = z.ctas;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (cache->dtype == SVX_BF16)
-    e = cache->head_dim == 128 ? svx::launch_all<__nv_bfloat16, 128>(p, z.one, cache->device, s)
-                               : svx::launch_all<__nv_bfloat16, 64>(p, z.one, cache->device, s);
+    e = cache->head_dim == 128 ? svx::launch_all<__nv_bfloat16, 128>(p, cache->device, s)
+                               : svx::launch_all<__nv_bfloat16, 64>(p, cache->device, s);
   else
-    e = cache->head_dim == 128 ? svx::launch_all<__half, 128>(p, z.one, cache->device, s)
-                               : svx::launch_all<__half, 64>(p, z.one, cache->device, s);
+    e = cache->head_dim == 128 ? svx::launch_all<__half, 128>(p, cache->device, s)
+                               : svx::launch_all<__half, 64>(p, cache->device, s);
   if (e != cudaSuccess) return paged_fail(SVX_ERR_CUDA, "decode kernel launch failed: %s", cudaGetErrorString(e));
   return SVX_OK;
 }

@@ -258,6 +258,18 @@ def test_decode(svx, case):
     check_decode(case, got, decode64(q, k64, v64, table, case[0], case[3] ** -0.5, acc), acc)
 
 
+@pytest.mark.parametrize("hkv", [1, 8])
+@pytest.mark.parametrize("d,longest", [(128, 512), (128, 513), (64, 1024), (64, 1025)])
+def test_decode_short_items_whole_and_split(svx, d, longest, hkv):
+    """Items of 32 chunks stay in one CTA, one slot more and they are split; 8 heads of 20 requests are too many for it."""
+    g = np.random.default_rng(longest + hkv)
+    lens = (longest, 0, 1, *(int(x) for x in g.integers(0, longest + 1, 17)))
+    case = (lens, 20 * hkv, hkv, d, 16, "bf16", "token", False)  # 20 query heads a KV head: two blocks
+    table, kp, vp, k64, v64, q, acc = decode_inputs(case, seed=9)
+    got = run_decode(svx, case, table, kp, vp, q, acc, max_len=longest)
+    check_decode(case, got, decode64(q, k64, v64, table, case[0], d ** -0.5, acc), acc)
+
+
 @pytest.mark.parametrize("q_scale", [0.0, 20.0])
 def test_decode_flat_and_peaked(svx, q_scale):
     """Equal scores (the mean of V), and scores that leap: the running reference moves many times."""
