@@ -781,6 +781,11 @@ class Rope:
             raise SvxError(st, lib.svx_last_error(None).decode())
         self.address = ctypes.addressof(self.table)
 
+    def __setstate__(self, state):
+        """Copies (copy.deepcopy, pickle) point to their own table."""
+        self.__dict__.update(state)
+        self.address = ctypes.addressof(self.table)
+
 
 def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None, k_norm=None,
                  eps: Optional[float] = 1e-6, n_new=None, status=None, stream=None):

@@ -33,6 +33,16 @@ def test_turns_are_the_fraction_of_a_turn_per_position(svx):
     assert (r.table.rot_dim, r.table.neighbours, r.table.scale) == (16, 0, 1.0)
 
 
+def test_copies_of_a_rope_have_their_own_table(svx):
+    """A model that holds one may be copied and the original freed."""
+    import copy
+    import pickle
+    r = svx.Rope(16, theta=500.0)
+    for c in (copy.deepcopy(r), pickle.loads(pickle.dumps(r)), copy.copy(r)):
+        assert c.address == ctypes.addressof(c.table) and list(c.table.turns) == list(r.table.turns)
+    assert copy.deepcopy(r).address != r.address
+
+
 def test_rope_refusals(svx):
     ok = [0.5] * 64
     for rot, inv in ((8, ok[:4]), (-16, []), (24, ok[:12]), (144, [0.5] * 72), (16, ok[:7]), (16, [float("nan")] * 8),
