@@ -806,7 +806,8 @@ class PagedCache:
     """K and V pages of one layer, for a model that takes its tokens one at a time (svx_paged_*).
 
     k_pages, v_pages: device bf16 or fp16 [pages][page_size][Hkv][d], equally strided; any order of the first three
-    dimensions in memory, rows of d dense.  The tensors stay the caller's.  Page tables are int32 [B][max_pages]: slot t
+    dimensions in memory, rows of d dense.  Their memory is the caller's and is used in place: a tensor that gets
+    other memory later (``.data = ...``) needs another PagedCache, and a PagedCache is not copied deeply.  Page tables are int32 [B][max_pages]: slot t
     of request b is slot t % page_size of page table[b][t // page_size].  Calls run on the current stream (or
     ``stream``), allocate nothing but a workspace from torch's caching allocator (or take ``workspace``) and may be
     captured into CUDA graphs, after one eager call.  Lengths, slots and page ids are read on the device; ``check()`` tells
@@ -817,10 +818,24 @@ class PagedCache:
         import torch
         if k_pages.device.type != "cuda":
             raise SvxError(ERR_INVALID_ARG, f"k_pages is on {k_pages.device}, not on a CUDA device")
-        self.k_pages, self.v_pages, self.device = k_pages, v_pages, k_pages.get_device()
-        self.status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
+        # aliases: the memory that the addresses in _pages name stays, whatever becomes of the caller's tensor objects
+        self._k, self._v = k_pages.detach(), v_pages.detach()
+        self.device = k_pages.get_device()
+        self._status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
         self._native = _native()
-        self._pages = self._native.pages(k_pages, v_pages, self.status)
+        self._pages = self._native.pages(self._k, self._v, self._status)
+
+    @property
+    def k_pages(self):
+        return self._k
+
+    @property
+    def v_pages(self):
+        return self._v
+
+    @property
+    def status(self):
+        return self._status
 
     def check(self) -> bool:
         """True if, since the last check, a call met a length, slot or page id out of its bounds (outputs that depend

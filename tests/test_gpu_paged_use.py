@@ -447,3 +447,32 @@ def test_evict_in_other_layouts(svx, layout):
                     k0[int(table[b, t // page]), t % page, h] = k0[int(table[b, f // page]), f % page, h]
                     v0[int(table[b, t // page]), t % page, h] = v0[int(table[b, f // page]), f % page, h]
     assert torch.equal(kp.cpu(), k0) and torch.equal(vp.cpu(), v0)
+
+
+def test_a_cache_keeps_the_memory_that_it_was_given(svx):
+    """The caller's tensors get other memory: the cache still works on the first, which it holds."""
+    import copy
+    kp = torch.randn((4, 16, 1, 64), device="cuda", dtype=torch.bfloat16)
+    vp = torch.randn_like(kp)
+    q = torch.randn((1, 1, 1, 64), device="cuda", dtype=torch.bfloat16)
+    table = torch.tensor([[2, 0, 3]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([40], dtype=torch.int32, device="cuda")
+    cache = svx.PagedCache(kp, vp)
+    at = kp.data_ptr()
+
+    def step():
+        o, lse = torch.empty_like(q), torch.empty((1, 1, 1), device="cuda")
+        cache.decode(q, table, lens, o, lse)
+        assert not cache.check()
+        return o, lse
+    first = step()
+    kp.data, vp.data = torch.zeros_like(kp), torch.zeros_like(vp)
+    del kp, vp
+    junk = [torch.full((4, 16, 1, 64), 9.0, device="cuda", dtype=torch.bfloat16) for _ in range(8)]
+    assert cache.k_pages.data_ptr() == at and all(j.data_ptr() != at for j in junk)
+    assert all(torch.equal(a, b) for a, b in zip(first, step()))
+    for name in ("k_pages", "v_pages", "status"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, junk[0])
+    with pytest.raises(TypeError):
+        copy.deepcopy(cache)
