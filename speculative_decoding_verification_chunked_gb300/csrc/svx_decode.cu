@@ -941,19 +941,23 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   if (st != SVX_OK) return st;
   if ((acc_in == nullptr) != (acc_out == nullptr))
     return paged_fail(SVX_ERR_INVALID_ARG, "give both acc_in and acc_out, or neither");
-  if (acc_in && acc_in != acc_out) {
-    const size_t n = static_cast<size_t>(n_req) * p.pages.n_kv_heads * p.pages.cap * 4;
-    const char *a = reinterpret_cast<const char*>(acc_in), *b = reinterpret_cast<const char*>(acc_out);
-    if (a < b + n && b < a + n) return paged_fail(SVX_ERR_INVALID_ARG, "acc_out must be acc_in or not overlap it");
-  }
   if (!q || !o || !lse || !len || !svx::is_aligned(q, 16) || !svx::is_aligned(o, 16) || !svx::is_aligned(lse, 4))
     return paged_fail(SVX_ERR_INVALID_ARG, "q, len, o and lse must be device pointers, q and o 16-byte aligned");
   if (!(scale >= 0.f) || scale > 3.0e38f) return paged_fail(SVX_ERR_INVALID_ARG, "scale must be positive and finite, or 0");
+  const size_t n_rows = static_cast<size_t>(n_req) * std::max(n_q_heads, 0), per_req = static_cast<size_t>(n_req) * 4;
+  const size_t row = static_cast<size_t>(cache->head_dim) * 2, acc = per_req * p.pages.n_kv_heads * p.pages.cap;
+  const svx::Span q_span = {q, n_rows * row}, o_span = {o, n_rows * row}, lse_span = {lse, n_rows * 4}, out_span = {acc_out, acc},
+                  in_span = {acc_in == acc_out ? nullptr : acc_in, acc}, len_span = {len, per_req},
+                  table_span = {cache->table, per_req * cache->max_pages};
+  if (svx::any_overlap({o_span, lse_span, out_span, {cache->status, 4}}, {q_span, len_span, table_span, in_span}))
+    return paged_fail(SVX_ERR_INVALID_ARG, "an output overlaps an input or another output (acc_out may be acc_in)");
   svx::Sizes z = {};
   st = svx::sizes(cache, n_req, n_q_heads, max_len, acc_in != nullptr, &z);
   if (st != SVX_OK) return st;
   if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(z.total))
     return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", z.total);
+  if (svx::any_overlap({{workspace, z.total}}, {q_span, o_span, lse_span, in_span, out_span, len_span, table_span, {cache->status, 4}}))
+    return paged_fail(SVX_ERR_INVALID_ARG, "the workspace overlaps another buffer");
   svx::PagedDevice dev(cache->device);
   if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", cache->device);
   const void* ptrs[] = {cache->k, cache->v, cache->table, cache->status, q, len, o, lse, acc_in, acc_out, workspace};

@@ -563,16 +563,17 @@ extern "C" svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, con
   if (!len || !next_pos || !acc_in || !pos_in || !acc_out || !pos_out || !len_out)
     return paged_fail(SVX_ERR_INVALID_ARG, "len, next_pos, acc, pos and len_out must be device pointers");
   const size_t meta = static_cast<size_t>(n_req) * p.pages.n_kv_heads * p.pages.cap * 4;
-  auto meets = [](const void* a, const void* b, size_t n) {
-    const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
-    return x != y && x < y + n && y < x + n;
-  };
-  if (meets(acc_in, acc_out, meta) || meets(pos_in, pos_out, meta) || meets(len, len_out, static_cast<size_t>(n_req) * 4))
-    return paged_fail(SVX_ERR_INVALID_ARG, "acc_out, pos_out and len_out must be their inputs or not overlap them");
-  if (next_pos == len_out || meets(next_pos, len_out, static_cast<size_t>(n_req) * 4))
-    return paged_fail(SVX_ERR_INVALID_ARG, "len_out must not overlap next_pos");
+  const size_t per_req = static_cast<size_t>(n_req) * 4;
   if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(z.total))
     return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", z.total);
+  if (svx::any_overlap({{acc_out, meta}, {pos_out, meta}, {len_out, per_req}, {workspace, z.total}, {cache->status, 4}},
+                       {{acc_in == acc_out ? nullptr : acc_in, meta},
+                        {pos_in == pos_out ? nullptr : pos_in, meta},
+                        {len == len_out ? nullptr : len, per_req},
+                        {next_pos, per_req},
+                        {cache->table, per_req * cache->max_pages}}))
+    return paged_fail(SVX_ERR_INVALID_ARG, "an output or the workspace overlaps an input or another output (acc_out, pos_out and "
+                                           "len_out may be their inputs)");
   svx::PagedDevice dev(cache->device);
   if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", cache->device);
   const void* ptrs[] = {cache->k, cache->v, cache->table, cache->status, len,     next_pos, acc_in,

@@ -312,12 +312,6 @@ cudaError_t launch(HeadsParams& p, cudaStream_t stream, int sms) {
                     : launch_pdl(heads_kernel<T, D, false>, grid, dim3(kThreads), 0, stream, p);
 }
 
-struct Range {
-  const char* a;
-  const char* b;
-};
-bool overlap(const Range& x, const Range& y) { return x.a && y.a && x.a < y.b && y.a < x.b; }
-
 svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages* cache, const int32_t* start, void* q_out,
                      void* k_out, void* v_out, float* acc, int32_t* slot_pos, void* stream) {
   if (!in || !rope) return paged_fail(SVX_ERR_INVALID_ARG, "heads or rope is NULL");
@@ -364,23 +358,24 @@ svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages*
     if (!k_out || !is_aligned(k_out, 16) || has_v != (v_out != nullptr) || (v_out && !is_aligned(v_out, 16)))
       return paged_fail(SVX_ERR_INVALID_ARG, "k_out (and v_out with v) must be 16-byte aligned device pointers");
   }
-  const int64_t es = 2;
-  auto range = [es](const void* a, int64_t elems) {
-    const char* c = static_cast<const char*>(a);
-    return Range{c, c + elems * es};
-  };
-  // the span of a strided input covers what lies between its rows: outputs there are taken for overlapping
-  // only if they meet a row of it, so rows are compared by span for dense inputs and refused alike for views
-  const Range ins[3] = {range(in->q, (tokens - 1) * str[0] + row[0]), range(in->k, (tokens - 1) * str[1] + row[1]),
-                        has_v ? range(in->v, (tokens - 1) * str[2] + row[2]) : Range{nullptr, nullptr}};
-  const Range outs[5] = {range(q_out, tokens * q_row),
-                         cache ? range(cache->k, p.pages.extent) : range(k_out, tokens * kv_row),
-                         cache ? range(cache->v, p.pages.extent) : v_out ? range(v_out, tokens * kv_row) : Range{nullptr, nullptr}};
-  for (const Range& i : ins)
-    for (int o = 0; o < 3; ++o)
-      if (overlap(i, outs[o])) return paged_fail(SVX_ERR_INVALID_ARG, "an output overlaps an input");
-  if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || (!cache && overlap(outs[1], outs[2])))
-    return paged_fail(SVX_ERR_INVALID_ARG, "two outputs overlap");
+  // (a strided input or pool takes what lies between its rows along: outputs there are refused alike)
+  const size_t per_req = static_cast<size_t>(in->n_req) * 4, per_tok = static_cast<size_t>(tokens) * 4;
+  auto span = [](const void* a, int64_t elems) { return Span{a, static_cast<size_t>(elems) * 2}; };
+  const Span qi = span(in->q, (tokens - 1) * str[0] + row[0]), ki = span(in->k, (tokens - 1) * str[1] + row[1]),
+             vi = has_v ? span(in->v, (tokens - 1) * str[2] + row[2]) : Span{nullptr, 0}, qo = span(q_out, tokens * q_row),
+             wq = span(in->q_norm, d), wk = span(in->k_norm, d), pos = {in->pos, per_tok}, n_new = {in->n_new, per_req};
+  bool bad;
+  if (cache) {  // (the two pools may be interleaved)
+    const size_t meta = static_cast<size_t>(in->n_req) * in->n_kv_heads * p.pages.cap * 4;
+    const Span kp = span(cache->k, p.pages.extent), vp = span(cache->v, p.pages.extent);
+    bad = any_overlap({qo, {acc, meta}, {slot_pos, meta}, {cache->status, 4}},
+                      {qi, ki, vi, kp, vp, wq, wk, pos, n_new, {start, per_req}, {cache->table, per_req * cache->max_pages}}) ||
+          any_overlap({kp}, {qi, ki, vi}) || any_overlap({vp}, {qi, ki, vi});
+  } else {
+    bad = any_overlap({qo, span(k_out, tokens * kv_row), span(v_out, tokens * kv_row), {in->status, 4}},
+                      {qi, ki, vi, wq, wk, pos, n_new});
+  }
+  if (bad) return paged_fail(SVX_ERR_INVALID_ARG, "an output overlaps an input or another output");
 
   PagedDevice dev(in->device);
   if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", in->device);

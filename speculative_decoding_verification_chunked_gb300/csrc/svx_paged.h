@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "svx.h"
 #include "svx_internal.h"
 
@@ -58,6 +60,25 @@ svx_status paged_view(const svx_pages* c, int32_t n_req, PageView* out);
 bool on_device(const void* p, int device);
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int sm_count(int device);
+// A buffer of a call; p NULL: none.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+// True if a written buffer meets another written one or one that is read.
+inline bool any_overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* o = w + 1; o != written.end(); ++o)
+      if (meet(*w, *o)) return true;
+    for (const Span& r : read)
+      if (meet(*w, r)) return true;
+  }
+  return false;
+}
 
 // Makes `device` current for the entry point's duration.
 struct PagedDevice {

@@ -159,6 +159,51 @@ def test_heads_refusals(svx):
     assert svx.lib.svx_paged_append(ctypes.byref(heads(svx)), ctypes.byref(rope.table), None, LEN, O, None, None, None) == svx.ERR_INVALID_ARG
 
 
+def test_outputs_over_inputs_or_each_other_are_refused(svx):
+    """Every such pair of every call, by one element at either end; the pairs that may be one buffer get past it."""
+    rope = ctypes.byref(svx.Rope(128).table)
+    p = ctypes.byref(pages(svx))
+    row, meta, ints = 2 * 4 * 128 * 2, 2 * 2 * 64 * 4, 2 * 4
+
+    def message():
+        return svx.lib.svx_last_error(None).decode()
+
+    def decode(q=Q, ln=LEN, o=O, lse=LSE, a=ACC, b=ACC2):
+        st = svx.lib.svx_paged_decode(p, 2, 4, q, ln, 0, 0.0, o, lse, a, b, WS, 1 << 40, None)
+        return st == svx.ERR_INVALID_ARG and "overlap" in message()
+    assert not decode() and not decode(b=ACC)
+    for kw in (dict(o=Q), dict(o=Q + row - 16), dict(o=Q - row + 16), dict(lse=Q + row - 4), dict(lse=O), dict(lse=LEN), dict(b=TABLE),
+               dict(b=O - meta + 4), dict(b=ACC - meta + 4), dict(a=O), dict(lse=STATUS), dict(ln=LSE + 28), dict(ln=STATUS)):
+        assert decode(**kw), kw
+    for kw in (dict(o=Q + row), dict(o=Q - row), dict(lse=Q + row), dict(ln=LSE + 32), dict(b=ACC + meta)):
+        assert not decode(**kw), kw
+
+    def evict(ln=LEN, nxt=NEXT, a=ACC, q=POS, a2=ACC2, q2=POS2, l2=LEN2, ws=WS):
+        st = svx.lib.svx_paged_evict(p, 2, ln, 0, 8, 1, 2, nxt, a, q, a2, q2, l2, ws, 1 << 40, None)
+        return st == svx.ERR_INVALID_ARG and "overlap" in message()
+    assert not evict() and not evict(a2=ACC, q2=POS, l2=LEN)
+    for kw in (dict(a2=POS), dict(q2=ACC + meta - 4), dict(a2=ACC + 4), dict(q2=POS - 8), dict(l2=LEN + 4), dict(l2=NEXT), dict(l2=NEXT - 4),
+               dict(a2=TABLE), dict(a2=POS2), dict(l2=ACC2 + meta - 4), dict(ws=ACC), dict(ws=LEN), dict(ws=POS2), dict(l2=STATUS), dict(q=ACC2)):
+        assert evict(**kw), kw
+    assert not evict(a2=ACC + meta) and not evict(l2=LEN + ints)
+
+    def append(acc=ACC, pos=POS2, start=LEN, q_out=O, **kw):
+        c = pages(svx, k=KOUT, v=VOUT)
+        st = svx.lib.svx_paged_append(ctypes.byref(heads(svx, **kw)), rope, ctypes.byref(c), start, q_out, acc, pos, None)
+        return st == svx.ERR_INVALID_ARG and "overlap" in message()
+    assert not append()
+    for kw in (dict(acc=POS), dict(pos=POS), dict(pos=ACC + 4), dict(acc=LEN - meta + 4), dict(pos=TABLE), dict(acc=O), dict(acc=STATUS),
+               dict(q_out=LEN), dict(acc=Q), dict(pos=KOUT), dict(q_out=POS), dict(q_norm=O), dict(n_new=ACC)):
+        assert append(**kw), kw
+
+    def dense(q_out=O, k_out=KOUT, v_out=VOUT, **kw):
+        st = svx.lib.svx_qk_norm_rope(ctypes.byref(heads(svx, **kw)), rope, q_out, k_out, v_out, None)
+        return st == svx.ERR_INVALID_ARG and "overlap" in message()
+    assert not dense()
+    for kw in (dict(q_out=POS), dict(k_out=KOUT, q_norm=KOUT), dict(v_out=O), dict(n_new=VOUT), dict(status=O), dict(k_out=V)):
+        assert dense(**kw), kw
+
+
 def test_binding_refuses_tensors_off_the_gpu(svx):
     import torch
     k = torch.zeros((2, 4, 2, 64), dtype=torch.bfloat16)
