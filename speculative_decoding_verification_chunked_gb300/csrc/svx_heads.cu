@@ -8,8 +8,10 @@
 //
 // Phase.  t is needed mod 2 pi, and an fp32 product pos * inv_freq has lost it for far positions (2^17 * 2^-24 is
 // 8e-3 rad).  The host keeps inv_freq / 2 pi as a 64-bit fraction of a turn, so pos * turns mod 2^64 is
-// the fraction of a turn exactly, in three integer multiply-adds instead of FP64; its upper 32 bits give an angle in
-// [-pi, pi), rounded to fp32 (2^-22), on which the fast sine and cosine hold 2^-21 (sincospif: 40 instructions more an angle).
+// the fraction of a turn exactly, in three integer multiply-adds instead of FP64.  Its top bits name the nearest quarter
+// turn, and what is left of all 64 goes to fp32 without cancelling, so that the smallest angle keeps its relative precision:
+// a pair with y_a = 0 puts out y_b sin t alone, and is owed that to one rounding.  (The hardware's fast sine is within
+// 2^-21 of any sine, however small: outputs of small angles were up to 9% off.)
 //
 // Layout.  A head is d / 16 lanes; a lane holds 16 elements as two 16-byte vectors, chosen so that both members
 // of each rotated pair sit in one lane: vectors l and l + rot/16 of the rotated part, or two neighbouring vectors of the
@@ -17,10 +19,10 @@
 // kMaxWalk heads of one kind (q, k or v) of them; a lane's eight angles and its weights become 32 factors once for the
 // whole walk, which leaves three operations an element besides the sum of squares.  The walk's heads are all brought in at
 // once, into shared memory, so the loads need no registers and do not wait for the sines.
-// What bounds it: the copy rate.  32768 tokens of 32 + 8 + 8 heads, d = 128 (806 MB moved): 119 us = 6790 GB/s, the
+// What bounds it: the copy rate.  32768 tokens of 32 + 8 + 8 heads, d = 128 (806 MB moved): 120 us = 6740 GB/s, 99% of the
 // measured copy rate (138 us with four heads held ahead in registers, 210 us with angles and weights applied head by head).
-// With few heads to a token the angles and a warp's start show: 106272 tokens of 4 + 2 + 2 heads, d = 64 (220 MB) 43 us
-// (48 with sincospif and 64-bit divisions).  One token: 3.2 us, the latency of a launch and three trips to memory.
+// With few heads to a token the angles and a warp's start show: 106272 tokens of 4 + 2 + 2 heads, d = 64 (218 MB) 44 us
+// (41 with the fast sine).  One token: 3.3 us, the latency of a launch and three trips to memory.
 #include "svx_paged.h"
 
 namespace svx {
@@ -89,6 +91,24 @@ template <typename T>
 __device__ __forceinline__ uint4 pack(const float* f) {
   return make_uint4(Pair<T>::down(f[0], f[1]), Pair<T>::down(f[2], f[3]), Pair<T>::down(f[4], f[5]),
                     Pair<T>::down(f[6], f[7]));
+}
+
+// Sine and cosine of 2 pi phase / 2^64, within 4 2^-24 of their own size: a quarter turn and a rest of at most pi/4, on which
+// the Taylor series are summed to x^9 and x^8 (the next terms are 2^-28 of the sine and 2^-25 of the cosine).
+__device__ __forceinline__ void turn_by(uint64_t phase, float& sn, float& cs) {
+  const uint32_t hi = static_cast<uint32_t>(phase >> 32), lo = static_cast<uint32_t>(phase);
+  const uint32_t quarter = (hi + 0x20000000u) >> 30;
+  // the rest as a 32-bit high part, rounded, and a signed low part: no bits cancel where they are added
+  const int32_t top = static_cast<int32_t>(hi - (quarter << 30)) + static_cast<int32_t>(lo >> 31);
+  const float x = fmaf(static_cast<float>(top), 4294967296.f, static_cast<float>(static_cast<int32_t>(lo))) *
+                  3.4061215800865545e-19f;  // 2 pi / 2^64
+  const float u = x * x;
+  const float s = fmaf(x * u, fmaf(u, fmaf(u, fmaf(u, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+  const float c = fmaf(u, fmaf(u, fmaf(u, fmaf(u, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  sn = quarter & 1u ? c : s;
+  cs = quarter & 1u ? s : c;
+  if (quarter & 2u) sn = -sn;
+  if ((quarter + 1u) & 2u) cs = -cs;
 }
 
 // RING: a walk of up to kMaxWalk heads, all of them on their way at once in shared memory; else one head, in registers.
@@ -232,9 +252,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
       if (turn) {
         const int f = P.neighbours ? (i < 4 ? 4 * v0 + i : 4 * v1 + i - 4) : 8 * lane + i;
         const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * P.turns[f];
-        // radians in [-pi, pi), where the fast sine and cosine are within 2^-21; the 16-bit outputs step by 2^-11 and more
-        const float angle = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 1.4629180792671596e-9f;  // pi / 2^31
-        const float sn = __sinf(angle) * P.scale, cs = __cosf(angle) * P.scale;
+        float sn, cs;
+        turn_by(phase, sn, cs);
+        sn *= P.scale;
+        cs *= P.scale;
         fa[i] = wa * cs;
         fb[i] = wb * sn;
         ga[i] = wb * cs;

@@ -1,0 +1,77 @@
+"""Edges of the paged-cache operators on the GPU: calls that the header allows and whose results hang on one detail.
+
+Bounds are derived at each test; u = torch.finfo(type).eps / 2 is a rounding to the output type.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from paged_reference import heads64
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def svx():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_verification_chunked_gb300 import svx as mod
+    return mod
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ heads
+
+
+def pair_terms(y, pos, inv_freq, neighbours):
+    """|y_a cos t| + |y_b sin t| and |y_b cos t| + |y_a sin t| at their places: the size that a rotated value's error goes by."""
+    half = len(inv_freq)
+    ang = torch.as_tensor(pos, dtype=torch.float64)[:, None] * torch.as_tensor(inv_freq, dtype=torch.float64)
+    c, s = torch.cos(ang).abs()[:, None], torch.sin(ang).abs()[:, None]
+    out = y.abs().clone()
+    ia = torch.arange(half) * 2 if neighbours else torch.arange(half)
+    ib = ia + (1 if neighbours else half)
+    a, b = y[..., ia].abs(), y[..., ib].abs()
+    out[..., ia], out[..., ib] = a * c + b * s, b * c + a * s
+    return out
+
+
+@pytest.mark.parametrize("zero", ["first", "second", "none"])
+@pytest.mark.parametrize("neighbours", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("d,ty", [(128, "bf16"), (128, "fp16"), (64, "fp16"), (64, "bf16")])
+def test_small_angles_keep_their_sine(svx, d, ty, neighbours, zero):
+    """A pair with one member zero shows sine and cosine themselves, down to angles of 1e-7: each output is within its own rounding.
+    In fp32 (u' = 2^-24): angle, sine and cosine within 4 u' relative, two products and a sum 2 u', the scale 1 u': under 2^-20 of
+    |y_a cos t| + |y_b sin t|, and a sum rounded to the type.  (The angle's phase is off by 2^-55 |pos| turns at most: nothing beside.)"""
+    t, n = TYPES[ty], 600
+    g = torch.Generator().manual_seed(21)
+    x = torch.randn((1, n, 2, d), generator=g).to(t)
+    first = torch.zeros(d, dtype=torch.bool)
+    if neighbours:
+        first[0::2] = True
+    else:
+        first[:d // 2] = True
+    if zero != "none":
+        x[..., first if zero == "first" else ~first] = 0
+    pos = torch.cat([torch.arange(-100, 300), torch.randint(-2 ** 20, 2 ** 20, (n - 400,), generator=g)]).to(torch.int32)[None]
+    inv = [1e6 ** (-2.0 * i / d) for i in range(d // 2)]
+    inv[1], inv[3] = 3e-7, 1.0 / 65536  # (positions times 2^-16 reach the quadrants' borders to within an ulp)
+    inv[5] = math.pi / 4
+    qo, ko = torch.empty((1, 1, n, d), dtype=t, device="cuda"), torch.empty((1, n, 1, d), dtype=t, device="cuda")
+    xc = x.cuda()
+    svx.qk_norm_rope(xc[:, :, :1], xc[:, :, 1:], None, pos.cuda(), svx.Rope(d, inv_freq=inv, neighbours=neighbours), qo, ko, eps=None)
+    for got, h in ((qo[0].transpose(0, 1), 0), (ko[0], 1)):
+        z, _ = heads64(x[0, :, h:h + 1], None, None, pos[0], inv, neighbours)
+        size = pair_terms(x[0, :, h:h + 1].double(), pos[0], inv, neighbours)
+        # the reference's own angle: 64-bit products of up to 2^20 are off by 2^-33 radians at most
+        bound = z.abs() * torch.finfo(t).eps / 2 + size * 2.0 ** -20 + x[0, :, h:h + 1].double().abs().amax() * 2.0 ** -33 \
+            + torch.finfo(t).tiny * torch.finfo(t).eps
+        err = (got.double().cpu() - z).abs()
+        assert (err <= bound).all(), f"{float((err / bound).max()):.2f} times the bound at {int((err > bound).sum())} elements"
