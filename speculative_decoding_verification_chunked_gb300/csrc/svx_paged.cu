@@ -97,6 +97,23 @@ svx_status paged_view(const svx_pages* c, int32_t n_req, PageView* out) {
   return SVX_OK;
 }
 
+// f / (2 pi) mod 1 in units of 2^-64, rounded down (a negative one up), for |f| < 2^20: whole turns drop out, since positions
+// are whole numbers.  f = m 2^e with a whole m < 2^53, so m times 1 / (2 pi) in 128 bits, shifted, is the fraction to its last
+// bit; a product in double has lost it for the fast pairs (f = 1e5 at position 2^31: 2^-9 of a turn).
+static uint64_t turn_fraction(double f) {
+  constexpr uint64_t kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f47d4d3770ull;  // 2^128 / (2 pi)
+  int e = 0;
+  const double scaled = std::frexp(std::fabs(f), &e);
+  const uint64_t m = static_cast<uint64_t>(std::ldexp(scaled, 53));
+  // f = m 2^(e - 53): shift the product's 128 fraction bits to 64 and by the exponent
+  const int shift = 64 + 53 - e;
+  if (shift >= 192) return 0;  // below 2^-64 of a turn (the product has 181 bits)
+  const unsigned __int128 low = static_cast<unsigned __int128>(m) * kLow;
+  const unsigned __int128 high = static_cast<unsigned __int128>(m) * kHigh + (low >> 64);  // in units of 2^64
+  const uint64_t turns = static_cast<uint64_t>(high >> (shift - 64));  // shift - 64 = 53 - e >= 33
+  return f < 0 ? 0 - turns : turns;
+}
+
 }  // namespace svx
 
 extern "C" svx_status svx_rope_init(svx_rope* rope, int32_t rot_dim, int32_t neighbours, const double* inv_freq,
@@ -111,11 +128,7 @@ extern "C" svx_status svx_rope_init(svx_rope* rope, int32_t rot_dim, int32_t nei
   for (int i = 0; i < rot_dim / 2; ++i) {
     if (!(std::fabs(inv_freq[i]) < 1048576.0))
       return paged_fail(SVX_ERR_INVALID_ARG, "inv_freq[%d] must be finite, below 2^20 in magnitude", i);
-    // The fraction of a turn per position: whole turns drop out, since positions are whole numbers.
-    const double turns = inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    const double frac = turns - std::floor(turns);              // [0, 1)
-    const double scaled = std::ldexp(frac, 64);                 // exact: a power of two
-    r.turns[i] = scaled >= 18446744073709551616.0 ? 0u : static_cast<uint64_t>(scaled);
+    r.turns[i] = svx::turn_fraction(inv_freq[i]);
   }
   r.scale = scale;
   r.rot_dim = rot_dim;
