@@ -949,14 +949,17 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   const svx::Span q_span = {q, n_rows * row}, o_span = {o, n_rows * row}, lse_span = {lse, n_rows * 4}, out_span = {acc_out, acc},
                   in_span = {acc_in == acc_out ? nullptr : acc_in, acc}, len_span = {len, per_req},
                   table_span = {cache->table, per_req * cache->max_pages};
-  if (svx::any_overlap({o_span, lse_span, out_span, {cache->status, 4}}, {q_span, len_span, table_span, in_span}))
+  // (a strided pool takes what lies between its rows along)
+  const size_t pool = static_cast<size_t>(p.pages.extent) * 2;
+  const svx::Span k_span = {cache->k, pool}, v_span = {cache->v, pool};
+  if (svx::any_overlap({o_span, lse_span, out_span, {cache->status, 4}}, {q_span, len_span, table_span, in_span, k_span, v_span}))
     return paged_fail(SVX_ERR_INVALID_ARG, "an output overlaps an input or another output (acc_out may be acc_in)");
   svx::Sizes z = {};
   st = svx::sizes(cache, n_req, n_q_heads, max_len, acc_in != nullptr, &z);
   if (st != SVX_OK) return st;
   if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(z.total))
     return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", z.total);
-  if (svx::any_overlap({{workspace, z.total}}, {q_span, o_span, lse_span, in_span, out_span, len_span, table_span, {cache->status, 4}}))
+  if (svx::any_overlap({{workspace, z.total}}, {q_span, o_span, lse_span, in_span, out_span, len_span, table_span, k_span, v_span, {cache->status, 4}}))
     return paged_fail(SVX_ERR_INVALID_ARG, "the workspace overlaps another buffer");
   svx::PagedDevice dev(cache->device);
   if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", cache->device);

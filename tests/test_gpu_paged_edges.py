@@ -75,3 +75,30 @@ def test_small_angles_keep_their_sine(svx, d, ty, neighbours, zero):
             + torch.finfo(t).tiny * torch.finfo(t).eps
         err = (got.double().cpu() - z).abs()
         assert (err <= bound).all(), f"{float((err / bound).max()):.2f} times the bound at {int((err > bound).sum())} elements"
+
+
+# ------------------------------------------------------------------ one-token attention
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_decode_refuses_a_workspace_in_the_pools(svx, which):
+    """The workspace's size needs the device's SM count, so this is seen here: a workspace that begins in a pool, ends in it, or lies
+    beside it."""
+    n = 4 * 16 * 2 * 64
+    need = svx.ctypes.c_int64(0)
+    arena = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    mine = arena[1 << 23:(1 << 23) + 2 * n].view(torch.bfloat16).view(4, 16, 2, 64)
+    other = torch.zeros_like(mine)
+    cache = svx.PagedCache(*((mine, other) if which == "k" else (other, mine)))
+    q, o = (torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse, table, lens = torch.zeros((1, 4, 1), device="cuda"), i32([[0, 1, 2]]), i32([40])
+    p = svx.Pages.from_buffer_copy(cache._pages)
+    p.table, p.max_pages = table.data_ptr(), 3
+    assert svx.lib.svx_paged_decode_workspace(svx.ctypes.byref(p), 1, 4, 0, 0, svx.ctypes.byref(need)) == svx.OK
+    size = (need.value + 255) // 256 * 256
+    for at in ((1 << 23), (1 << 23) + 2 * n - 256, (1 << 23) - size + 256):
+        with pytest.raises(svx.SvxError, match="overlap"):
+            cache.decode(q, table, lens, o, lse, workspace=arena[at:at + size])
+    for at in ((1 << 23) + 2 * n, (1 << 23) - size):
+        cache.decode(q, table, lens, o, lse, workspace=arena[at:at + size])
+    assert not cache.check()

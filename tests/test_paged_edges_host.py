@@ -1,5 +1,6 @@
 """Edges of the paged-cache entry points without a GPU: exact phases, and refusals that come before the first CUDA call (fake addresses,
 which no call may follow)."""
+import ctypes
 import os
 from fractions import Fraction
 
@@ -33,3 +34,45 @@ def test_turns_are_exact_for_every_frequency(svx):
             for pos in (2 ** 31 - 1, -2 ** 31, 131071):
                 phase = Fraction((pos * r.table.turns[i]) % (1 << 64), 1 << 64) - pos * exact
                 assert min(phase % 1, 1 - phase % 1) <= Fraction(1, 1 << 33)
+
+
+# ------------------------------------------------------------------ buffers that meet the pools
+
+# Addresses that no refused call may read; 256-byte aligned.
+K, V, TABLE, STATUS, Q, O, LSE, LEN, ACC, ACC2, WS, POS, NEXT, POS2, LEN2, KIN, VIN, NORM = (0x100000000 * (i + 1) for i in range(18))
+POOL = 2 * (9 * 4096 + 15 * 256 + 128 + 128)  # bytes from the first row of pages() to behind its last
+
+
+def pages(svx, **kw):
+    f = dict(k=K, v=V, table=TABLE, status=STATUS, page_stride=16 * 2 * 128, tok_stride=2 * 128, head_stride=128, n_pages=10,
+             page_size=16, max_pages=4, n_kv_heads=2, head_dim=128, dtype=0, device=0, flags=0, pad=0)
+    f.update(kw)
+    return svx.Pages(*[f[n] for n, _ in svx.Pages._fields_])
+
+
+def heads(svx, **kw):
+    f = dict(q=Q, k=KIN, v=VIN, q_stride=1024, k_stride=1024, v_stride=1024, q_norm=None, k_norm=None, pos=POS, n_new=None, status=None,
+             n_req=2, n_tok=3, n_q_heads=4, n_kv_heads=2, head_dim=128, dtype=0, device=0, eps=1e-6, flags=0, pad=0)
+    f.update(kw)
+    return svx.Heads(*[f[n] for n, _ in svx.Heads._fields_])
+
+
+def refused(svx, status, words=("overlap", "share memory")):
+    return status == svx.ERR_INVALID_ARG and any(w in svx.lib.svx_last_error(None).decode() for w in words)
+
+
+def decode(svx, cache=None, q=Q, ln=LEN, o=O, lse=LSE, a=ACC, b=ACC2, ws=WS, scale=0.0):
+    c = cache or pages(svx)
+    return svx.lib.svx_paged_decode(ctypes.byref(c), 2, 4, q, ln, 0, scale, o, lse, a, b, ws, 1 << 30, None)
+
+
+@pytest.mark.parametrize("pool", [K, V], ids=["k", "v"])
+def test_decode_refuses_outputs_in_the_pools(svx, pool):
+    row, meta = 2 * 4 * 128 * 2, 2 * 2 * 64 * 4
+    for kw in (dict(o=pool), dict(o=pool + POOL - 16), dict(o=pool - row + 16), dict(lse=pool), dict(lse=pool + POOL - 4), dict(b=pool),
+               dict(a=pool, b=pool), dict(b=pool - meta + 4),
+               dict(cache=pages(svx, status=pool + 64))):
+        assert refused(svx, decode(svx, **kw)), kw
+    for kw in (dict(o=pool + POOL), dict(o=pool - row), dict(lse=pool + POOL), dict(b=pool + POOL), dict(q=pool),
+               dict(cache=pages(svx, k=V))):  # (one buffer read twice is no overlap)
+        assert not refused(svx, decode(svx, **kw)), kw
