@@ -566,14 +566,23 @@ extern "C" svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, con
   const size_t per_req = static_cast<size_t>(n_req) * 4;
   if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(z.total))
     return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", z.total);
+  // The pools are written too (a strided one takes what lies between its rows along).
+  const size_t pool = static_cast<size_t>(p.pages.extent) * 2;
+  const svx::Span k_span = {cache->k, pool}, v_span = {cache->v, pool}, next_span = {next_pos, per_req},
+                  table_span = {cache->table, per_req * cache->max_pages};
+  auto meets_pool = [&](const svx::Span& s) { return svx::any_overlap({s}, {k_span, v_span}); };
   if (svx::any_overlap({{acc_out, meta}, {pos_out, meta}, {len_out, per_req}, {workspace, z.total}, {cache->status, 4}},
                        {{acc_in == acc_out ? nullptr : acc_in, meta},
                         {pos_in == pos_out ? nullptr : pos_in, meta},
                         {len == len_out ? nullptr : len, per_req},
-                        {next_pos, per_req},
-                        {cache->table, per_req * cache->max_pages}}))
-    return paged_fail(SVX_ERR_INVALID_ARG, "an output or the workspace overlaps an input or another output (acc_out, pos_out and "
-                                           "len_out may be their inputs)");
+                        next_span,
+                        table_span,
+                        k_span,
+                        v_span}) ||
+      meets_pool({acc_in, meta}) || meets_pool({pos_in, meta}) || meets_pool({len, per_req}) || meets_pool(next_span) ||
+      meets_pool(table_span))
+    return paged_fail(SVX_ERR_INVALID_ARG, "an output or the workspace overlaps an input, another output or the pools "
+                                           "(acc_out, pos_out and len_out may be their inputs)");
   svx::PagedDevice dev(cache->device);
   if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", cache->device);
   const void* ptrs[] = {cache->k, cache->v, cache->table, cache->status, len,     next_pos, acc_in,

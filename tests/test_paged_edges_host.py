@@ -76,3 +76,21 @@ def test_decode_refuses_outputs_in_the_pools(svx, pool):
     for kw in (dict(o=pool + POOL), dict(o=pool - row), dict(lse=pool + POOL), dict(b=pool + POOL), dict(q=pool),
                dict(cache=pages(svx, k=V))):  # (one buffer read twice is no overlap)
         assert not refused(svx, decode(svx, **kw)), kw
+
+
+def evict(svx, cache=None, ln=LEN, nxt=NEXT, a=ACC, q=POS, a2=ACC2, q2=POS2, l2=LEN2, ws=WS):
+    c = cache or pages(svx)
+    return svx.lib.svx_paged_evict(ctypes.byref(c), 2, ln, 0, 8, 1, 2, nxt, a, q, a2, q2, l2, ws, 1 << 30, None)
+
+
+@pytest.mark.parametrize("pool", [K, V], ids=["k", "v"])
+def test_evict_refuses_buffers_in_the_pools(svx, pool):
+    """Eviction writes the pools: neither its outputs, its workspace nor its inputs may lie there."""
+    meta = 2 * 2 * 64 * 4
+    for kw in (dict(a2=pool), dict(q2=pool + POOL - 4), dict(l2=pool), dict(l2=pool - 4), dict(ws=pool), dict(ws=pool + POOL - 256),
+               dict(ws=pool - 256), dict(a=pool), dict(a=pool - meta + 4), dict(q=pool + 4096), dict(ln=pool), dict(nxt=pool + POOL - 4),
+               dict(a=pool, a2=pool), dict(q=pool, q2=pool), dict(ln=pool, l2=pool), dict(cache=pages(svx, table=pool + 64)),
+               dict(cache=pages(svx, status=pool + POOL - 4))):
+        assert refused(svx, evict(svx, **kw)), kw
+    for kw in (dict(), dict(a2=pool + POOL), dict(l2=pool - 8), dict(ws=pool + POOL), dict(a=pool - meta), dict(a2=ACC, q2=POS, l2=LEN)):
+        assert not refused(svx, evict(svx, **kw)), kw
