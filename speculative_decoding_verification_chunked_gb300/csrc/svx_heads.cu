@@ -389,9 +389,10 @@ svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages*
   if (cache) {  // (the two pools may be interleaved)
     const size_t meta = static_cast<size_t>(in->n_req) * in->n_kv_heads * p.pages.cap * 4;
     const Span kp = span(cache->k, p.pages.extent), vp = span(cache->v, p.pages.extent);
+    const Span first = {start, per_req}, table = {cache->table, per_req * cache->max_pages};
     bad = any_overlap({qo, {acc, meta}, {slot_pos, meta}, {cache->status, 4}},
-                      {qi, ki, vi, kp, vp, wq, wk, pos, n_new, {start, per_req}, {cache->table, per_req * cache->max_pages}}) ||
-          any_overlap({kp}, {qi, ki, vi}) || any_overlap({vp}, {qi, ki, vi});
+                      {qi, ki, vi, kp, vp, wq, wk, pos, n_new, first, table});
+    for (const Span& pool : {kp, vp}) bad = bad || any_overlap({pool}, {qi, ki, vi, wq, wk, pos, n_new, first, table});
   } else {
     bad = any_overlap({qo, span(k_out, tokens * kv_row), span(v_out, tokens * kv_row), {in->status, 4}},
                       {qi, ki, vi, wq, wk, pos, n_new});

@@ -94,3 +94,22 @@ def test_evict_refuses_buffers_in_the_pools(svx, pool):
         assert refused(svx, evict(svx, **kw)), kw
     for kw in (dict(), dict(a2=pool + POOL), dict(l2=pool - 8), dict(ws=pool + POOL), dict(a=pool - meta), dict(a2=ACC, q2=POS, l2=LEN)):
         assert not refused(svx, evict(svx, **kw)), kw
+
+
+def append(svx, cache=None, start=LEN, q_out=O, acc=ACC, pos=POS2, **kw):
+    c, rope = cache or pages(svx), svx.Rope(128)
+    return svx.lib.svx_paged_append(ctypes.byref(heads(svx, **kw)), ctypes.byref(rope.table), ctypes.byref(c), start, q_out, acc, pos, None)
+
+
+@pytest.mark.parametrize("pool", [K, V], ids=["k", "v"])
+def test_append_refuses_buffers_in_the_pools(svx, pool):
+    inputs = 2 * (5 * 1024 + 512)
+    for kw in (dict(pos=pool), dict(acc=pool + POOL - 4), dict(q_out=pool), dict(start=pool), dict(start=pool - 4), dict(q_norm=pool + 256),
+               dict(k_norm=pool + POOL - 16), dict(n_new=pool), dict(q=pool), dict(k=pool + POOL - 16), dict(v=pool - 16),
+               dict(cache=pages(svx, table=pool)), dict(cache=pages(svx, status=pool))):
+        assert refused(svx, append(svx, **kw)), kw
+    h = heads(svx, pos=pool + 1024)  # (the tokens' positions, an input)
+    assert refused(svx, svx.lib.svx_paged_append(ctypes.byref(h), ctypes.byref(svx.Rope(128).table), ctypes.byref(pages(svx)), LEN, O, ACC, POS2,
+                                                 None))
+    for kw in (dict(), dict(start=pool + POOL), dict(start=pool - 8), dict(q_norm=pool - 256), dict(q=pool + POOL), dict(q=pool - inputs)):
+        assert not refused(svx, append(svx, **kw)), kw
