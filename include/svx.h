@@ -563,7 +563,8 @@ typedef struct {
 /* q and k heads: x_i * w_i / sqrt(mean(x^2) + eps), then the rotation; v heads: as they are.  All in fp32,
  * rounded once.  q_out [n_req][n_q_heads][n_tok][head_dim] and k_out, v_out [n_req][n_tok][n_kv_heads][head_dim]
  * are what svx_round_begin and svx_candidate_attn take (n_tok = n_query).  v and v_out may both be NULL.  Rows
- * of tokens past n_new[b] are left as they were.  Outputs must not overlap inputs or one another. */
+ * of tokens past n_new[b] are left as they were.  Outputs must not overlap inputs or one another (a strided input or pool
+ * counts whole, from its first element to its last, in this and the following calls). */
 svx_status svx_qk_norm_rope(const svx_heads* in, const svx_rope* rope, void* q_out, void* k_out, void* v_out,
                             void* stream);
 
@@ -571,7 +572,9 @@ svx_status svx_qk_norm_rope(const svx_heads* in, const svx_rope* rope, void* q_o
  * at page * page_stride + slot * tok_stride + head * head_stride elements (strides multiples of 8, rows of
  * head_dim contiguous, pointers 16-byte aligned): [page][slot][head][d] and [page][head][slot][d] alike.  Slot t
  * of request b is slot t mod page_size of page table[b][t / page_size]; entries behind a request's length
- * are not read.  max_pages * page_size < 2^31, n_pages < 2^31. */
+ * are not read.  max_pages * page_size < 2^31, n_pages < 2^31.  k and v may be interleaved, with rows apart: append and eviction
+ * refuse pools of which two rows share memory, or whose strides do not nest (each at least the span of the smaller ones'
+ * dimensions); append refuses k == v too. */
 typedef struct {
   void* k;
   void* v;
@@ -590,7 +593,7 @@ typedef struct {
 /* svx_qk_norm_rope with K and V going into the cache: token j of request b becomes slot start[b] + j (device
  * int32[n_req]).  acc (device float [n_req][n_kv_heads][max_pages * page_size], or NULL) is set to 0 and slot_pos
  * (int32, the same shape, or NULL) to the token's position at the new slots.  Pages written must not be
- * shared by two of the call's slots.  v is required. */
+ * shared by two of the call's slots.  v is required.  No other buffer may lie in the pools. */
 svx_status svx_paged_append(const svx_heads* in, const svx_rope* rope, const svx_pages* cache, const int32_t* start,
                             void* q_out, float* acc, int32_t* slot_pos, void* stream);
 
@@ -607,7 +610,7 @@ svx_status svx_paged_decode_workspace(const svx_pages* cache, int32_t n_req, int
  * must be finite; what lies behind a request's length is not used, whatever it holds.
  * acc_in, acc_out (device float [n_req][n_kv_heads][max_pages * page_size], or both NULL): acc_out[t] =
  * acc_in[t] + the sum over the KV head's query heads of slot t's softmax weight, t < len[b]; the rest is left as
- * it was.  They may be one buffer; otherwise outputs and workspace must not overlap inputs or one another.  With weights max_len is at most 134,215,680.  workspace: device, 256-byte aligned; contents need no set-up. */
+ * it was.  They may be one buffer; otherwise outputs and workspace must not overlap inputs, the pools or one another.  With weights max_len is at most 134,215,680.  workspace: device, 256-byte aligned; contents need no set-up. */
 svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, int32_t n_q_heads, const void* q, const int32_t* len,
                             int64_t max_len, float scale, void* o, float* lse, const float* acc_in, float* acc_out,
                             void* workspace, int64_t workspace_bytes, void* stream);
@@ -626,7 +629,8 @@ svx_status svx_paged_evict_workspace(const svx_pages* cache, int32_t n_req, int6
  * their first n entries written (the rest is left as it was).  Every other slot keeps its place, so slots are in no
  * order of position; attention does not depend on it.  len_out[b] = n.  len, next_pos, len_out: device
  * int32[n_req]; acc, pos: device [n_req][n_kv_heads][max_pages * page_size]; acc_out may be acc_in, pos_out pos_in and
- * len_out len; otherwise outputs and workspace must not overlap inputs or one another.  1 <= budget, sink, recent >= 0, sink + recent <= budget.  max_len: as svx_paged_decode, at most
+ * len_out len; otherwise outputs and workspace must not overlap inputs or one another, and no buffer may lie in
+ * the pools.  1 <= budget, sink, recent >= 0, sink + recent <= budget.  max_len: as svx_paged_decode, at most
  * SVX_EVICT_MAX_LEN (0: the smaller of that and max_pages * page_size).  Pages below the lengths must belong to
  * one request each: a page shared by two requests would be rewritten for both. */
 svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, const int32_t* len, int64_t max_len, int32_t budget,

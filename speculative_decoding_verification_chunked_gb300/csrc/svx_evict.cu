@@ -583,6 +583,8 @@ extern "C" svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, con
       meets_pool(table_span))
     return paged_fail(SVX_ERR_INVALID_ARG, "an output or the workspace overlaps an input, another output or the pools "
                                            "(acc_out, pos_out and len_out may be their inputs)");
+  // (one buffer for K and V moves its rows twice, to the same places: no harm)
+  if (svx::pools_collide(cache, false)) return paged_fail(SVX_ERR_INVALID_ARG, "rows of the K and V pages share memory");
   svx::PagedDevice dev(cache->device);
   if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", cache->device);
   const void* ptrs[] = {cache->k, cache->v, cache->table, cache->status, len,     next_pos, acc_in,

@@ -373,6 +373,7 @@ svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages*
         cache->device != in->device)
       return paged_fail(SVX_ERR_INVALID_ARG, "heads and cache differ in KV heads, head_dim, dtype or device");
     if (!start || !has_v) return paged_fail(SVX_ERR_INVALID_ARG, "start and v are required");
+    if (pools_collide(cache, true)) return paged_fail(SVX_ERR_INVALID_ARG, "rows of the K and V pages share memory");
     p.paged = 1;
     p.status = cache->status;
   } else {

@@ -97,6 +97,48 @@ svx_status paged_view(const svx_pages* c, int32_t n_req, PageView* out) {
   return SVX_OK;
 }
 
+namespace {
+
+// True if a row that begins `off` elements behind a row of the pool shares elements with one of the first `dims` dimensions'
+// rows (strides ascending, each at least the span of those before it, so that only the two nearest multiples of the largest
+// can come within reach).
+bool meets_a_row(int64_t off, const int64_t* stride, const int64_t* n, int dims, int64_t d) {
+  if (dims == 0) return off < d && -off < d;
+  const int64_t s = stride[dims - 1], most = n[dims - 1] - 1;
+  int64_t a = off / s;
+  if (off < 0 && a * s != off) --a;  // rounded down
+  for (int i = 0; i < 2; ++i, ++a)
+    if (a <= most && -a <= most && meets_a_row(off - a * s, stride, n, dims - 1, d)) return true;
+  return false;
+}
+
+}  // namespace
+
+bool pools_collide(const svx_pages* c, bool same_pool_too) {
+  int64_t stride[3], n[3];
+  int dims = 0;
+  const int64_t s[3] = {c->page_stride, c->tok_stride, c->head_stride}, count[3] = {c->n_pages, c->page_size, c->n_kv_heads};
+  for (int i = 0; i < 3; ++i) {
+    if (count[i] == 1) continue;
+    int at = dims++;
+    for (; at > 0 && stride[at - 1] > s[i]; --at) {
+      stride[at] = stride[at - 1];
+      n[at] = n[at - 1];
+    }
+    stride[at] = s[i];
+    n[at] = count[i];
+  }
+  int64_t span = c->head_dim;
+  for (int i = 0; i < dims; ++i) {
+    if (stride[i] < span) return true;  // rows of one pool overlap
+    span += (n[i] - 1) * stride[i];
+  }
+  if (c->k == c->v) return same_pool_too;
+  // (16-byte aligned pointers: whole elements apart)
+  const int64_t apart = (static_cast<const char*>(c->v) - static_cast<const char*>(c->k)) / 2;
+  return apart < span && -apart < span && meets_a_row(apart, stride, n, dims, c->head_dim);
+}
+
 // f / (2 pi) mod 1 in units of 2^-64, rounded down (a negative one up), for |f| < 2^20: whole turns drop out, since positions
 // are whole numbers.  f = m 2^e with a whole m < 2^53, so m times 1 / (2 pi) in 128 bits, shifted, is the fraction to its last
 // bit; a product in double has lost it for the fast pairs (f = 1e5 at position 2^31: 2^-9 of a turn).

@@ -56,6 +56,9 @@ __device__ __forceinline__ int64_t slot_offset(const PageView& p, int32_t page_i
 svx_status paged_fail(svx_status st, const char* fmt, ...);
 // Checks a svx_pages and fills the view (with n_req rows in the table).  SVX_OK or the failure reported.
 svx_status paged_view(const svx_pages* c, int32_t n_req, PageView* out);
+// For calls that write the pools: true if two slots' rows share memory, of one pool (strides that fold onto each other) or of
+// K and V; same_pool_too: also if K and V are one buffer.  The pools may be interleaved.
+bool pools_collide(const svx_pages* c, bool same_pool_too);
 // True for device (or managed) memory of `device`.
 bool on_device(const void* p, int device);
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -2,6 +2,7 @@
 which no call may follow)."""
 import ctypes
 import os
+import random
 from fractions import Fraction
 
 import pytest
@@ -113,3 +114,57 @@ def test_append_refuses_buffers_in_the_pools(svx, pool):
                                                  None))
     for kw in (dict(), dict(start=pool + POOL), dict(start=pool - 8), dict(q_norm=pool - 256), dict(q=pool + POOL), dict(q=pool - inputs)):
         assert not refused(svx, append(svx, **kw)), kw
+
+
+def test_pools_whose_rows_share_memory_are_refused_where_they_are_written(svx):
+    """K and V may be interleaved in one tensor, in any way that keeps their rows apart; rows that coincide, in part or whole, of the two
+    pools or of one, are refused by append and eviction.  One buffer read as both (decode) is fine, and so is moving its rows."""
+    page, tok = 16 * 2 * 128, 2 * 128
+
+    def both(**kw):
+        c = pages(svx, **kw)
+        a, e, r = append(svx, cache=c), evict(svx, cache=c), decode(svx, cache=c)
+        return (a == svx.ERR_INVALID_ARG, e == svx.ERR_INVALID_ARG, r == svx.ERR_INVALID_ARG)
+    apart = [dict(v=K + 2 * 128, head_stride=256, tok_stride=512, page_stride=16 * 512),          # [page][slot][head][K, V][d]
+             dict(v=K + 2 * 2 * 128, tok_stride=512, page_stride=16 * 512),                        # [page][slot][K, V][head][d]
+             dict(v=K + 2 * page, page_stride=2 * page),                                           # [page][K, V][slot][head][d]
+             dict(v=K + 2 * 10 * page), dict(v=K - 2 * 10 * page),                                 # [K, V][page]..
+             dict(v=K - 2 * page, page_stride=2 * page),                                           # V first
+             dict(head_stride=16 * 128, tok_stride=128, v=K + 2 * page, page_stride=2 * page),     # heads outside the slots
+             dict(page_stride=128, tok_stride=10 * 128, head_stride=16 * 10 * 128)]                # pages innermost
+    for kw in apart:
+        assert both(**kw) == (False, False, False), kw
+    collide = [dict(v=K + 16), dict(v=K - 16), dict(v=K + 2 * 128 * 2), dict(v=K + 2 * page), dict(v=K + 2 * (9 * page)), dict(v=K + POOL - 16),
+               dict(v=K - POOL + 16), dict(v=K + 2 * page - 16, page_stride=2 * page), dict(v=K + 2 * page + 16, page_stride=2 * page),
+               dict(v=K + 2 * 128 + 16, head_stride=256, tok_stride=512, page_stride=16 * 512),
+               dict(tok_stride=128), dict(page_stride=page - 8), dict(page_stride=tok), dict(head_stride=136, tok_stride=256)]
+    for kw in collide:
+        assert both(**kw) == (True, True, False), kw
+    assert both(v=K) == (True, False, False)
+    # against all pairs of rows, at small sizes
+    rng = random.Random(5)
+    seen = [0, 0]
+    for _ in range(300):
+        n = [rng.randint(1, 3) for _ in range(3)]
+        s = [64 + 8 * rng.randrange(0, 60) for _ in range(3)]
+        if rng.random() < 0.8:  # a nested layout, with gaps or without, in any order
+            span, order = 64, rng.sample(range(3), 3)
+            for i in order:
+                s[i] = span + 8 * rng.choice([0, 0, 8, 24])
+                span = s[i] * n[i]
+        off = 8 * rng.randrange(-90, 90)
+        kw = dict(v=K + 2 * off, n_pages=n[0], page_size=n[1], n_kv_heads=n[2], page_stride=s[0], tok_stride=s[1], head_stride=s[2], head_dim=64,
+                  max_pages=4)
+        begin = [a * s[0] + b * s[1] + c * s[2] for a in range(n[0]) for b in range(n[1]) for c in range(n[2])]
+        own = any(abs(x - y) < 64 for i, x in enumerate(begin) for y in begin[:i])
+        cross = off != 0 and any(abs(off + x - y) < 64 for x in begin for y in begin)
+        got = evict(svx, cache=pages(svx, **kw)) == svx.ERR_INVALID_ARG
+        if own or cross:
+            assert got, kw
+        nested, span = True, 64
+        for stride, count in sorted((x, y) for x, y in zip(s, n) if y > 1):
+            nested, span = nested and stride >= span, span + (count - 1) * stride
+        if nested:  # (where strides do not nest, rows that happen to lie apart are refused too)
+            assert got == cross, kw
+        seen[got] += 1
+    assert min(seen) > 40
