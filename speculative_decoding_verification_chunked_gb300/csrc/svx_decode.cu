@@ -941,8 +941,10 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   if (st != SVX_OK) return st;
   if ((acc_in == nullptr) != (acc_out == nullptr))
     return paged_fail(SVX_ERR_INVALID_ARG, "give both acc_in and acc_out, or neither");
-  if (!q || !o || !lse || !len || !svx::is_aligned(q, 16) || !svx::is_aligned(o, 16) || !svx::is_aligned(lse, 4))
+  if (!q || !o || !lse || !len || !svx::is_aligned(q, 16) || !svx::is_aligned(o, 16))
     return paged_fail(SVX_ERR_INVALID_ARG, "q, len, o and lse must be device pointers, q and o 16-byte aligned");
+  if (!svx::words_aligned({len, lse, acc_in, acc_out}))
+    return paged_fail(SVX_ERR_INVALID_ARG, "len, lse and acc must be 4-byte aligned");
   if (!(scale >= 0.f) || scale > 3.0e38f) return paged_fail(SVX_ERR_INVALID_ARG, "scale must be positive and finite, or 0");
   const size_t n_rows = static_cast<size_t>(n_req) * std::max(n_q_heads, 0), per_req = static_cast<size_t>(n_req) * 4;
   const size_t row = static_cast<size_t>(cache->head_dim) * 2, acc = per_req * p.pages.n_kv_heads * p.pages.cap;

@@ -562,6 +562,8 @@ extern "C" svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, con
     return paged_fail(SVX_ERR_INVALID_ARG, "sink and recent must be >= 0, with a sum of at most budget");
   if (!len || !next_pos || !acc_in || !pos_in || !acc_out || !pos_out || !len_out)
     return paged_fail(SVX_ERR_INVALID_ARG, "len, next_pos, acc, pos and len_out must be device pointers");
+  if (!svx::words_aligned({len, next_pos, acc_in, pos_in, acc_out, pos_out, len_out}))
+    return paged_fail(SVX_ERR_INVALID_ARG, "len, next_pos, acc, pos and len_out must be 4-byte aligned");
   const size_t meta = static_cast<size_t>(n_req) * p.pages.n_kv_heads * p.pages.cap * 4;
   const size_t per_req = static_cast<size_t>(n_req) * 4;
   if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(z.total))

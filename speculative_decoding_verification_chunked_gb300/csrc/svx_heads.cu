@@ -359,6 +359,8 @@ svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages*
       (has_v && !is_aligned(in->v, 16)))
     return paged_fail(SVX_ERR_INVALID_ARG, "q, k, v and q_out must be 16-byte aligned device pointers");
   if (!in->pos) return paged_fail(SVX_ERR_INVALID_ARG, "pos must be a device pointer");
+  if (!words_aligned({in->pos, in->n_new, in->status, start, acc, slot_pos}))
+    return paged_fail(SVX_ERR_INVALID_ARG, "pos, n_new, status, start, acc and slot_pos must be 4-byte aligned");
   if (!(in->eps >= 0.f) && !(in->eps < 0.f)) return paged_fail(SVX_ERR_INVALID_ARG, "eps is not a number");
   if (in->eps < 0.f && (in->q_norm || in->k_norm))
     return paged_fail(SVX_ERR_INVALID_ARG, "norm weights given with eps < 0 (no norms)");

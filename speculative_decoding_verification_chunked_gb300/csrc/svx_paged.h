@@ -62,6 +62,12 @@ bool pools_collide(const svx_pages* c, bool same_pool_too);
 // True for device (or managed) memory of `device`.
 bool on_device(const void* p, int device);
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// True if no pointer is off the 4-byte grid of its int32 or fp32 elements (NULL: none).
+inline bool words_aligned(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (!is_aligned(p, 4)) return false;
+  return true;
+}
 int sm_count(int device);
 // A buffer of a call; p NULL: none.
 struct Span {

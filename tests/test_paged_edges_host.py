@@ -168,3 +168,22 @@ def test_pools_whose_rows_share_memory_are_refused_where_they_are_written(svx):
             assert got == cross, kw
         seen[got] += 1
     assert min(seen) > 40
+
+
+def test_words_off_their_alignment_are_refused(svx):
+    """int32 and fp32 buffers off the 4-byte grid (the kernels' loads and stores of them would be misaligned)."""
+    def misaligned(status):
+        return status == svx.ERR_INVALID_ARG and "aligned" in svx.lib.svx_last_error(None).decode()
+    for by in (1, 2, 3):
+        for kw in (dict(ln=LEN + by), dict(lse=LSE + by), dict(a=ACC + by), dict(b=ACC2 + by), dict(a=ACC + by, b=ACC + by)):
+            assert misaligned(decode(svx, **kw)), kw
+        for kw in (dict(ln=LEN + by), dict(nxt=NEXT + by), dict(a=ACC + by), dict(q=POS + by), dict(a2=ACC2 + by), dict(q2=POS2 + by),
+                   dict(l2=LEN2 + by), dict(ln=LEN + by, l2=LEN + by)):
+            assert misaligned(evict(svx, **kw)), kw
+        for kw in (dict(start=LEN + by), dict(acc=ACC + by), dict(pos=POS2 + by), dict(n_new=NEXT + by)):
+            assert misaligned(append(svx, **kw)), kw
+        for kw in (dict(pos=POS + by), dict(n_new=NEXT + by), dict(status=STATUS + by)):
+            h = heads(svx, **kw)
+            assert misaligned(svx.lib.svx_qk_norm_rope(ctypes.byref(h), ctypes.byref(svx.Rope(128).table), O, K, V, None)), kw
+            assert "status" in kw or misaligned(svx.lib.svx_paged_append(ctypes.byref(h), ctypes.byref(svx.Rope(128).table),
+                                                                        ctypes.byref(pages(svx)), LEN, O, None, None, None)), kw
