@@ -606,7 +606,7 @@ svx_status svx_paged_decode_workspace(const svx_pages* cache, int32_t n_req, int
  * -inf) gets O = 0, LSE = -inf.  q, o [n_req][n_q_heads][head_dim] and lse [n_req][n_q_heads], device; query head
  * h reads KV head h / (n_q_heads / n_kv_heads).  len: device int32[n_req], 0 <= len[b] <= max_len.  max_len:
  * upper bound known on the host, 0 for max_pages * page_size; it sizes the launch and the workspace, so a
- * captured call stays valid for all lengths up to it.  scale: 0 means 1/sqrt(head_dim).  K and V of the slots read
+ * captured call stays valid for all lengths up to it.  scale: 0 means 1/sqrt(head_dim); below 2^128 ln 2.  K and V of the slots read
  * must be finite; what lies behind a request's length is not used, whatever it holds.
  * acc_in, acc_out (device float [n_req][n_kv_heads][max_pages * page_size], or both NULL): acc_out[t] =
  * acc_in[t] + the sum over the KV head's query heads of slot t's softmax weight, t < len[b]; the rest is left as

@@ -31,6 +31,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 
 namespace svx {
 namespace {
@@ -945,7 +946,11 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
     return paged_fail(SVX_ERR_INVALID_ARG, "q, len, o and lse must be device pointers, q and o 16-byte aligned");
   if (!svx::words_aligned({len, lse, acc_in, acc_out}))
     return paged_fail(SVX_ERR_INVALID_ARG, "len, lse and acc must be 4-byte aligned");
-  if (!(scale >= 0.f) || scale > 3.0e38f) return paged_fail(SVX_ERR_INVALID_ARG, "scale must be positive and finite, or 0");
+  // (scores are held in log2 units: the scale times log2 e has to be finite in fp32)
+  const double sc = scale > 0.f ? static_cast<double>(scale) : 1.0 / sqrt(static_cast<double>(cache->head_dim));
+  const double scale_log2 = sc * 1.4426950408889634074;
+  if (!(scale >= 0.f) || scale_log2 > FLT_MAX)
+    return paged_fail(SVX_ERR_INVALID_ARG, "scale must be positive and below 2^128 ln 2, or 0");
   const size_t n_rows = static_cast<size_t>(n_req) * std::max(n_q_heads, 0), per_req = static_cast<size_t>(n_req) * 4;
   const size_t row = static_cast<size_t>(cache->head_dim) * 2, acc = per_req * p.pages.n_kv_heads * p.pages.cap;
   const svx::Span q_span = {q, n_rows * row}, o_span = {o, n_rows * row}, lse_span = {lse, n_rows * 4}, out_span = {acc_out, acc},
@@ -984,8 +989,7 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
   p.row_ml = acc_in ? reinterpret_cast<float2*>(ws + z.row_ml) : nullptr;
   p.scores = acc_in ? reinterpret_cast<float*>(ws + z.scores) : nullptr;
   p.score_stride = z.score_stride;
-  const double sc = scale > 0.f ? static_cast<double>(scale) : 1.0 / sqrt(static_cast<double>(cache->head_dim));
-  p.scale = static_cast<float>(sc * 1.4426950408889634074);
+  p.scale = static_cast<float>(scale_log2);
   p.max_len = z.max_len;
   p.n_q = n_q_heads;
   p.group = n_q_heads / cache->n_kv_heads;

@@ -187,3 +187,11 @@ def test_words_off_their_alignment_are_refused(svx):
             assert misaligned(svx.lib.svx_qk_norm_rope(ctypes.byref(h), ctypes.byref(svx.Rope(128).table), O, K, V, None)), kw
             assert "status" in kw or misaligned(svx.lib.svx_paged_append(ctypes.byref(h), ctypes.byref(svx.Rope(128).table),
                                                                         ctypes.byref(pages(svx)), LEN, O, None, None, None)), kw
+
+
+def test_scales_that_overflow_in_log2_units_are_refused(svx):
+    """The kernel holds scores in log2 units: scale log2 e must be a finite fp32 number (an infinite one makes NaN of a score of 0)."""
+    def status(scale):
+        return refused(svx, decode(svx, scale=scale), words=("scale",))
+    assert all(status(x) for x in (2.9e38, 2.4e38, 3.3e38, float("inf"), float("nan"), -1.0, -1e-45))
+    assert not any(status(x) for x in (0.0, 1e-45, 0.125, 1e30, 2.3e38))
