@@ -5,7 +5,8 @@ the device error word instead of making it).
 
 Each translation unit is compiled by its own nvcc process (all in parallel), then
 linked into one shared library next to this file.  The binding's native part,
-``svx_torch.so`` (a Python extension against this machine's PyTorch), is compiled beside them.
+``svx_torch.so`` (a Python extension against this machine's PyTorch), is compiled beside them;
+the libraries need no PyTorch and are built without it too.
 """
 from __future__ import annotations
 
@@ -43,6 +44,8 @@ def torch_command(out: str) -> list:
     import sysconfig
 
     import torch
+    if torch.version.cuda is None:
+        raise ImportError("this PyTorch is built without CUDA")
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
@@ -55,7 +58,9 @@ def torch_command(out: str) -> list:
 
 def build(verbose: bool = False, extra_flags: tuple = (), checked: bool = True) -> str:
     """Compiles every translation unit (both variants at once when `checked`) and links libsvx.so, then
-    libsvx_checked.so.  Returns the path of libsvx.so."""
+    libsvx_checked.so; svx_torch.so too where PyTorch with CUDA is installed (else the binding's calls that need it raise
+    ImportError).  A failure to compile svx_torch.so is raised once the libraries are linked.  Returns the path
+    of libsvx.so."""
     cc = nvcc()
     variants = [("", LIB, ())] + ([("checked", LIB_CHECKED, ("-DSVX_BOUNDS_CHECK",))] if checked else [])
     procs, objs = [], {}
@@ -69,20 +74,30 @@ def build(verbose: bool = False, extra_flags: tuple = (), checked: bool = True) 
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
             objs.setdefault(lib, []).append(obj)
-    cmd = torch_command(LIB_TORCH + ".tmp")
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    procs.append(("svx_torch.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    binding, why = None, ""
+    try:
+        cmd = torch_command(LIB_TORCH + ".tmp")
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        binding = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    except ImportError as e:
+        print(f"svx_torch.so is not built: {e}", file=sys.stderr)
+    except OSError as e:  # no host compiler of that name
+        why = str(e)
     failed = []
-    for src, p in procs:
+
+    def finish(src, p):
         out, _ = p.communicate()
         if p.returncode != 0:
             failed.append(f"--- {src}\n{out}")
         elif verbose and out.strip():
             print(out, file=sys.stderr)
+    for src, p in procs:
+        finish(src, p)
     if failed:
+        if binding:
+            binding.communicate()
         raise RuntimeError("compilation failed:\n" + "\n".join(failed))
-    os.replace(LIB_TORCH + ".tmp", LIB_TORCH)
     for _sub, lib, _flags in variants:
         tmp = lib + ".tmp"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs[lib]]
@@ -90,6 +105,16 @@ def build(verbose: bool = False, extra_flags: tuple = (), checked: bool = True) 
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout)
         os.replace(tmp, lib)
+    if binding:
+        finish("svx_torch.cpp", binding)
+        if not failed:
+            os.replace(LIB_TORCH + ".tmp", LIB_TORCH)
+            return LIB
+    # no binding of an earlier build beside new libraries
+    if os.path.exists(LIB_TORCH):
+        os.remove(LIB_TORCH)
+    if failed or why:
+        raise RuntimeError("the libraries are built; svx_torch.so is not:\n" + "\n".join(failed or [why]))
     return LIB
 
 
