@@ -638,6 +638,13 @@ svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, const int32_t*
                            const int32_t* pos_in, float* acc_out, int32_t* pos_out, int32_t* len_out, void* workspace,
                            int64_t workspace_bytes, void* stream);
 
+/* Test hook of the bounds-checked library (as svx_debug_clip_q_rows, for the calls above).  Until it is called again, this
+ * thread's calls describe a kind of buffer as holding at most `elements` elements (< 0: the real number again); buffer
+ * 0: q, k and v of svx_heads; 1: q_out, k_out and v_out; 2: the K and V pages.  The real buffers are larger, so no access
+ * leaves them: in libsvx_checked.so the kernels skip the rows past the end and set bit 4 and the buffer's bit (0: 2^17,
+ * 1: 2^18, 2: 2^19) of the status word; in libsvx.so nothing changes. */
+svx_status svx_debug_clip_paged(int32_t buffer, int64_t elements);
+
 /* Library version string. */
 const char* svx_version(void);
 

@@ -975,6 +975,7 @@ extern "C" svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, in
     if (x && !(cache->flags & SVX_POINTERS_CHECKED) && !svx::on_device(x, cache->device))
       return paged_fail(SVX_ERR_INVALID_ARG, "a pointer is not memory of device %d", cache->device);
 
+  p.pages.extent = svx::clipped(svx::kClipPool, p.pages.extent);
   char* ws = static_cast<char*>(workspace);
   p.q = q;
   p.len = len;

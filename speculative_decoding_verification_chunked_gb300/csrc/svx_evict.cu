@@ -597,6 +597,7 @@ extern "C" svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, con
   const int sms = svx::sm_count(cache->device);
   if (sms <= 0) return paged_fail(SVX_ERR_CUDA, "cannot read the SM count");
 
+  p.pages.extent = svx::clipped(svx::kClipPool, p.pages.extent);
   char* ws = static_cast<char*>(workspace);
   p.len = len;
   p.next_pos = next_pos;

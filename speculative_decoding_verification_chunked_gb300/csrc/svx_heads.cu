@@ -47,7 +47,8 @@ struct HeadsParams {
   PageView pages;
   uint64_t turns[64];
   int64_t tokens;               // n_req * n_tok
-  int64_t q_ext, k_ext, v_ext;  // elements of the inputs (checked build)
+  int64_t q_ext, k_ext, v_ext;    // elements of the inputs (checked build)
+  int64_t q_out_ext, kv_out_ext;  // and of the dense outputs
   float eps, scale;
   int32_t n_tok, n_q, n_kv;
   int32_t walk;                 // heads that a warp walks
@@ -193,11 +194,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
     out = static_cast<T*>(P.q_out);
     step = static_cast<int64_t>(P.n_tok) * D;
     at = ((static_cast<int64_t>(b) * P.n_q + h0) * P.n_tok + j) * D;
-    out_ext = P.tokens * P.n_q * D;
+    out_ext = P.q_out_ext;
   } else if (!P.paged) {
     out = static_cast<T*>(is_v ? P.v_out : P.k_out);
     at = (token * P.n_kv + h0) * D;
-    out_ext = P.tokens * P.n_kv * D;
+    out_ext = P.kv_out_ext;
   } else if (live) {
     out = static_cast<T*>(is_v ? P.pages.v : P.pages.k);
     step = P.pages.head_stride;
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
     }
   }
   if (at < 0) live = false;
+  const int out_site = P.paged && !is_q ? kSitePool : kSiteHeadsOut;
 
   const int walk = RING ? count : 1;
   if (is_v) {
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
       uint4 raw[2];
       fetch(i, raw);
       T* dst = out + at + i * step;
-      if (live && in_bounds(dst, D, out, out_ext, P.status, kSitePool)) {
+      if (live && in_bounds(dst, D, out, out_ext, P.status, out_site)) {
         reinterpret_cast<uint4*>(dst)[v0] = raw[0];
         reinterpret_cast<uint4*>(dst)[v1] = raw[1];
       }
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) heads_kernel(const __grid_con
       }
     }
     T* dst = out + at + i * step;
-    if (!live || !in_bounds(dst, D, out, out_ext, P.status, kSiteHeadsOut)) continue;
+    if (!live || !in_bounds(dst, D, out, out_ext, P.status, out_site)) continue;
     reinterpret_cast<uint4*>(dst)[v0] = pack<T>(x);
     reinterpret_cast<uint4*>(dst)[v1] = pack<T>(x + 8);
     if (P.paged && !is_q && lane == 0) {
@@ -430,9 +432,12 @@ svx_status run_heads(const svx_heads* in, const svx_rope* rope, const svx_pages*
   p.slot_pos = slot_pos;
   for (int i = 0; i < 64; ++i) p.turns[i] = rope->turns[i];
   p.tokens = tokens;
-  p.q_ext = (tokens - 1) * str[0] + row[0];
-  p.k_ext = (tokens - 1) * str[1] + row[1];
-  p.v_ext = has_v ? (tokens - 1) * str[2] + row[2] : 0;
+  p.q_ext = clipped(kClipInputs, (tokens - 1) * str[0] + row[0]);
+  p.k_ext = clipped(kClipInputs, (tokens - 1) * str[1] + row[1]);
+  p.v_ext = has_v ? clipped(kClipInputs, (tokens - 1) * str[2] + row[2]) : 0;
+  p.q_out_ext = clipped(kClipOutputs, tokens * q_row);
+  p.kv_out_ext = clipped(kClipOutputs, tokens * kv_row);
+  p.pages.extent = clipped(kClipPool, p.pages.extent);
   p.eps = in->eps;
   p.scale = rope->scale;
   p.n_tok = in->n_tok;

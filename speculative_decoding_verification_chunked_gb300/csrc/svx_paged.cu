@@ -98,6 +98,14 @@ svx_status paged_view(const svx_pages* c, int32_t n_req, PageView* out) {
 }
 
 namespace {
+thread_local int64_t t_clip[kClips] = {-1, -1, -1};
+}
+
+int64_t clipped(PagedBuffer kind, int64_t extent) {
+  return t_clip[kind] >= 0 && t_clip[kind] < extent ? t_clip[kind] : extent;
+}
+
+namespace {
 
 // True if a row that begins `off` elements behind a row of the pool shares elements with one of the first `dims` dimensions'
 // rows (strides ascending, each at least the span of those before it, so that only the two nearest multiples of the largest
@@ -157,6 +165,12 @@ static uint64_t turn_fraction(double f) {
 }
 
 }  // namespace svx
+
+extern "C" svx_status svx_debug_clip_paged(int32_t buffer, int64_t elements) {
+  if (buffer < 0 || buffer >= svx::kClips) return svx::paged_fail(SVX_ERR_INVALID_ARG, "buffer must be 0, 1 or 2");
+  svx::t_clip[buffer] = elements < 0 ? -1 : elements;
+  return SVX_OK;
+}
 
 extern "C" svx_status svx_rope_init(svx_rope* rope, int32_t rot_dim, int32_t neighbours, const double* inv_freq,
                                     float scale) {

@@ -52,6 +52,10 @@ __device__ __forceinline__ int64_t slot_offset(const PageView& p, int32_t page_i
   return static_cast<int64_t>(page_id) * p.page_stride + static_cast<int64_t>(in_page) * p.tok_stride;
 }
 
+// svx_debug_clip_paged: the most elements that this thread's calls describe a buffer of a kind as holding.
+enum PagedBuffer : int { kClipInputs = 0, kClipOutputs = 1, kClipPool = 2, kClips = 3 };
+int64_t clipped(PagedBuffer kind, int64_t extent);
+
 // Host side, shared by the entry points (svx_paged.cu).
 svx_status paged_fail(svx_status st, const char* fmt, ...);
 // Checks a svx_pages and fills the view (with n_req rows in the table).  SVX_OK or the failure reported.

@@ -194,6 +194,7 @@ _SIGS = {
                                                  ctypes.POINTER(ctypes.c_int64)]),
     "svx_paged_evict": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32,
                                        ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, _P]),
+    "svx_debug_clip_paged": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64]),
     "svx_version": (ctypes.c_char_p, []),
     "svx_abi_sizes": (ctypes.c_int32, [ctypes.POINTER(ctypes.c_int64), ctypes.c_int32]),
 }

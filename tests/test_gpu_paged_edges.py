@@ -102,3 +102,66 @@ def test_decode_refuses_a_workspace_in_the_pools(svx, which):
     for at in ((1 << 23) + 2 * n, (1 << 23) - size):
         cache.decode(q, table, lens, o, lse, workspace=arena[at:at + size])
     assert not cache.check()
+
+
+# ------------------------------------------------------------------ the bounds-checked library
+
+
+def test_strays_name_the_buffer_that_they_left(svx):
+    """With buffers described as smaller than they are (svx_debug_clip_paged), the checked library skips what lies past the end and names the
+    buffer; the other library, and the next call, do all of it."""
+    checked = "bounds-checked" in svx.version()
+    g = torch.Generator().manual_seed(22)
+    n, hq, hkv, d, page, t = 6, 4, 2, 64, 4, torch.bfloat16
+    x = torch.randn((1, n, hq + 2 * hkv, d), generator=g).to(t).cuda()
+    q, k, v = x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:]
+    pos, rope, table, start = i32([list(range(n))]), svx.Rope(d), i32([[0, 1]]), i32([1])
+    qo = torch.zeros((1, hq, n, d), dtype=t, device="cuda")
+    ko, vo = (torch.zeros((1, n, hkv, d), dtype=t, device="cuda") for _ in range(2))
+    kp, vp = (torch.zeros((2, page, hkv, d), dtype=t, device="cuda") for _ in range(2))
+    cache, status = svx.PagedCache(kp, vp), i32([0])
+    o, lse, lens = torch.zeros((1, hq, 1, d), dtype=t, device="cuda"), torch.zeros((1, hq, 1), device="cuda"), i32([n + 1])
+    acc = torch.zeros((1, hkv, 2 * page), device="cuda")
+    spos = torch.zeros((1, hkv, 2 * page), dtype=torch.int32, device="cuda")
+
+    def dense():
+        svx.qk_norm_rope(q, k, v, pos, rope, qo, ko, vo, status=status)
+        return status
+
+    def append():
+        cache.append(q, k, v, pos, rope, table, start, qo)
+        return cache.status
+
+    def decode():
+        cache.decode(q[:, :1].transpose(1, 2).contiguous(), table, lens, o, lse)
+        return cache.status
+
+    def evict():
+        cache.evict(table, lens, 3, 0, 3, i32([8]), acc, spos.copy_(torch.arange(2 * page, device="cuda").int().expand_as(spos)), acc,
+                    spos, i32([0]))
+        return cache.status
+
+    def clip(buffer, elements):
+        assert svx.lib.svx_debug_clip_paged(buffer, elements) == svx.OK
+    inside, outside, pool = 1 << 17, 1 << 18, 1 << 19
+    cases = [(dense, 0, 3 * (hq + 2 * hkv) * d, inside), (append, 0, 3 * (hq + 2 * hkv) * d, inside), (dense, 1, 2 * hkv * d, outside),
+             (append, 1, 2 * hkv * d, outside), (append, 2, page * hkv * d, pool), (decode, 2, page * hkv * d, pool), (evict, 2, page * hkv * d, pool)]
+    for call, buffer, elements, bit in cases:
+        word = call()
+        assert int(word) == 0, call.__name__
+        for y in (qo, ko, vo):
+            y.zero_()
+        try:
+            clip(buffer, elements)
+            call()
+        finally:
+            clip(buffer, -1)
+        assert int(word) == (4 | bit if checked else 0), (call.__name__, buffer, hex(int(word)))
+        word.zero_()
+        if checked and buffer == 1:
+            assert (qo.view(-1)[2 * hkv * d:] == 0).all() and (qo.view(-1)[:2 * hkv * d] != 0).any()
+            if call is dense:
+                assert (ko.view(-1)[2 * hkv * d:] == 0).all() and (vo.view(-1)[2 * hkv * d:] == 0).all() and (vo.view(-1)[:2 * hkv * d] != 0).any()
+        call()
+        assert int(word) == 0
+    assert svx.lib.svx_debug_clip_paged(3, 0) == svx.ERR_INVALID_ARG
