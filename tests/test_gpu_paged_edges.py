@@ -4,11 +4,11 @@ Bounds are derived at each test; u = torch.finfo(type).eps / 2 is a rounding to 
 """
 import math
 
-import numpy as np
 import pytest
 import torch
 
-from paged_reference import heads64
+from paged_reference import decode64, evict64, heads64
+from test_gpu_paged import HEADS, check_decode, decode_inputs, heads_inputs, heads_reference, make_table, near, run_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -165,3 +165,136 @@ def test_strays_name_the_buffer_that_they_left(svx):
         call()
         assert int(word) == 0
     assert svx.lib.svx_debug_clip_paged(3, 0) == svx.ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ eviction: every kernel that the lengths choose
+
+# longest, rows (requests x KV heads), d, page, evicted slots, most moves: by the longest row 256, 512 or 1024 threads of 4 to 32 keys and
+# clusters of 1 to 8; with up to 64 (256 threads) or 128 (512) moves and a length of its own they are made in the selecting kernel
+SELECT = [
+    (1000, (2, 2), 64, 24, 41),       # 256 threads, moves in several warps, a remainder
+    (1000, (1, 3), 64, 7, 9),
+    (1024, (2, 1), 128, 16, 64),      # at the limits: 4 keys, 64 moves
+    (1025, (2, 2), 128, 16, 65),      # one past both
+    (2048, (1, 2), 128, 32, 58),
+    (2049, (1, 2), 64, 32, 63),
+    (2560, (2, 1), 64, 64, 33),
+    (2561, (2, 1), 128, 64, 100),     # 512 threads
+    (4096, (1, 2), 64, 16, 127),
+    (4097, (1, 2), 128, 16, 128),
+    (6144, (1, 1), 64, 100, 128),
+    (6145, (1, 1), 64, 100, 129),
+    (8192, (2, 1), 128, 128, 77),
+    (8193, (2, 1), 128, 128, 77),     # 1024 threads
+    (12289, (1, 2), 64, 128, 5000),
+    (16384, (1, 1), 64, 128, 300),
+    (16385, (1, 1), 64, 128, 300),    # two CTAs to a row
+    (17000, (10, 8), 64, 128, 700),   # as long, but the rows fill the card: 32 keys a thread
+    (70000, (5, 4), 64, 256, 900),    # four CTAs, 32 keys
+    (262144, (1, 2), 64, 1024, 2000),  # the longest: eight
+]
+
+
+PLACES = ["apart", "weights in place", "all in place"]
+
+
+@pytest.mark.parametrize("case,place", [(c, p) for c in SELECT for p in PLACES if c[0] < 16385 or p != "weights in place"],
+                         ids=lambda c: c if isinstance(c, str) else f"len{c[0]}-rows{c[1][0]}x{c[1][1]}-d{c[2]}-gone{c[4]}")
+def test_evict_with_every_selecting_kernel(svx, case, place):
+    """Each row loses exactly `gone` slots in front, so that as many rows of K and V move; a shorter request moves fewer.  Exact."""
+    longest, (B, hkv), d, page, gone = case
+    g = torch.Generator().manual_seed(longest)
+    lens = [longest - (11 * b if b else 0) for b in range(B)]
+    budget = longest - gone
+    table, total = make_table(g, lens, page)
+    kp, vp = (torch.randn((total, page, hkv, d), generator=g).to(torch.float16).cuda() for _ in range(2))
+    k0, v0 = kp.clone(), vp.clone()
+    room = table.shape[1] * page
+    acc = 1 + torch.rand((B, hkv, room), generator=g)
+    pos = torch.stack([torch.stack([torch.randperm(room, generator=g) for _ in range(hkv)]) for _ in range(B)]).to(torch.int32)
+    recent = budget // 8
+    for b, n in enumerate(lens):
+        for h in range(hkv):  # the lightest lie in front, and none of them is protected by its position
+            low = torch.randperm(budget, generator=g)[:gone]
+            acc[b, h, low] = torch.rand(gone, generator=g)
+            late = pos[b, h, low] >= room - recent
+            pos[b, h, low[late]] = 5
+    nxt = i32([room] * B)
+    a, p, ln = acc.cuda(), pos.cuda(), i32(lens)
+    ao, po = (a, p) if "place" in place else (torch.full_like(a, 7.0), torch.full_like(p, 7))
+    lo = ln if place == "all in place" else torch.full_like(ln, 7)
+    cache = svx.PagedCache(kp, vp)
+    cache.evict(table.cuda(), ln, budget, 0, recent, nxt, a, p, ao, po, lo, max_len=longest)
+    assert not cache.check() and lo.tolist() == [min(n, budget) for n in lens]
+    td = table.cuda().long()
+    for b, n in enumerate(lens):
+        m = min(n, budget)
+        for h in range(hkv):
+            order = torch.tensor(evict64(acc[b, h].numpy(), pos[b, h].numpy(), n, room, budget, 0, recent))
+            assert int((order != torch.arange(m)).sum()) == n - m
+            assert torch.equal(ao[b, h, :m].cpu(), acc[b, h][order]) and torch.equal(po[b, h, :m].cpu(), pos[b, h][order])
+            to, fro = torch.arange(m).cuda(), order.cuda()
+            for pool, old in ((kp, k0), (vp, v0)):
+                assert torch.equal(pool[td[b, to // page], to % page, h], old[td[b, fro // page], fro % page, h])
+            rest = torch.arange(m, n).cuda()  # what lies behind stays
+            assert torch.equal(kp[td[b, rest // page], rest % page, h], k0[td[b, rest // page], rest % page, h])
+            if place == "apart":
+                assert (ao[b, h, m:] == 7.0).all() and (po[b, h, m:] == 7).all()
+            else:
+                assert torch.equal(ao[b, h, m:].cpu(), acc[b, h, m:]) and torch.equal(po[b, h, m:].cpu(), pos[b, h, m:])
+
+
+# ------------------------------------------------------------------ what is reported, and what it leaves right
+
+
+@pytest.mark.parametrize("case", HEADS, ids=str)
+def test_heads_with_a_status_word_report_nothing(svx, case):
+    """The dense form with a status word (without one the checked library has nowhere to report a stray): clear, and the values right."""
+    b, n, hq, hkv, d, rot, nb, norm, ty, scale = case
+    qkv, pos, wq, wk, inv = heads_inputs(case, seed=23)
+    t, status, x = TYPES[ty], i32([0]), qkv.cuda()
+    qo, ko, vo = (torch.full(s, 7.0, dtype=t, device="cuda") for s in ((b, hq, n, d), (b, n, hkv, d), (b, n, hkv, d)))
+    cu = lambda w: None if w is None else w.cuda()  # noqa: E731
+    svx.qk_norm_rope(x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:], pos.cuda(), svx.Rope(rot, inv_freq=inv, neighbours=nb, scale=scale),
+                     qo, ko, vo, q_norm=cu(wq), k_norm=cu(wk), eps=1e-6 if norm else None, status=status)
+    assert int(status) == 0
+    q, qs, k, ks, v = heads_reference(case, qkv, pos, wq, wk, inv)
+    near(qo.transpose(1, 2), q, qs, t)
+    near(ko, k, ks, t)
+    assert torch.equal(vo.cpu(), v)
+
+
+def test_lengths_out_of_bounds_are_clamped(svx):
+    """As the header says of what lies on the device: a negative length counts as none, one above max_len as max_len; other requests'
+    rows are those of a call without the fault, bit for bit."""
+    case = ((3000, 17, 900), 12, 3, 64, 16, "bf16", "token", True)
+    table, kp, vp, k64, v64, q, acc = decode_inputs(case, seed=24)
+    for lens, right, max_len in (((3000, -5, 900), (3000, 0, 900), 0), ((3000, -2 ** 31, 900), (3000, 0, 900), 0), ((901, 17, 900), (900, 17, 900), 900),
+                                 ((2 ** 31 - 1, 17, 900), (900, 17, 900), 900)):
+        cache = svx.PagedCache(kp, vp)
+        want = run_decode(svx, (right, *case[1:]), table, kp, vp, q, acc, max_len=max_len)
+        check_decode((right, *case[1:]), want, decode64(q, k64, v64, table, right, case[3] ** -0.5, acc), acc)
+        o, lse, out = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0), torch.full_like(want[2], 7.0)
+        cache.decode(q.cuda(), table.cuda(), i32(lens), o, lse, max_len=max_len, acc_in=acc.cuda(), acc_out=out)
+        assert cache.check() and not cache.check()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(out, want[2])
+        if right[1] == 0:
+            assert (o[1] == 0).all() and (lse[1] == -float("inf")).all() and (out[1] == 7.0).all()
+
+
+def test_values_that_are_not_finite_stay_with_their_request(svx):
+    """K and V below a length have to be finite; one that is not spoils its own request and KV head, and no other."""
+    case = ((70, 700, 300), 8, 2, 128, 16, "bf16", "token", True)
+    table, kp, vp, k64, v64, q, acc = decode_inputs(case, seed=25)
+    good = run_decode(svx, case, table, kp, vp, q, acc)
+    for pool in (kp, vp):
+        old = pool.clone()
+        for value in (float("inf"), float("nan"), -float("inf")):
+            pool.copy_(old)
+            pool[int(table[1, 200 // 16]), 200 % 16, 1, 3] = value
+            o, lse, out = run_decode(svx, case, table, kp, vp, q, acc)
+            assert math.isinf(value) and pool is kp or not torch.isfinite(o[1, 4:]).all()  # (a score of -inf is a weight of 0)
+            assert torch.equal(o[1, :4], good[0][1, :4]) and torch.equal(lse[1, :4], good[1][1, :4]) and torch.equal(out[1, 0], good[2][1, 0])
+            for b in (0, 2):
+                assert all(torch.equal(x[b], y[b]) for x, y in zip((o, lse, out), good))
+        pool.copy_(old)

@@ -195,3 +195,18 @@ def test_scales_that_overflow_in_log2_units_are_refused(svx):
         return refused(svx, decode(svx, scale=scale), words=("scale",))
     assert all(status(x) for x in (2.9e38, 2.4e38, 3.3e38, float("inf"), float("nan"), -1.0, -1e-45))
     assert not any(status(x) for x in (0.0, 1e-45, 0.125, 1e30, 2.3e38))
+
+
+def test_split_in_32_bits_is_the_exact_split():
+    """The kernels' begin(c) = c q + floor(c r / used + 0.001) with c r / used as an fp32 product by the rounded reciprocal: for every used <= 256,
+    r < used and c <= used it is c q + (c r) // used."""
+    import numpy as np
+    f = np.float32
+    for used in range(1, 257):
+        per = f(1) / f(used)  # rounded to nearest
+        c, r = np.meshgrid(np.arange(used + 1), np.arange(used), indexing="ij")
+        cr = (c * r).astype(f)
+        assert (cr == c * r).all()
+        # one rounding: the product of two fp32 numbers is exact in fp64, and the sum keeps 2^-37 beside quotients below 256
+        got = np.floor((cr.astype(np.float64) * float(per) + float(f(0.001))).astype(f))
+        assert (got == (c * r) // used).all(), used
