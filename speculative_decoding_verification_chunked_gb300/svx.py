@@ -759,7 +759,12 @@ def _native():
 def _on_stream(stream, device: int):
     """A context in which ``stream`` (a torch stream or a raw handle) is the current one."""
     import torch
-    if not isinstance(stream, torch.cuda.Stream):
+    if device < 0:
+        raise SvxError(ERR_INVALID_ARG, "a stream is given with tensors that are not on a CUDA device")
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != device:  # (it would not become the current one of the tensors' device)
+            raise SvxError(ERR_INVALID_ARG, f"stream: of cuda:{stream.device_index}, expected one of cuda:{device}")
+    else:
         stream = torch.cuda.ExternalStream(_stream_handle(stream), device=torch.device("cuda", device))
     return torch.cuda.stream(stream)
 

@@ -210,3 +210,21 @@ def test_split_in_32_bits_is_the_exact_split():
         # one rounding: the product of two fp32 numbers is exact in fp64, and the sum keeps 2^-37 beside quotients below 256
         got = np.floor((cr.astype(np.float64) * float(per) + float(f(0.001))).astype(f))
         assert (got == (c * r) // used).all(), used
+
+
+def test_streams_of_another_device_are_refused(svx, monkeypatch):
+    """The call would run on the current stream of its tensors' device in place of the one that was asked for."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        device_index = 1
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: ("current", s))
+    with pytest.raises(svx.SvxError, match="cuda:1"):
+        svx._on_stream(Stream(), 0)
+    mine = Stream()
+    assert svx._on_stream(mine, 1) == ("current", mine)
+    q, pos = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16), torch.zeros((1, 1), dtype=torch.int32)
+    for stream in (0, mine):  # tensors on the CPU, whatever the stream
+        with pytest.raises(svx.SvxError):
+            svx.qk_norm_rope(q, q, None, pos, svx.Rope(64), q, q, stream=stream)
