@@ -219,6 +219,12 @@ PyObject* guarded(F&& f) {
       PyErr_SetObject(g_error, e);
       Py_DECREF(e);
     }
+  } catch (const c10::OutOfMemoryError& e) {  // no room for a workspace: torch.OutOfMemoryError, as of torch's own calls
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }

@@ -298,3 +298,17 @@ def test_values_that_are_not_finite_stay_with_their_request(svx):
             for b in (0, 2):
                 assert all(torch.equal(x[b], y[b]) for x, y in zip((o, lse, out), good))
         pool.copy_(old)
+
+
+def test_no_room_for_a_workspace_is_an_out_of_memory_error(svx):
+    """Scores of 4096 heads over 2^25 slots are 512 GiB: torch's allocator refuses, as it does in torch's own calls, and the next call runs."""
+    page, room = 1 << 15, 1 << 25
+    kp, vp = (torch.zeros((1, page, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache, table = svx.PagedCache(kp, vp), torch.zeros((1, room // page), dtype=torch.int32, device="cuda")
+    q, lens = torch.zeros((1, 4096, 1, 64), dtype=torch.bfloat16, device="cuda"), i32([3])
+    o, lse, acc = torch.full_like(q, 7.0), torch.empty((1, 4096, 1), device="cuda"), torch.zeros((1, 1, room), device="cuda")
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        cache.decode(q, table, lens, o, lse, acc_in=acc, acc_out=acc)
+    cache.decode(q, table, lens, o, lse, max_len=64, acc_in=acc, acc_out=acc)
+    assert not cache.check() and (o == 0).all()
+    assert torch.allclose(acc[0, 0, :3], torch.full((3,), 4096 / 3, device="cuda"), rtol=1e-4) and (acc[0, 0, 3:] == 0).all()
