@@ -606,8 +606,10 @@ svx_status svx_paged_decode_workspace(const svx_pages* cache, int32_t n_req, int
  * -inf) gets O = 0, LSE = -inf.  q, o [n_req][n_q_heads][head_dim] and lse [n_req][n_q_heads], device; query head
  * h reads KV head h / (n_q_heads / n_kv_heads).  len: device int32[n_req], 0 <= len[b] <= max_len.  max_len:
  * upper bound known on the host, 0 for max_pages * page_size; it sizes the launch and the workspace, so a
- * captured call stays valid for all lengths up to it.  scale: 0 means 1/sqrt(head_dim); below 2^128 ln 2.  K and V of the slots read
- * must be finite; what lies behind a request's length is not used, whatever it holds.
+ * captured call stays valid for all lengths up to it.  scale: 0 means 1/sqrt(head_dim); below 2^128 ln 2.
+ * K and V of the slots read must be finite (an infinity may give NaN), and 2^8 times the sum of a request's |V| in one
+ * dimension within fp32's range; one that is not spoils its request and KV head only.  What lies behind a request's length
+ * is not used, whatever it holds.
  * acc_in, acc_out (device float [n_req][n_kv_heads][max_pages * page_size], or both NULL): acc_out[t] =
  * acc_in[t] + the sum over the KV head's query heads of slot t's softmax weight, t < len[b]; the rest is left as
  * it was.  They may be one buffer; otherwise outputs and workspace must not overlap inputs, the pools or one another.  With weights max_len is at most 134,215,680.  workspace: device, 256-byte aligned; contents need no set-up. */
@@ -623,8 +625,9 @@ svx_status svx_paged_evict_workspace(const svx_pages* cache, int32_t n_req, int6
 #define SVX_EVICT_MAX_LEN 262144
 
 /* Eviction by accumulated attention weight.  Per request and KV head, of the slots [0, len[b]) keeps
- * n = min(len[b], budget): first those at positions < sink or >= next_pos[b] - recent, then those with the largest
- * acc_in; equal ones by the lower slot; NaN counts as -inf.  The kept slots >= n, in order, move into the
+ * n = min(len[b], budget): first those at positions < sink or >= next_pos[b] - recent (if positions that repeat make them more
+ * than n: the lowest slots of them, whatever their acc_in), then those with the largest acc_in; equal ones by the lower
+ * slot; NaN counts as -inf.  The kept slots >= n, in order, move into the
  * evicted slots < n, in order: K and V rows inside the pages, and acc_in, pos_in into acc_out, pos_out, which get
  * their first n entries written (the rest is left as it was).  Every other slot keeps its place, so slots are in no
  * order of position; attention does not depend on it.  len_out[b] = n.  len, next_pos, len_out: device

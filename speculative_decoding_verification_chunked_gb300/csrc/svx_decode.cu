@@ -23,8 +23,9 @@
 //
 // Products: mma.sync m16n8k16, query heads on M.  They cost a few percent of the time (32 a chunk), so the
 // tensor memory path, which wants 64 rows or more on M and a second trip through it, gains nothing here.  With up to 8
-// query heads per KV head the upper 8 rows would be idle: they carry what is left of p after its rounding to 16 bits,
-// so P.V has p to 16 bits or more at no extra product.  With 9 to 16 the remainder is a second product.
+// query heads per KV head the upper 8 rows would be idle: they carry what is left of p after its rounding to a 16-bit type,
+// so P.V has p to 2^-16 of itself (bf16) or better at no extra product, far within the output's own rounding.  With 9 to
+// 16 the remainder is a second product.
 // Softmax state, scores and sums are fp32.  m is not the maximum but a reference that moves only when a score passes it
 // by more than kTau, so most chunks need no exchange between lanes; every merge takes (m, l, O) with any reference.
 #include "svx_paged.h"
@@ -871,7 +872,8 @@ svx_status sizes(const svx_pages* c, int32_t n_req, int32_t n_q, int64_t max_len
                       static_cast<long long>(chunks), ct);
   // Whole items to the CTAs where they are few and short: the longest takes a CTA kWholeItem / 8 chunks a warp, and the join's
   // launch and wait go.  Split and whole: one KV head of 64, 512 slots, 6.2 and 5.9 us; 8 KV heads of 128, 8 requests of 1 to 512
-  // slots 9.4 and 8.7, 8 of 512 slots 8.3 and 8.5; 2 of 1024 slots (64 chunks, and so split) 8.0 and 11.7.
+  // slots 9.4 and 8.7, 8 of 256 slots 6.9 and 6.7; 2 of 1024 slots (64 chunks, and so split) 8.0 and 11.7.  At the limit itself, 8 of
+  // 512 slots, all as long as max_len, 8.3 and 8.5: the host knows the bound only, and ragged lengths below it gain more.
   const int64_t per_item = (max_len + ct - 1) / ct;
   z->whole = !weights && per_item <= kWholeItem && chunks <= sms * per_item;
   z->ctas = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kMaxCtas), std::max<int64_t>((chunks + kMinChunks - 1) / kMinChunks, 1)));

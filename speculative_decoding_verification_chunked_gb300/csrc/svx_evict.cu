@@ -14,7 +14,7 @@
 // move_kernel: a lane works out a move, then the warp brings up to 32 rows of K and V (512 bytes each at d = 128) into
 // shared memory with asynchronous copies and writes them out, so a warp has 16 KiB in flight without holding registers.
 // Floor: 8 bytes a slot read, 8 a kept slot written, 8 d bytes a moved slot.
-// Measured, d = 128, 64 rows: 2112 to 2048 slots 9.2 us (latency: lengths, keys, four histogram passes of 0.7 us, pages,
+// Measured, d = 128, 64 rows: 2112 to 2048 slots 8.0 us (latency: lengths, keys, four histogram passes of 0.7 us, pages,
 // rows); 32768 to 4096 61 us, of which selection 18 us (6 to load, 6 for three passes, each with a cluster barrier) and the
 // moves 40 us, 235 MB at 5.9 TB/s.  Before: bisection over 32 bits in place of the histograms 137 us in all.
 #include <cooperative_groups.h>
@@ -501,9 +501,9 @@ cudaError_t launch_selects(EvictParams& p, int rows, int sms, cudaStream_t s) {
          (keys(p.cluster) > kMaxKeys || (keys(p.cluster) > kSplitKeys && rows * p.cluster * 2 <= sms)))
     p.cluster *= 2;
   // Moves in the same kernel where a small CTA has one turn of its warps of them, which saves a launch and a trip through
-  // memory: 64 rows of 2112 slots to 2048 took 9.2 us so and 9.6 us in two kernels, 256 rows of 1040 to 1024 7.2 and 8.0 us;
-  // with four turns it is 14.4 and 11.8 us.  Not where the new lengths go over the old, which other heads' CTAs may
-  // still have to read.
+  // memory: 64 rows of 2112 slots to 2048 take 8.0 us so and 8.7 us in two kernels.  With two turns it is slower: 64 rows of
+  // 2176 to 2048 9.8 and 9.2 us, 256 rows of 1152 to 1024 14.6 and 13.0; 64 rows of 4352 to 4096 15.6 and 12.7.  Not
+  // where the new lengths go over the old, which other heads' CTAs may still have to read.
   p.fused = threads <= kFewThreads && p.cluster == 1 && p.most <= kFewMoves * (threads / 32) && p.len_out != p.len;
   const int per = keys(p.cluster);
   if (threads == 256)

@@ -319,7 +319,10 @@ template <typename T, int D>
 cudaError_t launch(HeadsParams& p, cudaStream_t stream, int sms) {
   // Heads that a warp walks (its tokens' heads of one kind): one where tokens are few (latency: every head its own
   // warp), more once the grid half fills the card anyway, so that a lane's eight sines and cosines serve several heads.
-  // (d = 64: 2331 tokens of 15 heads 6.7 us with four, 6.1 with two; 20436 tokens of 6 9.7 us with eight, 11.2 with four.)
+  // Walks of 1, 2, 4 and 8, in us: 20436 tokens of 4 + 1 + 1 heads (d = 64) 13.3, 11.4, 10.3, 10.3 and 1024 tokens of
+  // 32 + 8 + 8 (d = 128) 10.7, 8.3, 6.9, 6.2, eight taken in both.  Around one filling of the card it depends on where the last
+  // warps fall, which the rule does not see: 2331 tokens of 12 + 3 + 3 (d = 64) 5.6, 5.4, 4.1, 5.2, two taken; 5 x 777 places,
+  // 2331 of them live, 7.8, 6.8, 7.6, 7.2, four taken (dead places count: how many live is known on the device only).
   const int64_t blocks_of_tokens = (p.tokens * (D / 16) + 31) / 32;
   const int64_t room = static_cast<int64_t>(sms) * 32;  // warps
   const int64_t warps = blocks_of_tokens * (p.n_q + p.n_kv);

@@ -772,7 +772,7 @@ def _on_stream(stream, device: int):
 class Rope:
     """Rotation of heads by position (svx_rope_init): pair i of the first rot_dim dimensions turns by
     position * inv_freq[i], by default theta^(-2 i / rot_dim).  neighbours: pairs (2i, 2i + 1) instead of
-    (i, i + rot_dim / 2).  scale: factor on the rotated values."""
+    (i, i + rot_dim / 2).  scale: factor on the rotated values.  Phases are exact for every 32-bit position."""
 
     def __init__(self, rot_dim: int, theta: float = 10000.0, inv_freq: Optional[Sequence[float]] = None,
                  neighbours: bool = False, scale: float = 1.0):
@@ -879,7 +879,7 @@ class PagedCache:
     def evict(self, table, lens, budget: int, sink: int, recent: int, next_pos, acc_in, pos_in, acc_out, pos_out, len_out,
               max_len: int = 0, workspace=None, stream=None):
         """svx_paged_evict: per request and KV head keeps min(lens[b], budget) slots: positions < sink or >= next_pos[b] -
-        recent, then the largest acc_in (ties: the lower slot).  Kept slots behind the new length move into the
+        recent (the lowest slots of them, if they are more), then the largest acc_in (ties: the lower slot).  Kept slots behind the new length move into the
         evicted ones before it, with their acc and position; len_out gets the new lengths.  acc (fp32), pos (int32):
         [B][Hkv][max_pages * page_size]; lens, next_pos, len_out: int32 [B]; outputs may be their inputs."""
         if stream is not None:
