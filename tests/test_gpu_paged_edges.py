@@ -312,3 +312,27 @@ def test_no_room_for_a_workspace_is_an_out_of_memory_error(svx):
     cache.decode(q, table, lens, o, lse, max_len=64, acc_in=acc, acc_out=acc)
     assert not cache.check() and (o == 0).all()
     assert torch.allclose(acc[0, 0, :3], torch.full((3,), 4096 / 3, device="cuda"), rtol=1e-4) and (acc[0, 0, 3:] == 0).all()
+
+
+@pytest.mark.parametrize("page", [77, 100, 1000, 4097, 65535, 99991, (1 << 20) + 7])
+def test_slots_find_their_page_up_to_the_last(svx, page):
+    """The division by page_size that the kernels make by multiplication, as the host sets it up: single tokens at slots around page borders up
+    to 2^31 - 1, in a table whose only page is the right one."""
+    pages = (2 ** 31 - 1) // page
+    kp, vp = (torch.zeros((1, page, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache, rope = svx.PagedCache(kp, vp), svx.Rope(64)
+    table = torch.full((1, pages), -1, dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(page)
+    slots = {0, page - 1, page, pages * page - 1, pages * page - page}
+    for p in torch.randint(0, pages, (12,), generator=g).tolist():
+        slots |= {p * page, p * page + page - 1, p * page + page // 2}
+    qo = torch.empty((1, 1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for i, slot in enumerate(sorted(slots)):
+        table[0, slot // page] = 0
+        x = torch.full((1, 1, 3, 64), float(i + 1), dtype=torch.bfloat16, device="cuda")
+        cache.append(x[:, :, :1], x[:, :, 1:2], x[:, :, 2:], i32([[0]]), rope, table, i32([slot]), qo, eps=None)
+        assert not cache.check(), slot
+        assert (vp[0, slot % page] == i + 1).all() and (kp[0, slot % page] == i + 1).all(), slot
+        table[0, slot // page] = -1
+        vp[0, slot % page] = 0
+    assert not vp.any()  # nothing went anywhere else
