@@ -517,6 +517,8 @@ svx_status svx_width_cost(svx_width w, int32_t q, double* cost_out);
 /* Element types of q, K, V, O and the norms' weights. */
 #define SVX_BF16 0
 #define SVX_FP16 1
+/* of a residual stream alone */
+#define SVX_FP32 2
 
 /* svx_heads.flags, svx_pages.flags: the caller has made sure that every pointer of the call is memory of `device`, and
  * the call does not ask the driver about each again (0.1 to 0.3 us a pointer). */
@@ -648,12 +650,56 @@ svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, const int32_t*
  * 1: 2^18, 2: 2^19) of the status word; in libsvx.so nothing changes. */
 svx_status svx_debug_clip_paged(int32_t buffer, int64_t elements);
 
+/* ---- the residual stream between two blocks ------------------------------------------------------ */
+
+/* svx_residual.gate_kind: none, one number for all, one for each of the dim channels, or one for each element. */
+#define SVX_GATE_NONE 0
+#define SVX_GATE_SCALAR 1
+#define SVX_GATE_CHANNEL 2
+#define SVX_GATE_ELEMENT 3
+/* svx_residual.act: what the gate goes through. */
+#define SVX_ACT_NONE 0
+#define SVX_ACT_TANH 1
+#define SVX_ACT_SIGMOID 2
+
+/* rows of dim elements, device memory; row r of a buffer begins r * its stride (elements) from the pointer.  dim: a multiple of 8
+ * up to 16384.  Pointers 16-byte aligned (a scalar gate: 2), strides multiples of 8; those of inputs may be 0. */
+typedef struct {
+  const void* h;          /* the residual stream, of type stream_dtype */
+  const void* y;          /* the block's output, dtype; NULL: no block (no gate and no norm after it either) */
+  const void* gate;       /* dtype; NULL for SVX_GATE_NONE */
+  const void* norm;       /* [dim] weights, dtype, or NULL: ones */
+  const void* post_norm;
+  void* h_out;            /* stream_dtype, or NULL */
+  void* x_out;            /* dtype, or NULL */
+  int64_t h_stride, y_stride, gate_stride, h_out_stride, x_stride; /* gate_stride: of SVX_GATE_ELEMENT */
+  int64_t rows;           /* 1 .. 2^31 - 1 */
+  int32_t dim;
+  int32_t dtype;          /* SVX_BF16 or SVX_FP16 */
+  int32_t stream_dtype;   /* dtype or SVX_FP32 */
+  int32_t gate_kind, act;
+  int32_t device;
+  float alpha, beta;
+  float eps;              /* of the norm before the next block, >= 0 (not read without x_out) */
+  float post_eps;         /* of the norm after the block; < 0: no such norm (post_norm NULL) */
+  uint32_t flags;         /* SVX_POINTERS_CHECKED */
+  int32_t pad;
+} svx_residual;
+
+/* Between two blocks of a layer, row by row:
+ *   u = y, or y * post_norm / sqrt(mean(y^2) + post_eps);   h_out = alpha h + beta act(gate) u;
+ *   x_out = h_out * norm / sqrt(mean(h_out^2) + eps)   (of h_out before its rounding)
+ * all in fp32, rounded once.  Mean squares have to be within fp32's range.  h_out may be h and x_out may be y (same stride);
+ * otherwise outputs must not overlap inputs or one another (a strided buffer counts from its first element to its last).
+ * Enqueued on `stream` (cudaStream_t) of `device`; allocates and keeps nothing. */
+svx_status svx_residual_norm(const svx_residual* in, void* stream);
+
 /* Library version string. */
 const char* svx_version(void);
 
 /* sizeof of the ABI's structs, for bindings to check their layouts: svx_config, svx_part, svx_stats,
  * svx_window_summary, svx_plan_entry, svx_tier_state, svx_sched_config, svx_draft_instr, svx_rope, svx_heads,
- * svx_pages, in this order.
+ * svx_pages, svx_residual, in this order.
  * Writes min(cap, count) entries to out and returns the count.  Host-only. */
 int32_t svx_abi_sizes(int64_t* out, int32_t cap);
 

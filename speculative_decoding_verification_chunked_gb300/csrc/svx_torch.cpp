@@ -26,6 +26,7 @@ struct Calls {
   decltype(&svx_paged_decode) decode = nullptr;
   decltype(&svx_paged_evict_workspace) evict_workspace = nullptr;
   decltype(&svx_paged_evict) evict = nullptr;
+  decltype(&svx_residual_norm) residual_norm = nullptr;
   decltype(&svx_last_error) last_error = nullptr;
 } g;
 PyObject* g_error = nullptr;  // svx.SvxError
@@ -246,7 +247,7 @@ svx_status without_gil(F&& call) {
 const svx_rope* rope_at(PyObject* o) { return reinterpret_cast<const svx_rope*>(integer(o, "rope")); }
 
 PyObject* set_up(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!expect(n, 8)) return nullptr;
+  if (!expect(n, 9)) return nullptr;
   return guarded([&] {
     g_error = a[0];
     Py_INCREF(g_error);
@@ -257,7 +258,8 @@ PyObject* set_up(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.decode = reinterpret_cast<decltype(g.decode)>(at(4));
     g.evict_workspace = reinterpret_cast<decltype(g.evict_workspace)>(at(5));
     g.evict = reinterpret_cast<decltype(g.evict)>(at(6));
-    g.last_error = reinterpret_cast<decltype(g.last_error)>(at(7));
+    g.residual_norm = reinterpret_cast<decltype(g.residual_norm)>(at(7));
+    g.last_error = reinterpret_cast<decltype(g.last_error)>(at(8));
   });
 }
 
@@ -387,9 +389,91 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Elements between the rows of a tensor [..., dim], evenly spaced over its leading dimensions; 0: one row.
+int64_t row_stride(const at::Tensor& t, const char* what) {
+  int64_t stride = 0, next = 0;  // of the last dimension with more than one entry, and what the one before it needs
+  bool any = false, even = t.dim() >= 1 && (t.size(-1) <= 1 || t.stride(-1) == 1);
+  for (int64_t i = t.dim() - 2; i >= 0; --i) {
+    if (t.size(i) <= 1) continue;
+    if (!any) stride = t.stride(i);
+    else even = even && t.stride(i) == next;
+    any = true;
+    next = t.stride(i) * t.size(i);
+  }
+  if (!even) {
+    std::ostringstream s;
+    s << what << ": strides " << t.strides() << ": rows must be dense, and evenly spaced over the leading dimensions";
+    refuse(SVX_ERR_INVALID_ARG, s.str());
+  }
+  return stride;
+}
+
+// residual_norm(h, y, h_out, x_out, norm, eps, post_norm, post_eps, gate, act, alpha, beta)
+PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!expect(n, 12)) return nullptr;
+  return guarded([&] {
+    const at::Tensor& h = tensor(a[0], "h");
+    if (!h.is_cuda() || h.dim() < 1 || h.numel() == 0 || h.size(-1) > INT32_MAX)
+      refuse(SVX_ERR_INVALID_ARG, "h: " + describe(h) + ", expected [..., dim] on a CUDA device");
+    svx_residual r = {};
+    r.device = h.get_device();
+    r.dim = static_cast<int32_t>(h.size(-1));
+    r.rows = h.numel() / r.dim;
+    // the type of everything but the stream: that of the first of these that is given
+    const int of = a[1] != Py_None ? 1 : a[3] != Py_None ? 3 : 0;
+    r.dtype = type_code(tensor(a[of], of == 1 ? "y" : of == 3 ? "x_out" : "h"), of == 1 ? "y" : of == 3 ? "x_out" : "h");
+    const at::ScalarType type = scalar_of(r.dtype), stream_type = h.scalar_type();
+    if (stream_type != type && stream_type != at::kFloat)
+      refuse(SVX_ERR_UNSUPPORTED, "h: " + describe(h) + "; expected the type of the block's output or torch.float32");
+    r.stream_dtype = stream_type == at::kFloat ? SVX_FP32 : r.dtype;
+    auto rows = [&](int i, at::ScalarType t, const char* what, int64_t* stride) -> void* {
+      if (a[i] == Py_None) return nullptr;
+      const at::Tensor& x = tensor(a[i], what);
+      if (x.scalar_type() != t || x.sizes() != h.sizes() || !x.is_cuda() || x.get_device() != r.device) {
+        std::ostringstream s;
+        s << what << ": " << describe(x) << "; expected " << t << " " << h.sizes() << " on cuda:" << r.device;
+        refuse(SVX_ERR_INVALID_ARG, s.str());
+      }
+      *stride = row_stride(x, what);
+      return x.data_ptr();
+    };
+    r.h = rows(0, stream_type, "h", &r.h_stride);
+    r.y = rows(1, type, "y", &r.y_stride);
+    r.h_out = rows(2, stream_type, "h_out", &r.h_out_stride);
+    r.x_out = rows(3, type, "x_out", &r.x_stride);
+    r.norm = optional(a[4], type, {r.dim}, r.device, "norm");
+    r.eps = real(a[5], "eps");
+    r.post_norm = optional(a[6], type, {r.dim}, r.device, "post_norm");
+    r.post_eps = -1.f;
+    if (a[7] != Py_None) {
+      r.post_eps = real(a[7], "post_eps");
+      if (!(r.post_eps >= 0.f)) refuse(SVX_ERR_INVALID_ARG, "post_eps must be >= 0, or None for no norm after the block");
+    }
+    if (a[8] != Py_None) {
+      const at::Tensor& gate = tensor(a[8], "gate");
+      if (gate.dim() == 1 && gate.size(0) == 1) {
+        r.gate_kind = SVX_GATE_SCALAR;
+        r.gate = dense(a[8], type, {1}, r.device, "gate");
+      } else if (gate.dim() == 1) {
+        r.gate_kind = SVX_GATE_CHANNEL;
+        r.gate = dense(a[8], type, {r.dim}, r.device, "gate");
+      } else {
+        r.gate_kind = SVX_GATE_ELEMENT;
+        r.gate = rows(8, type, "gate", &r.gate_stride);
+      }
+    }
+    r.act = integer32(a[9], "act");
+    r.alpha = real(a[10], "alpha");
+    r.beta = real(a[11], "beta");
+    r.flags = SVX_POINTERS_CHECKED;
+    void* stream = current_stream(r.device);
+    check(without_gil([&] { return g.residual_norm(&r, stream); }));
+  });
+}
+
 #define SVX_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SVX_METHOD(set_up), SVX_METHOD(pages), SVX_METHOD(qk_norm_rope), SVX_METHOD(append), SVX_METHOD(decode),
-                         SVX_METHOD(evict), {nullptr, nullptr, 0, nullptr}};
+                         SVX_METHOD(evict), SVX_METHOD(residual_norm), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "svx_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -109,6 +109,17 @@ class Pages(ctypes.Structure):
                 ("device", ctypes.c_int32), ("flags", ctypes.c_uint32), ("pad", ctypes.c_int32)]
 
 
+class Residual(ctypes.Structure):
+    _fields_ = [("h", ctypes.c_void_p), ("y", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("norm", ctypes.c_void_p),
+                ("post_norm", ctypes.c_void_p), ("h_out", ctypes.c_void_p), ("x_out", ctypes.c_void_p),
+                ("h_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64),
+                ("h_out_stride", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("stream_dtype", ctypes.c_int32),
+                ("gate_kind", ctypes.c_int32), ("act", ctypes.c_int32), ("device", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("eps", ctypes.c_float), ("post_eps", ctypes.c_float),
+                ("flags", ctypes.c_uint32), ("pad", ctypes.c_int32)]
+
+
 # name -> (restype, argtypes); every symbol declared in include/svx.h
 _P = ctypes.c_void_p
 _SIGS = {
@@ -194,6 +205,7 @@ _SIGS = {
                                                  ctypes.POINTER(ctypes.c_int64)]),
     "svx_paged_evict": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32,
                                        ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, _P]),
+    "svx_residual_norm": (ctypes.c_int, [ctypes.POINTER(Residual), _P]),
     "svx_debug_clip_paged": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64]),
     "svx_version": (ctypes.c_char_p, []),
     "svx_abi_sizes": (ctypes.c_int32, [ctypes.POINTER(ctypes.c_int64), ctypes.c_int32]),
@@ -220,7 +232,7 @@ def version() -> str:
 
 
 ABI_STRUCTS = ("Config", "Part", "Stats", "WindowStats", "PlanEntry", "TierState", "SchedConfig", "DraftInstr",
-               "RopeTable", "Heads", "Pages")
+               "RopeTable", "Heads", "Pages", "Residual")
 
 
 def abi_sizes() -> dict:
@@ -751,7 +763,7 @@ def _native():
         spec.loader.exec_module(mod)
         mod.set_up(SvxError, *[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "svx_qk_norm_rope", "svx_paged_append", "svx_paged_decode_workspace", "svx_paged_decode",
-            "svx_paged_evict_workspace", "svx_paged_evict", "svx_last_error")])
+            "svx_paged_evict_workspace", "svx_paged_evict", "svx_residual_norm", "svx_last_error")])
         _native_module = mod
     return _native_module
 
@@ -806,6 +818,30 @@ def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None
         with _on_stream(stream, q.get_device()):
             return qk_norm_rope(q, k, v, pos, rope, q_out, k_out, v_out, q_norm, k_norm, eps, n_new, status)
     (_native_module or _native()).qk_norm_rope(q, k, v, pos, rope.address, q_out, k_out, v_out, q_norm, k_norm, eps, n_new, status)
+
+
+_ACTS = {None: 0, "tanh": 1, "sigmoid": 2}
+
+
+def residual_norm(h, y=None, h_out=None, x_out=None, norm=None, eps: float = 1e-6, post_norm=None,
+                  post_eps: Optional[float] = None, gate=None, act: Optional[str] = None, alpha: float = 1.0,
+                  beta: float = 1.0, stream=None):
+    """svx_residual_norm: the residual stream between two blocks.
+
+        u = y, or y * post_norm / sqrt(mean(y^2) + post_eps);   h_out = alpha h + beta act(gate) u
+        x_out = h_out * norm / sqrt(mean(h_out^2) + eps)
+
+    y (the block's output) and x_out (the next block's input): device bf16 or fp16 [..., dim]; h and h_out (the residual stream): of that
+    type or fp32, the same shape.  Rows dense, evenly spaced over the leading dimensions; dim a multiple of 8 up to 16384.
+    norm, post_norm: [dim] of y's type, or None: ones.  post_eps None: no norm after the block.  gate: [1], [dim] or of y's
+    shape, y's type; act: None, "tanh" or "sigmoid" of it.  y None: no block, x_out is the norm of alpha h.  h_out or
+    x_out may be None; h_out may be h and x_out may be y."""
+    if stream is not None:
+        with _on_stream(stream, h.get_device()):
+            return residual_norm(h, y, h_out, x_out, norm, eps, post_norm, post_eps, gate, act, alpha, beta)
+    if act not in _ACTS:
+        raise SvxError(ERR_INVALID_ARG, f"act: {act!r}, expected None, 'tanh' or 'sigmoid'")
+    (_native_module or _native()).residual_norm(h, y, h_out, x_out, norm, eps, post_norm, post_eps, gate, _ACTS[act], alpha, beta)
 
 
 class PagedCache:
