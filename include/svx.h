@@ -619,6 +619,30 @@ svx_status svx_paged_decode(const svx_pages* cache, int32_t n_req, int32_t n_q_h
                             int64_t max_len, float scale, void* o, float* lse, const float* acc_in, float* acc_out,
                             void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Prefixes that several requests of a call share, in the pages of its cache.  Requests of one prefix are neighbours:
+ * those of prefix p are [first[p], first[p + 1]); first does not fall, and requests outside [first[0], first[n_prefix]) have none. */
+typedef struct {
+  const int32_t* table;  /* device [n_prefix][max_pages], as svx_pages.table */
+  const int32_t* len;    /* device [n_prefix], 0 <= len[p] <= max_len */
+  const int32_t* first;  /* device [n_prefix + 1], within [0, n_req] */
+  int64_t max_len;       /* upper bound known on the host; 0: max_pages * page_size */
+  int32_t n_prefix;      /* 1 .. 256 */
+  int32_t max_pages;     /* max_pages * page_size < 2^31 */
+} svx_prefixes;
+
+/* Bytes of workspace that svx_paged_decode_shared needs for these arguments (pointers of `prefixes` are not read).  Host-only but
+ * for the SM count. */
+svx_status svx_paged_decode_shared_workspace(const svx_pages* cache, int32_t n_req, int32_t n_q_heads,
+                                             const svx_prefixes* prefixes, int64_t max_len, int64_t* bytes);
+
+/* svx_paged_decode for requests that share prefixes: request b attends to the slots of its prefix and then to its own slots
+ * [0, len[b]) of cache->table (either may be none; with neither O = 0, LSE = -inf).  A prefix's K and V are read once for all its
+ * requests, not once for each.  q, len, max_len, scale, o, lse and what K, V hold: as svx_paged_decode.  first, like lengths and
+ * page ids, is checked on the device.  Outputs and workspace must not overlap inputs, the pools or one another. */
+svx_status svx_paged_decode_shared(const svx_pages* cache, int32_t n_req, int32_t n_q_heads, const void* q,
+                                   const svx_prefixes* prefixes, const int32_t* len, int64_t max_len, float scale, void* o,
+                                   float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Bytes of workspace that svx_paged_evict needs for these arguments.  Host-only. */
 svx_status svx_paged_evict_workspace(const svx_pages* cache, int32_t n_req, int64_t max_len, int32_t budget,
                                      int64_t* bytes);
@@ -649,6 +673,45 @@ svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, const int32_t*
  * leaves them: in libsvx_checked.so the kernels skip the rows past the end and set bit 4 and the buffer's bit (0: 2^17,
  * 1: 2^18, 2: 2^19) of the status word; in libsvx.so nothing changes. */
 svx_status svx_debug_clip_paged(int32_t buffer, int64_t elements);
+
+/* ---- attention to an encoder's states -------------------------------------------------------- */
+
+/* n_tok tokens of each of n_req requests against n_states states of each.  Row (b, h, j) of q is at b * q_req + h * q_head + j * q_tok
+ * elements, of o likewise; row (b, t, g) of k and v at b * kv_req + t * kv_state + g * kv_head; rows of head_dim elements dense, pointers
+ * 16-byte aligned, strides multiples of 8 elements, not negative (0: all of them the same, but not in o, whose rows must
+ * not overlap: sorted, each stride at least the span of the smaller ones' dimensions). */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;              /* device [n_req][n_q_heads][n_tok], or NULL */
+  const int32_t* len;      /* device [n_req]: only the first len[b] states of a request count, 0..n_states; NULL: all */
+  const uint8_t* mask;     /* device, state t of request b at b * mask_req + t: 0: it does not count; NULL: all do */
+  int32_t* status;         /* device status word (as in svx_pages), or NULL */
+  int64_t q_req, q_head, q_tok;
+  int64_t kv_req, kv_head, kv_state;
+  int64_t o_req, o_head, o_tok;
+  int64_t mask_req;
+  int32_t n_req;           /* 1 .. 256 */
+  int32_t n_tok;           /* >= 1 */
+  int32_t n_states;        /* >= 0 */
+  int32_t n_q_heads, n_kv_heads, head_dim; /* head_dim 64 or 128; n_q_heads a multiple of n_kv_heads, at most 4096 */
+  int32_t dtype;           /* SVX_BF16 or SVX_FP16 */
+  int32_t device;
+  float scale;             /* 0 means 1/sqrt(head_dim); below 2^128 ln 2 */
+  uint32_t flags;          /* SVX_POINTERS_CHECKED */
+} svx_cross;
+
+/* Bytes of workspace that svx_cross_attn needs (no pointer is read).  Host-only but for the SM count. */
+svx_status svx_cross_attn_workspace(const svx_cross* c, int64_t* bytes);
+
+/* O = softmax(q K^T scale) V over the states that count, LSE = natural log of the softmax denominator; O = 0 and LSE = -inf where
+ * none does.  Query head h reads KV head h / (n_q_heads / n_kv_heads).  States that count must be finite, as in svx_paged_decode; what
+ * the others hold is not used, whatever it is.  Outputs and workspace must not overlap inputs or one another (a strided buffer
+ * counts from its first element to its last).  workspace: device, 256-byte aligned; contents need no set-up.
+ * Enqueued on `stream` (cudaStream_t) of `device`; allocates and keeps nothing, so it may be captured (after one eager call). */
+svx_status svx_cross_attn(const svx_cross* c, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---- the residual stream between two blocks ------------------------------------------------------ */
 
@@ -699,7 +762,7 @@ const char* svx_version(void);
 
 /* sizeof of the ABI's structs, for bindings to check their layouts: svx_config, svx_part, svx_stats,
  * svx_window_summary, svx_plan_entry, svx_tier_state, svx_sched_config, svx_draft_instr, svx_rope, svx_heads,
- * svx_pages, svx_residual, in this order.
+ * svx_pages, svx_residual, svx_prefixes, svx_cross, in this order.
  * Writes min(cap, count) entries to out and returns the count.  Host-only. */
 int32_t svx_abi_sizes(int64_t* out, int32_t cap);
 

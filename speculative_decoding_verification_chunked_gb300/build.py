@@ -26,7 +26,7 @@ LIB_TORCH = os.path.join(PKG, "svx_torch.so")
 
 SOURCES = ["svx_kernels.cu", "svx_tc_kernel.cu", "svx_runtime.cu", "svx_static.cu", "svx_tier.cu", "svx_sched.cu", "svx_width.cu",
            "svx_paged.cu", "svx_heads.cu", "svx_decode.cu", "svx_evict.cu",
-           "svx_residual.cu"]
+           "svx_residual.cu", "svx_cross.cu", "svx_shared.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-Xcompiler", "-ffp-contract=off",

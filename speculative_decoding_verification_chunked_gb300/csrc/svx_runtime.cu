@@ -364,7 +364,8 @@ int32_t svx_abi_sizes(int64_t* out, int32_t cap) {
                         static_cast<int64_t>(sizeof(svx_plan_entry)), static_cast<int64_t>(sizeof(svx_tier_state)),
                         static_cast<int64_t>(sizeof(svx_sched_config)), static_cast<int64_t>(sizeof(svx_draft_instr)),
                         static_cast<int64_t>(sizeof(svx_rope)),       static_cast<int64_t>(sizeof(svx_heads)),
-                        static_cast<int64_t>(sizeof(svx_pages)),      static_cast<int64_t>(sizeof(svx_residual))};
+                        static_cast<int64_t>(sizeof(svx_pages)),      static_cast<int64_t>(sizeof(svx_residual)),
+                        static_cast<int64_t>(sizeof(svx_prefixes)),   static_cast<int64_t>(sizeof(svx_cross))};
   const int32_t n = static_cast<int32_t>(sizeof(sz) / sizeof(sz[0]));
   for (int32_t i = 0; i < n && i < cap; ++i) out[i] = sz[i];
   return n;

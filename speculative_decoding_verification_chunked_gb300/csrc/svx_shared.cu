@@ -1,0 +1,259 @@
+// Attention of one new token per request over a paged cache, for requests that share prefixes: a prefix's K and V are read once
+// for all its requests, whose tokens' query heads are the rows of one product with them.
+//
+// Two kinds of sequences lie in one flat range of chunks (svx_attend.cuh): the prefixes, with the rows of all their requests, and
+// the requests' own slots.  Every row then has two lots of states (m, l, O), which join_shared merges.
+#include "svx_attend.cuh"
+
+namespace svx {
+namespace {
+
+constexpr int kMaxPieces = 2 * kMaxCtas;  // of a row: of its prefix, and of its own slots
+
+// CTA (x, y): KV head x of all requests' heads; block of 16 query heads y.
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant__ AttendParams P) {
+  constexpr int CT = kChunkBytes / (2 * D);
+  // Where the pieces of a row's lot lie: one is a finished state; else piece c is in slot 0 of CTA first + c, or (c = 0) slot 1.
+  struct Lot {
+    int32_t first, pieces, row;  // row: in the pieces' blocks, or of the finished states
+  };
+  __shared__ Plan<kShared> plan;
+  __shared__ float s_f[kMaxPieces * kRowsMax];
+  __shared__ float2 s_ml[kRowsMax];
+  __shared__ Lot s_lot[2][kRowsMax];
+  __shared__ float4 s_o[kWarps * 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the lengths were there before the attention kernel began, which had waited for whoever wrote them)
+  const int T_all = build_plan<kShared, CT>(P, plan, false);
+  const int b = blockIdx.x / P.pages.n_kv_heads, h = blockIdx.x - b * P.pages.n_kv_heads, blk = blockIdx.y;
+  const int rows = min(P.group - blk * kRowsMax, kRowsMax);
+  const Split split(P, T_all);
+  int prefix = 0;  // the first that ends behind the request
+  for (int i = 0; i < P.n_prefix; i += 32)
+    prefix += __popc(__ballot_sync(0xffffffffu, i + lane < P.n_prefix && plan.req0[i + lane + 1] <= b));
+  if (tid < 2 * kRowsMax) {
+    const int r = tid % kRowsMax, lot = tid / kRowsMax;  // 0: the prefix, 1: the request's own
+    Lot x{0, 0, 0};
+    int seq = kMaxReq + b, block = blk, blocks = P.blocks;
+    x.row = r;
+    bool any = r < rows;
+    if (lot == 0) {
+      any = any && prefix < P.n_prefix && plan.req0[prefix] <= b;
+      if (any) {
+        const int R = (b - plan.req0[prefix]) * P.group + blk * kRowsMax + r;
+        seq = prefix;
+        block = R / kRowsMax;
+        blocks = (seq_rows(P, plan, prefix) + kRowsMax - 1) / kRowsMax;
+        x.row = R % kRowsMax;
+      }
+    }
+    const int n = any ? plan.n[seq] : 0;
+    if (n > 0) {
+      const int first = plan.first[seq] + (h * blocks + block) * n;
+      x.first = split.of(first);
+      x.pieces = split.of(first + n - 1) - x.first + 1;
+      if (x.pieces == 1) x.row = (lot * P.pages.n_req + b) * P.n_q + h * P.group + blk * kRowsMax + r;
+    }
+    s_lot[lot][r] = x;
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  allow_dependents();
+  auto ml_at = [&](int r, int c) {
+    const int lot = c < s_lot[0][r].pieces ? 0 : 1;
+    if (lot) c -= s_lot[0][r].pieces;
+    const Lot x = s_lot[lot][r];
+    if (x.pieces == 1) return __ldcg(P.state_ml + x.row);
+    return __ldcg(P.part_ml + ((x.first + c) * 2 + (c == 0 ? 1 : 0)) * kRowsMax + x.row);
+  };
+  auto o_at = [&](int r, int c, int d4) {
+    const int lot = c < s_lot[0][r].pieces ? 0 : 1;
+    if (lot) c -= s_lot[0][r].pieces;
+    const Lot x = s_lot[lot][r];
+    const float* at = x.pieces == 1 ? P.state_o + static_cast<int64_t>(x.row) * D
+                                    : P.part_o + static_cast<int64_t>(((x.first + c) * 2 + (c == 0 ? 1 : 0)) * kRowsMax + x.row) * D;
+    return __ldcg(reinterpret_cast<const float4*>(at + d4));
+  };
+  for (int r = warp; r < rows; r += kWarps) {
+    const int pieces = s_lot[0][r].pieces + s_lot[1][r].pieces;
+    float M = kNegInf;
+    for (int c = lane; c < pieces; c += 32) M = fmaxf(M, ml_at(r, c).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == kNegInf ? 0.f : M;
+    float L = 0.f;
+    for (int c = lane; c < pieces; c += 32) {
+      const float2 ml = ml_at(r, c);
+      const float f = ex2(ml.x - base);
+      s_f[c * kRowsMax + r] = f;
+      L = fmaf(ml.y, f, L);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) s_ml[r] = make_float2(M, L);
+  }
+  __syncthreads();
+  // the outputs over the threads: several share one where there are more of them than outputs
+  const int outs = rows * (D / 4), share = max(kWarps * 32 / outs, 1);
+  const int part = share > 1 ? tid / outs : 0;
+  for (int i = share > 1 ? tid - part * outs : tid; i - tid < outs; i += kWarps * 32) {  // (alike for all threads of a round)
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int r = i / (D / 4), d4 = (i - r * (D / 4)) * 4;
+    if (i < outs && part < share) {
+      const int pieces = s_lot[0][r].pieces + s_lot[1][r].pieces;
+#pragma unroll 4
+      for (int c = part; c < pieces; c += share) {
+        const float4 x = o_at(r, c, d4);
+        const float f = s_f[c * kRowsMax + r];
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+      }
+    }
+    if (share > 1) {
+      s_o[tid] = o;
+      __syncthreads();
+      if (part == 0)
+        for (int p = 1; p < share; ++p) {
+          const float4 x = s_o[p * outs + i];
+          o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+        }
+    }
+    if (i < outs && part == 0) write_row<T>(P, place<kShared, D>(P, plan, kMaxReq + b, h, blk, r), d4, s_ml[r].x, s_ml[r].y, o);
+    if (share > 1) break;
+  }
+}
+
+struct SharedSizes {
+  Sizes z;
+  int32_t max_prefix;
+};
+
+svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const svx_prefixes* f, int64_t max_len, SharedSizes* out) {
+  if (n_q < c->n_kv_heads || n_q % c->n_kv_heads || n_q > 4096)
+    return paged_fail(SVX_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads, at most 4096");
+  if (!f) return paged_fail(SVX_ERR_INVALID_ARG, "prefixes is NULL");
+  if (f->n_prefix < 1 || f->n_prefix > kMaxReq) return paged_fail(SVX_ERR_INVALID_ARG, "n_prefix must be in [1, %d]", kMaxReq);
+  const int64_t cap = static_cast<int64_t>(c->page_size) * c->max_pages, room = static_cast<int64_t>(c->page_size) * f->max_pages;
+  if (f->max_pages < 1 || room > 0x7fffffffLL)
+    return paged_fail(SVX_ERR_INVALID_ARG, "the prefixes' max_pages must be positive, its product with page_size below 2^31");
+  if (max_len < 0 || max_len > cap) return paged_fail(SVX_ERR_INVALID_ARG, "max_len must be in [0, max_pages * page_size]");
+  if (f->max_len < 0 || f->max_len > room)
+    return paged_fail(SVX_ERR_INVALID_ARG, "the prefixes' max_len must be in [0, their max_pages * page_size]");
+  if (max_len == 0) max_len = cap;
+  const int64_t max_prefix = f->max_len ? f->max_len : room;
+  const int sms = sm_count(c->device);
+  if (sms <= 0) return paged_fail(SVX_ERR_CUDA, "cannot read the SM count");
+  const int group = n_q / c->n_kv_heads, ct = kChunkBytes / (2 * c->head_dim);
+  Sizes& z = out->z;
+  z.max_len = static_cast<int32_t>(max_len);
+  out->max_prefix = static_cast<int32_t>(max_prefix);
+  z.blocks = (group + kRowsMax - 1) / kRowsMax;
+  // (a prefix's last block of rows may not be full)
+  const int64_t blocks = static_cast<int64_t>(n_req) * group / kRowsMax + std::min(f->n_prefix, n_req);
+  const int64_t chunks = c->n_kv_heads * (blocks * ((max_prefix + ct - 1) / ct) +
+                                          static_cast<int64_t>(n_req) * z.blocks * ((max_len + ct - 1) / ct));
+  if (chunks > 0x7fffffff)
+    return paged_fail(SVX_ERR_UNSUPPORTED, "heads times lengths are too large (%lld chunks of %d slots, at most 2^31 - 1)",
+                      static_cast<long long>(chunks), ct);
+  size_pieces(&z, chunks, c->head_dim, sms);
+  const size_t rows = static_cast<size_t>(2) * n_req * n_q;
+  z.state_o = z.total;
+  z.state_ml = z.state_o + up256(rows * c->head_dim * 4);
+  z.total = z.state_ml + up256(rows * 8);
+  return SVX_OK;
+}
+
+template <typename T, int D>
+cudaError_t launch_shared(const AttendParams& p, int device, cudaStream_t s) {
+  // (rows of a prefix: those of all its requests)
+  const bool wide = static_cast<int64_t>(p.group) * p.pages.n_req > 8;
+  const cudaError_t e = wide ? launch_attend<T, kShared, D, true, false>(p, device, s) : launch_attend<T, kShared, D, false, false>(p, device, s);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(join_shared<T, D>, dim3(p.pages.n_req * p.pages.n_kv_heads, p.blocks), dim3(kWarps * 32), 0, s, p);
+}
+
+}  // namespace
+}  // namespace svx
+
+extern "C" svx_status svx_paged_decode_shared_workspace(const svx_pages* cache, int32_t n_req, int32_t n_q_heads,
+                                                        const svx_prefixes* prefixes, int64_t max_len, int64_t* bytes) {
+  if (!bytes) return svx::paged_fail(SVX_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = 0;
+  svx::PageView v;
+  svx_status st = svx::paged_view(cache, n_req, &v);
+  if (st != SVX_OK) return st;
+  svx::SharedSizes z = {};
+  st = svx::shared_sizes(cache, n_req, n_q_heads, prefixes, max_len, &z);
+  if (st == SVX_OK) *bytes = static_cast<int64_t>(z.z.total);
+  return st;
+}
+
+extern "C" svx_status svx_paged_decode_shared(const svx_pages* cache, int32_t n_req, int32_t n_q_heads, const void* q,
+                                              const svx_prefixes* prefixes, const int32_t* len, int64_t max_len, float scale,
+                                              void* o, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  using svx::paged_fail;
+  svx::AttendParams p = {};
+  svx_status st = svx::paged_view(cache, n_req, &p.pages);
+  if (st != SVX_OK) return st;
+  svx::SharedSizes z = {};
+  st = svx::shared_sizes(cache, n_req, n_q_heads, prefixes, max_len, &z);
+  if (st != SVX_OK) return st;
+  const svx_prefixes& f = *prefixes;
+  if (!q || !o || !lse || !len || !svx::is_aligned(q, 16) || !svx::is_aligned(o, 16))
+    return paged_fail(SVX_ERR_INVALID_ARG, "q, len, o and lse must be device pointers, q and o 16-byte aligned");
+  if (!f.table || !f.len || !f.first || !svx::words_aligned({f.table, f.len, f.first, len, lse}))
+    return paged_fail(SVX_ERR_INVALID_ARG, "the prefixes' table, len and first, and len and lse, must be 4-byte aligned device pointers");
+  if (!svx::log2_scale(scale, cache->head_dim, &p.scale))
+    return paged_fail(SVX_ERR_INVALID_ARG, "scale must be positive and below 2^128 ln 2, or 0");
+  const size_t n_rows = static_cast<size_t>(n_req) * n_q_heads, row = static_cast<size_t>(cache->head_dim) * 2;
+  const size_t per_req = static_cast<size_t>(n_req) * 4, per_prefix = static_cast<size_t>(f.n_prefix) * 4;
+  const size_t pool = static_cast<size_t>(p.pages.extent) * 2;
+  const svx::Span q_span = {q, n_rows * row}, o_span = {o, n_rows * row}, lse_span = {lse, n_rows * 4}, len_span = {len, per_req},
+                  table_span = {cache->table, per_req * cache->max_pages}, far_table = {f.table, per_prefix * f.max_pages},
+                  far_len = {f.len, per_prefix}, first_span = {f.first, per_prefix + 4}, k_span = {cache->k, pool},
+                  v_span = {cache->v, pool}, status = {cache->status, 4};
+  if (svx::any_overlap({o_span, lse_span, status}, {q_span, len_span, table_span, far_table, far_len, first_span, k_span, v_span}))
+    return paged_fail(SVX_ERR_INVALID_ARG, "an output overlaps an input or another output");
+  if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(z.z.total))
+    return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", z.z.total);
+  if (svx::any_overlap({{workspace, z.z.total}},
+                       {q_span, o_span, lse_span, len_span, table_span, far_table, far_len, first_span, k_span, v_span, status}))
+    return paged_fail(SVX_ERR_INVALID_ARG, "the workspace overlaps another buffer");
+  svx::PagedDevice dev(cache->device);
+  if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", cache->device);
+  const void* ptrs[] = {cache->k, cache->v, cache->table, cache->status, q, f.table, f.len, f.first, len, o, lse, workspace};
+  for (const void* x : ptrs)
+    if (!(cache->flags & SVX_POINTERS_CHECKED) && !svx::on_device(x, cache->device))
+      return paged_fail(SVX_ERR_INVALID_ARG, "a pointer is not memory of device %d", cache->device);
+
+  p.pages.extent = svx::clipped(svx::kClipPool, p.pages.extent);
+  char* ws = static_cast<char*>(workspace);
+  svx::place_pieces(p, z.z, ws);
+  p.state_o = reinterpret_cast<float*>(ws + z.z.state_o);
+  p.state_ml = reinterpret_cast<float2*>(ws + z.z.state_ml);
+  p.q = q;
+  p.len = len;
+  p.o = o;
+  p.lse = lse;
+  p.n_q = n_q_heads;
+  p.group = n_q_heads / cache->n_kv_heads;
+  p.prefix_table = f.table;
+  p.prefix_len = f.len;
+  p.first = f.first;
+  p.n_prefix = f.n_prefix;
+  p.prefix_max_pages = f.max_pages;
+  p.max_prefix = z.max_prefix;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (cache->dtype == SVX_BF16)
+    e = cache->head_dim == 128 ? svx::launch_shared<__nv_bfloat16, 128>(p, cache->device, s)
+                               : svx::launch_shared<__nv_bfloat16, 64>(p, cache->device, s);
+  else
+    e = cache->head_dim == 128 ? svx::launch_shared<__half, 128>(p, cache->device, s)
+                               : svx::launch_shared<__half, 64>(p, cache->device, s);
+  if (e != cudaSuccess) return paged_fail(SVX_ERR_CUDA, "shared-prefix kernel launch failed: %s", cudaGetErrorString(e));
+  return SVX_OK;
+}

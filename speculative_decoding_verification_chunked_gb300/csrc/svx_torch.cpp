@@ -27,6 +27,10 @@ struct Calls {
   decltype(&svx_paged_evict_workspace) evict_workspace = nullptr;
   decltype(&svx_paged_evict) evict = nullptr;
   decltype(&svx_residual_norm) residual_norm = nullptr;
+  decltype(&svx_paged_decode_shared_workspace) decode_shared_workspace = nullptr;
+  decltype(&svx_paged_decode_shared) decode_shared = nullptr;
+  decltype(&svx_cross_attn_workspace) cross_attn_workspace = nullptr;
+  decltype(&svx_cross_attn) cross_attn = nullptr;
   decltype(&svx_last_error) last_error = nullptr;
 } g;
 PyObject* g_error = nullptr;  // svx.SvxError
@@ -247,7 +251,7 @@ svx_status without_gil(F&& call) {
 const svx_rope* rope_at(PyObject* o) { return reinterpret_cast<const svx_rope*>(integer(o, "rope")); }
 
 PyObject* set_up(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!expect(n, 9)) return nullptr;
+  if (!expect(n, 13)) return nullptr;
   return guarded([&] {
     g_error = a[0];
     Py_INCREF(g_error);
@@ -259,7 +263,11 @@ PyObject* set_up(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.evict_workspace = reinterpret_cast<decltype(g.evict_workspace)>(at(5));
     g.evict = reinterpret_cast<decltype(g.evict)>(at(6));
     g.residual_norm = reinterpret_cast<decltype(g.residual_norm)>(at(7));
-    g.last_error = reinterpret_cast<decltype(g.last_error)>(at(8));
+    g.decode_shared_workspace = reinterpret_cast<decltype(g.decode_shared_workspace)>(at(8));
+    g.decode_shared = reinterpret_cast<decltype(g.decode_shared)>(at(9));
+    g.cross_attn_workspace = reinterpret_cast<decltype(g.cross_attn_workspace)>(at(10));
+    g.cross_attn = reinterpret_cast<decltype(g.cross_attn)>(at(11));
+    g.last_error = reinterpret_cast<decltype(g.last_error)>(at(12));
   });
 }
 
@@ -358,6 +366,111 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return g.decode(&p, static_cast<int32_t>(b), static_cast<int32_t>(hq), qp, lens, max_len, scale, o, lse, acc_in, acc_out, ws.at,
                       ws.bytes, stream);
     }));
+  });
+}
+
+// decode_shared(pages, q, prefix_table, prefix_lens, first, table, lens, o, lse, max_prefix, max_len, scale, workspace)
+PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!expect(n, 13)) return nullptr;
+  return guarded([&] {
+    svx_pages p = pages_of(a[0]);
+    const at::Tensor& q = tensor(a[1], "q");
+    if (q.dim() != 4 || q.size(0) > INT32_MAX || q.size(1) > INT32_MAX)
+      refuse(SVX_ERR_INVALID_ARG, "q: " + describe(q) + ", expected [requests, heads, 1, head_dim]");
+    const int64_t b = q.size(0), hq = q.size(1);
+    const at::ScalarType type = scalar_of(p.dtype);
+    with_table(p, a[5], b);
+    svx_prefixes f = {};
+    const at::Tensor& far = tensor(a[2], "prefix_table");
+    if (far.dim() != 2 || far.size(0) > INT32_MAX || far.size(1) > INT32_MAX)
+      refuse(SVX_ERR_INVALID_ARG, "prefix_table: " + describe(far) + ", expected [prefixes, max_pages]");
+    f.n_prefix = static_cast<int32_t>(far.size(0));
+    f.max_pages = static_cast<int32_t>(far.size(1));
+    f.table = static_cast<const int32_t*>(dense(a[2], at::kInt, {far.size(0), far.size(1)}, p.device, "prefix_table"));
+    f.len = static_cast<const int32_t*>(dense(a[3], at::kInt, {far.size(0)}, p.device, "prefix_lens"));
+    f.first = static_cast<const int32_t*>(dense(a[4], at::kInt, {far.size(0) + 1}, p.device, "first"));
+    f.max_len = integer(a[9], "max_prefix");
+    const void* qp = dense(a[1], type, {b, hq, 1, p.head_dim}, p.device, "q");
+    const int32_t* lens = static_cast<const int32_t*>(dense(a[6], at::kInt, {b}, p.device, "lens"));
+    void* o = dense(a[7], type, {b, hq, 1, p.head_dim}, p.device, "o");
+    float* lse = static_cast<float*>(dense(a[8], at::kFloat, {b, hq, 1}, p.device, "lse"));
+    const int64_t max_len = integer(a[10], "max_len");
+    const float scale = real(a[11], "scale");
+    int64_t need = 0;
+    check(g.decode_shared_workspace(&p, static_cast<int32_t>(b), static_cast<int32_t>(hq), &f, max_len, &need));
+    const Workspace ws(a[12], need, p.device);
+    void* stream = current_stream(p.device);
+    check(without_gil([&] {
+      return g.decode_shared(&p, static_cast<int32_t>(b), static_cast<int32_t>(hq), qp, &f, lens, max_len, scale, o, lse, ws.at, ws.bytes,
+                             stream);
+    }));
+  });
+}
+
+// cross_attn(q, k, v, o, lse, lens, mask, scale, status, workspace)
+PyObject* cross_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!expect(n, 10)) return nullptr;
+  return guarded([&] {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &o = tensor(a[3], "o");
+    svx_cross c = {};
+    c.dtype = type_code(q, "q");
+    const at::ScalarType type = q.scalar_type();
+    if (q.dim() != 4 || !q.is_cuda())
+      refuse(SVX_ERR_INVALID_ARG, "q: " + describe(q) + ", expected [requests, heads, tokens, head_dim] on a CUDA device");
+    c.device = q.get_device();
+    for (int64_t i = 0; i < 4; ++i)
+      if (q.size(i) > INT32_MAX || (k.dim() == 4 && k.size(i) > INT32_MAX))
+        refuse(SVX_ERR_INVALID_ARG, "q or k: a dimension does not fit 32 bits");
+    auto rows_dense = [&](const at::Tensor& t, const char* what) {
+      if (t.scalar_type() != type || !t.is_cuda() || t.get_device() != c.device || t.dim() != 4 || (t.size(3) > 1 && t.stride(3) != 1)) {
+        std::ostringstream s;
+        s << what << ": " << describe(t) << "; expected " << type << " with four dimensions, the last dense, on cuda:" << c.device;
+        refuse(SVX_ERR_INVALID_ARG, s.str());
+      }
+    };
+    rows_dense(q, "q");
+    rows_dense(k, "k");
+    rows_dense(v, "v");
+    rows_dense(o, "o");
+    if (o.sizes() != q.sizes()) refuse(SVX_ERR_INVALID_ARG, "o: " + describe(o) + ", expected q's shape");
+    if (v.sizes() != k.sizes() || v.strides() != k.strides())
+      refuse(SVX_ERR_INVALID_ARG, "v: " + describe(v) + ", expected k's shape and strides: " + describe(k));
+    if (k.size(0) != q.size(0) || k.size(3) != q.size(3))
+      refuse(SVX_ERR_INVALID_ARG, "k: " + describe(k) + ", expected [requests, states, KV heads, head_dim] of q's requests and head_dim");
+    c.n_req = static_cast<int32_t>(q.size(0));
+    c.n_q_heads = static_cast<int32_t>(q.size(1));
+    c.n_tok = static_cast<int32_t>(q.size(2));
+    c.head_dim = static_cast<int32_t>(q.size(3));
+    c.n_states = static_cast<int32_t>(k.size(1));
+    c.n_kv_heads = static_cast<int32_t>(k.size(2));
+    c.q = q.data_ptr();
+    c.k = k.data_ptr();
+    c.v = v.data_ptr();
+    c.o = o.data_ptr();
+    c.q_req = q.stride(0), c.q_head = q.stride(1), c.q_tok = q.stride(2);
+    c.kv_req = k.stride(0), c.kv_state = k.stride(1), c.kv_head = k.stride(2);
+    c.o_req = o.stride(0), c.o_head = o.stride(1), c.o_tok = o.stride(2);
+    c.lse = static_cast<float*>(optional(a[4], at::kFloat, {c.n_req, c.n_q_heads, c.n_tok}, c.device, "lse"));
+    c.len = static_cast<const int32_t*>(optional(a[5], at::kInt, {c.n_req}, c.device, "lens"));
+    if (a[6] != Py_None) {
+      const at::Tensor& m = tensor(a[6], "mask");
+      if (m.scalar_type() != at::kBool || m.dim() != 2 || m.size(0) != c.n_req || m.size(1) != c.n_states || !m.is_cuda() ||
+          m.get_device() != c.device || (c.n_states > 1 && m.stride(1) != 1)) {
+        std::ostringstream s;
+        s << "mask: " << describe(m) << "; expected bool [" << c.n_req << ", " << c.n_states << "] with dense rows on cuda:" << c.device;
+        refuse(SVX_ERR_INVALID_ARG, s.str());
+      }
+      c.mask = static_cast<const uint8_t*>(m.data_ptr());
+      c.mask_req = c.n_req > 1 ? m.stride(0) : 0;
+    }
+    c.scale = real(a[7], "scale");
+    c.status = static_cast<int32_t*>(optional(a[8], at::kInt, {1}, c.device, "status"));
+    c.flags = SVX_POINTERS_CHECKED;
+    int64_t need = 0;
+    check(g.cross_attn_workspace(&c, &need));
+    const Workspace ws(a[9], need, c.device);
+    void* stream = current_stream(c.device);
+    check(without_gil([&] { return g.cross_attn(&c, ws.at, ws.bytes, stream); }));
   });
 }
 
@@ -473,7 +586,8 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define SVX_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SVX_METHOD(set_up), SVX_METHOD(pages), SVX_METHOD(qk_norm_rope), SVX_METHOD(append), SVX_METHOD(decode),
-                         SVX_METHOD(evict), SVX_METHOD(residual_norm), {nullptr, nullptr, 0, nullptr}};
+                         SVX_METHOD(evict), SVX_METHOD(residual_norm),
+                         SVX_METHOD(decode_shared), SVX_METHOD(cross_attn), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "svx_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

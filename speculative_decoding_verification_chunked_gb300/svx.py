@@ -120,6 +120,22 @@ class Residual(ctypes.Structure):
                 ("flags", ctypes.c_uint32), ("pad", ctypes.c_int32)]
 
 
+class Prefixes(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("first", ctypes.c_void_p), ("max_len", ctypes.c_int64),
+                ("n_prefix", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class Cross(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("o", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("len", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("q_req", ctypes.c_int64), ("q_head", ctypes.c_int64), ("q_tok", ctypes.c_int64), ("kv_req", ctypes.c_int64),
+                ("kv_head", ctypes.c_int64), ("kv_state", ctypes.c_int64), ("o_req", ctypes.c_int64), ("o_head", ctypes.c_int64),
+                ("o_tok", ctypes.c_int64), ("mask_req", ctypes.c_int64), ("n_req", ctypes.c_int32), ("n_tok", ctypes.c_int32),
+                ("n_states", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("device", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
+
+
 # name -> (restype, argtypes); every symbol declared in include/svx.h
 _P = ctypes.c_void_p
 _SIGS = {
@@ -205,6 +221,12 @@ _SIGS = {
                                                  ctypes.POINTER(ctypes.c_int64)]),
     "svx_paged_evict": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32,
                                        ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, _P]),
+    "svx_paged_decode_shared_workspace": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int32,
+                                                         ctypes.POINTER(Prefixes), ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
+    "svx_paged_decode_shared": (ctypes.c_int, [ctypes.POINTER(Pages), ctypes.c_int32, ctypes.c_int32, _P, ctypes.POINTER(Prefixes),
+                                               _P, ctypes.c_int64, ctypes.c_float, _P, _P, _P, ctypes.c_int64, _P]),
+    "svx_cross_attn_workspace": (ctypes.c_int, [ctypes.POINTER(Cross), ctypes.POINTER(ctypes.c_int64)]),
+    "svx_cross_attn": (ctypes.c_int, [ctypes.POINTER(Cross), _P, ctypes.c_int64, _P]),
     "svx_residual_norm": (ctypes.c_int, [ctypes.POINTER(Residual), _P]),
     "svx_debug_clip_paged": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64]),
     "svx_version": (ctypes.c_char_p, []),
@@ -232,7 +254,7 @@ def version() -> str:
 
 
 ABI_STRUCTS = ("Config", "Part", "Stats", "WindowStats", "PlanEntry", "TierState", "SchedConfig", "DraftInstr",
-               "RopeTable", "Heads", "Pages", "Residual")
+               "RopeTable", "Heads", "Pages", "Residual", "Prefixes", "Cross")
 
 
 def abi_sizes() -> dict:
@@ -763,7 +785,9 @@ def _native():
         spec.loader.exec_module(mod)
         mod.set_up(SvxError, *[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "svx_qk_norm_rope", "svx_paged_append", "svx_paged_decode_workspace", "svx_paged_decode",
-            "svx_paged_evict_workspace", "svx_paged_evict", "svx_residual_norm", "svx_last_error")])
+            "svx_paged_evict_workspace", "svx_paged_evict", "svx_residual_norm",
+            "svx_paged_decode_shared_workspace", "svx_paged_decode_shared", "svx_cross_attn_workspace", "svx_cross_attn",
+            "svx_last_error")])
         _native_module = mod
     return _native_module
 
@@ -818,6 +842,21 @@ def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None
         with _on_stream(stream, q.get_device()):
             return qk_norm_rope(q, k, v, pos, rope, q_out, k_out, v_out, q_norm, k_norm, eps, n_new, status)
     (_native_module or _native()).qk_norm_rope(q, k, v, pos, rope.address, q_out, k_out, v_out, q_norm, k_norm, eps, n_new, status)
+
+
+def cross_attn(q, k, v, o, lse=None, lens=None, mask=None, scale: float = 0.0, status=None, workspace=None, stream=None):
+    """svx_cross_attn: tokens of a decoder attend to an encoder's states, of another length and in no order.
+
+    q, o: device bf16 or fp16 [B][Hq][n][d]; k, v: [B][S][Hkv][d], equally strided; rows of d dense, the other dimensions in any
+    order (transposed views of projections; all but o may be broadcast).  n from a single token up; S may be 0.  lse: fp32
+    [B][Hq][n], or None.  lens: int32 [B], states of each request that count (None: all); mask: bool [B][S], False: a state that does
+    not count; what such states hold is not used.  O = 0, LSE = -inf where none counts.  scale: 0 means 1/sqrt(d).  status: int32 [1]
+    that becomes non-zero if a length leaves [0, S], or None.  Several samples of one encoded input: their rows as tokens
+    (q viewed as [B][Hq][samples * n][d]), so that its states are read once for all of them."""
+    if stream is not None:
+        with _on_stream(stream, q.get_device()):
+            return cross_attn(q, k, v, o, lse, lens, mask, scale, status, workspace)
+    (_native_module or _native()).cross_attn(q, k, v, o, lse, lens, mask, scale, status, workspace)
 
 
 _ACTS = {None: 0, "tanh": 1, "sigmoid": 2}
@@ -911,6 +950,20 @@ class PagedCache:
             with _on_stream(stream, self.device):
                 return self.decode(q, table, lens, o, lse, max_len, scale, acc_in, acc_out, workspace)
         self._native.decode(self._pages, q, table, lens, o, lse, max_len, scale, acc_in, acc_out, workspace)
+
+    def decode_shared(self, q, prefix_table, prefix_lens, first, table, lens, o, lse, max_prefix: int = 0, max_len: int = 0,
+                      scale: float = 0.0, workspace=None, stream=None):
+        """svx_paged_decode_shared: decode for requests that share prefixes, which are read once for all their requests.
+
+        prefix_table: int32 [P][max_prefix_pages], prefix_lens: int32 [P]; first: int32 [P + 1]: requests [first[p], first[p + 1]) have
+        prefix p (neighbours in the batch; those outside [first[0], first[P]) have none).  table, lens: the requests' own slots,
+        behind the prefix (lens may be 0).  q, o: [B][Hq][1][d]; lse: fp32 [B][Hq][1].  max_prefix, max_len: bounds on the lengths
+        known on the host (0: what the tables hold)."""
+        if stream is not None:
+            with _on_stream(stream, self.device):
+                return self.decode_shared(q, prefix_table, prefix_lens, first, table, lens, o, lse, max_prefix, max_len, scale, workspace)
+        self._native.decode_shared(self._pages, q, prefix_table, prefix_lens, first, table, lens, o, lse, max_prefix, max_len, scale,
+                                   workspace)
 
     def evict(self, table, lens, budget: int, sink: int, recent: int, next_pos, acc_in, pos_in, acc_out, pos_out, len_out,
               max_len: int = 0, workspace=None, stream=None):
