@@ -88,6 +88,10 @@ struct AttendParams {
   int32_t prefix_apart;         // the prefixes are another kernel's work
   float* state_o;               // [2][n_req * n_q][D]: finished states, of the prefix and of the request's own slots
   float2* state_ml;             // [2][n_req * n_q]
+  // of rows_kernel (svx_rows.cuh)
+  float4* rows_o;               // [row_ctas][2][D / 4][item_rows]: states of items that more than one CTA works on
+  float2* rows_ml;              // [row_ctas][2][item_rows]
+  int32_t item_rows, row_ctas, min_tiles;
 };
 
 // The flat range of chunks, as every kernel of the call computes it from the lengths.  Sequences: the requests;
@@ -102,7 +106,7 @@ struct Plan {
   int32_t req0[SRC == kShared ? kMaxReq + 1 : 1];  // the first request of each prefix, and one past the last one's
 };
 
-// Sums x over the block's threads up to this one, and all of them into `total`.
+// Sums x over the first kMaxReq threads of the block up to this one, and all of theirs into `total`.
 __device__ __forceinline__ int block_scan(int x, int32_t* warp_sum, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -110,7 +114,7 @@ __device__ __forceinline__ int block_scan(int x, int32_t* warp_sum, int& total) 
     const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) warp_sum[warp] = x;
+  if (lane == 31 && warp < kWarps) warp_sum[warp] = x;
   __syncthreads();
   int base = 0;
   total = 0;
@@ -134,7 +138,7 @@ __device__ __forceinline__ void prefix_requests(const int32_t* first, int n_pref
     const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x = max(x, y);
   }
-  if (lane == 31) warp_top[warp] = x;
+  if (lane == 31 && warp < kWarps) warp_top[warp] = x;
   __syncthreads();
   int top = 0;
 #pragma unroll
@@ -143,7 +147,7 @@ __device__ __forceinline__ void prefix_requests(const int32_t* first, int n_pref
     if (w < warp) x = max(x, v);
     top = max(top, v);  // (threads behind the prefixes have 0)
   }
-  req0[t] = t < n_prefix ? x : top;  // (a prefix's end is the next one's begin)
+  if (t < kMaxReq) req0[t] = t < n_prefix ? x : top;  // (a prefix's end is the next one's begin)
   if (status && t < n_prefix && x != raw) atomicOr(status, kErrInput);
   __syncthreads();
   if (t == 0) {

@@ -4,7 +4,7 @@
 //
 // There is no order among states, so the tokens of a request and the query heads of a KV head are alike: rows of one product
 // with the same keys.
-#include "svx_attend.cuh"
+#include "svx_rows.cuh"
 
 namespace svx {
 namespace {
@@ -12,7 +12,10 @@ namespace {
 constexpr int64_t kMaxBlocks = 65535;
 
 struct CrossView {
+  bool many;  // rows of a request and KV head: more than one-token attention's kernels take at a time
   Sizes z;
+  RowSizes rz;
+  size_t total;
   AttendParams p;
 };
 
@@ -76,6 +79,12 @@ svx_status cross_view(const svx_cross* c, CrossView* out) {
   z.blocks = static_cast<int32_t>(blocks);
   z.whole = per_item <= kWholeItem && chunks <= sms * per_item;  // as in one-token attention over pages
   size_pieces(&z, chunks, a.head_dim, sms);
+  out->many = rows > kRowsMax;
+  if (out->many) {
+    const int64_t items = B * Hkv * ((rows + kRowTile - 1) / kRowTile), tiles = items * ((S + kTile - 1) / kTile);
+    size_rows(&out->rz, tiles, rows, a.head_dim, sms, 0);
+  }
+  out->total = out->many ? out->rz.total : z.total;
   AttendParams& p = out->p;
   p.pages.page_stride = B > 1 ? a.kv_req : 0;
   p.pages.tok_stride = S > 1 ? a.kv_state : 0;
@@ -102,7 +111,13 @@ svx_status cross_view(const svx_cross* c, CrossView* out) {
 }
 
 template <typename T, int D>
-cudaError_t launch_cross(const AttendParams& p, int device, cudaStream_t s) {
+cudaError_t launch_cross(const AttendParams& p, bool many, int device, cudaStream_t s) {
+  if (many) {
+    const cudaError_t e = launch_rows<T, kDense, D>(p, device, s);
+    if (e != cudaSuccess || p.row_ctas == 1) return e;
+    const int per = kWarps / (D / 16), jobs = (p.row_ctas - 1) * (p.item_rows / 8);
+    return launch_pdl(join_rows<T, kDense, D>, dim3(std::min((jobs + per - 1) / per, 8 * p.row_ctas)), dim3(kWarps * 32), 0, s, p);
+  }
   const cudaError_t e =
       p.rows > 8 ? launch_attend<T, kDense, D, true, false>(p, device, s) : launch_attend<T, kDense, D, false, false>(p, device, s);
   if (e != cudaSuccess || p.whole) return e;
@@ -117,7 +132,7 @@ extern "C" svx_status svx_cross_attn_workspace(const svx_cross* c, int64_t* byte
   *bytes = 0;
   svx::CrossView v = {};
   const svx_status st = svx::cross_view(c, &v);
-  if (st == SVX_OK) *bytes = static_cast<int64_t>(v.z.total);
+  if (st == SVX_OK) *bytes = static_cast<int64_t>(v.total);
   return st;
 }
 
@@ -145,9 +160,9 @@ extern "C" svx_status svx_cross_attn(const svx_cross* c, void* workspace, int64_
                   k = {a.n_states ? a.k : nullptr, states}, v_span = {a.n_states ? a.v : nullptr, states};
   if (svx::any_overlap({o, lse, status}, {q, k, v_span, len, mask}))
     return paged_fail(SVX_ERR_INVALID_ARG, "an output overlaps an input or another output");
-  if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(v.z.total))
-    return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", v.z.total);
-  if (svx::any_overlap({{workspace, v.z.total}}, {q, k, v_span, len, mask, o, lse, status}))
+  if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(v.total))
+    return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", v.total);
+  if (svx::any_overlap({{workspace, v.total}}, {q, k, v_span, len, mask, o, lse, status}))
     return paged_fail(SVX_ERR_INVALID_ARG, "the workspace overlaps another buffer");
   svx::PagedDevice dev(a.device);
   if (!dev.ok) return paged_fail(SVX_ERR_CUDA, "cannot use device %d", a.device);
@@ -166,12 +181,13 @@ extern "C" svx_status svx_cross_attn(const svx_cross* c, void* workspace, int64_
   p.o = a.o;
   p.lse = a.lse;
   svx::place_pieces(p, v.z, static_cast<char*>(workspace));
+  if (v.many) svx::place_rows(p, v.rz, static_cast<char*>(workspace));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a.dtype == SVX_BF16)
-    e = a.head_dim == 128 ? svx::launch_cross<__nv_bfloat16, 128>(p, a.device, s) : svx::launch_cross<__nv_bfloat16, 64>(p, a.device, s);
+    e = a.head_dim == 128 ? svx::launch_cross<__nv_bfloat16, 128>(p, v.many, a.device, s) : svx::launch_cross<__nv_bfloat16, 64>(p, v.many, a.device, s);
   else
-    e = a.head_dim == 128 ? svx::launch_cross<__half, 128>(p, a.device, s) : svx::launch_cross<__half, 64>(p, a.device, s);
+    e = a.head_dim == 128 ? svx::launch_cross<__half, 128>(p, v.many, a.device, s) : svx::launch_cross<__half, 64>(p, v.many, a.device, s);
   if (e != cudaSuccess) return paged_fail(SVX_ERR_CUDA, "cross attention launch failed: %s", cudaGetErrorString(e));
   return SVX_OK;
 }

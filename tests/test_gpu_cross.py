@@ -1,5 +1,7 @@
-"""Attention to an encoder's states on the GPU against a plain 64-bit implementation (bounds: attention_reference.near; a softmax
-weight enters the product with V in two 16-bit pieces, within 2^-15 of itself with its exponential and its sum)."""
+"""Attention to an encoder's states on the GPU against a plain 64-bit implementation (bounds: attention_reference.near).
+
+With up to 128 rows (query heads of a KV head times tokens) a softmax weight enters the product with V in two 16-bit pieces, within 2^-15 of
+itself with its exponential and its sum; with more it is rounded to the inputs' type once, by half a step."""
 import pytest
 import torch
 
@@ -8,7 +10,10 @@ from attention_reference import attend64, near
 pytestmark = pytest.mark.gpu
 
 TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
-P_ERROR = {"bf16": 2.0 ** -15, "fp16": 2.0 ** -15}
+
+
+def p_error(rows, ty):
+    return 2.0 ** -15 + (torch.finfo(TYPES[ty]).eps / 2 if rows > 128 else 0.0)
 
 
 @pytest.fixture(scope="module")
@@ -51,7 +56,7 @@ def check(q, k, v, o, lse, live, ty, scale=None):
         for h in range(hkv):
             heads = slice(h * group, (h + 1) * group)
             want = attend64(q[i, heads].reshape(-1, d), k[i, at, h], v[i, at, h], scale or d ** -0.5)
-            near(o[i, heads].reshape(-1, d), lse[i, heads].reshape(-1), want, P_ERROR[ty], len(at))
+            near(o[i, heads].reshape(-1, d), lse[i, heads].reshape(-1), want, p_error(group * n, ty), len(at))
 
 
 CASES = [  # b, n, hq, hkv, d, states, type, layout, lens, masked
