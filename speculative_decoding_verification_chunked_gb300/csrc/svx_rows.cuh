@@ -40,15 +40,17 @@ constexpr int kRowThreads = 384;
 template <int D, int QT>
 struct RowsCfg {
   static constexpr uint32_t TILE = kTile * D * 2;  // K or V
-  // with one row tile the bytes in flight decide: 5 tiles of 32 KiB (d = 128), 9 of 16 KiB (d = 64)
+  // with one row tile the bytes in flight decide: 5 tiles of 32 KiB (d = 128), 8 of 16 KiB (d = 64)
   static constexpr int KST = D == 128 ? 2 : 4;
-  static constexpr int VST = D == 128 ? 4 - QT : 5;
+  static constexpr int VST = D == 128 ? 4 - QT : 4;
+  static constexpr int QST = D == 128 ? 1 : 2;  // segments' Q: where there is room, the next one's comes in meanwhile
   static constexpr uint32_t Q_TILE = kRowTile * D * 2;
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_V = OFF_K + KST * TILE;
   static constexpr uint32_t OFF_Q = OFF_V + VST * TILE;
-  static constexpr uint32_t OFF_ML = OFF_Q + QT * Q_TILE;  // float2 [2][128]: the streams' states at a segment's end
-  static constexpr int N_BAR = 2 * KST + 2 * VST + 2 + 2 + 2 + 2 + 1 + 1;
+  static constexpr uint32_t OFF_OUT = OFF_Q + QST * QT * Q_TILE;  // [8 warps][32 rows][32 dimensions]: outputs on their way
+  static constexpr uint32_t OFF_ML = OFF_OUT + 8 * 2048;  // float2 [2][128]: the streams' states at a segment's end
+  static constexpr int N_BAR = 2 * KST + 2 * VST + 2 * QST + 2 + 2 + 2 + 1 + 1;
   static constexpr uint32_t OFF_BAR = OFF_ML + 2 * kRowTile * 8;
   static constexpr uint32_t OFF_MISC = OFF_BAR + N_BAR * 8;  // [0] TMEM base, [1] abort flag
   static constexpr uint32_t BYTES = OFF_MISC + 16;
@@ -100,24 +102,39 @@ __device__ __forceinline__ bool softmax_sync(bool ok) {
       : "memory");
   return r != 0;
 }
-// D = A B (+ D), operands as the low words of shared-memory descriptors (the high word is the same for all).
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool add) {
+// Shared-memory descriptor, 128-byte swizzle: high word (stride between groups of 8 rows 1024 bytes, version, swizzle mode); low word:
+// desc_of (address, leading-dimension offset).
+constexpr uint32_t kRowsDescHi = (1024u >> 4) | (1u << (46 - 32)) | (2u << (61 - 32));
+// One lane of a converged warp.  The warp that issues the products stays converged and holds their operands alike in all lanes: then they
+// are in uniform registers, where the instructions take them from (issued from a branch of one lane, a product took 60 to 70
+// cycles to issue, as long as it takes to run, and a commit 100).
+__device__ __forceinline__ uint32_t one_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e) :: "memory");
+  return e;
+}
+// D = A B (+ D), issued by the lane with `one`; operands as the low words of shared-memory descriptors (the high word is the same
+// for all).
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\tmov.b64 da, {%1, %3};\n\t"
+      "mov.b64 db, {%2, %3};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kRowsDescHi), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(one)
       : "memory");
 }
 // The same with A in tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\tmov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kRowsDescHi), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
+      : "memory");
 }
 
 // 32 columns of this warp's 32 lanes (a thread: its lane); the wait is in the same statement, so that no value is used early.
@@ -136,6 +153,39 @@ __device__ __forceinline__ void tmem_read32(uint32_t at, float (&v)[N]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[OFF + i] = __uint_as_float(r[i]);
+}
+// 128 columns.
+__device__ __forceinline__ void tmem_read128(uint32_t at, float (&v)[128]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
+      "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
+      "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
+        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
+        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]),
+        "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
+        "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63]), "=f"(v[64]),
+        "=f"(v[65]), "=f"(v[66]), "=f"(v[67]), "=f"(v[68]), "=f"(v[69]), "=f"(v[70]), "=f"(v[71]), "=f"(v[72]),
+        "=f"(v[73]), "=f"(v[74]), "=f"(v[75]), "=f"(v[76]), "=f"(v[77]), "=f"(v[78]), "=f"(v[79]), "=f"(v[80]),
+        "=f"(v[81]), "=f"(v[82]), "=f"(v[83]), "=f"(v[84]), "=f"(v[85]), "=f"(v[86]), "=f"(v[87]), "=f"(v[88]),
+        "=f"(v[89]), "=f"(v[90]), "=f"(v[91]), "=f"(v[92]), "=f"(v[93]), "=f"(v[94]), "=f"(v[95]), "=f"(v[96]),
+        "=f"(v[97]), "=f"(v[98]), "=f"(v[99]), "=f"(v[100]), "=f"(v[101]), "=f"(v[102]), "=f"(v[103]), "=f"(v[104]),
+        "=f"(v[105]), "=f"(v[106]), "=f"(v[107]), "=f"(v[108]), "=f"(v[109]), "=f"(v[110]), "=f"(v[111]),
+        "=f"(v[112]), "=f"(v[113]), "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]),
+        "=f"(v[119]), "=f"(v[120]), "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]),
+        "=f"(v[126]), "=f"(v[127])
+      : "r"(at)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_write32(uint32_t at, const float (&v)[32]) {
   asm volatile(
@@ -163,9 +213,6 @@ constexpr uint32_t rows_idesc(int N, bool b_mn_major) {
   return (1u << 4) | (type << 7) | (type << 10) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(kRowTile >> 4) << 24);
 }
-// Shared-memory descriptor, 128-byte swizzle: high word (stride between groups of 8 rows 1024 bytes, version, swizzle mode), low word
-// (address, leading-dimension offset).
-constexpr uint32_t kRowsDescHi = (1024u >> 4) | (1u << (46 - 32)) | (2u << (61 - 32));
 __device__ __forceinline__ uint32_t desc_of(uint32_t addr, uint32_t lead) {
   return ((addr >> 4) & 0x3FFFu) | (((lead >> 4) & 0x3FFFu) << 16);
 }
@@ -290,6 +337,8 @@ struct RowWaiter {
     *abort = 1u;
     if (status) atomicOr(status, kErrWait);
   }
+  // (a converged warp stays so: all lanes' results are the same)
+  __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); }
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
     if (bar_try(bar, parity)) return true;
     const uint64_t t0 = now_ns();
@@ -318,8 +367,63 @@ struct RowWaiter {
 // Which keys of a tile count, bit r % 32 of word r / 32; a warp's lanes together.
 struct Seen {
   uint32_t w[4];
-  __device__ __forceinline__ bool at(int r) const { return w[r >> 5] >> (r & 31) & 1u; }
 };
+// Scores of keys that do not count become -inf (out of line, so that the loop's usual path stays short).
+__device__ __noinline__ void hide_keys(uint32_t at, Seen seen) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t w = c < 2 ? (c == 0 ? seen.w[0] : seen.w[1]) : c == 2 ? seen.w[2] : seen.w[3];
+    if (w == 0xffffffffu) continue;
+    float v[32];
+    tmem_read32<0>(at + c * 32, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = w >> k & 1u ? v[k] : kNegInf;
+    tmem_write32(at + c * 32, v);
+  }
+  tmem_written();
+}
+__device__ __noinline__ void scale_columns(uint32_t at, int n, float f) {
+#pragma unroll 1
+  for (int c = 0; c < n; c += 32) {
+    float v[32];
+    tmem_read32<0>(at + c, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] *= f;
+    tmem_write32(at + c, v);
+  }
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max128(const float (&v)[kTile]) {
+  float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int k = 4; k < 124; k += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = max3(m[e], v[k + 2 * e], v[k + 2 * e + 1]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], v[124 + e]);
+  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+// two fp32 values in one register pair
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 template <int SRC>
 __device__ __forceinline__ Seen keys_seen(const AttendParams& P, const RowSeg& g, int t0) {
   const int lane = threadIdx.x & 31;
@@ -343,9 +447,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
   __shared__ RowPlan plan;
   const uint32_t raw = smem_at(smem_raw), base = (raw + 1023u) & ~1023u;
   unsigned char* const gbase = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t KFULL = base + C::OFF_BAR, KEMPTY = KFULL + 8u * C::KST, VFULL = KEMPTY + 8u * C::KST,
-                 VEMPTY = VFULL + 8u * C::VST, QFULL = VEMPTY + 8u * C::VST, QEMPTY = QFULL + 8u, SFULL = QEMPTY + 8u,
+                 VEMPTY = VFULL + 8u * C::VST, QFULL = VEMPTY + 8u * C::VST, QEMPTY = QFULL + 8u * C::QST, SFULL = QEMPTY + 8u * C::QST,
                  PFULL = SFULL + 16u, OFULL = PFULL + 16u, OEMPTY = OFULL + 16u, DRAIN = OEMPTY + 8u;
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(gbase + C::OFF_MISC);
   if (threadIdx.x == 0) {
@@ -357,8 +461,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       bar_init(VFULL + 8u * i, 32);
       bar_init(VEMPTY + 8u * i, 1);
     }
-    bar_init(QFULL, 32);
-    bar_init(QEMPTY, 1);
+    for (int i = 0; i < C::QST; ++i) {
+      bar_init(QFULL + 8u * i, 32);
+      bar_init(QEMPTY + 8u * i, 1);
+    }
     for (int i = 0; i < 2; ++i) {
       bar_init(SFULL + 8u * i, 1);
       bar_init(PFULL + 8u * i, 128);
@@ -380,7 +486,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
   allow_dependents();
   const int T_all = build_row_plan<SRC>(P, plan, blockIdx.x == 0);  // (its barriers also show the lines above to all threads)
   tc_after();
-  const uint32_t tmem = misc[0];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
   const RowSplit split(P, T_all);
   const int x0 = blockIdx.x < split.used ? split.begin(blockIdx.x) : 0, x1 = blockIdx.x < split.used ? split.begin(blockIdx.x + 1) : 0;
   RowWaiter W{misc + 1, P.pages.status};
@@ -434,11 +540,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
           if (off[u] >= 0 && !in_bounds(pool + off[u], D, pool, P.pages.extent, P.pages.status, kSitePool)) off[u] = -1;
         }
         const int stage = i % stages;
-        if (i >= stages && !__all_sync(0xffffffffu, W.wait(empty + 8u * stage, (i / stages - 1) & 1u))) {
+        if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
           ok = false;
           break;
         }
         const uint32_t dst = ring + stage * C::TILE + (piece >> 3) * kHalf;
+        if (!kBoundsChecked && SRC == kDense && (seen.w[0] & seen.w[1] & seen.w[2] & seen.w[3]) == 0xffffffffu) {
+          const T* src = pool + g.b * P.pages.page_stride + (t0 + r0) * P.pages.tok_stride + g.h * P.pages.head_stride + piece * 8;
+          const int64_t step = RPI * P.pages.tok_stride;
+#pragma unroll 8
+          for (int r = r0; r < kTile; r += RPI, src += step) copy16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), src, 16);
+          copies_arrive(full + 8u * stage);
+          continue;
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll 8
@@ -453,90 +567,96 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 11) {
-    // ---- Q: the segment's rows, once the products of the last one's are done
-    const T* const q = static_cast<const T*>(P.q);
+    // ---- Q: a segment's rows, once the products of the one before it in the same place are done
+    constexpr int PIECES = D / 8, RPI = 32 / PIECES;
+    const int piece = lane % PIECES, r0 = lane / PIECES;
+    const T* const q = static_cast<const T*>(P.q) + piece * 8;
     int seg = 0;
     for (int x = x0; x < x1; ++seg) {
       const RowSeg g = row_seg<SRC>(P, plan, x, x1);
-      if (seg > 0 && !__all_sync(0xffffffffu, W.wait(QEMPTY, (seg - 1) & 1u))) break;
-      constexpr int PIECES = D / 8, RPI = 32 / PIECES;
-      const int piece = lane % PIECES, rows = g.rows > kRowTile ? 2 * kRowTile : kRowTile;
-#pragma unroll 4
-      for (int r = lane / PIECES; r < rows; r += RPI) {
-        const bool in = r < g.rows;
-        copy16(base + C::OFF_Q + (r / kRowTile) * C::Q_TILE + (piece >> 3) * kHalf + (r % kRowTile) * 128 + (((piece & 7) ^ (r & 7)) << 4),
-               q + (in ? row_q<SRC, D>(P, plan, g, r) + piece * 8 : 0), in ? 16 : 0);
+      const int buf = seg % C::QST;
+      const uint32_t dst = base + C::OFF_Q + buf * (QT * C::Q_TILE) + (piece >> 3) * kHalf;
+      // lane l works out the places of rows l, l + 32, ..
+      int64_t off[QT * 4];
+#pragma unroll
+      for (int u = 0; u < QT * 4; ++u) off[u] = u * 32 + lane < g.rows ? row_q<SRC, D>(P, plan, g, u * 32 + lane) : -1;
+      if (seg >= C::QST && !W.warp_wait(QEMPTY + 8u * buf, (seg / C::QST - 1) & 1u)) break;
+#pragma unroll
+      for (int u = 0; u < QT * 4; ++u) {
+        if (QT == 2 && u >= 4 && g.rows <= kRowTile) break;
+#pragma unroll 8
+        for (int j = 0; j < 32 / RPI; ++j) {
+          const int in32 = j * RPI + r0, r = (u & 3) * 32 + in32;
+          const int64_t ro = __shfl_sync(0xffffffffu, off[u], in32);
+          copy16(dst + (u >> 2) * C::Q_TILE + r * 128 + (((piece & 7) ^ (r & 7)) << 4), q + (ro >= 0 ? ro : 0), ro >= 0 ? 16 : 0);
+        }
       }
-      copies_arrive(QFULL);
+      copies_arrive(QFULL + 8u * buf);
       x += g.n;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ---- the products.  Step u of a segment: stream u & 1; S(u + 2) follows P V(u), whose P lies over it
     constexpr uint32_t idesc_s = rows_idesc<T>(kTile, false), idesc_o = rows_idesc<T>(D, true);
-    int seg = 0, kt = 0, vt = 0;  // segments, and tiles of K and V used, so far
-    uint32_t np[2] = {0, 0};      // P's of each stream so far
+    const uint32_t one = one_lane();
+    int seg = 0, kt = 0, vt = 0, qb = 0;     // segments so far, and the places of the next K, V and Q
+    uint32_t kp = 0, vp = 0, qp = 0, np = 0; // parities: of the rings' rounds, and of each stream's P's (bit s)
     bool ok = true;
     for (int x = x0; x < x1 && ok; ++seg) {
       const RowSeg g = row_seg<SRC>(P, plan, x, x1);
-      if (lane == 0) {
-        const bool two = QT == 2 && g.rows > kRowTile;
-        const int steps = two ? 2 * g.n : g.n;
-        auto issue_s = [&](int u) {
-          const int s = u & 1;
-          const bool opens = !two || s == 0, closes = !two || s == 1;  // the first and last use of the tile
-          const int stage = kt % C::KST;
-          if (opens && !W.wait(KFULL + 8u * stage, (kt / C::KST) & 1u)) return false;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // copies (generic proxy) before the tensor cores' reads
-          tc_after();
-          const uint32_t a = desc_of(base + C::OFF_Q + (two ? s : 0) * C::Q_TILE, 16), b = desc_of(base + C::OFF_K + stage * C::TILE, 16);
+      const bool two = QT == 2 && __shfl_sync(0xffffffffu, g.rows, 0) > kRowTile;
+      const int steps = __shfl_sync(0xffffffffu, g.n, 0) << (two ? 1 : 0);
+      auto issue_s = [&](int u) {
+        const int s = u & 1;
+        const bool opens = !two || s == 0, closes = !two || s == 1;  // the first and last use of the tile
+        if (opens && !W.warp_wait(KFULL + 8u * kt, kp)) return false;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // copies (generic proxy) before the tensor cores' reads
+        tc_after();
+        const uint32_t a = desc_of(base + C::OFF_Q, 16) + (qb * QT * C::Q_TILE >> 4) + (two && s ? C::Q_TILE >> 4 : 0), b = desc_of(base + C::OFF_K, 16) + kt * (C::TILE >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t adv = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-            mma_ss(tmem + s * 128, a + adv, b + adv, kRowsDescHi, idesc_s, k > 0);
-          }
-          commit(SFULL + 8u * s);
-          if (closes) {
-            commit(KEMPTY + 8u * stage);
-            ++kt;
-          }
-          if (u == steps - 1) commit(QEMPTY);
-          return true;
-        };
-        ok = W.wait(QFULL, seg & 1u) && issue_s(0) && (steps == 1 || issue_s(1));
-        for (int u = 0; u < steps && ok; ++u) {
-          const int s = u & 1;
-          const bool opens = !two || s == 0, closes = !two || s == 1;
-          const int stage = vt % C::VST;
-          ok = (!opens || W.wait(VFULL + 8u * stage, (vt / C::VST) & 1u)) && (u > 0 || seg == 0 || W.wait(OEMPTY, (seg - 1) & 1u)) &&
-               W.wait(PFULL + 8u * s, np[s] & 1u);
-          if (!ok) break;
-          ++np[s];
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          tc_after();
-          const uint32_t a = tmem + s * 128, d = tmem + C::O_COL + s * D;
-          const uint32_t b = desc_of(base + C::OFF_V + stage * C::TILE, kHalf);
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a + k * 8, b + ((k * 2048) >> 4), kRowsDescHi, idesc_o, u > 1 || k > 0);
-          if (!two) {
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a + 64 + k * 8, b + ((k * 2048) >> 4), kRowsDescHi, idesc_o, true);
-          }
-          if (closes) {
-            commit(VEMPTY + 8u * stage);
-            ++vt;
-          }
-          if (u + 2 >= steps) commit(OFULL + 8u * s);  // the stream's last
-          else ok = issue_s(u + 2);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t adv = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+          mma_ss(one, tmem + s * 128, a + adv, b + adv, idesc_s, k > 0);
         }
+        commit(one, SFULL + 8u * s);
+        if (closes) {
+          commit(one, KEMPTY + 8u * kt);
+          if (++kt == C::KST) kt = 0, kp ^= 1u;
+        }
+        if (u == steps - 1) commit(one, QEMPTY + 8u * qb);
+        return true;
+      };
+      ok = W.warp_wait(QFULL + 8u * qb, qp) && issue_s(0) && (steps == 1 || issue_s(1));
+      for (int u = 0; u < steps && ok; ++u) {
+        const int s = u & 1;
+        const bool opens = !two || s == 0, closes = !two || s == 1;
+        ok = (!opens || W.warp_wait(VFULL + 8u * vt, vp)) && (u > 0 || seg == 0 || W.warp_wait(OEMPTY, (seg - 1) & 1u)) &&
+             W.warp_wait(PFULL + 8u * s, np >> s & 1u);
+        if (!ok) break;
+        np ^= 1u << s;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_after();
+        const uint32_t a = tmem + s * 128, d = tmem + C::O_COL + s * D;
+        const uint32_t b = desc_of(base + C::OFF_V, kHalf) + vt * (C::TILE >> 4);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k) mma_ts(one, d, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 2048) >> 4), idesc_o, u > 1 || k > 0);
+        if constexpr (QT == 1) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) mma_ts(one, d, a + (k >> 1) * 32 + 16 + (k & 1) * 8, b + ((k * 2048) >> 4), idesc_o, true);
+        }
+        if (closes) {
+          commit(one, VEMPTY + 8u * vt);
+          if (++vt == C::VST) vt = 0, vp ^= 1u;
+        }
+        if (u + 2 >= steps) commit(one, OFULL + 8u * s);  // the stream's last
+        else ok = issue_s(u + 2);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (++qb == C::QST) qb = 0, qp ^= 1u;
       x += g.n;
     }
-    if (lane == 0) {  // every product issued here has ended before the tensor memory is given back
-      commit(DRAIN);
-      W.drain(DRAIN, 0u);
-    }
+    // every product issued here has ended before the tensor memory is given back
+    commit(one, DRAIN);
+    W.drain(DRAIN, 0u);
     __syncwarp();
   }
   } else {
@@ -546,6 +666,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, in an address's upper half
     const uint32_t at_s = tmem + lanes + s * 128;
     float2* const s_ml = reinterpret_cast<float2*>(gbase + C::OFF_ML);
+    uint4* const out = reinterpret_cast<uint4*>(gbase + C::OFF_OUT) + warp * 128;
     uint32_t ns = 0, no[2] = {0, 0};  // S's of this stream, and ends of both, so far
     bool ok = true;
     for (int x = x0; x < x1;) {
@@ -559,60 +680,48 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       for (int i = 0; i < mine; ++i, ++ns) {
         const int t0 = (g.tile0 + (two ? i : 2 * i + s)) * kTile;
         const bool all = (SRC != kDense || !P.mask) && t0 + kTile <= g.len;
-        Seen seen;
+        Seen seen = {};
         if (!all) seen = keys_seen<SRC>(P, g, t0);
-        if (!__all_sync(0xffffffffu, W.wait(SFULL + 8u * s, ns & 1u))) {
+        if (!W.warp_wait(SFULL + 8u * s, ns & 1u)) {
           ok = false;
           break;
         }
         if (busy) {
           tc_after();
+          if (!all) hide_keys(at_s, seen);
           float v[kTile];
-          tmem_read32<0>(at_s, v);
-          tmem_read32<32>(at_s + 32, v);
-          tmem_read32<64>(at_s + 64, v);
-          tmem_read32<96>(at_s + 96, v);
-          if (!all) {
-#pragma unroll
-            for (int k = 0; k < kTile; ++k) v[k] = seen.at(k) ? v[k] : kNegInf;
-          }
-          float top = v[0];
-#pragma unroll
-          for (int k = 1; k < kTile; ++k) top = fmaxf(top, v[k]);
-          top = top * P.scale;
+          tmem_read128(at_s, v);
+          const float top = max128(v) * P.scale;
           if (__any_sync(0xffffffffu, top > m + (kTau + Mma<T>::kLift))) {
             const float now = fmaxf(m, top - Mma<T>::kLift);
             const float f = now == kNegInf ? 1.f : ex2(m - now);
             m = now;
             l *= f;
-            if (i > 0) {  // S(i) was issued behind P V(i - 1), so O holds all up to it
-#pragma unroll
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_read32<0>(tmem + lanes + C::O_COL + s * D + c, o);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= f;
-                tmem_write32(tmem + lanes + C::O_COL + s * D + c, o);
-              }
-            }
+            if (i > 0) scale_columns(tmem + lanes + C::O_COL + s * D, D, f);  // S(i) was issued behind P V(i - 1): O holds all up to it
           }
           const float less = m == kNegInf ? 0.f : -m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t scale2 = pair(P.scale, P.scale), less2 = pair(less, less);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int c = 0; c < kTile; c += 32) {
+          for (int c = 0; c < 4; ++c) {
             uint32_t hi[16], lo[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float a = ex2(fmaf(v[c + 2 * k], P.scale, less)), b = ex2(fmaf(v[c + 2 * k + 1], P.scale, less));
-              sum[(2 * k) & 3] += a;
-              sum[(2 * k + 1) & 3] += b;
-              if (two) hi[k] = Mma<T>::down2(a, b);
-              else Mma<T>::split(a, b, hi[k], lo[k]);
+              float a, b;
+              unpair(fma2(pair(v[c * 32 + 2 * k], v[c * 32 + 2 * k + 1]), scale2, less2), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              sum[k & 1] = add2(sum[k & 1], pair(a, b));
+              if constexpr (QT == 1) Mma<T>::split(a, b, hi[k], lo[k]);
+              else hi[k] = Mma<T>::down2(a, b);
             }
-            tmem_write16(at_s + c / 2, hi);
-            if (!two) tmem_write16(at_s + 64 + c / 2, lo);
+            // P of 32 keys, and what its rounding left, over the 32 columns of their S
+            tmem_write16(at_s + c * 32, hi);
+            if constexpr (QT == 1) tmem_write16(at_s + c * 32 + 16, lo);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float a, b;
+          unpair(add2(sum[0], sum[1]), a, b);
+          l += a + b;
           tmem_written();
           tc_before();
         }
@@ -664,16 +773,27 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
               for (int k = 0; k < 32; ++k) o[k] = fmaf(o1[k], f1, o[k]);
             }
           }
-          if (!mine_too) continue;
           if (whole && SRC == kDense) {
+            // through shared memory, so that four lanes write 64 bytes of a row (a row a lane: 32 rows a store, and four
+            // times as long).  16-byte pieces are permuted by the row: no two of a store's or a load's 8 lanes share a bank
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
+            for (int k = 0; k < 4; ++k) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                w[e] = l == 0.f ? 0u : Mma<T>::down2(o[k + 2 * e] * inv, o[k + 2 * e + 1] * inv);
-              *reinterpret_cast<uint4*>(static_cast<T*>(P.o) + at.o + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                w[e] = l == 0.f ? 0u : Mma<T>::down2(o[k * 8 + 2 * e] * inv, o[k * 8 + 2 * e + 1] * inv);
+              out[lane * 4 + (k ^ (lane >> 1 & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int from = k * 8 + (lane >> 2);
+              const int64_t to = __shfl_sync(0xffffffffu, mine_too ? at.o : -1, from);
+              const uint4 w = out[from * 4 + ((lane & 3) ^ (from >> 1 & 3))];
+              if (to >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(P.o) + to + c + (lane & 3) * 8) = w;
+            }
+            __syncwarp();
+          } else if (!mine_too) {
           } else if (whole) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
@@ -701,49 +821,60 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
 }
 
-// Merges the pieces of the items that more than one CTA worked on.  A job: an item, found at the first boundary between CTAs that it
-// crosses, and 8 of its rows; a warp: 8 rows x 16 dimensions.
+// Merges the pieces of the items that more than one CTA worked on.  CTA (x, y): the item found at the first boundary between CTAs that it
+// crosses, and 32 of its rows, one a lane; of the dimensions, blocks y, y + gridDim.y, .. of 32.
 template <typename T, int SRC, int D>
 __global__ void __launch_bounds__(kWarps * 32) join_rows(const __grid_constant__ AttendParams P) {
-  constexpr int BLOCKS = D / 16, PER = kWarps / BLOCKS;  // blocks of dimensions; row groups at a time
   __shared__ RowPlan plan;
+  __shared__ float s_f[kMaxCtas][32];  // a piece's factor for each row
+  __shared__ float s_x[kWarps][32];
   const int T_all = build_row_plan<SRC>(P, plan, false);
   const RowSplit split(P, T_all);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r8 = lane & 7, d4 = (warp % BLOCKS) * 4 + (lane >> 3);
+  const int groups = P.item_rows / 32, c0 = blockIdx.x / groups, r = (blockIdx.x - c0 * groups) * 32 + lane;
   grid_dependency_wait();
   allow_dependents();
-  const int groups = P.item_rows / 8, jobs = max(static_cast<int>(split.used) - 1, 0) * groups;
-  for (int j = blockIdx.x * PER + warp / BLOCKS; j < jobs; j += gridDim.x * PER) {
-    const int c0 = j / groups, r = (j - c0 * groups) * 8 + r8;
-    const int x = split.begin(c0 + 1);
-    const RowSeg g = row_seg<SRC>(P, plan, x, x + 1);
-    if (g.first >= x || g.first < split.begin(c0) || r - r8 >= g.rows) continue;
-    const int pieces = split.of(g.end - 1) - c0 + 1;
-    const float2* ml = P.rows_ml + static_cast<int64_t>(c0) * 2 * P.item_rows + r;
-    const float4* po = P.rows_o + (static_cast<int64_t>(c0) * 2 * (D / 4) + d4) * P.item_rows + r;
-    auto slot = [](int c) { return c == 0 ? 1 : 2 * c; };
-    const bool in = r < g.rows;
-    float M = kNegInf;
-    for (int c = lane >> 3; c < pieces && in; c += 4) M = fmaxf(M, __ldcg(ml + static_cast<int64_t>(slot(c)) * P.item_rows).x);
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-    if (!in) continue;
-    const float less = M == kNegInf ? 0.f : -M;
-    float L = 0.f;
+  if (c0 + 1 >= static_cast<int>(split.used)) return;
+  const int x = split.begin(c0 + 1);
+  const RowSeg g = row_seg<SRC>(P, plan, x, x + 1);
+  if (g.first >= x || g.first < split.begin(c0) || r - lane >= g.rows) return;
+  const int pieces = split.of(g.end - 1) - c0 + 1;
+  auto slot = [&](int c) { return static_cast<int64_t>(c0) * 2 + (c == 0 ? 1 : 2 * c); };
+  const bool in = r < g.rows;
+  float M = kNegInf;
+  for (int c = warp; c < pieces && in; c += kWarps) M = fmaxf(M, __ldcg(P.rows_ml + slot(c) * P.item_rows + r).x);
+  s_x[warp][lane] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_x[w][lane]);
+  const float less = M == kNegInf ? 0.f : -M;
+  float L = 0.f;
+  for (int c = warp; c < pieces && in; c += kWarps) {
+    const float2 ml = __ldcg(P.rows_ml + slot(c) * P.item_rows + r);
+    const float f = ex2(ml.x + less);
+    s_f[c][lane] = f;
+    L = fmaf(ml.y, f, L);
+  }
+  __syncthreads();
+  s_x[warp][lane] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) L += s_x[w][lane];
+  if (!in) return;
+  const RowOut at = row_out<SRC, D>(P, plan, g, r);
+  for (int d4 = blockIdx.y * kWarps + warp; d4 < D / 4; d4 += gridDim.y * kWarps) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int c = 0; c < pieces; ++c) {
-      const float2 s = __ldcg(ml + static_cast<int64_t>(slot(c)) * P.item_rows);
-      const float4 v = __ldcg(po + static_cast<int64_t>(slot(c)) * (D / 4) * P.item_rows);
-      const float f = ex2(s.x + less);
-      L = fmaf(s.y, f, L);
+      const float4 v = __ldcg(P.rows_o + (slot(c) * (D / 4) + d4) * P.item_rows + r);
+      const float f = s_f[c][lane];
       o.x = fmaf(v.x, f, o.x);
       o.y = fmaf(v.y, f, o.y);
       o.z = fmaf(v.z, f, o.z);
       o.w = fmaf(v.w, f, o.w);
     }
-    write_row<T>(P, row_out<SRC, D>(P, plan, g, r), d4 * 4, M, L, o);
+    write_row<T>(P, at, d4 * 4, M, L, o);
   }
 }
 
