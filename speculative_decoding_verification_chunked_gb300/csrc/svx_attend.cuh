@@ -104,7 +104,10 @@ struct Plan {
   int32_t n[SEQS];          // chunks of one of a sequence's items
   int32_t len[SEQS];        // its length, within bounds
   int32_t req0[SRC == kShared ? kMaxReq + 1 : 1];  // the first request of each prefix, and one past the last one's
+  int32_t row_tiles;        // (join_shared) rows_kernel's tiles
 };
+
+constexpr int kTile = 128;  // keys of a tile of rows_kernel
 
 // Sums x over the first kMaxReq threads of the block up to this one, and all of theirs into `total`.
 __device__ __forceinline__ int block_scan(int x, int32_t* warp_sum, int& total) {
@@ -158,8 +161,9 @@ __device__ __forceinline__ void prefix_requests(const int32_t* first, int n_pref
   __syncthreads();
 }
 
+// `tiles`: the prefixes are rows_kernel's work, and `first` and `n` of theirs count its tiles, from 0 (the join's view).
 template <int SRC, int CT>
-__device__ __forceinline__ int build_plan(const AttendParams& P, Plan<SRC>& s, bool report) {
+__device__ __forceinline__ int build_plan(const AttendParams& P, Plan<SRC>& s, bool report, bool tiles = false) {
   // one request per thread (kMaxReq = threads of a block), prefix sum over the block
   static_assert(kMaxReq == kWarps * 32, "one thread per request");
   const int t = threadIdx.x;
@@ -173,11 +177,16 @@ __device__ __forceinline__ int build_plan(const AttendParams& P, Plan<SRC>& s, b
       if (report && n != raw) atomicOr(P.pages.status, kErrInput);
       rows = (s.req0[t + 1] - s.req0[t]) * P.group;
     }
-    const int chunks = P.prefix_apart || rows == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(n) + (CT - 1)) / CT);
+    const int per = tiles ? kTile : CT, block = tiles ? P.item_rows : kRowsMax;
+    const int chunks = (P.prefix_apart && !tiles) || rows == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(n) + (per - 1)) / per);
     s.n[t] = chunks;
     s.len[t] = n;
-    const int mine = P.pages.n_kv_heads * ((rows + kRowsMax - 1) / kRowsMax) * chunks;
+    const int mine = P.pages.n_kv_heads * ((rows + block - 1) / block) * chunks;
     s.first[t] = block_scan(mine, s.warp_sum, before) - mine;
+    if (tiles) {
+      if (t == 0) s.row_tiles = before;
+      before = 0;
+    }
     __syncthreads();
   }
   constexpr int at = SRC == kShared ? kMaxReq : 0;
@@ -426,10 +435,9 @@ __device__ __forceinline__ void write_row(const AttendParams& P, const RowOut& a
   if (d4 == 0 && P.lse) P.lse[at.lse] = L == 0.f ? kNegInf : (M + log2f(L)) * kLn2;
 }
 
-// Requests without slots: O = 0, LSE = -inf (kShared: the join's work).
+// Requests without slots: O = 0, LSE = -inf.
 template <typename T, int SRC, int D>
 __device__ __forceinline__ void write_empty(const AttendParams& P, const Plan<SRC>& plan) {
-  if constexpr (SRC == kShared) return;
   for (int b = blockIdx.x; b < P.pages.n_req; b += gridDim.x) {
     if (plan.first[b + 1] > plan.first[b]) continue;
     if constexpr (SRC == kDense) {
@@ -459,13 +467,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
   __shared__ Plan<SRC> plan;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  grid_dependency_wait();
+  // Behind rows_kernel, which takes the prefixes: neither reads what the other writes, and that one had waited for all
+  // that came before when it let this one start.  The wait is for the join, which relies on this kernel's end.
+  const bool beside = SRC == kShared && P.prefix_apart;
+  if (!beside) grid_dependency_wait();
   allow_dependents();
   const int T_all = build_plan<SRC, CT>(P, plan, blockIdx.x == 0);
 
   const Split split(P, T_all);
   if (blockIdx.x >= split.used) {
-    write_empty<T, SRC, D>(P, plan);
+    if constexpr (SRC != kShared) write_empty<T, SRC, D>(P, plan);  // (kShared: the join's work)
+    if (beside) grid_dependency_wait();
     return;
   }
   int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
@@ -851,7 +863,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
       if (d4 == 0) P.part_ml[slot] = make_float2(M, L);
     }
   }
-  write_empty<T, SRC, D>(P, plan);
+  if constexpr (SRC != kShared) write_empty<T, SRC, D>(P, plan);
+  if (beside) grid_dependency_wait();
 }
 
 // Merges the pieces of the items that more than one CTA worked on, and adds the weights.  CTA (x, y): KV head x of all

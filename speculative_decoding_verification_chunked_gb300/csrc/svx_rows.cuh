@@ -31,7 +31,6 @@ namespace svx {
 namespace {
 
 constexpr int kRowTile = 128;
-constexpr int kTile = 128;                   // keys
 constexpr uint32_t kHalf = kTile * 128;      // bytes of 64 dimensions of 128 rows (an operand's swizzle atoms: 8 rows of 128 bytes)
 constexpr uint64_t kWaitLimit = 2000000000ull;
 constexpr int kRowThreads = 384;

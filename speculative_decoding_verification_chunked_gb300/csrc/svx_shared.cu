@@ -1,9 +1,10 @@
 // Attention of one new token per request over a paged cache, for requests that share prefixes: a prefix's K and V are read once
 // for all its requests, whose tokens' query heads are the rows of one product with them.
 //
-// Two kinds of sequences lie in one flat range of chunks (svx_attend.cuh): the prefixes, with the rows of all their requests, and
-// the requests' own slots.  Every row then has two lots of states (m, l, O), which join_shared merges.
-#include "svx_attend.cuh"
+// With few rows to a prefix two kinds of sequences lie in one flat range of chunks (attend_kernel, svx_attend.cuh): the prefixes, with
+// the rows of all their requests, and the requests' own slots.  With many rows the prefixes are rows_kernel's work (svx_rows.cuh) and
+// attend_kernel beside it takes the requests' own slots.  Every row then has two lots of states (m, l, O), which join_shared merges.
+#include "svx_rows.cuh"
 
 namespace svx {
 namespace {
@@ -11,7 +12,8 @@ namespace {
 constexpr int kMaxPieces = 2 * kMaxCtas;  // of a row: of its prefix, and of its own slots
 
 // CTA (x, y): KV head x of all requests' heads; block of 16 query heads y.
-template <typename T, int D>
+// APART: the prefixes were rows_kernel's work.
+template <typename T, int D, bool APART>
 __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant__ AttendParams P) {
   constexpr int CT = kChunkBytes / (2 * D);
   // Where the pieces of a row's lot lie: one is a finished state; else piece c is in slot 0 of CTA first + c, or (c = 0) slot 1.
@@ -25,10 +27,11 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
   __shared__ float4 s_o[kWarps * 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // (the lengths were there before the attention kernel began, which had waited for whoever wrote them)
-  const int T_all = build_plan<kShared, CT>(P, plan, false);
+  const int T_all = build_plan<kShared, CT>(P, plan, false, APART);
   const int b = blockIdx.x / P.pages.n_kv_heads, h = blockIdx.x - b * P.pages.n_kv_heads, blk = blockIdx.y;
   const int rows = min(P.group - blk * kRowsMax, kRowsMax);
   const Split split(P, T_all);
+  const RowSplit row_split(P, APART ? plan.row_tiles : 0);
   int prefix = 0;  // the first that ends behind the request
   for (int i = 0; i < P.n_prefix; i += 32)
     prefix += __popc(__ballot_sync(0xffffffffu, i + lane < P.n_prefix && plan.req0[i + lane + 1] <= b));
@@ -43,16 +46,18 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
       if (any) {
         const int R = (b - plan.req0[prefix]) * P.group + blk * kRowsMax + r;
         seq = prefix;
-        block = R / kRowsMax;
-        blocks = (seq_rows(P, plan, prefix) + kRowsMax - 1) / kRowsMax;
-        x.row = R % kRowsMax;
+        const int per = APART ? P.item_rows : kRowsMax;
+        block = R / per;
+        blocks = (seq_rows(P, plan, prefix) + per - 1) / per;
+        x.row = R % per;
       }
     }
     const int n = any ? plan.n[seq] : 0;
     if (n > 0) {
       const int first = plan.first[seq] + (h * blocks + block) * n;
-      x.first = split.of(first);
-      x.pieces = split.of(first + n - 1) - x.first + 1;
+      const bool far = APART && lot == 0;
+      x.first = far ? row_split.of(first) : split.of(first);
+      x.pieces = (far ? row_split.of(first + n - 1) : split.of(first + n - 1)) - x.first + 1;
       if (x.pieces == 1) x.row = (lot * P.pages.n_req + b) * P.n_q + h * P.group + blk * kRowsMax + r;
     }
     s_lot[lot][r] = x;
@@ -65,14 +70,17 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
     if (lot) c -= s_lot[0][r].pieces;
     const Lot x = s_lot[lot][r];
     if (x.pieces == 1) return __ldcg(P.state_ml + x.row);
-    return __ldcg(P.part_ml + ((x.first + c) * 2 + (c == 0 ? 1 : 0)) * kRowsMax + x.row);
+    const int slot = (x.first + c) * 2 + (c == 0 ? 1 : 0);
+    return __ldcg(APART && lot == 0 ? P.rows_ml + slot * P.item_rows + x.row : P.part_ml + slot * kRowsMax + x.row);
   };
   auto o_at = [&](int r, int c, int d4) {
     const int lot = c < s_lot[0][r].pieces ? 0 : 1;
     if (lot) c -= s_lot[0][r].pieces;
     const Lot x = s_lot[lot][r];
-    const float* at = x.pieces == 1 ? P.state_o + static_cast<int64_t>(x.row) * D
-                                    : P.part_o + static_cast<int64_t>(((x.first + c) * 2 + (c == 0 ? 1 : 0)) * kRowsMax + x.row) * D;
+    const int slot = (x.first + c) * 2 + (c == 0 ? 1 : 0);
+    if (APART && lot == 0 && x.pieces > 1)
+      return __ldcg(P.rows_o + (static_cast<int64_t>(slot) * (D / 4) + d4 / 4) * P.item_rows + x.row);
+    const float* at = x.pieces == 1 ? P.state_o + static_cast<int64_t>(x.row) * D : P.part_o + static_cast<int64_t>(slot * kRowsMax + x.row) * D;
     return __ldcg(reinterpret_cast<const float4*>(at + d4));
   };
   for (int r = warp; r < rows; r += kWarps) {
@@ -99,7 +107,8 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
   const int part = share > 1 ? tid / outs : 0;
   for (int i = share > 1 ? tid - part * outs : tid; i - tid < outs; i += kWarps * 32) {  // (alike for all threads of a round)
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int r = i / (D / 4), d4 = (i - r * (D / 4)) * 4;
+    // (rows_kernel's pieces have a row's neighbours beside it, the others its dimensions)
+    const int r = APART ? i % rows : i / (D / 4), d4 = (APART ? i / rows : i - r * (D / 4)) * 4;
     if (i < outs && part < share) {
       const int pieces = s_lot[0][r].pieces + s_lot[1][r].pieces;
 #pragma unroll 4
@@ -128,6 +137,8 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
 
 struct SharedSizes {
   Sizes z;
+  RowSizes rz;
+  bool many;
   int32_t max_prefix;
 };
 
@@ -152,27 +163,40 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
   out->max_prefix = static_cast<int32_t>(max_prefix);
   z.blocks = (group + kRowsMax - 1) / kRowsMax;
   // (a prefix's last block of rows may not be full)
-  const int64_t blocks = static_cast<int64_t>(n_req) * group / kRowsMax + std::min(f->n_prefix, n_req);
-  const int64_t chunks = c->n_kv_heads * (blocks * ((max_prefix + ct - 1) / ct) +
-                                          static_cast<int64_t>(n_req) * z.blocks * ((max_len + ct - 1) / ct));
-  if (chunks > 0x7fffffff)
-    return paged_fail(SVX_ERR_UNSUPPORTED, "heads times lengths are too large (%lld chunks of %d slots, at most 2^31 - 1)",
-                      static_cast<long long>(chunks), ct);
+  const int64_t all_rows = static_cast<int64_t>(n_req) * group, used = std::min(f->n_prefix, n_req);
+  const int64_t own = static_cast<int64_t>(n_req) * c->n_kv_heads * z.blocks * ((max_len + ct - 1) / ct);
+  const int64_t far = c->n_kv_heads * (all_rows / kRowsMax + used) * ((max_prefix + ct - 1) / ct);
+  out->many = all_rows > static_cast<int64_t>(kRowsMax) * f->n_prefix;
+  const int64_t chunks = own + (out->many ? 0 : far);
+  if (own + far > 0x7fffffff) return paged_fail(SVX_ERR_UNSUPPORTED, "heads times lengths are too large (%lld chunks of %d slots, at most 2^31 - 1)",
+                      static_cast<long long>(own + far), ct);
   size_pieces(&z, chunks, c->head_dim, sms);
   const size_t rows = static_cast<size_t>(2) * n_req * n_q;
   z.state_o = z.total;
   z.state_ml = z.state_o + up256(rows * c->head_dim * 4);
   z.total = z.state_ml + up256(rows * 8);
+  if (out->many) {
+    const int64_t items = c->n_kv_heads * (all_rows / kRowTile + used);
+    size_rows(&out->rz, items * ((max_prefix + kTile - 1) / kTile), all_rows, c->head_dim, sms, z.total);
+    z.total = out->rz.total;
+  }
   return SVX_OK;
 }
 
 template <typename T, int D>
 cudaError_t launch_shared(const AttendParams& p, int device, cudaStream_t s) {
+  const dim3 grid(p.pages.n_req * p.pages.n_kv_heads, p.blocks);
+  cudaError_t e;
+  if (p.prefix_apart) {
+    e = launch_rows<T, kShared, D>(p, device, s);
+    if (e != cudaSuccess) return e;
+    e = p.group > 8 ? launch_attend<T, kShared, D, true, false>(p, device, s) : launch_attend<T, kShared, D, false, false>(p, device, s);
+    return e != cudaSuccess ? e : launch_pdl(join_shared<T, D, true>, grid, dim3(kWarps * 32), 0, s, p);
+  }
   // (rows of a prefix: those of all its requests)
   const bool wide = static_cast<int64_t>(p.group) * p.pages.n_req > 8;
-  const cudaError_t e = wide ? launch_attend<T, kShared, D, true, false>(p, device, s) : launch_attend<T, kShared, D, false, false>(p, device, s);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(join_shared<T, D>, dim3(p.pages.n_req * p.pages.n_kv_heads, p.blocks), dim3(kWarps * 32), 0, s, p);
+  e = wide ? launch_attend<T, kShared, D, true, false>(p, device, s) : launch_attend<T, kShared, D, false, false>(p, device, s);
+  return e != cudaSuccess ? e : launch_pdl(join_shared<T, D, false>, grid, dim3(kWarps * 32), 0, s, p);
 }
 
 }  // namespace
@@ -234,6 +258,8 @@ extern "C" svx_status svx_paged_decode_shared(const svx_pages* cache, int32_t n_
   svx::place_pieces(p, z.z, ws);
   p.state_o = reinterpret_cast<float*>(ws + z.z.state_o);
   p.state_ml = reinterpret_cast<float2*>(ws + z.z.state_ml);
+  if (z.many) svx::place_rows(p, z.rz, ws);
+  p.prefix_apart = z.many;
   p.q = q;
   p.len = len;
   p.o = o;

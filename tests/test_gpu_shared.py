@@ -1,5 +1,7 @@
-"""One-token attention behind shared prefixes on the GPU against a plain 64-bit implementation (bounds: attention_reference.near; a
-softmax weight enters the product with V in two 16-bit pieces, within 2^-15 of itself with its exponential and its sum)."""
+"""One-token attention behind shared prefixes on the GPU against a plain 64-bit implementation (bounds: attention_reference.near).
+
+With up to 128 rows (query heads of a KV head times requests) a softmax weight enters the product with V in two 16-bit pieces, within 2^-15 of
+itself with its exponential and its sum; with more it is rounded to the inputs' type once, by half a step."""
 import pytest
 import torch
 
@@ -8,7 +10,10 @@ from attention_reference import attend64, near, slots_of
 pytestmark = pytest.mark.gpu
 
 TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
-P_ERROR = {"bf16": 2.0 ** -15, "fp16": 2.0 ** -15}
+
+
+def p_error(rows, ty):
+    return 2.0 ** -15 + (torch.finfo(TYPES[ty]).eps / 2 if rows > 128 else 0.0)
 
 
 @pytest.fixture(scope="module")
@@ -72,7 +77,7 @@ def check(s, ty, scale=None, first=None, prefix_lens=None, lens=None):
         for h in range(hkv):
             heads = slice(h * group, (h + 1) * group)
             want = attend64(s["q"][b, heads, 0], mine[0][:, h], mine[1][:, h], scale or d ** -0.5)
-            near(s["o"][b, heads, 0], s["lse"][b, heads, 0], want, P_ERROR[ty], len(mine[0]))
+            near(s["o"][b, heads, 0], s["lse"][b, heads, 0], want, p_error(batch * group, ty), len(mine[0]))
 
 
 CASES = [  # groups, before, behind, prefix, own, hq, hkv, d, page, type, layout
