@@ -513,30 +513,49 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     const T* const pool = static_cast<const T*>(is_v ? P.pages.v : P.pages.k);
     constexpr int PIECES = D / 8, RPI = 32 / PIECES;  // a row's pieces of 16 bytes; rows that a warp copies at a time
     const int piece = lane % PIECES, r0 = lane / PIECES;
+    // runs of 16 keys lie in one page, or any keys a stride apart: one address for several copies
+    const bool runs = !kBoundsChecked && (SRC == kDense || P.pages.page_size % 16 == 0);
+    const int64_t step = RPI * P.pages.tok_stride;
     int i = 0;
     bool ok = true;
     for (int x = x0; x < x1 && ok;) {
       const RowSeg g = row_seg<SRC>(P, plan, x, x1);
+      const int32_t* const table = SRC == kShared ? P.prefix_table + static_cast<int64_t>(g.b) * P.prefix_max_pages : nullptr;
+      // lane l works out the places of keys l, l + 32, ..; their pages are looked up a tile ahead
+      int32_t page[4];
+      auto look = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int key = (g.tile0 + t) * kTile + u * 32 + lane;
+          page[u] = t < g.n && key < g.len ? __ldg(table + page_of(P.pages, static_cast<uint32_t>(key))) : 0;
+        }
+      };
+      if constexpr (SRC == kShared) look(0);
       for (int t = 0; t < g.n; ++t, ++i) {
         const int t0 = (g.tile0 + t) * kTile;
         const Seen seen = keys_seen<SRC>(P, g, t0);
-        // the rows' places: lane l works out rows l, l + 32, ..
+        const bool all = (seen.w[0] & seen.w[1] & seen.w[2] & seen.w[3]) == 0xffffffffu;
         int64_t off[4];
+        bool there = true;
+        if (SRC == kShared || !all || !runs) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          off[u] = -1;
-          const int key = t0 + u * 32 + lane;
-          if (!(seen.w[u] >> lane & 1u)) continue;
-          if constexpr (SRC == kShared) {
-            const uint32_t pg = page_of(P.pages, static_cast<uint32_t>(key));
-            off[u] = slot_offset(P.pages, __ldg(P.prefix_table + static_cast<int64_t>(g.b) * P.prefix_max_pages + pg),
-                                 key - pg * P.pages.page_size);
-            if (off[u] < 0) atomicOr(P.pages.status, kErrInput);
-          } else {
-            off[u] = g.b * P.pages.page_stride + key * P.pages.tok_stride;
+          for (int u = 0; u < 4; ++u) {
+            off[u] = -1;
+            const int key = t0 + u * 32 + lane;
+            if (!(seen.w[u] >> lane & 1u)) continue;
+            if constexpr (SRC == kShared) {
+              off[u] = slot_offset(P.pages, page[u], key - page_of(P.pages, static_cast<uint32_t>(key)) * P.pages.page_size);
+              if (off[u] < 0) atomicOr(P.pages.status, kErrInput);
+            } else {
+              off[u] = g.b * P.pages.page_stride + key * P.pages.tok_stride;
+            }
+            if (off[u] >= 0) off[u] += g.h * P.pages.head_stride;
+            if (off[u] >= 0 && !in_bounds(pool + off[u], D, pool, P.pages.extent, P.pages.status, kSitePool)) off[u] = -1;
           }
-          if (off[u] >= 0) off[u] += g.h * P.pages.head_stride;
-          if (off[u] >= 0 && !in_bounds(pool + off[u], D, pool, P.pages.extent, P.pages.status, kSitePool)) off[u] = -1;
+          if constexpr (SRC == kShared) {
+            there = __all_sync(0xffffffffu, off[0] >= 0 && off[1] >= 0 && off[2] >= 0 && off[3] >= 0);
+            look(t + 1);
+          }
         }
         const int stage = i % stages;
         if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
@@ -544,22 +563,33 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
           break;
         }
         const uint32_t dst = ring + stage * C::TILE + (piece >> 3) * kHalf;
-        if (!kBoundsChecked && SRC == kDense && (seen.w[0] & seen.w[1] & seen.w[2] & seen.w[3]) == 0xffffffffu) {
-          const T* src = pool + g.b * P.pages.page_stride + (t0 + r0) * P.pages.tok_stride + g.h * P.pages.head_stride + piece * 8;
-          const int64_t step = RPI * P.pages.tok_stride;
+        if (all && runs && there) {
+          constexpr int RUN = SRC == kShared ? 16 : kTile;
+#pragma unroll 1
+          for (int k = 0; k < kTile; k += RUN) {
+            const T* src = pool + piece * 8 + r0 * P.pages.tok_stride;
+            if constexpr (SRC == kShared) {
+              const int64_t o01 = k & 32 ? off[1] : off[0], o23 = k & 32 ? off[3] : off[2];
+              src += __shfl_sync(0xffffffffu, k & 64 ? o23 : o01, k & 31);
+            } else {
+              src += g.b * P.pages.page_stride + t0 * P.pages.tok_stride + g.h * P.pages.head_stride;
+            }
 #pragma unroll 8
-          for (int r = r0; r < kTile; r += RPI, src += step) copy16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), src, 16);
-          copies_arrive(full + 8u * stage);
-          continue;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll 8
-          for (int j = 0; j < 32 / RPI; ++j) {
-            const int in32 = j * RPI + r0, r = u * 32 + in32;
-            const int64_t ro = __shfl_sync(0xffffffffu, off[u], in32);
-            copy16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), pool + (ro >= 0 ? ro : 0) + piece * 8, ro >= 0 ? 16 : 0);
+            for (int j = 0; j < RUN; j += RPI, src += step) {
+              const int r = k + j + r0;
+              copy16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), src, 16);
+            }
           }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll 8
+            for (int j = 0; j < 32 / RPI; ++j) {
+              const int in32 = j * RPI + r0, r = u * 32 + in32;
+              const int64_t ro = __shfl_sync(0xffffffffu, off[u], in32);
+              copy16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), pool + (ro >= 0 ? ro : 0) + piece * 8, ro >= 0 ? 16 : 0);
+            }
+        }
         copies_arrive(full + 8u * stage);
       }
       x += g.n;

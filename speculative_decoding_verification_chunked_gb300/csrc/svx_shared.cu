@@ -9,9 +9,9 @@
 namespace svx {
 namespace {
 
-constexpr int kMaxPieces = 2 * kMaxCtas;  // of a row: of its prefix, and of its own slots
+constexpr int kBatch = 64;  // pieces of a row whose factors are worked out at a time
 
-// CTA (x, y): KV head x of all requests' heads; block of 16 query heads y.
+// CTA (x, y, z): KV head x of all requests' heads; block of 16 query heads y; of the dimensions, part z of gridDim.z.
 // APART: the prefixes were rows_kernel's work.
 template <typename T, int D, bool APART>
 __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant__ AttendParams P) {
@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
     int32_t first, pieces, row;  // row: in the pieces' blocks, or of the finished states
   };
   __shared__ Plan<kShared> plan;
-  __shared__ float s_f[kMaxPieces * kRowsMax];
+  __shared__ float s_f[kBatch * kRowsMax];
   __shared__ float2 s_ml[kRowsMax];
   __shared__ Lot s_lot[2][kRowsMax];
   __shared__ float4 s_o[kWarps * 32];
@@ -83,38 +83,51 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
     const float* at = x.pieces == 1 ? P.state_o + static_cast<int64_t>(x.row) * D : P.part_o + static_cast<int64_t>(slot * kRowsMax + x.row) * D;
     return __ldcg(reinterpret_cast<const float4*>(at + d4));
   };
+  // the outputs over the threads: several share one where there are more of them than outputs
+  const int quads = D / 4 / gridDim.z, outs = rows * quads, share = max(kWarps * 32 / outs, 1);
+  const int part = share > 1 ? tid / outs : 0;
+  int most = 0;  // pieces of any row
+  for (int r = 0; r < rows; ++r) most = max(most, s_lot[0][r].pieces + s_lot[1][r].pieces);
   for (int r = warp; r < rows; r += kWarps) {
     const int pieces = s_lot[0][r].pieces + s_lot[1][r].pieces;
     float M = kNegInf;
     for (int c = lane; c < pieces; c += 32) M = fmaxf(M, ml_at(r, c).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float base = M == kNegInf ? 0.f : M;
-    float L = 0.f;
-    for (int c = lane; c < pieces; c += 32) {
-      const float2 ml = ml_at(r, c);
-      const float f = ex2(ml.x - base);
-      s_f[c * kRowsMax + r] = f;
-      L = fmaf(ml.y, f, L);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) s_ml[r] = make_float2(M, L);
+    if (lane == 0) s_ml[r] = make_float2(M, 0.f);
   }
   __syncthreads();
-  // the outputs over the threads: several share one where there are more of them than outputs
-  const int outs = rows * (D / 4), share = max(kWarps * 32 / outs, 1);
-  const int part = share > 1 ? tid / outs : 0;
-  for (int i = share > 1 ? tid - part * outs : tid; i - tid < outs; i += kWarps * 32) {  // (alike for all threads of a round)
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < outs; i0 += kWarps * 32) {  // (once, unless there are more outputs than threads)
+    const int i = share > 1 ? tid - part * outs : i0 + tid;
     // (rows_kernel's pieces have a row's neighbours beside it, the others its dimensions)
-    const int r = APART ? i % rows : i / (D / 4), d4 = (APART ? i / rows : i - r * (D / 4)) * 4;
-    if (i < outs && part < share) {
-      const int pieces = s_lot[0][r].pieces + s_lot[1][r].pieces;
-#pragma unroll 4
-      for (int c = part; c < pieces; c += share) {
+    const int r = APART ? i % rows : i / quads, d4 = ((APART ? i / rows : i - r * quads) + blockIdx.z * quads) * 4;
+    const bool mine = i < outs && part < share;
+    const int pieces = mine ? s_lot[0][r].pieces + s_lot[1][r].pieces : 0;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < most; c0 += kBatch) {
+      if (c0 > 0 || i0 > 0) __syncthreads();  // (the last batch's factors have been used)
+      if (i0 == 0 || most > kBatch)
+        for (int q = warp; q < rows; q += kWarps) {
+          const int end = min(s_lot[0][q].pieces + s_lot[1][q].pieces, c0 + kBatch);
+          const float2 before = s_ml[q];
+          const float less = before.x == kNegInf ? 0.f : -before.x;
+          float L = 0.f;
+          for (int c = c0 + lane; c < end; c += 32) {
+            const float2 ml = ml_at(q, c);
+            const float f = ex2(ml.x + less);
+            s_f[(c - c0) * kRowsMax + q] = f;
+            L = fmaf(ml.y, f, L);
+          }
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
+          if (lane == 0 && i0 == 0) s_ml[q].y = before.y + L;
+        }
+      __syncthreads();
+      const int end = min(pieces, c0 + kBatch);
+#pragma unroll 8
+      for (int c = c0 + part; c < end; c += share) {
         const float4 x = o_at(r, c, d4);
-        const float f = s_f[c * kRowsMax + r];
+        const float f = s_f[(c - c0) * kRowsMax + r];
         o.x = fmaf(x.x, f, o.x);
         o.y = fmaf(x.y, f, o.y);
         o.z = fmaf(x.z, f, o.z);
@@ -130,8 +143,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
           o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
         }
     }
-    if (i < outs && part == 0) write_row<T>(P, place<kShared, D>(P, plan, kMaxReq + b, h, blk, r), d4, s_ml[r].x, s_ml[r].y, o);
-    if (share > 1) break;
+    if (mine && part == 0) write_row<T>(P, place<kShared, D>(P, plan, kMaxReq + b, h, blk, r), d4, s_ml[r].x, s_ml[r].y, o);
   }
 }
 
@@ -185,7 +197,10 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
 
 template <typename T, int D>
 cudaError_t launch_shared(const AttendParams& p, int device, cudaStream_t s) {
-  const dim3 grid(p.pages.n_req * p.pages.n_kv_heads, p.blocks);
+  const int sms = sm_count(device);
+  // parts of the dimensions: as many as let the CTAs be resident at a time (3 an SM), with 4 threads or more to an output of few rows
+  const int ctas = p.pages.n_req * p.pages.n_kv_heads * p.blocks;
+  const dim3 grid(p.pages.n_req * p.pages.n_kv_heads, p.blocks, ctas * 4 <= 3 * sms ? 4 : ctas * 2 <= 3 * sms ? 2 : 1);
   cudaError_t e;
   if (p.prefix_apart) {
     e = launch_rows<T, kShared, D>(p, device, s);
