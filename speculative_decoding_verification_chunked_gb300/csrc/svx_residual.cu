@@ -4,13 +4,14 @@
 //   h' = alpha h + beta act(gate) u                          (the gate, and the scaled residual sum)
 //   x  = h' rsqrt(mean h'^2 + eps) norm                      (the norm before the next block)
 //
-// A row is held in registers from its loads to its stores (kVec elements, 16 bytes of a 16-bit type, at a time), so that h, y and a
+// A row is held on the SM from its loads to its stores (kVec elements, 16 bytes of a 16-bit type, at a time), so that h, y and a
 // gate per element are read once and h', x written once: those bytes are the floor.  Two sums over the row, each a
 // shuffle within the warps and one exchange through shared memory between them.  Everything is fp32, rounded once on the way out; x is
 // the norm of the unrounded h'.
 #include "svx_paged.h"
 
-#include <cfloat>
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 
 namespace svx {
@@ -34,6 +35,7 @@ struct ResidualParams {
   int64_t rows;
   int32_t vecs;  // of a row
   int32_t gate_kind, act;
+  int32_t stages;  // rows that a block has on their way
   float alpha, beta, eps, post_eps;  // eps < 0: no such norm
   float inv_dim;
 };
@@ -68,12 +70,10 @@ __device__ __forceinline__ uint32_t pack2(__half, float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// kVec elements as they lie in memory.
+// kVec elements as they lie in memory: one 16-byte plane, or (fp32) two.
 template <typename T>
 struct Raw {
-  uint4 v;
-  __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float (&f)[kVec]) const { unpack<T>(v, f); }
+  static __device__ __forceinline__ void get(const uint4& a, const uint4&, float (&f)[kVec]) { unpack<T>(a, f); }
   static __device__ __forceinline__ void store(T* p, const float (&f)[kVec]) {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack2(T(), f[0], f[1]), pack2(T(), f[2], f[3]), pack2(T(), f[4], f[5]), pack2(T(), f[6], f[7]));
@@ -81,13 +81,10 @@ struct Raw {
 };
 template <>
 struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ void get(float (&f)[kVec]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  static __device__ __forceinline__ void get(const uint4& a, const uint4& b, float (&f)[kVec]) {
+    const uint32_t w[kVec] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) f[e] = __uint_as_float(w[e]);
   }
   static __device__ __forceinline__ void store(float* p, const float (&f)[kVec]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
@@ -95,11 +92,13 @@ struct Raw<float> {
   }
 };
 
+// (the sigmoid through the hardware's power of two and reciprocal: g log2 e is off by 2^-24 of itself, so the result by 2^-17 of
+// itself where it is below e^-80, by less elsewhere)
 __device__ __forceinline__ float activate(float g, int act) {
-  return act == SVX_ACT_TANH ? tanhf(g) : act == SVX_ACT_SIGMOID ? 1.f / (1.f + expf(-g)) : g;
+  return act == SVX_ACT_TANH ? tanhf(g) : act == SVX_ACT_SIGMOID ? __fdividef(1.f, 1.f + exp2f(-1.44269504089f * g)) : g;
 }
 
-// The sum over the threads of a row: a warp, or the block (every thread gets it; `s` is used once a call).
+// The sum over the threads of a row: a warp, or the block (every thread gets it; `s`: not the last call's).
 template <bool WARP_ROW>
 __device__ __forceinline__ float row_sum(float v, float* s) {
 #pragma unroll
@@ -115,103 +114,154 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
   return v;
 }
 
+__device__ __forceinline__ void bring16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void brought(int newer) {  // all but the `newer` last groups are in
+  if (newer == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (newer == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+
 // T: block outputs and weights; H: the residual stream.  WARP_ROW: a row to each warp, else to each block.  N: the most
-// kVec-element pieces of a row that a thread holds.
+// kVec-element pieces of a row that a thread holds.  A block takes every gridDim.x-th row (or four).  Rows come in through shared
+// memory, P.stages of them ahead; a thread brings in what it will read itself, so nobody waits for another's copies.
 template <typename T, typename H, bool WARP_ROW, int N>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads) residual_kernel(const __grid_constant__ ResidualParams P) {
-  __shared__ float s_post[32], s_pre[32];
-  const int64_t row = WARP_ROW ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  const int t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x, step = WARP_ROW ? 32 : blockDim.x;
+__global__ void __launch_bounds__(kMaxThreads) residual_kernel(const __grid_constant__ ResidualParams P) {
+  constexpr int HP = sizeof(H) / 2;  // 16-byte planes of a piece of h
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float s_sum[2][32];
+  const int threads = blockDim.x, t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x, step = WARP_ROW ? 32 : threads;
+  const int64_t rows_at_once = WARP_ROW ? static_cast<int64_t>(gridDim.x) * (threads / 32) : gridDim.x;
+  int64_t row = WARP_ROW ? static_cast<int64_t>(blockIdx.x) * (threads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  // planes of 16 bytes a thread: [stage][piece][y, h (one or two), gate]
+  const bool has_y = P.y != nullptr, has_g = P.gate_kind == kGateRow && P.gate_stride != 0;
+  const int planes = HP + (has_y ? 1 : 0) + (has_g ? 1 : 0);
+  auto plane = [&](int stage, int i, int k) { return ((stage * N + i) * planes + k) * threads + static_cast<int>(threadIdx.x); };
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const uint4* const held = reinterpret_cast<const uint4*>(smem);
+  auto bring = [&](int64_t r, int stage) {
+    if (r < P.rows) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int v = t + i * step;
+        if (v >= P.vecs) continue;
+        const H* h = static_cast<const H*>(P.h) + r * P.h_stride + v * kVec;
+        bring16(base + plane(stage, i, 0) * 16, h);
+        if constexpr (HP == 2) bring16(base + plane(stage, i, 1) * 16, h + 4);
+        if (has_y) bring16(base + plane(stage, i, HP) * 16, static_cast<const T*>(P.y) + r * P.y_stride + v * kVec);
+        if (has_g) bring16(base + plane(stage, i, planes - 1) * 16, static_cast<const T*>(P.gate) + r * P.gate_stride + v * kVec);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   grid_dependency_wait();
   allow_dependents();
-  if (row >= P.rows) return;  // (whole warps, and no barrier follows for them)
-  Raw<H> h[N];
-  Raw<T> y[N], g[N];
+  for (int k = 0; k < P.stages; ++k) bring(row + k * rows_at_once, k);
+  const float scalar =
+      P.gate_kind == kGateScalar ? P.beta * activate(static_cast<float>(*static_cast<const T*>(P.gate)), P.act) : P.beta;
+  // sums use two places in turn: one is written again only behind the other's barrier, when all have read it
+  int place = 0, stage = 0;
+  for (; row < P.rows; row += rows_at_once) {
+    brought(P.stages - 1);
+    float factor = scalar;
+    if (P.post_eps >= 0.f) {
+      float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int v = t + i * step;
-    if (v >= P.vecs) continue;
-    if (P.y) y[i].load(static_cast<const T*>(P.y) + row * P.y_stride + v * kVec);
-    h[i].load(static_cast<const H*>(P.h) + row * P.h_stride + v * kVec);
-    if (P.gate_kind == kGateRow) g[i].load(static_cast<const T*>(P.gate) + row * P.gate_stride + v * kVec);
-  }
-  float factor = P.beta;
-  if (P.y && P.post_eps >= 0.f) {
+      for (int i = 0; i < N; ++i) {
+        if (t + i * step >= P.vecs) continue;
+        float f[kVec];
+        unpack<T>(held[plane(stage, i, HP)], f);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum = fmaf(f[e], f[e], sum);
+      }
+      factor *= rsqrtf(fmaf(row_sum<WARP_ROW>(sum, s_sum[place]), P.inv_dim, P.post_eps));
+      place ^= 1;
+    }
+    float z[N][kVec];
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (t + i * step >= P.vecs) continue;
-      float f[kVec];
-      y[i].get(f);
+      const int v = t + i * step;
+      if (v >= P.vecs) continue;
+      Raw<H>::get(held[plane(stage, i, 0)], held[plane(stage, i, HP - 1)], z[i]);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) sum = fmaf(f[e], f[e], sum);
-    }
-    factor *= rsqrtf(fmaf(row_sum<WARP_ROW>(sum, s_post), P.inv_dim, P.post_eps));
-  }
-  if (P.gate_kind == kGateScalar) factor *= activate(static_cast<float>(*static_cast<const T*>(P.gate)), P.act);
-  float z[N][kVec];
-  float sum = 0.f;
+      for (int e = 0; e < kVec; ++e) z[i][e] *= P.alpha;
+      if (has_y) {
+        float u[kVec], w[kVec];
+        unpack<T>(held[plane(stage, i, HP)], u);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int v = t + i * step;
-    if (v >= P.vecs) continue;
-    h[i].get(z[i]);
+        for (int e = 0; e < kVec; ++e) u[e] *= factor;
+        if (P.post_norm) {
+          unpack<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(P.post_norm) + v * kVec), w);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) z[i][e] *= P.alpha;
-    if (P.y) {
-      float u[kVec], w[kVec];
-      y[i].get(u);
+          for (int e = 0; e < kVec; ++e) u[e] *= w[e];
+        }
+        if (P.gate_kind == kGateRow) {
+          unpack<T>(has_g ? held[plane(stage, i, planes - 1)] : *reinterpret_cast<const uint4*>(static_cast<const T*>(P.gate) + v * kVec), w);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) u[e] *= factor;
-      if (P.post_norm) {
-        Raw<T> r;
-        r.load(static_cast<const T*>(P.post_norm) + v * kVec);
-        r.get(w);
+          for (int e = 0; e < kVec; ++e) u[e] *= activate(w[e], P.act);
+        }
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) u[e] *= w[e];
-      }
-      if (P.gate_kind == kGateRow) {
-        g[i].get(w);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) u[e] *= activate(w[e], P.act);
+        for (int e = 0; e < kVec; ++e) z[i][e] += u[e];
       }
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) z[i][e] += u[e];
+      for (int e = 0; e < kVec; ++e) sum = fmaf(z[i][e], z[i][e], sum);
     }
+    bring(row + P.stages * rows_at_once, stage);  // (into places that this thread has read)
+    stage = stage + 1 == P.stages ? 0 : stage + 1;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) sum = fmaf(z[i][e], z[i][e], sum);
-    if (P.h_out) Raw<H>::store(static_cast<H*>(P.h_out) + row * P.h_out_stride + v * kVec, z[i]);
-  }
-  if (!P.x_out) return;
-  const float r = rsqrtf(fmaf(row_sum<WARP_ROW>(sum, s_pre), P.inv_dim, P.eps));
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int v = t + i * step;
-    if (v >= P.vecs) continue;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) z[i][e] *= r;
-    if (P.norm) {
-      float w[kVec];
-      Raw<T> raw;
-      raw.load(static_cast<const T*>(P.norm) + v * kVec);
-      raw.get(w);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) z[i][e] *= w[e];
+    for (int i = 0; i < N; ++i) {
+      const int v = t + i * step;
+      if (v < P.vecs && P.h_out) Raw<H>::store(static_cast<H*>(P.h_out) + row * P.h_out_stride + v * kVec, z[i]);
     }
-    Raw<T>::store(static_cast<T*>(P.x_out) + row * P.x_stride + v * kVec, z[i]);
+    if (!P.x_out) continue;
+    const float r = rsqrtf(fmaf(row_sum<WARP_ROW>(sum, s_sum[place]), P.inv_dim, P.eps));
+    place ^= 1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int v = t + i * step;
+      if (v >= P.vecs) continue;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) z[i][e] *= r;
+      if (P.norm) {
+        float w[kVec];
+        unpack<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(P.norm) + v * kVec), w);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) z[i][e] *= w[e];
+      }
+      Raw<T>::store(static_cast<T*>(P.x_out) + row * P.x_stride + v * kVec, z[i]);
+    }
   }
+  brought(0);
+}
+
+constexpr int kSmem = 200 * 1024;  // of rows on their way, of an SM
+
+template <typename T, typename H, bool WARP_ROW, int N>
+cudaError_t launch_of(ResidualParams p, int threads, int device, cudaStream_t s) {
+  static std::atomic<bool> done[64];
+  if (device >= 64 || !done[device].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(residual_kernel<T, H, WARP_ROW, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (device < 64) done[device].store(true, std::memory_order_release);
+  }
+  const int planes = sizeof(H) / 2 + (p.y ? 1 : 0) + (p.gate_kind == kGateRow && p.gate_stride ? 1 : 0);
+  const int bytes = threads * N * planes * 16;  // of a stage
+  const int64_t blocks = WARP_ROW ? (p.rows + threads / 32 - 1) / (threads / 32) : p.rows;
+  const int sms = sm_count(device), resident = std::min(std::max(1024 / threads, 1), kSmem / bytes);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(std::max(sms, 1)) * resident));
+  p.stages = std::min<int64_t>(std::min(kSmem / (resident * bytes), 3), (blocks + grid - 1) / grid);
+  return launch_pdl(residual_kernel<T, H, WARP_ROW, N>, dim3(grid), dim3(threads), p.stages * bytes, s, p);
 }
 
 template <typename T, typename H>
-cudaError_t launch_residual(const ResidualParams& p, cudaStream_t s) {
-  // a warp holds rows of up to 1024 elements; else as few threads as hold the row four pieces each
-  if (p.vecs <= 128) {
-    const dim3 grid(static_cast<unsigned>((p.rows + 3) / 4));
-    return p.vecs <= 32 ? launch_pdl(residual_kernel<T, H, true, 1>, grid, dim3(128), 0, s, p)
-                        : launch_pdl(residual_kernel<T, H, true, 4>, grid, dim3(128), 0, s, p);
-  }
-  const int threads = ((p.vecs + 3) / 4 + 31) / 32 * 32;
-  return launch_pdl(residual_kernel<T, H, false, 4>, dim3(static_cast<unsigned>(p.rows)), dim3(threads), 0, s, p);
+cudaError_t launch_residual(const ResidualParams& p, int device, cudaStream_t s) {
+  // a warp holds rows of up to 512 elements; else as few threads as hold the row two pieces each, or four
+  if (p.vecs <= 32) return launch_of<T, H, true, 1>(p, 128, device, s);
+  if (p.vecs <= 64) return launch_of<T, H, true, 2>(p, 128, device, s);
+  if (p.vecs <= 1024) return launch_of<T, H, false, 2>(p, ((p.vecs + 1) / 2 + 31) / 32 * 32, device, s);
+  return launch_of<T, H, false, 4>(p, 512, device, s);
 }
 
 }  // namespace
@@ -302,9 +352,9 @@ extern "C" svx_status svx_residual_norm(const svx_residual* in, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a.dtype == SVX_BF16)
-    e = a.stream_dtype == SVX_FP32 ? svx::launch_residual<__nv_bfloat16, float>(p, s) : svx::launch_residual<__nv_bfloat16, __nv_bfloat16>(p, s);
+    e = a.stream_dtype == SVX_FP32 ? svx::launch_residual<__nv_bfloat16, float>(p, a.device, s) : svx::launch_residual<__nv_bfloat16, __nv_bfloat16>(p, a.device, s);
   else
-    e = a.stream_dtype == SVX_FP32 ? svx::launch_residual<__half, float>(p, s) : svx::launch_residual<__half, __half>(p, s);
+    e = a.stream_dtype == SVX_FP32 ? svx::launch_residual<__half, float>(p, a.device, s) : svx::launch_residual<__half, __half>(p, a.device, s);
   if (e != cudaSuccess) return paged_fail(SVX_ERR_CUDA, "residual kernel launch failed: %s", cudaGetErrorString(e));
   return SVX_OK;
 }
