@@ -52,6 +52,29 @@ __device__ __forceinline__ int64_t slot_offset(const PageView& p, int32_t page_i
   return static_cast<int64_t>(page_id) * p.page_stride + static_cast<int64_t>(in_page) * p.tok_stride;
 }
 
+// two fp32 values in one register pair
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // svx_debug_clip_paged: the most elements that this thread's calls describe a buffer of a kind as holding.
 enum PagedBuffer : int { kClipInputs = 0, kClipOutputs = 1, kClipPool = 2, kClips = 3 };
 int64_t clipped(PagedBuffer kind, int64_t extent);

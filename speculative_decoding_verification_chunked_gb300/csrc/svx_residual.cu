@@ -36,66 +36,99 @@ struct ResidualParams {
   int32_t vecs;  // of a row
   int32_t gate_kind, act;
   int32_t stages;  // rows that a block has on their way
+  bool wide;       // (fp32) pieces of h_out lie on the grid of 32 bytes
   float alpha, beta, eps, post_eps;  // eps < 0: no such norm
   float inv_dim;
 };
 
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[kVec]);
-template <>
-__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& v, float (&f)[kVec]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// Values are worked on two at a time (fp32 pairs: half the instructions, which took longer than the bytes).  kVec elements as they
+// lie in memory: one 16-byte plane, or (fp32) two.
+constexpr int kPairs = kVec / 2;
+__device__ __forceinline__ uint64_t widen(__nv_bfloat16, uint32_t w) {
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-template <>
-__device__ __forceinline__ void unpack<__half>(const uint4& v, float (&f)[kVec]) {
-  const __half2* p = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = __half22float2(p[i]);
-    f[2 * i] = x.x;
-    f[2 * i + 1] = x.y;
-  }
+__device__ __forceinline__ uint64_t widen(__half, uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pair(f.x, f.y);
 }
-__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float a, float b) {
+__device__ __forceinline__ uint32_t narrow(__nv_bfloat16, uint64_t x) {
+  float a, b;
+  unpair(x, a, b);
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ uint32_t pack2(__half, float a, float b) {
+__device__ __forceinline__ uint32_t narrow(__half, uint64_t x) {
+  float a, b;
+  unpair(x, a, b);
   const __half2 p = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-
-// kVec elements as they lie in memory: one 16-byte plane, or (fp32) two.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, uint64_t (&f)[kPairs]) {
+  f[0] = widen(T(), v.x), f[1] = widen(T(), v.y), f[2] = widen(T(), v.z), f[3] = widen(T(), v.w);
+}
 template <typename T>
 struct Raw {
-  static __device__ __forceinline__ void get(const uint4& a, const uint4&, float (&f)[kVec]) { unpack<T>(a, f); }
-  static __device__ __forceinline__ void store(T* p, const float (&f)[kVec]) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack2(T(), f[0], f[1]), pack2(T(), f[2], f[3]), pack2(T(), f[4], f[5]), pack2(T(), f[6], f[7]));
+  static __device__ __forceinline__ void get(const uint4& a, const uint4&, uint64_t (&f)[kPairs]) { unpack<T>(a, f); }
+  static __device__ __forceinline__ void store(T* p, const uint64_t (&f)[kPairs], bool) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(narrow(T(), f[0]), narrow(T(), f[1]), narrow(T(), f[2]), narrow(T(), f[3]));
   }
 };
 template <>
 struct Raw<float> {
-  static __device__ __forceinline__ void get(const uint4& a, const uint4& b, float (&f)[kVec]) {
+  static __device__ __forceinline__ void get(const uint4& a, const uint4& b, uint64_t (&f)[kPairs]) {
     const uint32_t w[kVec] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) f[e] = __uint_as_float(w[e]);
+    for (int e = 0; e < kPairs; ++e) f[e] = pair(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
   }
-  static __device__ __forceinline__ void store(float* p, const float (&f)[kVec]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  static __device__ __forceinline__ void store(float* p, const uint64_t (&f)[kPairs], bool wide) {
+    if (wide) {  // a whole sector
+      asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(f[0]), "l"(f[1]), "l"(f[2]), "l"(f[3]) : "memory");
+      return;
+    }
+    float v[kVec];
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) unpair(f[e], v[2 * e], v[2 * e + 1]);
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
 };
 
-// (the sigmoid through the hardware's power of two and reciprocal: g log2 e is off by 2^-24 of itself, so the result by 2^-17 of
-// itself where it is below e^-80, by less elsewhere)
-__device__ __forceinline__ float activate(float g, int act) {
-  return act == SVX_ACT_TANH ? tanhf(g) : act == SVX_ACT_SIGMOID ? __fdividef(1.f, 1.f + exp2f(-1.44269504089f * g)) : g;
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+// 2^x and 1 / x, each within 2^-22 of itself
+__device__ __forceinline__ uint64_t exp2_2(uint64_t x) {
+  float a, b;
+  unpair(x, a, b);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return pair(a, b);
+}
+__device__ __forceinline__ uint64_t inverse2(uint64_t x) {
+  float a, b;
+  unpair(x, a, b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return pair(a, b);
+}
+// tanh and the sigmoid, within 2^-19 of themselves; the sigmoid loses up to 2^-17 where it is below e^-60 (its argument's product
+// with log2 e is off by 2^-24 of itself).  tanh: 1 - 2 / (1 + e^2g), and where that cancels, below 1/4, the series up to g^9.
+__device__ __forceinline__ uint64_t activate2(uint64_t g, int act) {
+  constexpr float kLog2e = 1.44269504089f;
+  if (act == SVX_ACT_SIGMOID) return inverse2(add2(both(1.f), exp2_2(mul2(g, both(-kLog2e)))));
+  if (act == SVX_ACT_TANH) {
+    const uint64_t far = fma2(both(-2.f), inverse2(add2(both(1.f), exp2_2(mul2(g, both(2.f * kLog2e))))), both(1.f));
+    const uint64_t x = mul2(g, g);
+    uint64_t s = fma2(x, both(62.f / 2835.f), both(-17.f / 315.f));
+    s = fma2(x, s, both(2.f / 15.f));
+    s = fma2(x, s, both(-1.f / 3.f));
+    s = fma2(mul2(x, s), g, g);
+    float g0, g1, f0, f1, s0, s1;
+    unpair(g, g0, g1);
+    unpair(far, f0, f1);
+    unpair(s, s0, s1);
+    return pair(fabsf(g0) < 0.25f ? s0 : f0, fabsf(g1) < 0.25f ? s1 : f1);
+  }
+  return g;
 }
 
 // The sum over the threads of a row: a warp, or the block (every thread gets it; `s`: not the last call's).
@@ -125,9 +158,10 @@ __device__ __forceinline__ void brought(int newer) {  // all but the `newer` las
 
 // T: block outputs and weights; H: the residual stream.  WARP_ROW: a row to each warp, else to each block.  N: the most
 // kVec-element pieces of a row that a thread holds.  A block takes every gridDim.x-th row (or four).  Rows come in through shared
-// memory, P.stages of them ahead; a thread brings in what it will read itself, so nobody waits for another's copies.
+// memory, P.stages of them ahead; a thread brings in what it will read itself, or (32-bit h) its warp does, so no warp waits for another's
+// copies.
 template <typename T, typename H, bool WARP_ROW, int N>
-__global__ void __launch_bounds__(kMaxThreads) residual_kernel(const __grid_constant__ ResidualParams P) {
+__global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads, WARP_ROW ? 8 : N == 4 ? 1 : 2) residual_kernel(const __grid_constant__ ResidualParams P) {
   constexpr int HP = sizeof(H) / 2;  // 16-byte planes of a piece of h
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float s_sum[2][32];
@@ -146,11 +180,22 @@ __global__ void __launch_bounds__(kMaxThreads) residual_kernel(const __grid_cons
       for (int i = 0; i < N; ++i) {
         const int v = t + i * step;
         if (v >= P.vecs) continue;
-        const H* h = static_cast<const H*>(P.h) + r * P.h_stride + v * kVec;
-        bring16(base + plane(stage, i, 0) * 16, h);
-        if constexpr (HP == 2) bring16(base + plane(stage, i, 1) * 16, h + 4);
+        if constexpr (HP == 1) bring16(base + plane(stage, i, 0) * 16, static_cast<const H*>(P.h) + r * P.h_stride + v * kVec);
         if (has_y) bring16(base + plane(stage, i, HP) * 16, static_cast<const T*>(P.y) + r * P.y_stride + v * kVec);
         if (has_g) bring16(base + plane(stage, i, planes - 1) * 16, static_cast<const T*>(P.gate) + r * P.gate_stride + v * kVec);
+      }
+      // two planes of a thread: a warp's copies in order of their addresses, 512 bytes at a time (its own 32 a thread would fetch
+      // every sector twice)
+      if constexpr (HP == 2) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int c = q * 32 + lane, other = (c >> 1) - lane, v = t + other + i * step;
+            if (v < P.vecs)
+              bring16(base + (plane(stage, i, c & 1) + other) * 16, static_cast<const H*>(P.h) + r * P.h_stride + v * kVec + (c & 1) * 4);
+          }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -158,79 +203,90 @@ __global__ void __launch_bounds__(kMaxThreads) residual_kernel(const __grid_cons
   grid_dependency_wait();
   allow_dependents();
   for (int k = 0; k < P.stages; ++k) bring(row + k * rows_at_once, k);
-  const float scalar =
-      P.gate_kind == kGateScalar ? P.beta * activate(static_cast<float>(*static_cast<const T*>(P.gate)), P.act) : P.beta;
+  float scalar = P.beta;
+  if (P.gate_kind == kGateScalar) {
+    float a, b;
+    unpair(activate2(both(static_cast<float>(*static_cast<const T*>(P.gate))), P.act), a, b);
+    scalar *= a;
+  }
   // sums use two places in turn: one is written again only behind the other's barrier, when all have read it
   int place = 0, stage = 0;
   for (; row < P.rows; row += rows_at_once) {
     brought(P.stages - 1);
+    if constexpr (HP == 2) __syncwarp();
+    uint64_t z[N][kPairs], u[N][kPairs];  // h' and the block's output; of pieces past the row's end: zeros
+    uint64_t sum2 = 0;
+    float lo, hi;
     float factor = scalar;
-    if (P.post_eps >= 0.f) {
-      float sum = 0.f;
+    if (has_y) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (t + i * step >= P.vecs) continue;
-        float f[kVec];
-        unpack<T>(held[plane(stage, i, HP)], f);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sum = fmaf(f[e], f[e], sum);
+        if (t + i * step < P.vecs) unpack<T>(held[plane(stage, i, HP)], u[i]);
+        else u[i][0] = u[i][1] = u[i][2] = u[i][3] = 0;
       }
-      factor *= rsqrtf(fmaf(row_sum<WARP_ROW>(sum, s_sum[place]), P.inv_dim, P.post_eps));
-      place ^= 1;
+      if (P.post_eps >= 0.f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) sum2 = fma2(u[i][e], u[i][e], sum2);
+        unpair(sum2, lo, hi);
+        factor *= rsqrtf(fmaf(row_sum<WARP_ROW>(lo + hi, s_sum[place]), P.inv_dim, P.post_eps));
+        place ^= 1;
+      }
     }
-    float z[N][kVec];
-    float sum = 0.f;
+    sum2 = 0;
+    const uint64_t factor2 = both(factor), alpha2 = both(P.alpha);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int v = t + i * step;
       if (v >= P.vecs) continue;
       Raw<H>::get(held[plane(stage, i, 0)], held[plane(stage, i, HP - 1)], z[i]);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) z[i][e] *= P.alpha;
       if (has_y) {
-        float u[kVec], w[kVec];
-        unpack<T>(held[plane(stage, i, HP)], u);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) u[e] *= factor;
+        uint64_t w[kPairs];
         if (P.post_norm) {
           unpack<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(P.post_norm) + v * kVec), w);
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) u[e] *= w[e];
+          for (int e = 0; e < kPairs; ++e) u[i][e] = mul2(u[i][e], w[e]);
         }
         if (P.gate_kind == kGateRow) {
           unpack<T>(has_g ? held[plane(stage, i, planes - 1)] : *reinterpret_cast<const uint4*>(static_cast<const T*>(P.gate) + v * kVec), w);
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) u[e] *= activate(w[e], P.act);
+          for (int e = 0; e < kPairs; ++e) u[i][e] = mul2(u[i][e], activate2(w[e], P.act));
         }
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) z[i][e] += u[e];
+        for (int e = 0; e < kPairs; ++e) z[i][e] = fma2(z[i][e], alpha2, mul2(u[i][e], factor2));
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) z[i][e] = mul2(z[i][e], alpha2);
       }
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) sum = fmaf(z[i][e], z[i][e], sum);
+      for (int e = 0; e < kPairs; ++e) sum2 = fma2(z[i][e], z[i][e], sum2);
     }
-    bring(row + P.stages * rows_at_once, stage);  // (into places that this thread has read)
+    if constexpr (HP == 2) __syncwarp();
+    bring(row + P.stages * rows_at_once, stage);  // (into places that this thread, or its warp, has read)
     stage = stage + 1 == P.stages ? 0 : stage + 1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int v = t + i * step;
-      if (v < P.vecs && P.h_out) Raw<H>::store(static_cast<H*>(P.h_out) + row * P.h_out_stride + v * kVec, z[i]);
+      if (v < P.vecs && P.h_out) Raw<H>::store(static_cast<H*>(P.h_out) + row * P.h_out_stride + v * kVec, z[i], P.wide);
     }
     if (!P.x_out) continue;
-    const float r = rsqrtf(fmaf(row_sum<WARP_ROW>(sum, s_sum[place]), P.inv_dim, P.eps));
+    unpair(sum2, lo, hi);
+    const uint64_t r = both(rsqrtf(fmaf(row_sum<WARP_ROW>(lo + hi, s_sum[place]), P.inv_dim, P.eps)));
     place ^= 1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int v = t + i * step;
       if (v >= P.vecs) continue;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) z[i][e] *= r;
+      for (int e = 0; e < kPairs; ++e) z[i][e] = mul2(z[i][e], r);
       if (P.norm) {
-        float w[kVec];
+        uint64_t w[kPairs];
         unpack<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(P.norm) + v * kVec), w);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) z[i][e] *= w[e];
+        for (int e = 0; e < kPairs; ++e) z[i][e] = mul2(z[i][e], w[e]);
       }
-      Raw<T>::store(static_cast<T*>(P.x_out) + row * P.x_stride + v * kVec, z[i]);
+      Raw<T>::store(static_cast<T*>(P.x_out) + row * P.x_stride + v * kVec, z[i], false);
     }
   }
   brought(0);
@@ -348,6 +404,7 @@ extern "C" svx_status svx_residual_norm(const svx_residual* in, void* stream) {
   p.beta = a.beta;
   p.eps = a.eps;
   p.post_eps = a.post_eps;
+  p.wide = svx::is_aligned(a.h_out, 32);
   p.inv_dim = 1.f / static_cast<float>(a.dim);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;

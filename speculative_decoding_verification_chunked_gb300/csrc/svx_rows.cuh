@@ -406,23 +406,6 @@ __device__ __forceinline__ float max128(const float (&v)[kTile]) {
   for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], v[124 + e]);
   return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
-// two fp32 values in one register pair
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 template <int SRC>
 __device__ __forceinline__ Seen keys_seen(const AttendParams& P, const RowSeg& g, int t0) {
   const int lane = threadIdx.x & 31;

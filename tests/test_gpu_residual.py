@@ -2,8 +2,8 @@
 
 Error bounds, derived before any run.  fp32 throughout, one rounding u = torch.finfo(type).eps / 2 at the end.  A mean of squares adds
 at most 32 of a thread's terms in a row and 10 levels of a tree, each within 2^-24, and its square root and the division
-stay under 2^-21: a norm is within 2^-18 of itself.  tanh and the sigmoid stay within 2^-20 (their arguments are 16-bit
-values), so the branch g u is within 2^-17 of itself and h' within e = 2^-22 |alpha h| + 2^-17 |beta g u| of its value.  The norm
+stay under 2^-21: a norm is within 2^-18 of itself.  tanh and the sigmoid stay within 2^-19 (their arguments are 16-bit
+values, here below 16), so the branch g u is within 2^-17 of itself and h' within e = 2^-22 |alpha h| + 2^-17 |beta g u| of its value.  The norm
 of h' divides by its root mean square, which such errors move by |e| / |h'| at most (norms over the row), so x is within
 2^-18 |x| + |norm| r e + |x| |e| / |h'|.
 """
