@@ -92,6 +92,8 @@ struct AttendParams {
   float4* rows_o;               // [row_ctas][2][D / 4][item_rows]: states of items that more than one CTA works on
   float2* rows_ml;              // [row_ctas][2][item_rows]
   int32_t item_rows, row_ctas, min_tiles;
+  int32_t row_whole;            // items are not split over CTAs
+  float group_inverse;          // 1 / group
 };
 
 // The flat range of chunks, as every kernel of the call computes it from the lengths.  Sequences: the requests;
@@ -467,17 +469,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
   __shared__ Plan<SRC> plan;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // Behind rows_kernel, which takes the prefixes: neither reads what the other writes, and that one had waited for all
-  // that came before when it let this one start.  The wait is for the join, which relies on this kernel's end.
-  const bool beside = SRC == kShared && P.prefix_apart;
-  if (!beside) grid_dependency_wait();
+  grid_dependency_wait();
   allow_dependents();
   const int T_all = build_plan<SRC, CT>(P, plan, blockIdx.x == 0);
 
   const Split split(P, T_all);
   if (blockIdx.x >= split.used) {
     if constexpr (SRC != kShared) write_empty<T, SRC, D>(P, plan);  // (kShared: the join's work)
-    if (beside) grid_dependency_wait();
     return;
   }
   int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
@@ -864,7 +862,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
     }
   }
   if constexpr (SRC != kShared) write_empty<T, SRC, D>(P, plan);
-  if (beside) grid_dependency_wait();
 }
 
 // Merges the pieces of the items that more than one CTA worked on, and adds the weights.  CTA (x, y): KV head x of all

@@ -81,8 +81,8 @@ svx_status cross_view(const svx_cross* c, CrossView* out) {
   size_pieces(&z, chunks, a.head_dim, sms);
   out->many = rows > kRowsMax;
   if (out->many) {
-    const int64_t items = B * Hkv * ((rows + kRowTile - 1) / kRowTile), tiles = items * ((S + kTile - 1) / kTile);
-    size_rows(&out->rz, tiles, rows, a.head_dim, sms, 0);
+    const int item_rows = item_rows_for(rows);
+    size_rows(&out->rz, B * Hkv * ((rows + item_rows - 1) / item_rows), (S + kTile - 1) / kTile, item_rows, a.head_dim, sms, 0, true);
   }
   out->total = out->many ? out->rz.total : z.total;
   AttendParams& p = out->p;
@@ -114,7 +114,7 @@ template <typename T, int D>
 cudaError_t launch_cross(const AttendParams& p, bool many, int device, cudaStream_t s) {
   if (many) {
     const cudaError_t e = launch_rows<T, kDense, D>(p, device, s);
-    if (e != cudaSuccess || p.row_ctas == 1) return e;
+    if (e != cudaSuccess || p.row_ctas == 1 || p.row_whole) return e;
     // as many CTAs as are resident at a time: 8 an SM
     const int row_groups = (p.row_ctas - 1) * (p.item_rows / 32), parts = std::min(std::max(8 * p.row_ctas / row_groups, 1), D / 32);
     return launch_pdl(join_rows<T, kDense, D>, dim3(row_groups, parts), dim3(kWarps * 32), 0, s, p);

@@ -49,7 +49,7 @@ struct RowsCfg {
   static constexpr uint32_t OFF_Q = OFF_V + VST * TILE;
   static constexpr uint32_t OFF_OUT = OFF_Q + QST * QT * Q_TILE;  // [8 warps][32 rows][32 dimensions]: outputs on their way
   static constexpr uint32_t OFF_ML = OFF_OUT + 8 * 2048;  // float2 [2][128]: the streams' states at a segment's end
-  static constexpr int N_BAR = 2 * KST + 2 * VST + 2 * QST + 2 + 2 + 2 + 1 + 1;
+  static constexpr int N_BAR = 2 * KST + 2 * VST + 2 * QST + 4 * 2 + 1;
   static constexpr uint32_t OFF_BAR = OFF_ML + 2 * kRowTile * 8;
   static constexpr uint32_t OFF_MISC = OFF_BAR + N_BAR * 8;  // [0] TMEM base, [1] abort flag
   static constexpr uint32_t BYTES = OFF_MISC + 16;
@@ -310,18 +310,35 @@ __device__ __forceinline__ RowSeg row_seg(const AttendParams& P, const RowPlan& 
   return g;
 }
 
+// The first tile at x or behind it that begins an item.
+template <int SRC>
+__device__ __forceinline__ int row_item_start(const AttendParams& P, const RowPlan& s, int x, int total) {
+  if (x >= total) return total;
+  const RowSeg g = row_seg<SRC>(P, s, x, total);
+  return g.tile0 == 0 ? x : g.end;
+}
+
+// x / n for x < 2^24: the float product with the inverse is off by less than one
+__device__ __forceinline__ int fast_div(int x, int n, float inverse) {
+  int q = static_cast<int>(static_cast<float>(x) * inverse);
+  const int left = x - q * n;
+  if (left < 0) --q;
+  else if (left >= n) ++q;
+  return q;
+}
+
 // Element offset of row r of a segment's block in q, and the places of its outputs.
 template <int SRC, int D>
 __device__ __forceinline__ int64_t row_q(const AttendParams& P, const RowPlan& s, const RowSeg& g, int r) {
   r += g.rt * P.item_rows;
-  const int j = r / P.group, head = g.h * P.group + (r - j * P.group);
+  const int j = fast_div(r, P.group, P.group_inverse), head = g.h * P.group + (r - j * P.group);
   if constexpr (SRC == kShared) return (static_cast<int64_t>(s.req0[g.b] + j) * P.n_q + head) * D;
   return g.b * P.q_b + head * P.q_h + j * P.q_n;
 }
 template <int SRC, int D>
 __device__ __forceinline__ RowOut row_out(const AttendParams& P, const RowPlan& s, const RowSeg& g, int r) {
   r += g.rt * P.item_rows;
-  const int j = r / P.group, head = g.h * P.group + (r - j * P.group);
+  const int j = fast_div(r, P.group, P.group_inverse), head = g.h * P.group + (r - j * P.group);
   if constexpr (SRC == kShared) {
     const int64_t row = static_cast<int64_t>(s.req0[g.b] + j) * P.n_q + head;
     return RowOut{row * D, row};
@@ -432,7 +449,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t KFULL = base + C::OFF_BAR, KEMPTY = KFULL + 8u * C::KST, VFULL = KEMPTY + 8u * C::KST,
                  VEMPTY = VFULL + 8u * C::VST, QFULL = VEMPTY + 8u * C::VST, QEMPTY = QFULL + 8u * C::QST, SFULL = QEMPTY + 8u * C::QST,
-                 PFULL = SFULL + 16u, OFULL = PFULL + 16u, OEMPTY = OFULL + 16u, DRAIN = OEMPTY + 8u;
+                 PFULL = SFULL + 16u, OFULL = PFULL + 16u, OEMPTY = OFULL + 16u, DRAIN = OEMPTY + 16u;
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(gbase + C::OFF_MISC);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KST; ++i) {
@@ -451,8 +468,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       bar_init(SFULL + 8u * i, 1);
       bar_init(PFULL + 8u * i, 128);
       bar_init(OFULL + 8u * i, 1);
+      bar_init(OEMPTY + 8u * i, 128);
     }
-    bar_init(OEMPTY, 256);
     bar_init(DRAIN, 1);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -464,13 +481,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_before();
-  grid_dependency_wait();
+  // Behind attend_kernel, which takes the requests' own slots: neither reads what the other writes, and that one had waited for all
+  // that came before when it let this one start.  The wait is for the join, which relies on this kernel's end.
+  if (SRC != kShared) grid_dependency_wait();
   allow_dependents();
   const int T_all = build_row_plan<SRC>(P, plan, blockIdx.x == 0);  // (its barriers also show the lines above to all threads)
   tc_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
   const RowSplit split(P, T_all);
-  const int x0 = blockIdx.x < split.used ? split.begin(blockIdx.x) : 0, x1 = blockIdx.x < split.used ? split.begin(blockIdx.x + 1) : 0;
+  int x0 = blockIdx.x < split.used ? split.begin(blockIdx.x) : 0, x1 = blockIdx.x < split.used ? split.begin(blockIdx.x + 1) : 0;
+  if (P.row_whole) {  // the items that begin in the range, whole
+    x0 = row_item_start<SRC>(P, plan, x0, T_all);
+    x1 = x1 ? row_item_start<SRC>(P, plan, x1, T_all) : x0;
+  }
   RowWaiter W{misc + 1, P.pages.status};
 
   // requests without keys
@@ -613,6 +636,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     const uint32_t one = one_lane();
     int seg = 0, kt = 0, vt = 0, qb = 0;     // segments so far, and the places of the next K, V and Q
     uint32_t kp = 0, vp = 0, qp = 0, np = 0; // parities: of the rings' rounds, and of each stream's P's (bit s)
+    uint32_t ends = 0, used = 0;  // of each stream's O: parity of its ends, and whether there were any
     bool ok = true;
     for (int x = x0; x < x1 && ok; ++seg) {
       const RowSeg g = row_seg<SRC>(P, plan, x, x1);
@@ -642,7 +666,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       for (int u = 0; u < steps && ok; ++u) {
         const int s = u & 1;
         const bool opens = !two || s == 0, closes = !two || s == 1;
-        ok = (!opens || W.warp_wait(VFULL + 8u * vt, vp)) && (u > 0 || seg == 0 || W.warp_wait(OEMPTY, (seg - 1) & 1u)) &&
+        ok = (!opens || W.warp_wait(VFULL + 8u * vt, vp)) && (u > 1 || !(used >> s & 1u) || W.warp_wait(OEMPTY + 8u * s, (ends >> s & 1u) ^ 1u)) &&
              W.warp_wait(PFULL + 8u * s, np >> s & 1u);
         if (!ok) break;
         np ^= 1u << s;
@@ -660,8 +684,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
           commit(one, VEMPTY + 8u * vt);
           if (++vt == C::VST) vt = 0, vp ^= 1u;
         }
-        if (u + 2 >= steps) commit(one, OFULL + 8u * s);  // the stream's last
-        else ok = issue_s(u + 2);
+        if (u + 2 >= steps) {  // the stream's last
+          commit(one, OFULL + 8u * s);
+          ends ^= 1u << s;
+          used |= 1u << s;
+        } else {
+          ok = issue_s(u + 2);
+        }
       }
       if (++qb == C::QST) qb = 0, qp ^= 1u;
       x += g.n;
@@ -680,16 +709,15 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     float2* const s_ml = reinterpret_cast<float2*>(gbase + C::OFF_ML);
     uint4* const out = reinterpret_cast<uint4*>(gbase + C::OFF_OUT) + warp * 128;
     uint32_t ns = 0, no[2] = {0, 0};  // S's of this stream, and ends of both, so far
-    bool ok = true;
+    bool ok = true;  // (once a wait has given up, all that follows is left out, but for the barriers of all softmax threads)
     for (int x = x0; x < x1;) {
-      if (!softmax_sync(ok)) break;  // (and the last segment's states have been read)
       const RowSeg g = row_seg<SRC>(P, plan, x, x1);
       const bool two = QT == 2 && g.rows > kRowTile;
       const int steps = two ? 2 * g.n : g.n, mine = (steps + 1 - s) / 2;  // steps of this stream
       const int my_rows = two ? g.rows - s * kRowTile : g.rows;
       const bool busy = (warp & 3) * 32 < my_rows;  // this warp has rows
       float m = kNegInf, l = 0.f;
-      for (int i = 0; i < mine; ++i, ++ns) {
+      for (int i = 0; i < mine && ok; ++i, ++ns) {
         const int t0 = (g.tile0 + (two ? i : 2 * i + s)) * kTile;
         const bool all = (SRC != kDense || !P.mask) && t0 + kTile <= g.len;
         Seen seen = {};
@@ -771,7 +799,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         const int c0 = two ? 0 : s * (D / 2), c1 = two ? D : c0 + D / 2;
         RowOut at{0, 0};
         if (mine_too) at = row_out<SRC, D>(P, plan, g, r);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+#pragma unroll 1
         for (int c = c0; c < c1; c += 32) {
           float o[32];
           tmem_read32<0>(tmem + lanes + C::O_COL + (two ? s * D : 0) + c, o);
@@ -819,14 +848,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         if (mine_too && (two || s == 0)) {
           if (!whole) P.rows_ml[static_cast<int64_t>(slot) * P.item_rows + r] = make_float2(m, l);
           else if (SRC == kShared) P.state_ml[at.lse] = make_float2(m, l);
-          else if (P.lse) P.lse[at.lse] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+          else if (P.lse) P.lse[at.lse] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
         }
         tc_before();
       }
-      bar_arrive(OEMPTY);
+      if (!two) ok = softmax_sync(ok);  // (both have read O and the states)
+      if (mine > 0) bar_arrive(OEMPTY + 8u * s);
       x += g.n;
     }
   }
+  if (SRC == kShared) grid_dependency_wait();
   tc_before();
   __syncthreads();
   tc_after();
@@ -892,16 +923,28 @@ __global__ void __launch_bounds__(kWarps * 32) join_rows(const __grid_constant__
 
 // ------------------------------------------------------------------ host
 
+constexpr int kJoinTiles = 8;  // what the join of split items costs, in tiles of a CTA
+
 struct RowSizes {
   int32_t item_rows, ctas, min_tiles;
+  bool whole;  // no item is split over CTAs
   size_t rows_o, rows_ml, total;
 };
 
-// CTAs for `tiles` tiles of items of at most `rows` rows, and where their pieces lie behind `at` bytes of a workspace.
-inline void size_rows(RowSizes* z, int64_t tiles, int64_t rows, int head_dim, int sms, size_t at) {
-  z->item_rows = rows > kRowTile ? 2 * kRowTile : kRowTile;
+// Rows of an item where the rows with the same keys are at most `rows`.
+inline int item_rows_for(int64_t rows) { return rows > kRowTile ? 2 * kRowTile : kRowTile; }
+
+// At most `most` CTAs for `items` items of up to `per` tiles, and where their pieces lie behind `at` bytes of a workspace.
+// may_whole: items may stay whole, and their join go, where the CTA with the most work has little more of it than the
+// others.
+inline void size_rows(RowSizes* z, int64_t items, int64_t per, int item_rows, int head_dim, int most, size_t at, bool may_whole) {
+  const int64_t tiles = items * per;
+  z->item_rows = item_rows;
   z->min_tiles = 2;
-  z->ctas = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kMaxCtas), std::max<int64_t>((tiles + z->min_tiles - 1) / z->min_tiles, 1)));
+  most = std::min(most, kMaxCtas);
+  z->whole = may_whole && (items + most - 1) / most * per <= tiles / most + kJoinTiles;
+  if (z->whole) z->min_tiles = 1;
+  z->ctas = static_cast<int32_t>(std::min<int64_t>(most, std::max<int64_t>((tiles + z->min_tiles - 1) / z->min_tiles, 1)));
   z->rows_o = up256(at);
   z->rows_ml = z->rows_o + static_cast<size_t>(z->ctas) * 2 * z->item_rows * head_dim * 4;
   z->total = z->rows_ml + up256(static_cast<size_t>(z->ctas) * 2 * z->item_rows * 8);
@@ -912,6 +955,8 @@ inline void place_rows(AttendParams& p, const RowSizes& z, char* ws) {
   p.item_rows = z.item_rows;
   p.row_ctas = z.ctas;
   p.min_tiles = z.min_tiles;
+  p.row_whole = z.whole;
+  p.group_inverse = 1.f / static_cast<float>(p.group);
 }
 
 template <typename T, int SRC, int D, int QT>

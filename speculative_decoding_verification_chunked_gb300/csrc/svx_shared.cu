@@ -11,7 +11,7 @@ namespace {
 
 constexpr int kBatch = 64;  // pieces of a row whose factors are worked out at a time
 
-// CTA (x, y, z): KV head x of all requests' heads; block of 16 query heads y; of the dimensions, part z of gridDim.z.
+// A CTA takes every gridDim.x-th of the requests' KV heads, block of 16 query heads y, and of the dimensions part z of gridDim.z.
 // APART: the prefixes were rows_kernel's work.
 template <typename T, int D, bool APART>
 __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant__ AttendParams P) {
@@ -28,43 +28,12 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // (the lengths were there before the attention kernel began, which had waited for whoever wrote them)
   const int T_all = build_plan<kShared, CT>(P, plan, false, APART);
-  const int b = blockIdx.x / P.pages.n_kv_heads, h = blockIdx.x - b * P.pages.n_kv_heads, blk = blockIdx.y;
-  const int rows = min(P.group - blk * kRowsMax, kRowsMax);
   const Split split(P, T_all);
   const RowSplit row_split(P, APART ? plan.row_tiles : 0);
-  int prefix = 0;  // the first that ends behind the request
-  for (int i = 0; i < P.n_prefix; i += 32)
-    prefix += __popc(__ballot_sync(0xffffffffu, i + lane < P.n_prefix && plan.req0[i + lane + 1] <= b));
-  if (tid < 2 * kRowsMax) {
-    const int r = tid % kRowsMax, lot = tid / kRowsMax;  // 0: the prefix, 1: the request's own
-    Lot x{0, 0, 0};
-    int seq = kMaxReq + b, block = blk, blocks = P.blocks;
-    x.row = r;
-    bool any = r < rows;
-    if (lot == 0) {
-      any = any && prefix < P.n_prefix && plan.req0[prefix] <= b;
-      if (any) {
-        const int R = (b - plan.req0[prefix]) * P.group + blk * kRowsMax + r;
-        seq = prefix;
-        const int per = APART ? P.item_rows : kRowsMax;
-        block = R / per;
-        blocks = (seq_rows(P, plan, prefix) + per - 1) / per;
-        x.row = R % per;
-      }
-    }
-    const int n = any ? plan.n[seq] : 0;
-    if (n > 0) {
-      const int first = plan.first[seq] + (h * blocks + block) * n;
-      const bool far = APART && lot == 0;
-      x.first = far ? row_split.of(first) : split.of(first);
-      x.pieces = (far ? row_split.of(first + n - 1) : split.of(first + n - 1)) - x.first + 1;
-      if (x.pieces == 1) x.row = (lot * P.pages.n_req + b) * P.n_q + h * P.group + blk * kRowsMax + r;
-    }
-    s_lot[lot][r] = x;
-  }
-  __syncthreads();
-  grid_dependency_wait();
-  allow_dependents();
+  const int blk = blockIdx.y, rows = min(P.group - blk * kRowsMax, kRowsMax);
+  // the outputs over the threads: several share one where there are more of them than outputs
+  const int quads = D / 4 / gridDim.z, outs = rows * quads, share = max(kWarps * 32 / outs, 1);
+  const int part = share > 1 ? tid / outs : 0;
   auto ml_at = [&](int r, int c) {
     const int lot = c < s_lot[0][r].pieces ? 0 : 1;
     if (lot) c -= s_lot[0][r].pieces;
@@ -83,67 +52,116 @@ __global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant
     const float* at = x.pieces == 1 ? P.state_o + static_cast<int64_t>(x.row) * D : P.part_o + static_cast<int64_t>(slot * kRowsMax + x.row) * D;
     return __ldcg(reinterpret_cast<const float4*>(at + d4));
   };
-  // the outputs over the threads: several share one where there are more of them than outputs
-  const int quads = D / 4 / gridDim.z, outs = rows * quads, share = max(kWarps * 32 / outs, 1);
-  const int part = share > 1 ? tid / outs : 0;
-  int most = 0;  // pieces of any row
-  for (int r = 0; r < rows; ++r) most = max(most, s_lot[0][r].pieces + s_lot[1][r].pieces);
-  for (int r = warp; r < rows; r += kWarps) {
-    const int pieces = s_lot[0][r].pieces + s_lot[1][r].pieces;
-    float M = kNegInf;
-    for (int c = lane; c < pieces; c += 32) M = fmaxf(M, ml_at(r, c).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) s_ml[r] = make_float2(M, 0.f);
-  }
-  __syncthreads();
-  for (int i0 = 0; i0 < outs; i0 += kWarps * 32) {  // (once, unless there are more outputs than threads)
-    const int i = share > 1 ? tid - part * outs : i0 + tid;
-    // (rows_kernel's pieces have a row's neighbours beside it, the others its dimensions)
-    const int r = APART ? i % rows : i / quads, d4 = ((APART ? i / rows : i - r * quads) + blockIdx.z * quads) * 4;
-    const bool mine = i < outs && part < share;
-    const int pieces = mine ? s_lot[0][r].pieces + s_lot[1][r].pieces : 0;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = 0; c0 < most; c0 += kBatch) {
-      if (c0 > 0 || i0 > 0) __syncthreads();  // (the last batch's factors have been used)
-      if (i0 == 0 || most > kBatch)
-        for (int q = warp; q < rows; q += kWarps) {
-          const int end = min(s_lot[0][q].pieces + s_lot[1][q].pieces, c0 + kBatch);
-          const float2 before = s_ml[q];
-          const float less = before.x == kNegInf ? 0.f : -before.x;
-          float L = 0.f;
-          for (int c = c0 + lane; c < end; c += 32) {
-            const float2 ml = ml_at(q, c);
-            const float f = ex2(ml.x + less);
-            s_f[(c - c0) * kRowsMax + q] = f;
-            L = fmaf(ml.y, f, L);
-          }
-#pragma unroll
-          for (int k = 16; k > 0; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
-          if (lane == 0 && i0 == 0) s_ml[q].y = before.y + L;
+  auto add = [](float4& o, const float4& x, float f) {
+    o.x = fmaf(x.x, f, o.x);
+    o.y = fmaf(x.y, f, o.y);
+    o.z = fmaf(x.z, f, o.z);
+    o.w = fmaf(x.w, f, o.w);
+  };
+  bool waited = false;
+  for (int bh = blockIdx.x; bh < P.pages.n_req * P.pages.n_kv_heads; bh += gridDim.x) {
+    const int b = bh / P.pages.n_kv_heads, h = bh - b * P.pages.n_kv_heads;
+    int prefix = 0;  // the first that ends behind the request
+    for (int i = 0; i < P.n_prefix; i += 32)
+      prefix += __popc(__ballot_sync(0xffffffffu, i + lane < P.n_prefix && plan.req0[i + lane + 1] <= b));
+    if (waited) __syncthreads();  // (the last one's are done with)
+    if (tid < 2 * kRowsMax) {
+      const int r = tid % kRowsMax, lot = tid / kRowsMax;  // 0: the prefix, 1: the request's own
+      Lot x{0, 0, 0};
+      int seq = kMaxReq + b, block = blk, blocks = P.blocks;
+      x.row = r;
+      bool any = r < rows;
+      if (lot == 0) {
+        any = any && prefix < P.n_prefix && plan.req0[prefix] <= b;
+        if (any) {
+          const int R = (b - plan.req0[prefix]) * P.group + blk * kRowsMax + r;
+          seq = prefix;
+          const int per = APART ? P.item_rows : kRowsMax;
+          block = R / per;
+          blocks = (seq_rows(P, plan, prefix) + per - 1) / per;
+          x.row = R % per;
         }
-      __syncthreads();
-      const int end = min(pieces, c0 + kBatch);
-#pragma unroll 8
-      for (int c = c0 + part; c < end; c += share) {
-        const float4 x = o_at(r, c, d4);
-        const float f = s_f[(c - c0) * kRowsMax + r];
-        o.x = fmaf(x.x, f, o.x);
-        o.y = fmaf(x.y, f, o.y);
-        o.z = fmaf(x.z, f, o.z);
-        o.w = fmaf(x.w, f, o.w);
       }
+      const int n = any ? plan.n[seq] : 0;
+      if (n > 0) {
+        const int first = plan.first[seq] + (h * blocks + block) * n;
+        const bool far = APART && lot == 0;
+        x.first = far ? row_split.of(first) : split.of(first);
+        x.pieces = (far ? row_split.of(first + n - 1) : split.of(first + n - 1)) - x.first + 1;
+        if (x.pieces == 1) x.row = (lot * P.pages.n_req + b) * P.n_q + h * P.group + blk * kRowsMax + r;
+      }
+      s_lot[lot][r] = x;
     }
-    if (share > 1) {
-      s_o[tid] = o;
-      __syncthreads();
-      if (part == 0)
-        for (int p = 1; p < share; ++p) {
-          const float4 x = s_o[p * outs + i];
-          o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+    __syncthreads();
+    if (!waited) {
+      grid_dependency_wait();
+      allow_dependents();
+      waited = true;
+    }
+    int most = 0;  // pieces of any row
+    for (int r = 0; r < rows; ++r) most = max(most, s_lot[0][r].pieces + s_lot[1][r].pieces);
+    for (int i0 = 0; i0 < outs; i0 += kWarps * 32) {  // (once, unless there are more outputs than threads)
+      const int i = share > 1 ? tid - part * outs : i0 + tid;
+      // (rows_kernel's pieces have a row's neighbours beside it, the others its dimensions)
+      const int r = APART ? i % rows : i / quads, d4 = ((APART ? i / rows : i - r * quads) + blockIdx.z * quads) * 4;
+      const bool mine = i < outs && part < share;
+      const int pieces = mine ? s_lot[0][r].pieces + s_lot[1][r].pieces : 0;
+      // this thread's first pieces are fetched along with the states
+      constexpr int kAhead = 4;
+      float4 ahead[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (part + u * share < pieces) ahead[u] = o_at(r, part + u * share, d4);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c0 = 0; c0 < max(most, 1); c0 += kBatch) {
+        if (c0 > 0 || i0 > 0) __syncthreads();  // (the last batch's factors have been used)
+        if (i0 == 0 || most > kBatch)
+          for (int q = warp; q < rows; q += kWarps) {
+            const int all = s_lot[0][q].pieces + s_lot[1][q].pieces, end = min(all, c0 + kBatch);
+            float2 ml = c0 + lane < end ? ml_at(q, c0 + lane) : make_float2(kNegInf, 0.f);
+            float M = ml.x, L = 0.f;
+            if (c0 == 0 && i0 == 0) {
+              for (int c = lane + 32; c < all; c += 32) M = fmaxf(M, ml_at(q, c).x);
+#pragma unroll
+              for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+            } else {
+              M = s_ml[q].x;
+              L = s_ml[q].y;
+            }
+            const float less = M == kNegInf ? 0.f : -M;
+            float sum = 0.f;
+            for (int c = c0 + lane; c < end; c += 32) {
+              if (c != c0 + lane) ml = ml_at(q, c);
+              const float f = ex2(ml.x + less);
+              s_f[(c - c0) * kRowsMax + q] = f;
+              sum = fmaf(ml.y, f, sum);
+            }
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+            if (lane == 0 && i0 == 0) s_ml[q] = make_float2(M, L + sum);
+          }
+        __syncthreads();
+        const int end = min(pieces, c0 + kBatch);
+        int c = c0 + part;
+        if (c0 == 0) {
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u, c += share)
+            if (c < end) add(o, ahead[u], s_f[c * kRowsMax + r]);
         }
+#pragma unroll 4
+        for (; c < end; c += share) add(o, o_at(r, c, d4), s_f[(c - c0) * kRowsMax + r]);
+      }
+      if (share > 1) {
+        s_o[tid] = o;
+        __syncthreads();
+        if (part == 0)
+          for (int p = 1; p < share; ++p) {
+            const float4 x = s_o[p * outs + i];
+            o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+          }
+      }
+      if (mine && part == 0) write_row<T>(P, place<kShared, D>(P, plan, kMaxReq + b, h, blk, r), d4, s_ml[r].x, s_ml[r].y, o);
     }
-    if (mine && part == 0) write_row<T>(P, place<kShared, D>(P, plan, kMaxReq + b, h, blk, r), d4, s_ml[r].x, s_ml[r].y, o);
   }
 }
 
@@ -182,15 +200,27 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
   const int64_t chunks = own + (out->many ? 0 : far);
   if (own + far > 0x7fffffff) return paged_fail(SVX_ERR_UNSUPPORTED, "heads times lengths are too large (%lld chunks of %d slots, at most 2^31 - 1)",
                       static_cast<long long>(own + far), ct);
-  size_pieces(&z, chunks, c->head_dim, sms);
+  // With many rows the SMs are shared out over the two kernels by their work, so that they end together: a CTA of attend_kernel brings in
+  // some 45 GB/s of short sequences; a tile of rows_kernel takes 1.4 us (0.8 for d = 64, where two row tiles' exponentials bound it, and with one row tile
+  // the copy rate).  (By the bounds known here: lengths may be shorter.)
+  int own_ctas = sms;
+  if (out->many) {
+    const int item_rows = item_rows_for(all_rows);
+    const int64_t items = c->n_kv_heads * (all_rows / item_rows + used), per = (max_prefix + kTile - 1) / kTile;
+    const double own_us = static_cast<double>(n_req) * c->n_kv_heads * max_len * c->head_dim * 4 / 45e3;
+    const double far_us = static_cast<double>(items) * per * (c->head_dim == 128 ? 1.4 : 0.8);
+    own_ctas = std::min(std::max(static_cast<int>(sms * own_us / (own_us + far_us) + 0.5), 4), sms - 4);
+    size_rows(&out->rz, items, per, item_rows, c->head_dim, sms - own_ctas, 0, false);
+  }
+  size_pieces(&z, chunks, c->head_dim, own_ctas);
   const size_t rows = static_cast<size_t>(2) * n_req * n_q;
   z.state_o = z.total;
   z.state_ml = z.state_o + up256(rows * c->head_dim * 4);
   z.total = z.state_ml + up256(rows * 8);
   if (out->many) {
-    const int64_t items = c->n_kv_heads * (all_rows / kRowTile + used);
-    size_rows(&out->rz, items * ((max_prefix + kTile - 1) / kTile), all_rows, c->head_dim, sms, z.total);
-    z.total = out->rz.total;
+    out->rz.rows_o += z.total;
+    out->rz.rows_ml += z.total;
+    z.total += out->rz.total;
   }
   return SVX_OK;
 }
@@ -198,14 +228,14 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
 template <typename T, int D>
 cudaError_t launch_shared(const AttendParams& p, int device, cudaStream_t s) {
   const int sms = sm_count(device);
-  // parts of the dimensions: as many as let the CTAs be resident at a time (3 an SM), with 4 threads or more to an output of few rows
-  const int ctas = p.pages.n_req * p.pages.n_kv_heads * p.blocks;
-  const dim3 grid(p.pages.n_req * p.pages.n_kv_heads, p.blocks, ctas * 4 <= 3 * sms ? 4 : ctas * 2 <= 3 * sms ? 2 : 1);
+  // the join: CTAs that are resident at a time (4 an SM); where the heads are fewer, several to a head, on parts of its dimensions
+  const int heads = p.pages.n_req * p.pages.n_kv_heads, ctas = heads * p.blocks;
+  const dim3 grid(std::min(heads, std::max(4 * sms / p.blocks, 1)), p.blocks, ctas * 4 <= 4 * sms ? 4 : ctas * 2 <= 4 * sms ? 2 : 1);
   cudaError_t e;
   if (p.prefix_apart) {
-    e = launch_rows<T, kShared, D>(p, device, s);
-    if (e != cudaSuccess) return e;
     e = p.group > 8 ? launch_attend<T, kShared, D, true, false>(p, device, s) : launch_attend<T, kShared, D, false, false>(p, device, s);
+    if (e != cudaSuccess) return e;
+    e = launch_rows<T, kShared, D>(p, device, s);
     return e != cudaSuccess ? e : launch_pdl(join_shared<T, D, true>, grid, dim3(kWarps * 32), 0, s, p);
   }
   // (rows of a prefix: those of all its requests)
@@ -273,7 +303,6 @@ extern "C" svx_status svx_paged_decode_shared(const svx_pages* cache, int32_t n_
   svx::place_pieces(p, z.z, ws);
   p.state_o = reinterpret_cast<float*>(ws + z.z.state_o);
   p.state_ml = reinterpret_cast<float2*>(ws + z.z.state_ml);
-  if (z.many) svx::place_rows(p, z.rz, ws);
   p.prefix_apart = z.many;
   p.q = q;
   p.len = len;
@@ -281,6 +310,7 @@ extern "C" svx_status svx_paged_decode_shared(const svx_pages* cache, int32_t n_
   p.lse = lse;
   p.n_q = n_q_heads;
   p.group = n_q_heads / cache->n_kv_heads;
+  if (z.many) svx::place_rows(p, z.rz, ws);
   p.prefix_table = f.table;
   p.prefix_len = f.len;
   p.first = f.first;
