@@ -25,6 +25,8 @@
 
 #include "svx_attend.cuh"
 
+#include <cuda.h>
+
 #include <type_traits>
 
 namespace svx {
@@ -59,6 +61,14 @@ struct RowsCfg {
   static_assert(SMEM + 5 * 1024 <= 232448, "shared memory per CTA, with the plan");
 };
 
+// The kernel's parameters: with tensor maps of K and V, of dimensions (d, KV head, slot, page) or (d, KV head, state, request), if their
+// strides allow.  A map's box is 64 dimensions of `box` slots of a head: a page's, or a part of them, at most a tile's.
+struct RowsParams : AttendParams {
+  CUtensorMap k_map, v_map;
+  int32_t box;                 // 0: no maps
+  int32_t head_step, page_step;  // 0 where all heads or requests are the same
+};
+
 // ------------------------------------------------------------------ PTX
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -88,6 +98,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
 // this thread's copies so far, once they are in, arrive on the barrier
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_expecting(uint32_t bar, uint32_t bytes) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes) : "memory");
+}
+// A box of a map, from (x, y, z, w), to shared memory; its bytes count on the barrier.
+__device__ __forceinline__ void bring_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -440,7 +460,7 @@ __device__ __forceinline__ Seen keys_seen(const AttendParams& P, const RowSeg& g
 // ------------------------------------------------------------------ the kernel
 
 template <typename T, int SRC, int D, int QT>
-__global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_constant__ AttendParams P) {
+__global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_constant__ RowsParams P) {
   using C = RowsCfg<D, QT>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ RowPlan plan;
@@ -519,9 +539,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     const T* const pool = static_cast<const T*>(is_v ? P.pages.v : P.pages.k);
     constexpr int PIECES = D / 8, RPI = 32 / PIECES;  // a row's pieces of 16 bytes; rows that a warp copies at a time
     const int piece = lane % PIECES, r0 = lane / PIECES;
-    // runs of 16 keys lie in one page, or any keys a stride apart: one address for several copies
-    const bool runs = !kBoundsChecked && (SRC == kDense || P.pages.page_size % 16 == 0);
-    const int64_t step = RPI * P.pages.tok_stride;
+    const CUtensorMap* const map = is_v ? &P.v_map : &P.k_map;
+    const bool maps = !kBoundsChecked && P.box > 0;
+    const int box = maps ? P.box : kTile;
+    if (maps && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
     int i = 0;
     bool ok = true;
     for (int x = x0; x < x1 && ok;) {
@@ -539,67 +560,73 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       if constexpr (SRC == kShared) look(0);
       for (int t = 0; t < g.n; ++t, ++i) {
         const int t0 = (g.tile0 + t) * kTile;
+        const int stage = i % stages;
+        const uint32_t dst = ring + stage * C::TILE;
         const Seen seen = keys_seen<SRC>(P, g, t0);
         const bool all = (seen.w[0] & seen.w[1] & seen.w[2] & seen.w[3]) == 0xffffffffu;
-        int64_t off[4];
-        bool there = true;
-        if (SRC == kShared || !all || !runs) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            off[u] = -1;
-            const int key = t0 + u * 32 + lane;
-            if (!(seen.w[u] >> lane & 1u)) continue;
-            if constexpr (SRC == kShared) {
-              off[u] = slot_offset(P.pages, page[u], key - page_of(P.pages, static_cast<uint32_t>(key)) * P.pages.page_size);
-              if (off[u] < 0) atomicOr(P.pages.status, kErrInput);
-            } else {
-              off[u] = g.b * P.pages.page_stride + key * P.pages.tok_stride;
-            }
-            if (off[u] >= 0) off[u] += g.h * P.pages.head_stride;
-            if (off[u] >= 0 && !in_bounds(pool + off[u], D, pool, P.pages.extent, P.pages.status, kSitePool)) off[u] = -1;
-          }
+        bool boxes = maps && all;
+        if constexpr (SRC == kShared) {
+          const uint32_t n = P.pages.n_pages;
+          boxes = boxes && __all_sync(0xffffffffu, static_cast<uint32_t>(page[0]) < n && static_cast<uint32_t>(page[1]) < n &&
+                                                       static_cast<uint32_t>(page[2]) < n && static_cast<uint32_t>(page[3]) < n);
+        }
+        if (boxes) {  // a tile whose keys all count: in boxes, one or more a lane
+          const int runs = kTile / box;
+          // lane l: half l / runs of the dimensions, run l % runs
+          const int run = lane % runs, key = run * box;
+          int w = g.b * P.page_step, z = t0;
           if constexpr (SRC == kShared) {
-            there = __all_sync(0xffffffffu, off[0] >= 0 && off[1] >= 0 && off[2] >= 0 && off[3] >= 0);
+            const int32_t p01 = __shfl_sync(0xffffffffu, page[0], key & 31), p1 = __shfl_sync(0xffffffffu, page[1], key & 31),
+                          p2 = __shfl_sync(0xffffffffu, page[2], key & 31), p3 = __shfl_sync(0xffffffffu, page[3], key & 31);
+            w = key < 64 ? (key < 32 ? p01 : p1) : key < 96 ? p2 : p3;
+            z = t0 + key - page_of(P.pages, static_cast<uint32_t>(t0 + key)) * P.pages.page_size;
             look(t + 1);
           }
+          if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) arrive_expecting(full + 8u * stage, C::TILE);
+          __syncwarp();
+          const int half = lane / runs;
+          if (half < D / 64) bring_box(dst + half * kHalf + key * 128, map, half * 64, g.h * P.head_step, z, w, full + 8u * stage);
+          if (lane != 0) bar_arrive(full + 8u * stage);
+          continue;
         }
-        const int stage = i % stages;
+        int64_t off[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          off[u] = -1;
+          const int key = t0 + u * 32 + lane;
+          if (!(seen.w[u] >> lane & 1u)) continue;
+          if constexpr (SRC == kShared) {
+            off[u] = slot_offset(P.pages, page[u], key - page_of(P.pages, static_cast<uint32_t>(key)) * P.pages.page_size);
+            if (off[u] < 0) atomicOr(P.pages.status, kErrInput);
+          } else {
+            off[u] = g.b * P.pages.page_stride + key * P.pages.tok_stride;
+          }
+          if (off[u] >= 0) off[u] += g.h * P.pages.head_stride;
+          if (off[u] >= 0 && !in_bounds(pool + off[u], D, pool, P.pages.extent, P.pages.status, kSitePool)) off[u] = -1;
+        }
+        if constexpr (SRC == kShared) look(t + 1);
         if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
           ok = false;
           break;
         }
-        const uint32_t dst = ring + stage * C::TILE + (piece >> 3) * kHalf;
-        if (all && runs && there) {
-          constexpr int RUN = SRC == kShared ? 16 : kTile;
-#pragma unroll 1
-          for (int k = 0; k < kTile; k += RUN) {
-            const T* src = pool + piece * 8 + r0 * P.pages.tok_stride;
-            if constexpr (SRC == kShared) {
-              const int64_t o01 = k & 32 ? off[1] : off[0], o23 = k & 32 ? off[3] : off[2];
-              src += __shfl_sync(0xffffffffu, k & 64 ? o23 : o01, k & 31);
-            } else {
-              src += g.b * P.pages.page_stride + t0 * P.pages.tok_stride + g.h * P.pages.head_stride;
-            }
-#pragma unroll 8
-            for (int j = 0; j < RUN; j += RPI, src += step) {
-              const int r = k + j + r0;
-              copy16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), src, 16);
-            }
-          }
-        } else {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u)
 #pragma unroll 8
-            for (int j = 0; j < 32 / RPI; ++j) {
-              const int in32 = j * RPI + r0, r = u * 32 + in32;
-              const int64_t ro = __shfl_sync(0xffffffffu, off[u], in32);
-              copy16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), pool + (ro >= 0 ? ro : 0) + piece * 8, ro >= 0 ? 16 : 0);
-            }
-        }
+          for (int j = 0; j < 32 / RPI; ++j) {
+            const int in32 = j * RPI + r0, r = u * 32 + in32;
+            const int64_t ro = __shfl_sync(0xffffffffu, off[u], in32);
+            copy16(dst + (piece >> 3) * kHalf + r * 128 + (((piece & 7) ^ (r & 7)) << 4), pool + (ro >= 0 ? ro : 0) + piece * 8, ro >= 0 ? 16 : 0);
+          }
         copies_arrive(full + 8u * stage);
       }
       x += g.n;
     }
+    // nothing is on its way to this CTA's memory any more (of interest where the others have given up)
+    for (int j = max(i - stages, 0); j < i; ++j) W.drain(full + 8u * (j % stages), (j / stages) & 1u);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 11) {
     // ---- Q: a segment's rows, once the products of the one before it in the same place are done
@@ -959,8 +986,54 @@ inline void place_rows(AttendParams& p, const RowSizes& z, char* ws) {
   p.group_inverse = 1.f / static_cast<float>(p.group);
 }
 
+// Tensor maps of K and V, where their pages (of a multiple of 16 slots) or states and their strides allow; else none, and rows are
+// copied one by one.
+inline void make_maps(RowsParams& p, int src, int D, bool bf16) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<void*> known{nullptr};
+  p.box = 0;
+  void* fn = known.load(std::memory_order_acquire);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess || !fn) {
+      cudaGetLastError();
+      return;
+    }
+    known.store(fn, std::memory_order_release);
+  }
+  int box = kTile;
+  if (src == kShared)
+    while (p.pages.page_size % box) box /= 2;
+  if (box < 16 || (p.pages.page_size > 1 && p.pages.tok_stride == 0) || !p.pages.k) return;
+  p.head_step = p.pages.n_kv_heads > 1 && p.pages.head_stride != 0;
+  p.page_step = p.pages.n_pages > 1 && p.pages.page_stride != 0;
+  // (a dimension of one entry, or whose entries are all the same, has any stride)
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.head_step ? p.pages.n_kv_heads : 1),
+                              static_cast<cuuint64_t>(p.pages.page_size), static_cast<cuuint64_t>(p.page_step ? p.pages.n_pages : 1)};
+  auto stride = [&](bool step, int64_t s) { return step ? static_cast<cuuint64_t>(s) * 2 : row; };
+  const cuuint64_t strides[3] = {stride(p.head_step, p.pages.head_stride), stride(p.pages.page_size > 1, p.pages.tok_stride),
+                                 stride(p.page_step, p.pages.page_stride)};
+  for (cuuint64_t s : strides)
+    if (s >= (cuuint64_t{1} << 40)) return;
+  const cuuint32_t boxes[4] = {64, 1, static_cast<cuuint32_t>(box), 1}, ones[4] = {1, 1, 1, 1};
+  void* const at[2] = {p.pages.k, p.pages.v};
+  CUtensorMap* const maps[2] = {&p.k_map, &p.v_map};
+  for (int i = 0; i < 2; ++i)
+    if (reinterpret_cast<Encode>(fn)(maps[i], bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, at[i], dims, strides,
+                                     boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return;
+  p.box = box;
+}
+
 template <typename T, int SRC, int D, int QT>
-cudaError_t launch_rows_of(const AttendParams& p, int device, cudaStream_t s) {
+cudaError_t launch_rows_of(const AttendParams& params, int device, cudaStream_t s) {
+  RowsParams p = {};
+  static_cast<AttendParams&>(p) = params;
+  make_maps(p, SRC, D, std::is_same<T, __nv_bfloat16>::value);
   constexpr int bytes = RowsCfg<D, QT>::SMEM;
   static std::atomic<bool> done[64];
   if (device >= 64 || !done[device].load(std::memory_order_acquire)) {
