@@ -62,10 +62,12 @@ struct RowsCfg {
 };
 
 // The kernel's parameters: with tensor maps of K and V, of dimensions (d, KV head, slot, page) or (d, KV head, state, request), if their
-// strides allow.  A map's box is 64 dimensions of `box` slots of a head: a page's, or a part of them, at most a tile's.
+// strides allow: a box is 64 dimensions of `box` slots of a head, a page's or a part of them, at most a tile's.  And one of Q, (d, query
+// head, token, request) or (d, query head, request, 1), where a row tile is a whole number of tokens or requests.
 struct RowsParams : AttendParams {
-  CUtensorMap k_map, v_map;
-  int32_t box;                 // 0: no maps
+  CUtensorMap k_map, v_map, q_map;
+  int32_t box;                 // 0: no maps of K and V
+  int32_t q_box;               // tokens or requests of a row tile; 0: no map of Q
   int32_t head_step, page_step;  // 0 where all heads or requests are the same
 };
 
@@ -637,7 +639,23 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     for (int x = x0; x < x1; ++seg) {
       const RowSeg g = row_seg<SRC>(P, plan, x, x1);
       const int buf = seg % C::QST;
-      const uint32_t dst = base + C::OFF_Q + buf * (QT * C::Q_TILE) + (piece >> 3) * kHalf;
+      const uint32_t full = QFULL + 8u * buf;
+      uint32_t dst = base + C::OFF_Q + buf * (QT * C::Q_TILE);
+      if (P.q_box) {
+        if (seg >= C::QST && !W.warp_wait(QEMPTY + 8u * buf, (seg / C::QST - 1) & 1u)) break;
+        const int boxes = (QT == 2 && g.rows > kRowTile ? 2 : 1) * (D / 64);
+        if (lane == 0) arrive_expecting(full, boxes * kHalf);
+        __syncwarp();
+        if (lane < boxes) {  // lane: a row tile and 64 of its dimensions
+          const int tile = lane / (D / 64), half = lane % (D / 64);
+          const int tok = (SRC == kShared ? plan.req0[g.b] : 0) + (g.rt * (P.item_rows / kRowTile) + tile) * P.q_box;
+          bring_box(dst + tile * C::Q_TILE + half * kHalf, &P.q_map, half * 64, g.h * P.group, tok, SRC == kShared ? 0 : g.b, full);
+        }
+        if (lane != 0) bar_arrive(full);
+        x += g.n;
+        continue;
+      }
+      dst += (piece >> 3) * kHalf;
       // lane l works out the places of rows l, l + 32, ..
       int64_t off[QT * 4];
 #pragma unroll
@@ -653,9 +671,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
           copy16(dst + (u >> 2) * C::Q_TILE + r * 128 + (((piece & 7) ^ (r & 7)) << 4), q + (ro >= 0 ? ro : 0), ro >= 0 ? 16 : 0);
         }
       }
-      copies_arrive(QFULL + 8u * buf);
+      copies_arrive(full);
       x += g.n;
     }
+    for (int j = max(seg - C::QST, 0); j < seg; ++j) W.drain(QFULL + 8u * (j % C::QST), (j / C::QST) & 1u);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ---- the products.  Step u of a segment: stream u & 1; S(u + 2) follows P V(u), whose P lies over it
@@ -986,13 +1005,11 @@ inline void place_rows(AttendParams& p, const RowSizes& z, char* ws) {
   p.group_inverse = 1.f / static_cast<float>(p.group);
 }
 
-// Tensor maps of K and V, where their pages (of a multiple of 16 slots) or states and their strides allow; else none, and rows are
-// copied one by one.
+// Tensor maps, where sizes and strides allow; what has none is copied row by row.
 inline void make_maps(RowsParams& p, int src, int D, bool bf16) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
   static std::atomic<void*> known{nullptr};
-  p.box = 0;
   void* fn = known.load(std::memory_order_acquire);
   if (!fn) {
     cudaDriverEntryPointQueryResult found;
@@ -1003,30 +1020,36 @@ inline void make_maps(RowsParams& p, int src, int D, bool bf16) {
     }
     known.store(fn, std::memory_order_release);
   }
+  // Dimensions (D, n[0], n[1], n[2]) with strides of s elements and boxes of (64, box[0], box[1], 1).  A dimension of one entry has any
+  // stride; a stride of 0 over more has no map.
+  auto encode = [&](CUtensorMap* map, const void* at, const int64_t (&n)[3], const int64_t (&s)[3], int b0, int b1) {
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D)}, strides[3];
+    for (int i = 0; i < 3; ++i) {
+      if (n[i] < 1 || (n[i] > 1 && (s[i] <= 0 || s[i] >= int64_t{1} << 39))) return false;
+      dims[i + 1] = static_cast<cuuint64_t>(n[i]);
+      strides[i] = static_cast<cuuint64_t>(n[i] > 1 ? s[i] : D) * 2;
+    }
+    const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1), 1}, ones[4] = {1, 1, 1, 1};
+    return reinterpret_cast<Encode>(fn)(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(at),
+                                        dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
   int box = kTile;
   if (src == kShared)
     while (p.pages.page_size % box) box /= 2;
-  if (box < 16 || (p.pages.page_size > 1 && p.pages.tok_stride == 0) || !p.pages.k) return;
-  p.head_step = p.pages.n_kv_heads > 1 && p.pages.head_stride != 0;
-  p.page_step = p.pages.n_pages > 1 && p.pages.page_stride != 0;
-  // (a dimension of one entry, or whose entries are all the same, has any stride)
-  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.head_step ? p.pages.n_kv_heads : 1),
-                              static_cast<cuuint64_t>(p.pages.page_size), static_cast<cuuint64_t>(p.page_step ? p.pages.n_pages : 1)};
-  auto stride = [&](bool step, int64_t s) { return step ? static_cast<cuuint64_t>(s) * 2 : row; };
-  const cuuint64_t strides[3] = {stride(p.head_step, p.pages.head_stride), stride(p.pages.page_size > 1, p.pages.tok_stride),
-                                 stride(p.page_step, p.pages.page_stride)};
-  for (cuuint64_t s : strides)
-    if (s >= (cuuint64_t{1} << 40)) return;
-  const cuuint32_t boxes[4] = {64, 1, static_cast<cuuint32_t>(box), 1}, ones[4] = {1, 1, 1, 1};
-  void* const at[2] = {p.pages.k, p.pages.v};
-  CUtensorMap* const maps[2] = {&p.k_map, &p.v_map};
-  for (int i = 0; i < 2; ++i)
-    if (reinterpret_cast<Encode>(fn)(maps[i], bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, at[i], dims, strides,
-                                     boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return;
-  p.box = box;
+  if (box >= 16 && p.pages.k) {
+    p.head_step = p.pages.n_kv_heads > 1 && p.pages.head_stride != 0;
+    p.page_step = p.pages.n_pages > 1 && p.pages.page_stride != 0;
+    const int64_t n[3] = {p.head_step ? p.pages.n_kv_heads : 1, p.pages.page_size, p.page_step ? p.pages.n_pages : 1};
+    const int64_t s[3] = {p.pages.head_stride, p.pages.tok_stride, p.pages.page_stride};
+    if (encode(&p.k_map, p.pages.k, n, s, 1, box) && encode(&p.v_map, p.pages.v, n, s, 1, box)) p.box = box;
+  }
+  if (kRowTile % p.group == 0) {
+    const int64_t one = static_cast<int64_t>(p.n_q) * D;
+    const int64_t n[3] = {p.n_q, src == kShared ? p.pages.n_req : p.n_tok, src == kShared ? 1 : p.pages.n_req};
+    const int64_t s[3] = {src == kShared ? D : p.q_h, src == kShared ? one : p.q_n, src == kShared ? one : p.q_b};
+    if (encode(&p.q_map, p.q, n, s, p.group, kRowTile / p.group)) p.q_box = kRowTile / p.group;
+  }
 }
 
 template <typename T, int SRC, int D, int QT>
