@@ -115,9 +115,8 @@ cudaError_t launch_cross(const AttendParams& p, bool many, int device, cudaStrea
   if (many) {
     const cudaError_t e = launch_rows<T, kDense, D>(p, device, s);
     if (e != cudaSuccess || p.row_ctas == 1 || p.row_whole) return e;
-    // as many CTAs as are resident at a time: 8 an SM
-    const int row_groups = (p.row_ctas - 1) * (p.item_rows / 32), parts = std::min(std::max(8 * p.row_ctas / row_groups, 1), D / 32);
-    return launch_pdl(join_rows<T, kDense, D>, dim3(row_groups, parts), dim3(kWarps * 32), 0, s, p);
+    const int jobs = (p.row_ctas - 1) * (p.item_rows / 32) * (D / 32);
+    return launch_pdl(join_rows<T, kDense, D>, dim3(std::min(jobs, 4 * p.row_ctas)), dim3(kWarps * 32), 0, s, p);  // (4 an SM are resident)
   }
   const cudaError_t e =
       p.rows > 8 ? launch_attend<T, kDense, D, true, false>(p, device, s) : launch_attend<T, kDense, D, false, false>(p, device, s);

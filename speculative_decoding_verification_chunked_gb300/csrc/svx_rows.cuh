@@ -309,16 +309,11 @@ struct RowSeg {
   int first, end;       // the item's tiles in the flat range
 };
 
-// (all lanes of a warp alike)
+// (of sequence b)
 template <int SRC>
-__device__ __forceinline__ RowSeg row_seg(const AttendParams& P, const RowPlan& s, int x, int x1) {
-  const int seqs = SRC == kShared ? P.n_prefix : P.pages.n_req;
+__device__ __forceinline__ RowSeg row_seg_of(const AttendParams& P, const RowPlan& s, int b, int x, int x1) {
   RowSeg g;
-  g.b = 0;
-  for (int i = 0; i < seqs; i += 32) {
-    const int r = i + (threadIdx.x & 31);
-    g.b += __popc(__ballot_sync(0xffffffffu, r < seqs && s.first[r + 1] <= x));
-  }
+  g.b = b;
   const int n = s.n[g.b], rows = row_rows<SRC>(P, s, g.b), blocks = (rows + P.item_rows - 1) / P.item_rows;
   const int i = (x - s.first[g.b]) / n;
   g.h = i / blocks;
@@ -330,6 +325,25 @@ __device__ __forceinline__ RowSeg row_seg(const AttendParams& P, const RowPlan& 
   g.tile0 = x - g.first;
   g.n = min(g.end, x1) - x;
   return g;
+}
+// (all lanes of a warp alike)
+template <int SRC>
+__device__ __forceinline__ RowSeg row_seg(const AttendParams& P, const RowPlan& s, int x, int x1) {
+  const int seqs = SRC == kShared ? P.n_prefix : P.pages.n_req;
+  int b = 0;  // as many sequences lie before x's as end at x or before
+  for (int i = 0; i < seqs; i += 32) {
+    const int r = i + (threadIdx.x & 31);
+    b += __popc(__ballot_sync(0xffffffffu, r < seqs && s.first[r + 1] <= x));
+  }
+  return row_seg_of<SRC>(P, s, b, x, x1);
+}
+// (each thread its own)
+template <int SRC>
+__device__ __forceinline__ RowSeg row_seg_at(const AttendParams& P, const RowPlan& s, int x) {
+  int b = 0;
+  for (int step = kMaxReq / 2; step > 0; step >>= 1)
+    if (s.first[b + step] <= x) b += step;
+  return row_seg_of<SRC>(P, s, b, x, x + 1);
 }
 
 // The first tile at x or behind it that begins an item.
@@ -910,60 +924,78 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
 }
 
-// Merges the pieces of the items that more than one CTA worked on.  CTA (x, y): the item found at the first boundary between CTAs that it
-// crosses, and 32 of its rows, one a lane; of the dimensions, blocks y, y + gridDim.y, .. of 32.
+// Merges the pieces of the items that more than one CTA worked on, each of which crosses a boundary between CTAs first.  A job: such an
+// item, 32 of its rows and 32 dimensions; a CTA takes every nth.  A thread: a row (its lane) and four dimensions (its warp);
+// four pieces are fetched at a time with their states, and merged as they come.
 template <typename T, int SRC, int D>
-__global__ void __launch_bounds__(kWarps * 32) join_rows(const __grid_constant__ AttendParams P) {
+__global__ void __launch_bounds__(kWarps * 32, 4) join_rows(const __grid_constant__ AttendParams P) {
+  constexpr int AT_ONCE = 4, PARTS = D / 32;
+  static_assert(kMaxCtas <= kWarps * 32, "a boundary for each thread");
+  struct Item {
+    int16_t b, pieces;
+    int32_t h, rt, rows, c0;  // c0: the first CTA
+  };
   __shared__ RowPlan plan;
-  __shared__ float s_f[kMaxCtas][32];  // a piece's factor for each row
-  __shared__ float s_x[kWarps][32];
+  __shared__ Item items[kMaxCtas];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int T_all = build_row_plan<SRC>(P, plan, false);
   const RowSplit split(P, T_all);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = P.item_rows / 32, c0 = blockIdx.x / groups, r = (blockIdx.x - c0 * groups) * 32 + lane;
-  grid_dependency_wait();
   allow_dependents();
-  if (c0 + 1 >= static_cast<int>(split.used)) return;
-  const int x = split.begin(c0 + 1);
-  const RowSeg g = row_seg<SRC>(P, plan, x, x + 1);
-  if (g.first >= x || g.first < split.begin(c0) || r - lane >= g.rows) return;
-  const int pieces = split.of(g.end - 1) - c0 + 1;
-  auto slot = [&](int c) { return static_cast<int64_t>(c0) * 2 + (c == 0 ? 1 : 2 * c); };
-  const bool in = r < g.rows;
-  float M = kNegInf;
-  for (int c = warp; c < pieces && in; c += kWarps) M = fmaxf(M, __ldcg(P.rows_ml + slot(c) * P.item_rows + r).x);
-  s_x[warp][lane] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_x[w][lane]);
-  const float less = M == kNegInf ? 0.f : -M;
-  float L = 0.f;
-  for (int c = warp; c < pieces && in; c += kWarps) {
-    const float2 ml = __ldcg(P.rows_ml + slot(c) * P.item_rows + r);
-    const float f = ex2(ml.x + less);
-    s_f[c][lane] = f;
-    L = fmaf(ml.y, f, L);
+  int n_items;
+  {
+    const int c0 = threadIdx.x, x = c0 + 1 < static_cast<int>(split.used) ? split.begin(c0 + 1) : -1;
+    RowSeg g{};
+    if (x >= 0) g = row_seg_at<SRC>(P, plan, x);
+    const bool is = x >= 0 && g.first < x && g.first >= split.begin(c0);
+    const int at = block_scan(is, plan.warp_sum, n_items) - 1;
+    if (is) items[at] = Item{static_cast<int16_t>(g.b), static_cast<int16_t>(split.of(g.end - 1) - c0 + 1), g.h, g.rt, g.rows, c0};
   }
   __syncthreads();
-  s_x[warp][lane] = L;
-  __syncthreads();
-  L = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) L += s_x[w][lane];
-  if (!in) return;
-  const RowOut at = row_out<SRC, D>(P, plan, g, r);
-  for (int d4 = blockIdx.y * kWarps + warp; d4 < D / 4; d4 += gridDim.y * kWarps) {
+  grid_dependency_wait();
+  const int per = P.item_rows / 32 * PARTS;
+  for (int j = blockIdx.x; j < n_items * per; j += gridDim.x) {
+    const Item& it = items[j / per];
+    const int k = j % per, r = k / PARTS * 32 + lane, d4 = k % PARTS * 8 + warp;
+    if (r >= it.rows) continue;  // (no lane is waited for below)
+    const int pieces = it.pieces;
+    // (slot 1 of the first CTA, slot 0 of the others)
+    const float2* const ml = P.rows_ml + static_cast<int64_t>(it.c0) * 2 * P.item_rows + r;
+    const float4* const po = P.rows_o + (static_cast<int64_t>(it.c0) * 2 * (D / 4) + d4) * P.item_rows + r;
+    float M = kNegInf, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int c = 0; c < pieces; ++c) {
-      const float4 v = __ldcg(P.rows_o + (slot(c) * (D / 4) + d4) * P.item_rows + r);
-      const float f = s_f[c][lane];
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
+#pragma unroll 1
+    for (int c = 0; c < pieces; c += AT_ONCE) {
+      float2 s[AT_ONCE];
+      float4 v[AT_ONCE];
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) {
+        const int slot = c + u == 0 ? 1 : 2 * (c + u);
+        const bool is = c + u < pieces;
+        s[u] = is ? __ldcg(ml + slot * P.item_rows) : make_float2(kNegInf, 0.f);
+        v[u] = is ? __ldcg(po + static_cast<int64_t>(slot) * (D / 4) * P.item_rows) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) top = fmaxf(top, s[u].x);
+      const float less = top == kNegInf ? 0.f : -top, back = ex2(M + less);
+      M = top;
+      L *= back;
+      o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) {
+        const float f = ex2(s[u].x + less);
+        L = fmaf(s[u].y, f, L);
+        o.x = fmaf(v[u].x, f, o.x);
+        o.y = fmaf(v[u].y, f, o.y);
+        o.z = fmaf(v[u].z, f, o.z);
+        o.w = fmaf(v[u].w, f, o.w);
+      }
     }
-    write_row<T>(P, at, d4 * 4, M, L, o);
+    RowSeg g{};
+    g.b = it.b;
+    g.h = it.h;
+    g.rt = it.rt;
+    write_row<T>(P, row_out<SRC, D>(P, plan, g, r), d4 * 4, M, L, o);
   }
 }
 
