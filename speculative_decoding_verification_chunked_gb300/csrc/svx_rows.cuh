@@ -449,14 +449,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float max128(const float (&v)[kTile]) {
+template <int N>
+__device__ __forceinline__ float max_of(const float (&v)[N]) {
   float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-  for (int k = 4; k < 124; k += 8)
+  for (int k = 4; k < N - 4; k += 8)
 #pragma unroll
     for (int e = 0; e < 4; ++e) m[e] = max3(m[e], v[k + 2 * e], v[k + 2 * e + 1]);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], v[124 + e]);
+  for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], v[N - 4 + e]);
   return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 template <int SRC>
@@ -789,35 +790,64 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         if (busy) {
           tc_after();
           if (!all) hide_keys(at_s, seen);
-          float v[kTile];
-          tmem_read128(at_s, v);
-          const float top = max128(v) * P.scale;
-          if (__any_sync(0xffffffffu, top > m + (kTau + Mma<T>::kLift))) {
-            const float now = fmaxf(m, top - Mma<T>::kLift);
-            const float f = now == kNegInf ? 1.f : ex2(m - now);
-            m = now;
-            l *= f;
-            if (i > 0) scale_columns(tmem + lanes + C::O_COL + s * D, D, f);  // S(i) was issued behind P V(i - 1): O holds all up to it
-          }
-          const float less = m == kNegInf ? 0.f : -m;
-          const uint64_t scale2 = pair(P.scale, P.scale), less2 = pair(less, less);
-          uint64_t sum[2] = {0, 0};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float a, b;
-              unpair(fma2(pair(v[c * 32 + 2 * k], v[c * 32 + 2 * k + 1]), scale2, less2), a, b);
-              a = ex2(a);
-              b = ex2(b);
-              sum[k & 1] = add2(sum[k & 1], pair(a, b));
-              if constexpr (QT == 1) Mma<T>::split(a, b, hi[k], lo[k]);
-              else hi[k] = Mma<T>::down2(a, b);
+          const uint64_t scale2 = pair(P.scale, P.scale);
+          uint64_t sum[2] = {0, 0}, less2;
+          auto move_reference = [&](float top) {  // where the row's largest score has passed it
+            if (__any_sync(0xffffffffu, top > m + (kTau + Mma<T>::kLift))) {
+              const float now = fmaxf(m, top - Mma<T>::kLift);
+              const float f = now == kNegInf ? 1.f : ex2(m - now);
+              m = now;
+              l *= f;
+              if (i > 0) scale_columns(tmem + lanes + C::O_COL + s * D, D, f);  // S(i) was issued behind P V(i - 1): O holds all up to it
             }
-            // P of 32 keys, and what its rounding left, over the 32 columns of their S
-            tmem_write16(at_s + c * 32, hi);
-            if constexpr (QT == 1) tmem_write16(at_s + c * 32 + 16, lo);
+            const float less = m == kNegInf ? 0.f : -m;
+            less2 = pair(less, less);
+          };
+          auto weights = [&](float& x, float& y, int k) {
+            unpair(fma2(pair(x, y), scale2, less2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum[k & 1] = add2(sum[k & 1], pair(x, y));
+          };
+          if constexpr (QT == 1) {
+            // 32 columns at a time, and S read twice: four times as long as the bytes allow would do, and the instructions, which
+            // what came before has often put out of the caches, take 2 us to come in, not 7
+            float top = kNegInf;
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+              float v[32];
+              tmem_read32<0>(at_s + c, v);
+              top = fmaxf(top, max_of(v));
+            }
+            move_reference(top * P.scale);
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+              float v[32];
+              tmem_read32<0>(at_s + c, v);
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                weights(v[2 * k], v[2 * k + 1], k);
+                Mma<T>::split(v[2 * k], v[2 * k + 1], hi[k], lo[k]);
+              }
+              // P of 32 keys, and what its rounding left, over the 32 columns of their S
+              tmem_write16(at_s + c, hi);
+              tmem_write16(at_s + c + 16, lo);
+            }
+          } else {
+            float v[kTile];
+            tmem_read128(at_s, v);
+            move_reference(max_of(v) * P.scale);
+#pragma unroll
+            for (int c = 0; c < kTile; c += 32) {
+              uint32_t hi[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                weights(v[c + 2 * k], v[c + 2 * k + 1], k);
+                hi[k] = Mma<T>::down2(v[c + 2 * k], v[c + 2 * k + 1]);
+              }
+              tmem_write16(at_s + c, hi);
+            }
           }
           float a, b;
           unpair(add2(sum[0], sum[1]), a, b);

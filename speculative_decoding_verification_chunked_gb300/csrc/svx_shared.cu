@@ -14,7 +14,7 @@ constexpr int kBatch = 64;  // pieces of a row whose factors are worked out at a
 // A CTA takes every gridDim.x-th of the requests' KV heads, block of 16 query heads y, and of the dimensions part z of gridDim.z.
 // APART: the prefixes were rows_kernel's work.
 template <typename T, int D, bool APART>
-__global__ void __launch_bounds__(kWarps * 32) join_shared(const __grid_constant__ AttendParams P) {
+__global__ void __launch_bounds__(kWarps * 32, 4) join_shared(const __grid_constant__ AttendParams P) {
   constexpr int CT = kChunkBytes / (2 * D);
   // Where the pieces of a row's lot lie: one is a finished state; else piece c is in slot 0 of CTA first + c, or (c = 0) slot 1.
   struct Lot {
