@@ -281,16 +281,21 @@ __device__ __forceinline__ int build_row_plan(const AttendParams& P, RowPlan& s,
   return total;
 }
 
-// The T tiles over the CTAs, as Split, but a CTA takes at least P.min_tiles.
+// The T tiles over the CTAs, as Split, but a single tile is enough for a CTA (5 tiles of an item: 9.4 us; two or four tiles to a CTA 9.9
+// and 11.5).
 struct RowSplit {
   uint32_t used, q, r, total;
+  float per_used;
   __device__ __forceinline__ RowSplit(const AttendParams& P, int T) {
     total = T;
-    used = min((total + P.min_tiles - 1) / P.min_tiles, static_cast<uint32_t>(P.row_ctas));
+    used = min(total, static_cast<uint32_t>(P.row_ctas));
     q = used ? total / used : 0;
     r = total - q * used;
+    per_used = __frcp_rn(static_cast<float>(used));
   }
-  __device__ __forceinline__ int begin(uint32_t c) const { return used ? static_cast<int>(c * q + c * r / used) : 0; }
+  __device__ __forceinline__ int begin(uint32_t c) const {  // (the float product: see Split)
+    return used ? static_cast<int>(c * q) + __float2int_rd(fmaf(static_cast<float>(c * r), per_used, 0.001f)) : 0;
+  }
   __device__ __forceinline__ int of(int x) const {
     int c = min(static_cast<int>(static_cast<float>(x) * (static_cast<float>(used) / static_cast<float>(total))),
                 static_cast<int>(used) - 1);
@@ -1031,10 +1036,13 @@ __global__ void __launch_bounds__(kWarps * 32, 4) join_rows(const __grid_constan
 
 // ------------------------------------------------------------------ host
 
-constexpr int kJoinTiles = 8;  // what the join of split items costs, in tiles of a CTA
+// What splitting items over CTAs costs, their pieces written, read and joined, in tiles of a CTA: more where its pieces are 256 KiB
+// each.  (128 items of 16 tiles, two row tiles, d = 128: whole 31 us, split 46; 256 of 32: 95 and 103; d = 64, 256 of 12: 40 and 47;
+// 64 of 12: 21.8 and 21.4; 32 of 64 tiles: 89 and 39.)
+constexpr int kJoinTiles = 8, kJoinTilesLarge = 14;
 
 struct RowSizes {
-  int32_t item_rows, ctas, min_tiles;
+  int32_t item_rows, ctas;
   bool whole;  // no item is split over CTAs
   size_t rows_o, rows_ml, total;
 };
@@ -1048,11 +1056,9 @@ inline int item_rows_for(int64_t rows) { return rows > kRowTile ? 2 * kRowTile :
 inline void size_rows(RowSizes* z, int64_t items, int64_t per, int item_rows, int head_dim, int most, size_t at, bool may_whole) {
   const int64_t tiles = items * per;
   z->item_rows = item_rows;
-  z->min_tiles = 2;
   most = std::min(most, kMaxCtas);
-  z->whole = may_whole && (items + most - 1) / most * per <= tiles / most + kJoinTiles;
-  if (z->whole) z->min_tiles = 1;
-  z->ctas = static_cast<int32_t>(std::min<int64_t>(most, std::max<int64_t>((tiles + z->min_tiles - 1) / z->min_tiles, 1)));
+  z->whole = may_whole && (items + most - 1) / most * per <= tiles / most + (item_rows * head_dim > 2 * kRowTile * 64 ? kJoinTilesLarge : kJoinTiles);
+  z->ctas = static_cast<int32_t>(std::min<int64_t>(most, std::max<int64_t>(tiles, 1)));
   z->rows_o = up256(at);
   z->rows_ml = z->rows_o + static_cast<size_t>(z->ctas) * 2 * z->item_rows * head_dim * 4;
   z->total = z->rows_ml + up256(static_cast<size_t>(z->ctas) * 2 * z->item_rows * 8);
@@ -1062,7 +1068,6 @@ inline void place_rows(AttendParams& p, const RowSizes& z, char* ws) {
   p.rows_ml = reinterpret_cast<float2*>(ws + z.rows_ml);
   p.item_rows = z.item_rows;
   p.row_ctas = z.ctas;
-  p.min_tiles = z.min_tiles;
   p.row_whole = z.whole;
   p.group_inverse = 1.f / static_cast<float>(p.group);
 }

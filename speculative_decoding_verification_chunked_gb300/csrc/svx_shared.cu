@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) join_shared(const __grid_const
   __shared__ Plan<kShared> plan;
   __shared__ float s_f[kBatch * kRowsMax];
   __shared__ float2 s_ml[kRowsMax];
-  __shared__ Lot s_lot[2][kRowsMax];
+  __shared__ Lot s_lots[kWarps][2][kRowsMax];  // of the next heads, a warp's work each
   __shared__ float4 s_o[kWarps * 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // (the lengths were there before the attention kernel began, which had waited for whoever wrote them)
@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) join_shared(const __grid_const
   // the outputs over the threads: several share one where there are more of them than outputs
   const int quads = D / 4 / gridDim.z, outs = rows * quads, share = max(kWarps * 32 / outs, 1);
   const int part = share > 1 ? tid / outs : 0;
+  const Lot(*s_lot)[kRowsMax] = s_lots[0];
   auto ml_at = [&](int r, int c) {
     const int lot = c < s_lot[0][r].pieces ? 0 : 1;
     if (lot) c -= s_lot[0][r].pieces;
@@ -58,19 +59,20 @@ __global__ void __launch_bounds__(kWarps * 32, 4) join_shared(const __grid_const
     o.z = fmaf(x.z, f, o.z);
     o.w = fmaf(x.w, f, o.w);
   };
+  const int heads = P.pages.n_req * P.pages.n_kv_heads;
   bool waited = false;
-  for (int bh = blockIdx.x; bh < P.pages.n_req * P.pages.n_kv_heads; bh += gridDim.x) {
-    const int b = bh / P.pages.n_kv_heads, h = bh - b * P.pages.n_kv_heads;
-    int prefix = 0;  // the first that ends behind the request
-    for (int i = 0; i < P.n_prefix; i += 32)
-      prefix += __popc(__ballot_sync(0xffffffffu, i + lane < P.n_prefix && plan.req0[i + lane + 1] <= b));
-    if (waited) __syncthreads();  // (the last one's are done with)
-    if (tid < 2 * kRowsMax) {
-      const int r = tid % kRowsMax, lot = tid / kRowsMax;  // 0: the prefix, 1: the request's own
+  for (int bh0 = blockIdx.x; bh0 < heads; bh0 += kWarps * gridDim.x) {
+    if (waited) __syncthreads();  // (the last ones are done with)
+    {
+      const int bh = bh0 + warp * gridDim.x, b = bh / P.pages.n_kv_heads, h = bh - b * P.pages.n_kv_heads;
+      const int r = lane % kRowsMax, lot = lane / kRowsMax;  // 0: the prefix, 1: the request's own
+      int prefix = 0;  // the first that ends behind the request
+      for (int i = 0; i < P.n_prefix; i += 32)
+        prefix += __popc(__ballot_sync(0xffffffffu, i + lane < P.n_prefix && plan.req0[i + lane + 1] <= b));
       Lot x{0, 0, 0};
       int seq = kMaxReq + b, block = blk, blocks = P.blocks;
       x.row = r;
-      bool any = r < rows;
+      bool any = r < rows && bh < heads;
       if (lot == 0) {
         any = any && prefix < P.n_prefix && plan.req0[prefix] <= b;
         if (any) {
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) join_shared(const __grid_const
         x.pieces = (far ? row_split.of(first + n - 1) : split.of(first + n - 1)) - x.first + 1;
         if (x.pieces == 1) x.row = (lot * P.pages.n_req + b) * P.n_q + h * P.group + blk * kRowsMax + r;
       }
-      s_lot[lot][r] = x;
+      s_lots[warp][lot][r] = x;
     }
     __syncthreads();
     if (!waited) {
@@ -98,69 +100,74 @@ __global__ void __launch_bounds__(kWarps * 32, 4) join_shared(const __grid_const
       allow_dependents();
       waited = true;
     }
-    int most = 0;  // pieces of any row
-    for (int r = 0; r < rows; ++r) most = max(most, s_lot[0][r].pieces + s_lot[1][r].pieces);
-    for (int i0 = 0; i0 < outs; i0 += kWarps * 32) {  // (once, unless there are more outputs than threads)
-      const int i = share > 1 ? tid - part * outs : i0 + tid;
-      // (rows_kernel's pieces have a row's neighbours beside it, the others its dimensions)
-      const int r = APART ? i % rows : i / quads, d4 = ((APART ? i / rows : i - r * quads) + blockIdx.z * quads) * 4;
-      const bool mine = i < outs && part < share;
-      const int pieces = mine ? s_lot[0][r].pieces + s_lot[1][r].pieces : 0;
-      // this thread's first pieces are fetched along with the states
-      constexpr int kAhead = 4;
-      float4 ahead[kAhead];
+    for (int nth = 0; nth < kWarps && bh0 + nth * gridDim.x < heads; ++nth) {
+      const int bh = bh0 + nth * gridDim.x, b = bh / P.pages.n_kv_heads, h = bh - b * P.pages.n_kv_heads;
+      s_lot = s_lots[nth];
+      if (nth > 0) __syncthreads();  // (the last one's states and factors are done with)
+      int most = 0;  // pieces of any row
+      for (int r = 0; r < rows; ++r) most = max(most, s_lot[0][r].pieces + s_lot[1][r].pieces);
+      for (int i0 = 0; i0 < outs; i0 += kWarps * 32) {  // (once, unless there are more outputs than threads)
+        const int i = share > 1 ? tid - part * outs : i0 + tid;
+        // (rows_kernel's pieces have a row's neighbours beside it, the others its dimensions)
+        const int r = APART ? i % rows : i / quads, d4 = ((APART ? i / rows : i - r * quads) + blockIdx.z * quads) * 4;
+        const bool mine = i < outs && part < share;
+        const int pieces = mine ? s_lot[0][r].pieces + s_lot[1][r].pieces : 0;
+        // this thread's first pieces are fetched along with the states
+        constexpr int kAhead = 4;
+        float4 ahead[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (part + u * share < pieces) ahead[u] = o_at(r, part + u * share, d4);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c0 = 0; c0 < max(most, 1); c0 += kBatch) {
-        if (c0 > 0 || i0 > 0) __syncthreads();  // (the last batch's factors have been used)
-        if (i0 == 0 || most > kBatch)
-          for (int q = warp; q < rows; q += kWarps) {
-            const int all = s_lot[0][q].pieces + s_lot[1][q].pieces, end = min(all, c0 + kBatch);
-            float2 ml = c0 + lane < end ? ml_at(q, c0 + lane) : make_float2(kNegInf, 0.f);
-            float M = ml.x, L = 0.f;
-            if (c0 == 0 && i0 == 0) {
-              for (int c = lane + 32; c < all; c += 32) M = fmaxf(M, ml_at(q, c).x);
+        for (int u = 0; u < kAhead; ++u)
+          if (part + u * share < pieces) ahead[u] = o_at(r, part + u * share, d4);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < max(most, 1); c0 += kBatch) {
+          if (c0 > 0 || i0 > 0) __syncthreads();  // (the last batch's factors have been used)
+          if (i0 == 0 || most > kBatch)
+            for (int q = warp; q < rows; q += kWarps) {
+              const int all = s_lot[0][q].pieces + s_lot[1][q].pieces, end = min(all, c0 + kBatch);
+              float2 ml = c0 + lane < end ? ml_at(q, c0 + lane) : make_float2(kNegInf, 0.f);
+              float M = ml.x, L = 0.f;
+              if (c0 == 0 && i0 == 0) {
+                for (int c = lane + 32; c < all; c += 32) M = fmaxf(M, ml_at(q, c).x);
 #pragma unroll
-              for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
-            } else {
-              M = s_ml[q].x;
-              L = s_ml[q].y;
+                for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+              } else {
+                M = s_ml[q].x;
+                L = s_ml[q].y;
+              }
+              const float less = M == kNegInf ? 0.f : -M;
+              float sum = 0.f;
+              for (int c = c0 + lane; c < end; c += 32) {
+                if (c != c0 + lane) ml = ml_at(q, c);
+                const float f = ex2(ml.x + less);
+                s_f[(c - c0) * kRowsMax + q] = f;
+                sum = fmaf(ml.y, f, sum);
+              }
+#pragma unroll
+              for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+              if (lane == 0 && i0 == 0) s_ml[q] = make_float2(M, L + sum);
             }
-            const float less = M == kNegInf ? 0.f : -M;
-            float sum = 0.f;
-            for (int c = c0 + lane; c < end; c += 32) {
-              if (c != c0 + lane) ml = ml_at(q, c);
-              const float f = ex2(ml.x + less);
-              s_f[(c - c0) * kRowsMax + q] = f;
-              sum = fmaf(ml.y, f, sum);
-            }
+          __syncthreads();
+          const int end = min(pieces, c0 + kBatch);
+          int c = c0 + part;
+          if (c0 == 0) {
 #pragma unroll
-            for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-            if (lane == 0 && i0 == 0) s_ml[q] = make_float2(M, L + sum);
+            for (int u = 0; u < kAhead; ++u, c += share)
+              if (c < end) add(o, ahead[u], s_f[c * kRowsMax + r]);
           }
-        __syncthreads();
-        const int end = min(pieces, c0 + kBatch);
-        int c = c0 + part;
-        if (c0 == 0) {
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u, c += share)
-            if (c < end) add(o, ahead[u], s_f[c * kRowsMax + r]);
-        }
 #pragma unroll 4
-        for (; c < end; c += share) add(o, o_at(r, c, d4), s_f[(c - c0) * kRowsMax + r]);
+          for (; c < end; c += share) add(o, o_at(r, c, d4), s_f[(c - c0) * kRowsMax + r]);
+        }
+        if (share > 1) {
+          s_o[tid] = o;
+          __syncthreads();
+          if (part == 0)
+            for (int p = 1; p < share; ++p) {
+              const float4 x = s_o[p * outs + i];
+              o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+            }
+        }
+        if (mine && part == 0) write_row<T>(P, place<kShared, D>(P, plan, kMaxReq + b, h, blk, r), d4, s_ml[r].x, s_ml[r].y, o);
       }
-      if (share > 1) {
-        s_o[tid] = o;
-        __syncthreads();
-        if (part == 0)
-          for (int p = 1; p < share; ++p) {
-            const float4 x = s_o[p * outs + i];
-            o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
-          }
-      }
-      if (mine && part == 0) write_row<T>(P, place<kShared, D>(P, plan, kMaxReq + b, h, blk, r), d4, s_ml[r].x, s_ml[r].y, o);
     }
   }
 }
@@ -196,19 +203,21 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
   const int64_t all_rows = static_cast<int64_t>(n_req) * group, used = std::min(f->n_prefix, n_req);
   const int64_t own = static_cast<int64_t>(n_req) * c->n_kv_heads * z.blocks * ((max_len + ct - 1) / ct);
   const int64_t far = c->n_kv_heads * (all_rows / kRowsMax + used) * ((max_prefix + ct - 1) / ct);
+  // By the rows to a prefix, on average (32 heads, 8 KV heads, one prefix of 16384 slots: 16 rows 24.3 us by attend_kernel alone, 24.9 with
+  // rows_kernel; 32 rows 34 and 26; 64 rows and 32768 slots 87 and 48; eight prefixes of 4096 slots with 8 rows each 38 and 43).
   out->many = all_rows > static_cast<int64_t>(kRowsMax) * f->n_prefix;
   const int64_t chunks = own + (out->many ? 0 : far);
   if (own + far > 0x7fffffff) return paged_fail(SVX_ERR_UNSUPPORTED, "heads times lengths are too large (%lld chunks of %d slots, at most 2^31 - 1)",
                       static_cast<long long>(own + far), ct);
   // With many rows the SMs are shared out over the two kernels by their work, so that they end together: a CTA of attend_kernel brings in
-  // some 45 GB/s of short sequences; a tile of rows_kernel takes 1.4 us (0.8 for d = 64, where two row tiles' exponentials bound it, and with one row tile
-  // the copy rate).  (By the bounds known here: lengths may be shorter.)
+  // some 45 GB/s of short sequences; a tile of rows_kernel takes 1.4 us with two row tiles, 1.0 with one.  (By the bounds known here: lengths
+  // may be shorter.)
   int own_ctas = sms;
   if (out->many) {
     const int item_rows = item_rows_for(all_rows);
     const int64_t items = c->n_kv_heads * (all_rows / item_rows + used), per = (max_prefix + kTile - 1) / kTile;
     const double own_us = static_cast<double>(n_req) * c->n_kv_heads * max_len * c->head_dim * 4 / 45e3;
-    const double far_us = static_cast<double>(items) * per * (c->head_dim == 128 ? 1.4 : 0.8);
+    const double far_us = static_cast<double>(items) * per * (item_rows > kRowTile ? 1.4 : 1.0);
     own_ctas = std::min(std::max(static_cast<int>(sms * own_us / (own_us + far_us) + 0.5), 4), sms - 4);
     size_rows(&out->rz, items, per, item_rows, c->head_dim, sms - own_ctas, 0, false);
   }
