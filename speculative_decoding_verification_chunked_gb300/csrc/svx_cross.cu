@@ -45,7 +45,7 @@ bool rows_apart(int64_t (&n)[3], int64_t (&s)[3], int64_t d) {
   return true;
 }
 
-// Everything but the pointers.
+// Everything but the pointers, and but for the sizes that hang on the SMs.
 svx_status cross_view(const svx_cross* c, CrossView* out) {
   if (!c) return paged_fail(SVX_ERR_INVALID_ARG, "the arguments are NULL");
   const svx_cross& a = *c;
@@ -72,21 +72,11 @@ svx_status cross_view(const svx_cross* c, CrossView* out) {
   if (blocks > kMaxBlocks || chunks > 0x7fffffff)
     return paged_fail(SVX_ERR_UNSUPPORTED, "n_req * heads * n_tok * n_states is too large (%lld chunks, at most 2^31 - 1)",
                       static_cast<long long>(chunks));
-  const int sms = sm_count(a.device);
-  if (sms <= 0) return paged_fail(SVX_ERR_CUDA, "cannot read the SM count");
-  Sizes& z = out->z;
-  z.max_len = static_cast<int32_t>(S);
-  z.blocks = static_cast<int32_t>(blocks);
-  z.whole = per_item <= kWholeItem && chunks <= sms * per_item;  // as in one-token attention over pages
-  size_pieces(&z, chunks, a.head_dim, sms);
   // (8 requests of 32 heads and 8 KV heads, 16384 states: 16 rows 93 us by attend_kernel, 94 by rows_kernel; 20 rows 172 and 95; 1500
   // states 21 and 22, 26 and 22)
   out->many = rows > kRowsMax;
-  if (out->many) {
-    const int item_rows = item_rows_for(rows);
-    size_rows(&out->rz, B * Hkv * ((rows + item_rows - 1) / item_rows), (S + kTile - 1) / kTile, item_rows, a.head_dim, sms, 0, true);
-  }
-  out->total = out->many ? out->rz.total : z.total;
+  out->z.max_len = static_cast<int32_t>(S);
+  out->z.blocks = static_cast<int32_t>(blocks);
   AttendParams& p = out->p;
   p.pages.page_stride = B > 1 ? a.kv_req : 0;
   p.pages.tok_stride = S > 1 ? a.kv_state : 0;
@@ -112,6 +102,25 @@ svx_status cross_view(const svx_cross* c, CrossView* out) {
   return SVX_OK;
 }
 
+svx_status cross_sizes(const svx_cross& a, CrossView* v) {
+  const int sms = sm_count(a.device);
+  if (sms <= 0) return paged_fail(SVX_ERR_CUDA, "cannot read the SM count");
+  const int64_t items = static_cast<int64_t>(a.n_req) * a.n_kv_heads;
+  if (v->many) {
+    const int item_rows = item_rows_for(v->p.rows);
+    size_rows(&v->rz, items * ((v->p.rows + item_rows - 1) / item_rows), (static_cast<int64_t>(a.n_states) + kTile - 1) / kTile, item_rows,
+              a.head_dim, sms, 0, true);
+    v->total = v->rz.total;
+    return SVX_OK;
+  }
+  const int ct = kChunkBytes / (2 * a.head_dim);
+  const int64_t per_item = (static_cast<int64_t>(a.n_states) + ct - 1) / ct, chunks = items * v->z.blocks * per_item;
+  v->z.whole = per_item <= kWholeItem && chunks <= sms * per_item;  // as in one-token attention over pages
+  size_pieces(&v->z, chunks, a.head_dim, sms);
+  v->total = v->z.total;
+  return SVX_OK;
+}
+
 template <typename T, int D>
 cudaError_t launch_cross(const AttendParams& p, bool many, int device, cudaStream_t s) {
   if (many) {
@@ -133,7 +142,8 @@ extern "C" svx_status svx_cross_attn_workspace(const svx_cross* c, int64_t* byte
   if (!bytes) return svx::paged_fail(SVX_ERR_INVALID_ARG, "bytes is NULL");
   *bytes = 0;
   svx::CrossView v = {};
-  const svx_status st = svx::cross_view(c, &v);
+  svx_status st = svx::cross_view(c, &v);
+  if (st == SVX_OK) st = svx::cross_sizes(*c, &v);
   if (st == SVX_OK) *bytes = static_cast<int64_t>(v.total);
   return st;
 }
@@ -141,7 +151,7 @@ extern "C" svx_status svx_cross_attn_workspace(const svx_cross* c, int64_t* byte
 extern "C" svx_status svx_cross_attn(const svx_cross* c, void* workspace, int64_t workspace_bytes, void* stream) {
   using svx::paged_fail;
   svx::CrossView v = {};
-  const svx_status st = svx::cross_view(c, &v);
+  svx_status st = svx::cross_view(c, &v);
   if (st != SVX_OK) return st;
   const svx_cross& a = *c;
   svx::AttendParams& p = v.p;
@@ -162,6 +172,8 @@ extern "C" svx_status svx_cross_attn(const svx_cross* c, void* workspace, int64_
                   k = {a.n_states ? a.k : nullptr, states}, v_span = {a.n_states ? a.v : nullptr, states};
   if (svx::any_overlap({o, lse, status}, {q, k, v_span, len, mask}))
     return paged_fail(SVX_ERR_INVALID_ARG, "an output overlaps an input or another output");
+  st = svx::cross_sizes(a, &v);
+  if (st != SVX_OK) return st;
   if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(v.total))
     return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", v.total);
   if (svx::any_overlap({{workspace, v.total}}, {q, k, v_span, len, mask, o, lse, status}))
@@ -182,7 +194,7 @@ extern "C" svx_status svx_cross_attn(const svx_cross* c, void* workspace, int64_
   p.mask = a.mask;
   p.o = a.o;
   p.lse = a.lse;
-  svx::place_pieces(p, v.z, static_cast<char*>(workspace));
+  svx::place_pieces(p, v.z, static_cast<char*>(workspace));  // (with many rows: the bounds alone)
   if (v.many) svx::place_rows(p, v.rz, static_cast<char*>(workspace));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;

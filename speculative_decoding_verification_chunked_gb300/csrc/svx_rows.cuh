@@ -1060,6 +1060,11 @@ inline void size_rows(RowSizes* z, int64_t items, int64_t per, int item_rows, in
   z->whole = may_whole && (items + most - 1) / most * per <= tiles / most + (item_rows * head_dim > 2 * kRowTile * 64 ? kJoinTilesLarge : kJoinTiles);
   z->ctas = static_cast<int32_t>(std::min<int64_t>(most, std::max<int64_t>(tiles, 1)));
   z->rows_o = up256(at);
+  if (z->whole) {  // no pieces
+    z->rows_ml = z->rows_o;
+    z->total = z->rows_o + 256;
+    return;
+  }
   z->rows_ml = z->rows_o + static_cast<size_t>(z->ctas) * 2 * z->item_rows * head_dim * 4;
   z->total = z->rows_ml + up256(static_cast<size_t>(z->ctas) * 2 * z->item_rows * 8);
 }

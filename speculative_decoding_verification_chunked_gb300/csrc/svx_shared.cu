@@ -179,7 +179,8 @@ struct SharedSizes {
   int32_t max_prefix;
 };
 
-svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const svx_prefixes* f, int64_t max_len, SharedSizes* out) {
+// What can be told without the device.
+svx_status shared_check(const svx_pages* c, int32_t n_q, const svx_prefixes* f, int64_t max_len) {
   if (n_q < c->n_kv_heads || n_q % c->n_kv_heads || n_q > 4096)
     return paged_fail(SVX_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads, at most 4096");
   if (!f) return paged_fail(SVX_ERR_INVALID_ARG, "prefixes is NULL");
@@ -190,8 +191,13 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
   if (max_len < 0 || max_len > cap) return paged_fail(SVX_ERR_INVALID_ARG, "max_len must be in [0, max_pages * page_size]");
   if (f->max_len < 0 || f->max_len > room)
     return paged_fail(SVX_ERR_INVALID_ARG, "the prefixes' max_len must be in [0, their max_pages * page_size]");
-  if (max_len == 0) max_len = cap;
-  const int64_t max_prefix = f->max_len ? f->max_len : room;
+  return SVX_OK;
+}
+
+// (after shared_check)
+svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const svx_prefixes* f, int64_t max_len, SharedSizes* out) {
+  if (max_len == 0) max_len = static_cast<int64_t>(c->page_size) * c->max_pages;
+  const int64_t max_prefix = f->max_len ? f->max_len : static_cast<int64_t>(c->page_size) * f->max_pages;
   const int sms = sm_count(c->device);
   if (sms <= 0) return paged_fail(SVX_ERR_CUDA, "cannot read the SM count");
   const int group = n_q / c->n_kv_heads, ct = kChunkBytes / (2 * c->head_dim);
@@ -206,9 +212,10 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
   // By the rows to a prefix, on average (32 heads, 8 KV heads, one prefix of 16384 slots: 16 rows 24.3 us by attend_kernel alone, 24.9 with
   // rows_kernel; 32 rows 34 and 26; 64 rows and 32768 slots 87 and 48; eight prefixes of 4096 slots with 8 rows each 38 and 43).
   out->many = all_rows > static_cast<int64_t>(kRowsMax) * f->n_prefix;
-  const int64_t chunks = own + (out->many ? 0 : far);
-  if (own + far > 0x7fffffff) return paged_fail(SVX_ERR_UNSUPPORTED, "heads times lengths are too large (%lld chunks of %d slots, at most 2^31 - 1)",
+  if (own + far > 0x7fffffff)
+    return paged_fail(SVX_ERR_UNSUPPORTED, "heads times lengths are too large (%lld chunks of %d slots, at most 2^31 - 1)",
                       static_cast<long long>(own + far), ct);
+  const int64_t chunks = own + (out->many ? 0 : far);
   // With many rows the SMs are shared out over the two kernels by their work, so that they end together: a CTA of attend_kernel brings in
   // some 45 GB/s of short sequences; a tile of rows_kernel takes 1.4 us with two row tiles, 1.0 with one.  (By the bounds known here: lengths
   // may be shorter.)
@@ -264,7 +271,8 @@ extern "C" svx_status svx_paged_decode_shared_workspace(const svx_pages* cache, 
   svx_status st = svx::paged_view(cache, n_req, &v);
   if (st != SVX_OK) return st;
   svx::SharedSizes z = {};
-  st = svx::shared_sizes(cache, n_req, n_q_heads, prefixes, max_len, &z);
+  st = svx::shared_check(cache, n_q_heads, prefixes, max_len);
+  if (st == SVX_OK) st = svx::shared_sizes(cache, n_req, n_q_heads, prefixes, max_len, &z);
   if (st == SVX_OK) *bytes = static_cast<int64_t>(z.z.total);
   return st;
 }
@@ -276,8 +284,7 @@ extern "C" svx_status svx_paged_decode_shared(const svx_pages* cache, int32_t n_
   svx::AttendParams p = {};
   svx_status st = svx::paged_view(cache, n_req, &p.pages);
   if (st != SVX_OK) return st;
-  svx::SharedSizes z = {};
-  st = svx::shared_sizes(cache, n_req, n_q_heads, prefixes, max_len, &z);
+  st = svx::shared_check(cache, n_q_heads, prefixes, max_len);
   if (st != SVX_OK) return st;
   const svx_prefixes& f = *prefixes;
   if (!q || !o || !lse || !len || !svx::is_aligned(q, 16) || !svx::is_aligned(o, 16))
@@ -295,6 +302,9 @@ extern "C" svx_status svx_paged_decode_shared(const svx_pages* cache, int32_t n_
                   v_span = {cache->v, pool}, status = {cache->status, 4};
   if (svx::any_overlap({o_span, lse_span, status}, {q_span, len_span, table_span, far_table, far_len, first_span, k_span, v_span}))
     return paged_fail(SVX_ERR_INVALID_ARG, "an output overlaps an input or another output");
+  svx::SharedSizes z = {};
+  st = svx::shared_sizes(cache, n_req, n_q_heads, prefixes, max_len, &z);
+  if (st != SVX_OK) return st;
   if (!workspace || !svx::is_aligned(workspace, 256) || workspace_bytes < static_cast<int64_t>(z.z.total))
     return paged_fail(SVX_ERR_INVALID_ARG, "workspace must be 256-byte aligned, of at least %zu bytes", z.z.total);
   if (svx::any_overlap({{workspace, z.z.total}},

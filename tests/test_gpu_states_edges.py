@@ -1,0 +1,324 @@
+"""Edges of attention to an encoder's states and behind shared prefixes on the GPU: layouts, alignment, far offsets, every kernel that the
+rules choose, the bounds-checked library's hook, and a decoder layer that uses them together with the residual stream.  Bounds:
+attention_reference.near, with the roundings of test_gpu_cross.py and test_gpu_shared.py; test_gpu_residual.py for the stream."""
+import ctypes
+import math
+import os
+
+import pytest
+import torch
+
+from attention_reference import attend64, near, slots_of
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+CHECKED = os.environ.get("SVX_LIBRARY") == "checked"
+
+
+@pytest.fixture(scope="module")
+def svx():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_verification_chunked_gb300 import svx as mod
+    return mod
+
+
+def p_error(rows, t):
+    return 2.0 ** -15 + (torch.finfo(t).eps / 2 if rows > 128 else 0.0)
+
+
+def check_cross(q, k, v, o, lse, seen=None, heads=None):
+    b, hq, n, d = q.shape
+    group = hq // k.shape[2]
+    for i in range(b):
+        at = torch.arange(k.shape[1], device="cuda") if seen is None else seen[i].nonzero()[:, 0]
+        for h in range(k.shape[2]) if heads is None else heads:
+            x = slice(h * group, (h + 1) * group)
+            want = attend64(q[i, x].reshape(-1, d), k[i, at, h], v[i, at, h], d ** -0.5)
+            near(o[i, x].reshape(-1, d), lse[i, x].reshape(-1), want, p_error(group * n, q.dtype), len(at))
+
+
+@pytest.mark.parametrize("ty", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n, hq, hkv", [(3, 4, 1), (5, 10, 1), (20, 4, 2), (32, 4, 1), (33, 4, 1), (100, 3, 1), (64, 8, 2), (300, 2, 2)])
+def test_rows_around_the_limits_of_the_kernels(svx, n, hq, hkv, d, ty):
+    """12 to 300 rows: one block of 16, one row tile, two, more than two; whole tokens to a row tile and not."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(TYPES[ty])  # noqa: E731
+    for states in (127, 128, 385, 2000):
+        q, k, v = 2 * r(2, hq, n, d), r(2, states, hkv, d), r(2, states, hkv, d)
+        o, lse = torch.full_like(q, 7.0), torch.full((2, hq, n), 7.0, device="cuda")
+        svx.cross_attn(q, k, v, o, lse)
+        check_cross(q, k, v, o, lse)
+
+
+@pytest.mark.parametrize("n", [2, 50, 150])
+def test_addresses_on_the_16_byte_grid_only(svx, n):
+    """Every tensor begins 16 bytes behind a 256-byte boundary, with strides that are odd multiples of 16 bytes."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+
+    def odd(*shape):
+        rows = math.prod(shape[:-1])
+        wide = torch.randn(rows * (shape[-1] + 8) + 8, generator=g, device="cuda").half()
+        return wide[8:].view(rows, shape[-1] + 8)[:, :shape[-1]].view(*shape[:-1], shape[-1])
+
+    q, k, v, o = odd(2, n, 4, 128).transpose(1, 2), odd(2, 700, 2, 128), odd(2, 700, 2, 128), odd(2, n, 4, 128).transpose(1, 2)
+    lse = torch.zeros((2, 4, n), device="cuda")
+    svx.cross_attn(q, k, v, o, lse)
+    check_cross(q, k, v, o, lse)
+
+
+@pytest.mark.parametrize("n", [1, 40, 200])
+def test_a_mask_off_the_word_grid(svx, n):
+    g = torch.Generator(device="cuda").manual_seed(8)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    q, k, v = r(3, 2, n, 64), r(3, 301, 1, 64), r(3, 301, 1, 64)
+    mask = (torch.rand(3 * 307 + 3, generator=g, device="cuda") < 0.5)[3:].view(3, 307)[:, :301]
+    k[~mask], v[~mask] = float("nan"), float("-inf")
+    o, lse = torch.zeros_like(q), torch.zeros((3, 2, n), device="cuda")
+    svx.cross_attn(q, k, v, o, lse, mask=mask)
+    check_cross(q, k, v, o, lse, mask)
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_states_past_two_to_the_31_elements(svx, n):
+    """4.6 GB of states: the last of them decide."""
+    states, hkv, d = 1_110_000, 8, 128
+    kv = torch.zeros((1, states, 2, hkv, d), dtype=torch.bfloat16, device="cuda")
+    assert kv.numel() > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(9)
+    kv[:, -300:] = torch.randn((1, 300, 2, hkv, d), generator=g, device="cuda").bfloat16() * 2
+    k, v = kv[:, :, 0], kv[:, :, 1]
+    q = 2 * torch.randn((1, hkv, n, d), generator=g, device="cuda").bfloat16()
+    o, lse = torch.zeros_like(q), torch.zeros((1, hkv, n), device="cuda")
+    svx.cross_attn(q, k, v, o, lse)
+    for h in (0, 7):
+        check_cross(q[:, h:h + 1], k[:, :, h:h + 1], v[:, :, h:h + 1], o[:, h:h + 1], lse[:, h:h + 1])
+
+
+def shared_inputs(groups, prefix, own, hq, hkv, d, page, t, pool, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    batch = sum(groups)
+    need = [-(-n // page) for n in list(prefix) + [own] * batch]
+    order = torch.randperm(sum(need) + 1, generator=g).to(torch.int32)
+    far, table = (torch.full((n, max(x)), -1, dtype=torch.int32) for n, x in ((len(prefix), need[:len(prefix)]), (batch, need[len(prefix):])))
+    at = 0
+    for i, n in enumerate(need):
+        (far[i] if i < len(prefix) else table[i - len(prefix)])[:n] = order[at:at + n]
+        at += n
+    if pool == "pair":  # K and V side by side
+        both = torch.randn((len(order), 2, page, hkv, d), generator=g).to(t).cuda()
+        k, v = both[:, 0], both[:, 1]
+    elif pool == "slots":  # slots outermost
+        k, v = (torch.randn((page, hkv, len(order), d), generator=g).to(t).cuda().permute(2, 0, 1, 3) for _ in range(2))
+    else:
+        k, v = (torch.randn((len(order), page, hkv, d), generator=g).to(t).cuda() for _ in range(2))
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = 2 * torch.randn((batch, hq, 1, d), generator=g).to(t).cuda()
+    return dict(q=q, k=k, v=v, far=far.cuda(), table=table.cuda(), prefix_lens=ints(list(prefix)), lens=ints([own] * batch),
+                first=ints([sum(groups[:i]) for i in range(len(groups) + 1)]), o=torch.zeros_like(q),
+                lse=torch.zeros((batch, hq, 1), device="cuda"))
+
+
+def run_shared(c, s, **kw):
+    c.decode_shared(s["q"], s["far"], s["prefix_lens"], s["first"], s["table"], s["lens"], s["o"], s["lse"], **kw)
+
+
+def check_shared(s, rows=None):
+    batch, hq, _, d = s["q"].shape
+    group = hq // s["k"].shape[2]
+    first = s["first"].tolist()
+    for b in range(batch):
+        mine = [slots_of(s[x], s["table"][b], int(s["lens"][b])) for x in "kv"]
+        for p, n in enumerate(s["prefix_lens"].tolist()):
+            if first[p] <= b < first[p + 1]:
+                mine = [torch.cat((slots_of(s[x], s["far"][p], n), y)) for x, y in zip("kv", mine)]
+        for h in range(s["k"].shape[2]):
+            x = slice(h * group, (h + 1) * group)
+            want = attend64(s["q"][b, x, 0], mine[0][:, h], mine[1][:, h], d ** -0.5)
+            near(s["o"][b, x, 0], s["lse"][b, x, 0], want, p_error(rows or batch * group, s["q"].dtype), len(mine[0]))
+
+
+@pytest.mark.parametrize("pool", ["token", "pair", "slots"])
+@pytest.mark.parametrize("page", [1, 8, 16, 48, 64, 128, 256, 100])
+def test_pages_and_pools_of_many_rows(svx, page, pool):
+    """Pages that make 16, 64 or 128 slots of a tile's box, or none; pools in other orders."""
+    for groups, hq, hkv, d, t in (((9, 4), 8, 2, 128, torch.float16), ((70,), 4, 1, 64, torch.bfloat16)):
+        s = shared_inputs(groups, (400, 131)[:len(groups)], 19, hq, hkv, d, page, t, pool, seed=page)
+        c = svx.PagedCache(s["k"], s["v"])
+        run_shared(c, s)
+        check_shared(s)
+        assert not c.check()
+
+
+def test_a_page_that_is_not_there_spoils_its_prefix_only(svx):
+    s = shared_inputs((20, 21), (640, 900), 33, 4, 1, 128, 16, torch.bfloat16, "token", seed=3)
+    c = svx.PagedCache(s["k"], s["v"])
+    run_shared(c, s)
+    check_shared(s)
+    assert not c.check()
+    s["far"][0, 7] = -1
+    s["far"][0, 9] = s["k"].shape[0]
+    run_shared(c, s)
+    assert c.check()
+    good = {**s, "q": s["q"][20:], "o": s["o"][20:], "lse": s["lse"][20:], "table": s["table"][20:], "lens": s["lens"][20:],
+            "far": s["far"][1:], "prefix_lens": s["prefix_lens"][1:], "first": torch.tensor([0, 21])}
+    check_shared(good, rows=41 * 4)  # (of the call)
+
+
+def test_values_that_are_not_finite_stay_with_their_rows(svx):
+    """A query that is not a number spoils its own rows alone, among 40 and among 200 others of the same product."""
+    for batch in (10, 50):
+        s = shared_inputs((batch,), (500,), 20, 4, 1, 64, 32, torch.bfloat16, "token", seed=4)
+        s["q"][3, 1] = float("nan")
+        c = svx.PagedCache(s["k"], s["v"])
+        run_shared(c, s)
+        assert s["o"][3, 1].isnan().all()
+        s["q"][3, 1], s["o"][3, 1] = 0, 0
+        clean = {**s, "o": torch.zeros_like(s["o"]), "lse": torch.zeros_like(s["lse"])}
+        run_shared(c, clean)
+        clean["o"][3, 1] = 0
+        assert torch.equal(clean["o"], s["o"])
+
+
+def test_the_checked_library_finds_rows_past_a_clipped_extent(svx):
+    """svx_debug_clip_paged: states and pages described as shorter than they are.  The checked library reports it and reads nothing there."""
+    def clip(n):
+        assert svx.lib.svx_debug_clip_paged(2, n) == svx.OK
+
+    for n in (2, 40):
+        q, k, v = (torch.randn(s, device="cuda").bfloat16() for s in ((1, 2, n, 64), (1, 300, 1, 64), (1, 300, 1, 64)))
+        o, status = torch.zeros_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+        try:
+            clip(64 * 299)
+            svx.cross_attn(q, k, v, o, status=status)
+        finally:
+            clip(-1)
+        assert (status.item() != 0) == CHECKED
+        status.zero_()
+        svx.cross_attn(q, k, v, o, status=status)
+        assert status.item() == 0
+    for batch in (3, 40):
+        s = shared_inputs((batch,), (200,), 10, 2, 1, 64, 16, torch.bfloat16, "token", seed=5)
+        c = svx.PagedCache(s["k"], s["v"])
+        try:
+            clip(64 * 16)
+            run_shared(c, s)
+        finally:
+            clip(-1)
+        assert c.check() == CHECKED
+        run_shared(c, s)
+        check_shared(s)
+        assert not c.check()
+
+
+def test_structs_with_pointers_of_no_device_memory(svx):
+    """The C calls check what the binding has not: host memory is refused."""
+    s = shared_inputs((3,), (40,), 5, 4, 2, 64, 16, torch.bfloat16, "token")
+    host = torch.zeros(4096, dtype=torch.float32)
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    p = svx.Pages(s["k"].data_ptr(), s["v"].data_ptr(), s["table"].data_ptr(), torch.zeros(1, dtype=torch.int32, device="cuda").data_ptr(),
+                  16 * 128, 128, 64, s["k"].shape[0], 16, s["table"].shape[1], 2, 64, 0, 0, 0, 0)
+    f = svx.Prefixes(s["far"].data_ptr(), s["prefix_lens"].data_ptr(), s["first"].data_ptr(), 0, 1, s["far"].shape[1])
+    args = lambda lse: (ctypes.byref(p), 3, 4, s["q"].data_ptr(), ctypes.byref(f), s["lens"].data_ptr(), 0, 0.0, s["o"].data_ptr(), lse,  # noqa: E731
+                        ws.data_ptr(), ws.numel(), None)
+    torch.cuda.synchronize()
+    assert svx.lib.svx_paged_decode_shared(*args(host.data_ptr())) == svx.ERR_INVALID_ARG
+    assert svx.lib.svx_paged_decode_shared(*args(s["lse"].data_ptr())) == svx.OK
+    torch.cuda.synchronize()
+    check_shared(s)
+
+
+# ------------------------------------------------------------------ a layer
+
+def test_a_decoder_layer_over_branches_of_one_prompt(svx):
+    """What the operators are for, together: 6 branches of one prompt, each with slots of its own, and one encoded input that all of them
+    attend to; three tokens each.  Every step is checked on the inputs that it really had, and the same steps captured and replayed
+    give the same."""
+    B, D, hq, hkv, d, page, states, prompt = 6, 512, 8, 2, 64, 16, 333, 150
+    t = torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(11)
+    r = lambda *s, scale=1.0: (scale * torch.randn(s, generator=g, device="cuda")).to(t)  # noqa: E731
+    w = {name: r(*shape, scale=shape[0] ** -0.5) for name, shape in dict(qkv=(D, (hq + 2 * hkv) * d), o=(hq * d, D), cq=(D, hq * d),
+                                                                         ckv=(D, 2 * hkv * d), co=(hq * d, D)).items()}
+    norm = [(1 + 0.1 * torch.randn(D, generator=g, device="cuda")).to(t) for _ in range(4)]
+    gate = torch.tensor([0.5], dtype=t, device="cuda")
+    kv = (r(1, states, D) @ w["ckv"]).view(1, states, 2, hkv, d)
+    live = torch.rand((1, states), generator=g, device="cuda") < 0.9
+    pages = 2 + -(-prompt // page) + 2 * B
+    kp, vp = (torch.zeros((pages, page, hkv, d), dtype=t, device="cuda") for _ in range(2))
+    c = svx.PagedCache(kp, vp)
+    rope = svx.Rope(d)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    far = torch.arange(-(-prompt // page), dtype=torch.int32, device="cuda")[None]
+    table = ints([[far.shape[1] + 2 * b, far.shape[1] + 2 * b + 1] for b in range(B)])
+    first, prefix_lens = ints([0, B]), ints([prompt])
+    # the prompt into the prefix's pages
+    x = r(1, prompt, D)
+    heads = (x @ w["qkv"]).view(1, prompt, hq + 2 * hkv, d)
+    c.append(heads[:, :, :hq], heads[:, :, hq:hq + hkv], heads[:, :, hq + hkv:], torch.arange(prompt, dtype=torch.int32, device="cuda")[None],
+             rope, far, ints([0]), torch.empty((1, hq, prompt, d), dtype=t, device="cuda"))
+
+    h = r(B, D)
+    lens, pos = ints([0] * B), ints([[prompt]] * B)
+    buf = {k: torch.empty((B, D), dtype=t, device="cuda") for k in ("x0", "x1", "x2", "h1", "h2", "out", "cout")}
+    q1, a1 = (torch.empty((B, hq, 1, d), dtype=t, device="cuda") for _ in range(2))
+    l1, a2, l2 = torch.empty((B, hq, 1), device="cuda"), torch.empty((1, B, hq, d), dtype=t, device="cuda"), torch.empty((1, hq, B), device="cuda")
+    proj, cq = torch.empty((B, 1, hq + 2 * hkv, d), dtype=t, device="cuda"), torch.empty((1, B, hq, d), dtype=t, device="cuda")
+
+    def step():
+        svx.residual_norm(h, None, None, buf["x0"], norm=norm[0])
+        torch.matmul(buf["x0"], w["qkv"], out=proj.view(B, -1))
+        c.append(proj[:, :, :hq], proj[:, :, hq:hq + hkv], proj[:, :, hq + hkv:], pos, rope, table, lens, q1)
+        lens.add_(1)
+        pos.add_(1)
+        c.decode_shared(q1, far, prefix_lens, first, table, lens, a1, l1)
+        torch.matmul(a1.view(B, -1), w["o"], out=buf["out"])
+        svx.residual_norm(h, buf["out"], buf["h1"], buf["x1"], norm=norm[1])
+        torch.matmul(buf["x1"], w["cq"], out=cq.view(B, -1))
+        # the branches' tokens as tokens of the one encoded input
+        svx.cross_attn(cq.transpose(1, 2), kv[:, :, 0], kv[:, :, 1], a2.transpose(1, 2), l2, mask=live)
+        torch.matmul(a2.view(B, -1), w["co"], out=buf["cout"])
+        svx.residual_norm(buf["h1"], buf["cout"], buf["h2"], buf["x2"], norm=norm[2], post_norm=norm[3], post_eps=1e-6, gate=gate,
+                          act="tanh")
+        h.copy_(buf["h2"])
+
+    start = h.clone()
+    seen = []
+    for n in range(1, 4):
+        before = h.clone()
+        step()
+        s = dict(q=q1, k=kp, v=vp, far=far, table=table, prefix_lens=prefix_lens, lens=lens, first=first, o=a1, lse=l1)
+        check_shared(s)
+        at = live[0].nonzero()[:, 0]
+        for i in range(hkv):
+            heads_ = slice(i * hq // hkv, (i + 1) * hq // hkv)
+            want = attend64(cq[0, :, heads_].transpose(0, 1).reshape(-1, d), kv[0, at, 0, i], kv[0, at, 1, i], d ** -0.5)
+            near(a2[0, :, heads_].transpose(0, 1).reshape(-1, d), l2[0, heads_].reshape(-1), want, p_error(B * hq // hkv, t), len(at))
+        u = torch.finfo(t).eps / 2
+        h1 = before.double() + buf["out"].double()
+        assert ((buf["h1"].double() - h1).abs() <= h1.abs() * u + (before.double().abs() + buf["out"].double().abs()) * 2.0 ** -22).all()
+        y = buf["cout"].double()
+        y = y / torch.sqrt((y * y).mean(-1, keepdim=True) + 1e-6) * norm[3].double() * math.tanh(0.5)
+        h2 = buf["h1"].double() + y
+        assert ((buf["h2"].double() - h2).abs() <= h2.abs() * u + buf["h1"].double().abs() * 2.0 ** -22 + y.abs() * 2.0 ** -16).all()
+        seen.append(h.clone())
+    assert not c.check()
+    # the same three tokens again, captured once
+    h.copy_(start)
+    lens.zero_()
+    pos.fill_(prompt)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    keep = kp.clone()
+    with torch.cuda.graph(graph):
+        step()
+    h.copy_(start)
+    lens.zero_()
+    pos.fill_(prompt)
+    kp.copy_(keep)
+    for want in seen:
+        graph.replay()
+        assert torch.equal(h, want)
+    assert not c.check()
