@@ -637,8 +637,9 @@ svx_status svx_paged_decode_shared_workspace(const svx_pages* cache, int32_t n_r
 
 /* svx_paged_decode for requests that share prefixes: request b attends to the slots of its prefix and then to its own slots
  * [0, len[b]) of cache->table (either may be none; with neither O = 0, LSE = -inf).  A prefix's K and V are read once for all its
- * requests, not once for each.  q, len, max_len, scale, o, lse and what K, V hold: as svx_paged_decode.  first, like lengths and
- * page ids, is checked on the device.  Outputs and workspace must not overlap inputs, the pools or one another. */
+ * requests, not once for each.  q, len, max_len, scale, o, lse and what K, V hold: as svx_paged_decode (a value that is not finite
+ * spoils the rows that read it).  first, like lengths and page ids, is checked on the device.  Outputs and workspace must not overlap
+ * inputs, the pools or one another. */
 svx_status svx_paged_decode_shared(const svx_pages* cache, int32_t n_req, int32_t n_q_heads, const void* q,
                                    const svx_prefixes* prefixes, const int32_t* len, int64_t max_len, float scale, void* o,
                                    float* lse, void* workspace, int64_t workspace_bytes, void* stream);
@@ -669,7 +670,7 @@ svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, const int32_t*
 
 /* Test hook of the bounds-checked library (as svx_debug_clip_q_rows, for the calls above).  Until it is called again, this
  * thread's calls describe a kind of buffer as holding at most `elements` elements (< 0: the real number again); buffer
- * 0: q, k and v of svx_heads; 1: q_out, k_out and v_out; 2: the K and V pages.  The real buffers are larger, so no access
+ * 0: q, k and v of svx_heads; 1: q_out, k_out and v_out; 2: the K and V pages, and k and v of svx_cross.  The real buffers are larger, so no access
  * leaves them: in libsvx_checked.so the kernels skip the rows past the end and set bit 4 and the buffer's bit (0: 2^17,
  * 1: 2^18, 2: 2^19) of the status word; in libsvx.so nothing changes. */
 svx_status svx_debug_clip_paged(int32_t buffer, int64_t elements);
@@ -688,13 +689,13 @@ typedef struct {
   float* lse;              /* device [n_req][n_q_heads][n_tok], or NULL */
   const int32_t* len;      /* device [n_req]: only the first len[b] states of a request count, 0..n_states; NULL: all */
   const uint8_t* mask;     /* device, state t of request b at b * mask_req + t: 0: it does not count; NULL: all do */
-  int32_t* status;         /* device status word (as in svx_pages), or NULL */
+  int32_t* status;         /* device status word (as in svx_pages), or NULL; also raised if a bounded wait of the kernel gave up */
   int64_t q_req, q_head, q_tok;
   int64_t kv_req, kv_head, kv_state;
   int64_t o_req, o_head, o_tok;
   int64_t mask_req;
   int32_t n_req;           /* 1 .. 256 */
-  int32_t n_tok;           /* >= 1 */
+  int32_t n_tok;           /* >= 1; times n_q_heads / n_kv_heads at most 1048560 */
   int32_t n_states;        /* >= 0 */
   int32_t n_q_heads, n_kv_heads, head_dim; /* head_dim 64 or 128; n_q_heads a multiple of n_kv_heads, at most 4096 */
   int32_t dtype;           /* SVX_BF16 or SVX_FP16 */
@@ -710,7 +711,8 @@ svx_status svx_cross_attn_workspace(const svx_cross* c, int64_t* bytes);
  * none does.  Query head h reads KV head h / (n_q_heads / n_kv_heads).  States that count must be finite, as in svx_paged_decode; what
  * the others hold is not used, whatever it is.  Outputs and workspace must not overlap inputs or one another (a strided buffer
  * counts from its first element to its last).  workspace: device, 256-byte aligned; contents need no set-up.
- * Enqueued on `stream` (cudaStream_t) of `device`; allocates and keeps nothing, so it may be captured (after one eager call). */
+ * Enqueued on `stream` (cudaStream_t) of `device`; allocates and keeps nothing, so it may be captured (after one eager call).  Calls
+ * whose GPU work overlaps need workspaces and outputs of their own. */
 svx_status svx_cross_attn(const svx_cross* c, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---- the residual stream between two blocks ------------------------------------------------------ */

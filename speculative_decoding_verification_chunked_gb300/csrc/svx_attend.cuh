@@ -1,4 +1,5 @@
-// Attention of one new token per request over a paged cache.
+// Attention of few rows to the same keys: one new token per request over a paged cache (kPaged, which the figures below are of), a few
+// rows against an encoder's states (kDense), and rows of shared prefixes beside the requests' own slots (kShared).
 //
 //   s_t = scale q.k_t,  m = max s,  p_t = e^(s_t - m),  l = sum p,  O = sum p v / l,  LSE = m + ln l
 //
@@ -109,7 +110,7 @@ struct Plan {
   int32_t row_tiles;        // (join_shared) rows_kernel's tiles
 };
 
-constexpr int kTile = 128;  // keys of a tile of rows_kernel
+constexpr int kKeyTile = 128;  // keys of a tile of rows_kernel
 
 // Sums x over the first kMaxReq threads of the block up to this one, and all of theirs into `total`.
 __device__ __forceinline__ int block_scan(int x, int32_t* warp_sum, int& total) {
@@ -179,7 +180,7 @@ __device__ __forceinline__ int build_plan(const AttendParams& P, Plan<SRC>& s, b
       if (report && n != raw) atomicOr(P.pages.status, kErrInput);
       rows = (s.req0[t + 1] - s.req0[t]) * P.group;
     }
-    const int per = tiles ? kTile : CT, block = tiles ? P.item_rows : kRowsMax;
+    const int per = tiles ? kKeyTile : CT, block = tiles ? P.item_rows : kRowsMax;
     const int chunks = (P.prefix_apart && !tiles) || rows == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(n) + (per - 1)) / per);
     s.n[t] = chunks;
     s.len[t] = n;

@@ -4,6 +4,12 @@
 //
 // There is no order among states, so the tokens of a request and the query heads of a KV head are alike: rows of one product
 // with the same keys.
+//
+// Up to 16 rows (one token, few query heads to a KV head) attend_kernel brings K and V in once and its products are small beside them;
+// with more, rows_kernel.  A request whose states are all hidden costs its keys' words of the mask and nothing of K and V.
+// Measured: one token x 1500 states of 16 heads 9.0 us (two launches and their latencies); 32 requests of one token, 32 heads over 8 KV heads,
+// up to 6404 states of which 20% are hidden 59 us (the bytes of all states below the lengths: 63); 4 x 448 tokens x 701 to 1500
+// states of 16 heads 23 us; 8192 x 16384 1334 us among other passes, 1204 alone.
 #include "svx_rows.cuh"
 
 namespace svx {
@@ -108,7 +114,7 @@ svx_status cross_sizes(const svx_cross& a, CrossView* v) {
   const int64_t items = static_cast<int64_t>(a.n_req) * a.n_kv_heads;
   if (v->many) {
     const int item_rows = item_rows_for(v->p.rows);
-    size_rows(&v->rz, items * ((v->p.rows + item_rows - 1) / item_rows), (static_cast<int64_t>(a.n_states) + kTile - 1) / kTile, item_rows,
+    size_rows(&v->rz, items * ((v->p.rows + item_rows - 1) / item_rows), (static_cast<int64_t>(a.n_states) + kKeyTile - 1) / kKeyTile, item_rows,
               a.head_dim, sms, 0, true);
     v->total = v->rz.total;
     return SVX_OK;

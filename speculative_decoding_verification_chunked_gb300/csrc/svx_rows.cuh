@@ -14,11 +14,21 @@
 //   P               128 threads, one a row: read from tensor memory, exponentials, rounded, written over S in tensor memory
 //   O += P V        M = 128 rows, N = D, K = 128 keys: P from tensor memory, V from shared memory as it lies (MN-major)
 //   warps 0-3, 4-7  softmax of stream 0 and 1, and the segment's end
-//   warp 8          issues the products (one thread)
-//   warps 9, 10     bring K and V tiles in (16-byte cp.async, rows found through the page table or by stride)
-//   warp 11         brings Q in
+//   warp 8          issues the products (one lane, the warp converged)
+//   warps 9, 10     bring K and V tiles in: by tensor map, in boxes of a page or a tile, where all of a tile's keys count and pages and
+//                   strides allow, else in 16-byte cp.async, rows found through the page table or by stride
+//   warp 11         brings Q in: by tensor map where 128 rows are a whole number of tokens or requests
 // Up to 128 rows the tensor cores have time to spare (the bytes of K and V bound the time), and P enters the product in two 16-bit pieces:
-// O is then as exact as with fp32 weights.  With more rows the products bound the time, and P is rounded once.
+// O is then as exact as with fp32 weights.  Where a call has more than 128 rows to the same keys the products bound the time, and P is
+// rounded once: a weight is off by up to 2^-8 (bf16) or 2^-11 (fp16) of itself.
+//
+// What bounds it.  Two row tiles, d = 128: the products; 8192 x 16384 tokens of 32 heads 1204 us = 1827 TFLOP/s, 95% of the measured cuBLAS
+// rate.  d = 64: half the products to the same softmax, whose own steps decide (2 x 2048 x 4096 tokens of 16 heads: the tensor
+// pipe busy for 39%, the exponentials' for 39%, 43% of the issue slots).  One row tile: the bytes of K and V (16 samples behind 32768
+// slots, 8 KV heads, 134 MB: 44 us with the start, the join and the samples' own slots).  Few tiles to an item: the way from Q through S, P
+// and O to the output, which a stream takes while the other one computes, 6000 to 7000 cycles an item (8 x 4096 tokens x 77 states,
+// 16 heads of d = 64: 68 us, of which the bytes are 20).  There leaving out the chunks of 32 keys behind a length gained 0 to 4%, and
+// cost full tiles 3 to 5%; P beside S in tensor memory, so that S(i + 2) need not wait for P V(i), gained nothing at d = 64.
 //
 // Every wait is bounded (2 s of global time): one that gives up raises the status word and makes all roles stop, drain and leave.
 #pragma once
@@ -33,14 +43,14 @@ namespace svx {
 namespace {
 
 constexpr int kRowTile = 128;
-constexpr uint32_t kHalf = kTile * 128;      // bytes of 64 dimensions of 128 rows (an operand's swizzle atoms: 8 rows of 128 bytes)
+constexpr uint32_t kHalf = kKeyTile * 128;      // bytes of 64 dimensions of 128 rows (an operand's swizzle atoms: 8 rows of 128 bytes)
 constexpr uint64_t kWaitLimit = 2000000000ull;
 constexpr int kRowThreads = 384;
 
 // QT: row tiles of an item, 1 or 2.
 template <int D, int QT>
 struct RowsCfg {
-  static constexpr uint32_t TILE = kTile * D * 2;  // K or V
+  static constexpr uint32_t TILE = kKeyTile * D * 2;  // K or V
   // with one row tile the bytes in flight decide: 5 tiles of 32 KiB (d = 128), 8 of 16 KiB (d = 64)
   static constexpr int KST = D == 128 ? 2 : 4;
   static constexpr int VST = D == 128 ? 4 - QT : 4;
@@ -240,7 +250,7 @@ __device__ __forceinline__ uint32_t desc_of(uint32_t addr, uint32_t lead) {
 
 // ------------------------------------------------------------------ the flat range
 
-// As Plan, of items of up to P.item_rows rows and tiles of kTile keys.  Sequences: the requests, or (kShared) the prefixes.
+// As Plan, of items of up to P.item_rows rows and tiles of kKeyTile keys.  Sequences: the requests, or (kShared) the prefixes.
 struct RowPlan {
   int32_t first[kMaxReq + 1];
   int32_t warp_sum[kWarps];
@@ -267,7 +277,7 @@ __device__ __forceinline__ int build_row_plan(const AttendParams& P, RowPlan& s,
     if (status && n != raw) atomicOr(status, kErrInput);
     rows = row_rows<SRC>(P, s, t);
   }
-  const int tiles = rows ? static_cast<int>((static_cast<uint32_t>(n) + (kTile - 1)) / kTile) : 0;
+  const int tiles = rows ? static_cast<int>((static_cast<uint32_t>(n) + (kKeyTile - 1)) / kKeyTile) : 0;
   const int mine = P.pages.n_kv_heads * ((rows + P.item_rows - 1) / P.item_rows) * tiles;
   int total;
   const int upto = block_scan(mine, s.warp_sum, total);
@@ -517,6 +527,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  // (before the tensor memory is asked for: a kernel that still runs may hold it)
+  if (SRC != kShared) grid_dependency_wait();
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + C::OFF_MISC), "r"(C::TMEM_COLS)
                  : "memory");
@@ -525,7 +537,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
   tc_before();
   // Behind attend_kernel, which takes the requests' own slots: neither reads what the other writes, and that one had waited for all
   // that came before when it let this one start.  The wait is for the join, which relies on this kernel's end.
-  if (SRC != kShared) grid_dependency_wait();
   allow_dependents();
   const int T_all = build_row_plan<SRC>(P, plan, blockIdx.x == 0);  // (its barriers also show the lines above to all threads)
   tc_after();
@@ -563,7 +574,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     const int piece = lane % PIECES, r0 = lane / PIECES;
     const CUtensorMap* const map = is_v ? &P.v_map : &P.k_map;
     const bool maps = !kBoundsChecked && P.box > 0;
-    const int box = maps ? P.box : kTile;
+    const int box = maps ? P.box : kKeyTile;
     if (maps && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
     int i = 0;
     bool ok = true;
@@ -575,13 +586,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       auto look = [&](int t) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int key = (g.tile0 + t) * kTile + u * 32 + lane;
+          const int key = (g.tile0 + t) * kKeyTile + u * 32 + lane;
           page[u] = t < g.n && key < g.len ? __ldg(table + page_of(P.pages, static_cast<uint32_t>(key))) : 0;
         }
       };
       if constexpr (SRC == kShared) look(0);
       for (int t = 0; t < g.n; ++t, ++i) {
-        const int t0 = (g.tile0 + t) * kTile;
+        const int t0 = (g.tile0 + t) * kKeyTile;
         const int stage = i % stages;
         const uint32_t dst = ring + stage * C::TILE;
         const Seen seen = keys_seen<SRC>(P, g, t0);
@@ -593,7 +604,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
                                                        static_cast<uint32_t>(page[2]) < n && static_cast<uint32_t>(page[3]) < n);
         }
         if (boxes) {  // a tile whose keys all count: in boxes, one or more a lane
-          const int runs = kTile / box;
+          const int runs = kKeyTile / box;
           // lane l: half l / runs of the dimensions, run l % runs
           const int run = lane % runs, key = run * box;
           int w = g.b * P.page_step, z = t0;
@@ -698,7 +709,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ---- the products.  Step u of a segment: stream u & 1; S(u + 2) follows P V(u), whose P lies over it
-    constexpr uint32_t idesc_s = rows_idesc<T>(kTile, false), idesc_o = rows_idesc<T>(D, true);
+    constexpr uint32_t idesc_s = rows_idesc<T>(kKeyTile, false), idesc_o = rows_idesc<T>(D, true);
     const uint32_t one = one_lane();
     int seg = 0, kt = 0, vt = 0, qb = 0;     // segments so far, and the places of the next K, V and Q
     uint32_t kp = 0, vp = 0, qp = 0, np = 0; // parities: of the rings' rounds, and of each stream's P's (bit s)
@@ -741,10 +752,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         const uint32_t a = tmem + s * 128, d = tmem + C::O_COL + s * D;
         const uint32_t b = desc_of(base + C::OFF_V, kHalf) + vt * (C::TILE >> 4);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) mma_ts(one, d, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 2048) >> 4), idesc_o, u > 1 || k > 0);
+        for (int k = 0; k < kKeyTile / 16; ++k) mma_ts(one, d, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 2048) >> 4), idesc_o, u > 1 || k > 0);
         if constexpr (QT == 1) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) mma_ts(one, d, a + (k >> 1) * 32 + 16 + (k & 1) * 8, b + ((k * 2048) >> 4), idesc_o, true);
+          for (int k = 0; k < kKeyTile / 16; ++k) mma_ts(one, d, a + (k >> 1) * 32 + 16 + (k & 1) * 8, b + ((k * 2048) >> 4), idesc_o, true);
         }
         if (closes) {
           commit(one, VEMPTY + 8u * vt);
@@ -784,8 +795,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       const bool busy = (warp & 3) * 32 < my_rows;  // this warp has rows
       float m = kNegInf, l = 0.f;
       for (int i = 0; i < mine && ok; ++i, ++ns) {
-        const int t0 = (g.tile0 + (two ? i : 2 * i + s)) * kTile;
-        const bool all = (SRC != kDense || !P.mask) && t0 + kTile <= g.len;
+        const int t0 = (g.tile0 + (two ? i : 2 * i + s)) * kKeyTile;
+        const bool all = (SRC != kDense || !P.mask) && t0 + kKeyTile <= g.len;
         Seen seen = {};
         if (!all) seen = keys_seen<SRC>(P, g, t0);
         if (!W.warp_wait(SFULL + 8u * s, ns & 1u)) {
@@ -815,18 +826,18 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
             sum[k & 1] = add2(sum[k & 1], pair(x, y));
           };
           if constexpr (QT == 1) {
-            // 32 columns at a time, and S read twice: four times as long as the bytes allow would do, and the instructions, which
-            // what came before has often put out of the caches, take 2 us to come in, not 7
+            // 32 columns at a time, and S read twice: the bytes of K and V leave the time for it, and there are a quarter of the
+            // instructions, which what came before has often put out of the caches (the first tile of a launch 5 us, with all 128 unrolled 8)
             float top = kNegInf;
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
+            for (int c = 0; c < kKeyTile; c += 32) {
               float v[32];
               tmem_read32<0>(at_s + c, v);
               top = fmaxf(top, max_of(v));
             }
             move_reference(top * P.scale);
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
+            for (int c = 0; c < kKeyTile; c += 32) {
               float v[32];
               tmem_read32<0>(at_s + c, v);
               uint32_t hi[16], lo[16];
@@ -840,11 +851,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
               tmem_write16(at_s + c + 16, lo);
             }
           } else {
-            float v[kTile];
+            float v[kKeyTile];
             tmem_read128(at_s, v);
             move_reference(max_of(v) * P.scale);
 #pragma unroll
-            for (int c = 0; c < kTile; c += 32) {
+            for (int c = 0; c < kKeyTile; c += 32) {
               uint32_t hi[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
@@ -1106,7 +1117,7 @@ inline void make_maps(RowsParams& p, int src, int D, bool bf16) {
                                         dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  int box = kTile;
+  int box = kKeyTile;
   if (src == kShared)
     while (p.pages.page_size % box) box /= 2;
   if (box >= 16 && p.pages.k) {
