@@ -6,7 +6,7 @@
 // attend_kernel beside it takes the requests' own slots.  Every row then has two lots of states (m, l, O), which join_shared merges.
 //
 // Measured (32 heads, 8 KV heads, d = 128, bf16): 16 samples of a 32768-slot prompt with up to 512 slots of their own 44 us (the bytes 22);
-// 256 requests behind 65536 slots, read once, 257 us (the products 144; the requests' own slots are brought in by SMs of their
+// 256 requests behind 65536 slots, read once, 243 us (the products 144; the requests' own slots are brought in by SMs of their
 // own meanwhile).  Four branches of 2048 slots, 4 heads of d = 64: 11.7 us, two launches and their trips to memory.
 #include "svx_rows.cuh"
 
@@ -230,6 +230,13 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
     const double own_us = static_cast<double>(n_req) * c->n_kv_heads * max_len * c->head_dim * 4 / 45e3;
     const double far_us = static_cast<double>(items) * per * (item_rows > kRowTile ? 1.4 : 1.0);
     own_ctas = std::min(std::max(static_cast<int>(sms * own_us / (own_us + far_us) + 0.5), 4), sms - 4);
+    // Where a prefix's rows are several items, as many CTAs as make the items' halves whole: then the CTAs of a KV head's items go
+    // through the same keys at a time, and find them in L2 (256 requests behind 65536 slots, 32 such items: 107 CTAs 251 us, 112 233).
+    const int64_t blocks = (all_rows + used * item_rows - 1) / (used * item_rows), half = c->n_kv_heads * used * blocks / 2;
+    if (blocks > 1) {
+      const int64_t near = (sms - own_ctas + half / 2) / half * half;
+      if (near >= 4 && near <= sms - 4 && std::abs(near - (sms - own_ctas)) * 8 <= sms) own_ctas = sms - static_cast<int>(near);
+    }
     size_rows(&out->rz, items, per, item_rows, c->head_dim, sms - own_ctas, 0, false);
   }
   size_pieces(&z, chunks, c->head_dim, own_ctas);
