@@ -19,8 +19,8 @@
 //                   strides allow, else in 16-byte cp.async, rows found through the page table or by stride
 //   warp 11         brings Q in: by tensor map where 128 rows are a whole number of tokens or requests
 // Up to 128 rows the tensor cores have time to spare (the bytes of K and V bound the time), and P enters the product in two 16-bit pieces:
-// O is then as exact as with fp32 weights.  Where a call has more than 128 rows to the same keys the products bound the time, and P is
-// rounded once: a weight is off by up to 2^-8 (bf16) or 2^-11 (fp16) of itself.
+// O is then as exact as with fp32 weights.  Where there are more than 128 rows to the same keys (of prefixes: on average) the products
+// bound the time, and P is rounded once: a weight is off by up to 2^-8 (bf16) or 2^-11 (fp16) of itself.
 //
 // What bounds it.  Two row tiles, d = 128: the products; 8192 x 16384 tokens of 32 heads 1204 us = 1827 TFLOP/s, 95% of the measured cuBLAS
 // rate.  d = 64: half the products to the same softmax, whose own steps decide (2 x 2048 x 4096 tokens of 16 heads: the tensor

@@ -225,7 +225,9 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
   // may be shorter.)
   int own_ctas = sms;
   if (out->many) {
-    const int item_rows = item_rows_for(all_rows);
+    // (of a prefix, on average; 8 of 16 requests' 64 rows, 4096 slots, d = 64: in items of 128 rows 39 us, of 256 44; 16 such of 2048 slots,
+    // d = 128: 64 and 60)
+    const int item_rows = item_rows_for((all_rows + used - 1) / used);
     const int64_t items = c->n_kv_heads * (all_rows / item_rows + used), per = (max_prefix + kKeyTile - 1) / kKeyTile;
     const double own_us = static_cast<double>(n_req) * c->n_kv_heads * max_len * c->head_dim * 4 / 45e3;
     const double far_us = static_cast<double>(items) * per * (item_rows > kRowTile ? 1.4 : 1.0);

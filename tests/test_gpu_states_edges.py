@@ -322,3 +322,50 @@ def test_a_decoder_layer_over_branches_of_one_prompt(svx):
         graph.replay()
         assert torch.equal(h, want)
     assert not c.check()
+
+
+def test_prefixes_unlike_their_average(svx):
+    """Items of 128 rows by the average, where one prefix has more; prefixes without requests, more of them than requests; query heads
+    that fill a row tile by themselves; several row tiles whose halves are shared out over the CTAs."""
+    bf16, fp16 = torch.bfloat16, torch.float16
+    for groups, prefix, hq, hkv, d, page, t, rows in (((70, 1, 0, 2), (700, 300, 50, 129), 4, 1, 128, 16, bf16, 73),
+                                                      ((1, 0, 0, 2, 0, 0, 0, 1), (300, 5, 6, 1000, 7, 8, 9, 128), 64, 1, 64, 32, fp16, 64),
+                                                      ((2, 1), (513, 40), 130, 1, 128, 24, bf16, 195),
+                                                      ((150,), (5000,), 8, 2, 64, 64, fp16, 600)):
+        s = shared_inputs(groups, prefix, 21, hq, hkv, d, page, t, "token", seed=len(groups))
+        c = svx.PagedCache(s["k"], s["v"])
+        run_shared(c, s, max_len=21, max_prefix=max(prefix))
+        check_shared(s, rows=rows)
+        assert not c.check()
+
+
+def test_side_by_side_with_a_round(svx):
+    """Kernels that hold tensor memory on three streams at a time: a round's, those of states and those of shared prefixes."""
+    hq, hkv, d, nq, hist = 8, 2, 128, 5, (900, 1300)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    rounds = dict(q=r(2, hq, nq, d), k=[r(n, hkv, d) for n in hist], v=[r(n, hkv, d) for n in hist], kc=r(2, nq, hkv, d), vc=r(2, nq, hkv, d))
+    q, k, v = r(2, 8, 200, 64), r(2, 700, 2, 64), r(2, 700, 2, 64)
+    s = shared_inputs((40,), (3000,), 33, 8, 2, 128, 16, torch.bfloat16, "token", seed=9)
+    c = svx.PagedCache(s["k"], s["v"])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+
+    with svx.Verifier(2, hq, hkv, d, nq, 512, compute_stream=streams[0]) as verifier:
+        def go(a, b, e):
+            out = dict(ro=torch.empty_like(rounds["q"]), rl=torch.empty((2, hq, nq), device="cuda"), co=torch.empty_like(q),
+                       cl=torch.empty((2, 8, 200), device="cuda"), so=torch.zeros_like(s["o"]), sl=torch.zeros_like(s["lse"]))
+            torch.cuda.synchronize()
+            for _ in range(4):
+                with torch.cuda.stream(a):
+                    verifier.run_round(rounds["q"], hist, rounds["k"], rounds["v"], 512, out["ro"], out["rl"], cand_k=rounds["kc"], cand_v=rounds["vc"])
+                svx.cross_attn(q, k, v, out["co"], out["cl"], stream=b)
+                run_shared(c, {**s, "o": out["so"], "lse": out["sl"]}, stream=e)
+            torch.cuda.synchronize()
+            return out
+
+        alone = go(streams[0], streams[0], streams[0])
+        for _ in range(3):
+            for name, x in go(*streams).items():
+                assert torch.equal(x, alone[name]), name
+    check_cross(q, k, v, alone["co"], alone["cl"])
+    check_shared({**s, "o": alone["so"], "lse": alone["sl"]})
