@@ -549,15 +549,20 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
   }
   RowWaiter W{misc + 1, P.pages.status};
 
-  // requests without keys
+  // requests without keys: their rows over all threads
   if constexpr (SRC == kDense) {
-    for (int b = blockIdx.x; b < P.pages.n_req; b += gridDim.x) {
-      if (plan.first[b + 1] > plan.first[b]) continue;
-      for (int64_t i = threadIdx.x; i < static_cast<int64_t>(P.n_q) * P.n_tok; i += kRowThreads) {
-        const int j = static_cast<int>(i / P.n_q), head = static_cast<int>(i - static_cast<int64_t>(j) * P.n_q);
-        uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(P.o) + b * P.o_b + head * P.o_h + j * P.o_n);
-        for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (P.lse) P.lse[(static_cast<int64_t>(b) * P.n_q + head) * P.n_tok + j] = kNegInf;
+    for (int b0 = 0; b0 < P.pages.n_req; b0 += 32) {
+      const int mine = b0 + lane;
+      uint32_t none = __ballot_sync(0xffffffffu, mine < P.pages.n_req && plan.first[mine + 1] <= plan.first[mine]);
+      for (; none; none &= none - 1) {
+        const int b = b0 + __ffs(none) - 1;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; i < static_cast<int64_t>(P.n_q) * P.n_tok;
+             i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
+          const int j = static_cast<int>(i / P.n_q), head = static_cast<int>(i - static_cast<int64_t>(j) * P.n_q);
+          uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(P.o) + b * P.o_b + head * P.o_h + j * P.o_n);
+          for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (P.lse) P.lse[(static_cast<int64_t>(b) * P.n_q + head) * P.n_tok + j] = kNegInf;
+        }
       }
     }
   }
@@ -1069,7 +1074,7 @@ inline void size_rows(RowSizes* z, int64_t items, int64_t per, int item_rows, in
   z->item_rows = item_rows;
   most = std::min(most, kMaxCtas);
   z->whole = may_whole && (items + most - 1) / most * per <= tiles / most + (item_rows * head_dim > 2 * kRowTile * 64 ? kJoinTilesLarge : kJoinTiles);
-  z->ctas = static_cast<int32_t>(std::min<int64_t>(most, std::max<int64_t>(tiles, 1)));
+  z->ctas = static_cast<int32_t>(tiles ? std::min<int64_t>(most, tiles) : most);  // (without tiles: for the rows that have no keys)
   z->rows_o = up256(at);
   if (z->whole) {  // no pieces
     z->rows_ml = z->rows_o;

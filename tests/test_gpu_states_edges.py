@@ -369,3 +369,19 @@ def test_side_by_side_with_a_round(svx):
                 assert torch.equal(x, alone[name]), name
     check_cross(q, k, v, alone["co"], alone["cl"])
     check_shared({**s, "o": alone["so"], "lse": alone["sl"]})
+
+
+def test_requests_without_states_among_many_tokens(svx):
+    """Rows that have no keys are many CTAs' work: among requests that have some, alone, and without any state at all."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.float16)  # noqa: E731
+    q, k, v = r(35, 6, 700, 64), r(35, 130, 2, 64), r(35, 130, 2, 64)
+    for lens in ([0, 130, 0, 40] + [0] * 29 + [1, 0], [0] * 35):
+        o = torch.full((35, 700, 6, 64), 3.0, dtype=q.dtype, device="cuda").transpose(1, 2)
+        lse = torch.full((35, 6, 700), 3.0, device="cuda")
+        svx.cross_attn(q, k, v, o, lse, lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        check_cross(q, k, v, o, lse, seen=torch.arange(130, device="cuda") < torch.tensor(lens, device="cuda")[:, None])
+    o.fill_(3)
+    lse.fill_(3)
+    svx.cross_attn(q, k[:, :0], v[:, :0], o, lse)
+    assert (o == 0).all() and (lse == -math.inf).all()
