@@ -15,8 +15,9 @@
 //   O += P V        M = 128 rows, N = D, K = 128 keys: P from tensor memory, V from shared memory as it lies (MN-major)
 //   warps 0-3, 4-7  softmax of stream 0 and 1, and the segment's end
 //   warp 8          issues the products (one lane, the warp converged)
-//   warps 9, 10     bring K and V tiles in: by tensor map, in boxes of a page or a tile, where all of a tile's keys count and pages and
-//                   strides allow, else in 16-byte cp.async, rows found through the page table or by stride
+//   warps 9, 10     bring K and V tiles in: by tensor map, in boxes of a page or a tile, where pages and strides allow and all of the
+//                   tile's keys count (of K, an encoder's states: any of them), else in 16-byte cp.async, rows found through the
+//                   page table or by stride
 //   warp 11         brings Q in: by tensor map where 128 rows are a whole number of tokens or requests
 // Up to 128 rows the tensor cores have time to spare (the bytes of K and V bound the time), and P enters the product in two 16-bit pieces:
 // O is then as exact as with fp32 weights.  Where there are more than 128 rows to the same keys (of prefixes: on average) the products
@@ -184,6 +185,23 @@ __device__ __forceinline__ void tmem_read32(uint32_t at, float (&v)[N]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[OFF + i] = __uint_as_float(r[i]);
+}
+// 64 columns.
+__device__ __forceinline__ void tmem_read64(uint32_t at, float (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+        "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]),
+        "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]),
+        "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]),
+        "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]),
+        "=f"(v[54]), "=f"(v[55]), "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]),
+        "=f"(v[63])
+      : "r"(at)
+      : "memory");
 }
 // 128 columns.
 __device__ __forceinline__ void tmem_read128(uint32_t at, float (&v)[128]) {
@@ -438,14 +456,18 @@ struct Seen {
 // Scores of keys that do not count become -inf (out of line, so that the loop's usual path stays short).
 __device__ __noinline__ void hide_keys(uint32_t at, Seen seen) {
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t w = c < 2 ? (c == 0 ? seen.w[0] : seen.w[1]) : c == 2 ? seen.w[2] : seen.w[3];
-    if (w == 0xffffffffu) continue;
-    float v[32];
-    tmem_read32<0>(at + c * 32, v);
+  for (int c = 0; c < kKeyTile; c += 64) {
+    const uint32_t w0 = c ? seen.w[2] : seen.w[0], w1 = c ? seen.w[3] : seen.w[1];
+    if ((w0 & w1) == ~0u) continue;
+    float v[64];
+    tmem_read64(at + c, v);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = w >> k & 1u ? v[k] : kNegInf;
-    tmem_write32(at + c * 32, v);
+    for (int h = 0; h < 64; h += 32) {
+      float x[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] = (h ? w1 : w0) >> k & 1u ? v[h + k] : kNegInf;
+      tmem_write32(at + c + h, x);
+    }
   }
   tmem_written();
 }
@@ -602,7 +624,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         const uint32_t dst = ring + stage * C::TILE;
         const Seen seen = keys_seen<SRC>(P, g, t0);
         const bool all = (seen.w[0] & seen.w[1] & seen.w[2] & seen.w[3]) == 0xffffffffu;
-        bool boxes = maps && all;
+        // (keys that do not count: their scores are put out, whatever K holds; but V has to be zero there)
+        const bool any = (seen.w[0] | seen.w[1] | seen.w[2] | seen.w[3]) != 0u;
+        bool boxes = maps && (all || (SRC == kDense && !is_v && any && t0 + kKeyTile <= P.max_len));
         if constexpr (SRC == kShared) {
           const uint32_t n = P.pages.n_pages;
           boxes = boxes && __all_sync(0xffffffffu, static_cast<uint32_t>(page[0]) < n && static_cast<uint32_t>(page[1]) < n &&
@@ -631,34 +655,50 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
           if (lane != 0) bar_arrive(full + 8u * stage);
           continue;
         }
-        int64_t off[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          off[u] = -1;
-          const int key = t0 + u * 32 + lane;
-          if (!(seen.w[u] >> lane & 1u)) continue;
-          if constexpr (SRC == kShared) {
-            off[u] = slot_offset(P.pages, page[u], key - page_of(P.pages, static_cast<uint32_t>(key)) * P.pages.page_size);
-            if (off[u] < 0) atomicOr(P.pages.status, kErrInput);
-          } else {
-            off[u] = g.b * P.pages.page_stride + key * P.pages.tok_stride;
+        if constexpr (SRC == kDense && !kBoundsChecked) {  // rows a stride apart
+          const T* from = pool + g.b * P.pages.page_stride + g.h * P.pages.head_stride + (t0 + r0) * P.pages.tok_stride + piece * 8;
+          if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
+            ok = false;
+            break;
           }
-          if (off[u] >= 0) off[u] += g.h * P.pages.head_stride;
-          if (off[u] >= 0 && !in_bounds(pool + off[u], D, pool, P.pages.extent, P.pages.status, kSitePool)) off[u] = -1;
-        }
-        if constexpr (SRC == kShared) look(t + 1);
-        if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
-          ok = false;
-          break;
-        }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+          for (int u = 0; u < 4; ++u)
 #pragma unroll 8
-          for (int j = 0; j < 32 / RPI; ++j) {
-            const int in32 = j * RPI + r0, r = u * 32 + in32;
-            const int64_t ro = __shfl_sync(0xffffffffu, off[u], in32);
-            copy16(dst + (piece >> 3) * kHalf + r * 128 + (((piece & 7) ^ (r & 7)) << 4), pool + (ro >= 0 ? ro : 0) + piece * 8, ro >= 0 ? 16 : 0);
+            for (int j = 0; j < 32 / RPI; ++j, from += RPI * P.pages.tok_stride) {
+              const int in32 = j * RPI + r0, r = u * 32 + in32;
+              const bool is = seen.w[u] >> in32 & 1u;
+              copy16(dst + (piece >> 3) * kHalf + r * 128 + (((piece & 7) ^ (r & 7)) << 4), is ? from : pool, is ? 16 : 0);
+            }
+        } else {
+          int64_t off[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            off[u] = -1;
+            const int key = t0 + u * 32 + lane;
+            if (!(seen.w[u] >> lane & 1u)) continue;
+            if constexpr (SRC == kShared) {
+              off[u] = slot_offset(P.pages, page[u], key - page_of(P.pages, static_cast<uint32_t>(key)) * P.pages.page_size);
+              if (off[u] < 0) atomicOr(P.pages.status, kErrInput);
+            } else {
+              off[u] = g.b * P.pages.page_stride + key * P.pages.tok_stride;
+            }
+            if (off[u] >= 0) off[u] += g.h * P.pages.head_stride;
+            if (off[u] >= 0 && !in_bounds(pool + off[u], D, pool, P.pages.extent, P.pages.status, kSitePool)) off[u] = -1;
           }
+          if constexpr (SRC == kShared) look(t + 1);
+          if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll 8
+            for (int j = 0; j < 32 / RPI; ++j) {
+              const int in32 = j * RPI + r0, r = u * 32 + in32;
+              const int64_t ro = __shfl_sync(0xffffffffu, off[u], in32);
+              copy16(dst + (piece >> 3) * kHalf + r * 128 + (((piece & 7) ^ (r & 7)) << 4), pool + (ro >= 0 ? ro : 0) + piece * 8, ro >= 0 ? 16 : 0);
+            }
+        }
         copies_arrive(full + 8u * stage);
       }
       x += g.n;
@@ -810,7 +850,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         }
         if (busy) {
           tc_after();
-          if (!all) hide_keys(at_s, seen);
+          const bool some = !all && (seen.w[0] & seen.w[1] & seen.w[2] & seen.w[3]) != ~0u;
+          if (QT == 1 && some) hide_keys(at_s, seen);
           const uint64_t scale2 = pair(P.scale, P.scale);
           uint64_t sum[2] = {0, 0}, less2;
           auto move_reference = [&](float top) {  // where the row's largest score has passed it
@@ -858,6 +899,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
           } else {
             float v[kKeyTile];
             tmem_read128(at_s, v);
+            if (some) {  // (by hide_keys, 20% of the keys hidden: 4096 x 8192 tokens of 32 heads 480 us, so 440; none hidden: 320)
+#pragma unroll
+              for (int k = 0; k < kKeyTile; ++k) v[k] = seen.w[k / 32] >> (k % 32) & 1u ? v[k] : kNegInf;
+            }
             move_reference(max_of(v) * P.scale);
 #pragma unroll
             for (int c = 0; c < kKeyTile; c += 32) {

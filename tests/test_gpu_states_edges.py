@@ -385,3 +385,24 @@ def test_requests_without_states_among_many_tokens(svx):
     lse.fill_(3)
     svx.cross_attn(q, k[:, :0], v[:, :0], o, lse)
     assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [20, 150])
+@pytest.mark.parametrize("hold", [math.nan, math.inf, 6e4])
+def test_what_hidden_states_hold(svx, n, d, hold):
+    """Hidden states of whole tiles, of parts of tiles, behind the lengths, and all of a request's; none of them counts."""
+    g = torch.Generator(device="cuda").manual_seed(n + d)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.float16)  # noqa: E731
+    q, k, v = r(5, 4, n, d), r(5, 700, 2, d), r(5, 700, 2, d)
+    lens = torch.tensor([700, 640, 300, 700, 129], dtype=torch.int32, device="cuda")
+    mask = torch.rand((5, 700), generator=g, device="cuda") < 0.7
+    mask[0, :128] = False
+    mask[1, 128:256] = True
+    mask[3] = False
+    seen = mask & (torch.arange(700, device="cuda") < lens[:, None])
+    k[~seen], v[~seen] = hold, -hold
+    o, lse = torch.full_like(q, 3.0), torch.full((5, 4, n), 3.0, device="cuda")
+    svx.cross_attn(q, k, v, o, lse, lens=lens, mask=mask)
+    check_cross(q, k, v, o, lse, seen=seen)
+    assert (o[3] == 0).all() and (lse[3] == -math.inf).all()
