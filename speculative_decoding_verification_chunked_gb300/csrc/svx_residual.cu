@@ -140,12 +140,12 @@ __device__ __forceinline__ uint64_t activate2(uint64_t g, int act) {
   return g;
 }
 
-// The sum over the threads of a row: a warp, or the block (every thread gets it; `s`: not the last call's).
-template <bool WARP_ROW>
+// The sum over the threads of a row: LANES of a warp, or (0) the block (every thread gets it; `s`: not the last call's).
+template <int LANES>
 __device__ __forceinline__ float row_sum(float v, float* s) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (!WARP_ROW) {
+  for (int o = LANES ? LANES / 2 : 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (LANES == 0) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) s[warp] = v;
     __syncthreads();
@@ -165,18 +165,21 @@ __device__ __forceinline__ void brought(int newer) {  // all but the `newer` las
   else asm volatile("cp.async.wait_group 2;" ::: "memory");
 }
 
-// T: block outputs and weights; H: the residual stream.  WARP_ROW: a row to each warp, else to each block.  N: the most
-// kVec-element pieces of a row that a thread holds.  A block takes every gridDim.x-th row (or four).  Rows come in through shared
+// T: block outputs and weights; H: the residual stream.  LANES: a row to so many lanes of a warp, or (0) to each block.  N: the most
+// kVec-element pieces of a row that a thread holds.  A block takes every gridDim.x-th row (or as many at a time as it has).  Rows come in through shared
 // memory, P.stages of them ahead; a thread brings in what it will read itself, or (32-bit h) its warp does, so no warp waits for another's
 // copies.
-template <typename T, typename H, bool WARP_ROW, int N>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads, WARP_ROW ? 8 : N == 4 ? 1 : 2) residual_kernel(const __grid_constant__ ResidualParams P) {
+template <typename T, typename H, int LANES, int N>
+__global__ void __launch_bounds__(LANES ? 128 : kMaxThreads, LANES ? 8 : N > 2 ? 1 : 2) residual_kernel(const __grid_constant__ ResidualParams P) {
   constexpr int HP = sizeof(H) / 2;  // 16-byte planes of a piece of h
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float s_sum[2][32];
-  const int threads = blockDim.x, t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x, step = WARP_ROW ? 32 : threads;
-  const int64_t rows_at_once = WARP_ROW ? static_cast<int64_t>(gridDim.x) * (threads / 32) : gridDim.x;
-  int64_t row = WARP_ROW ? static_cast<int64_t>(blockIdx.x) * (threads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  constexpr int LANE_ROWS = LANES ? 32 / LANES : 1;  // rows of a warp
+  constexpr int PER = LANES ? LANES : 1;
+  const int threads = blockDim.x, t = LANES ? threadIdx.x % PER : threadIdx.x, step = LANES ? LANES : threads;
+  const int64_t rows_at_once = LANES ? static_cast<int64_t>(gridDim.x) * (threads / PER) : gridDim.x;
+  int64_t row = LANES ? static_cast<int64_t>(blockIdx.x) * (threads / PER) + threadIdx.x / PER : blockIdx.x;
+  const int nth = LANES ? (threadIdx.x & 31) / PER : 0;  // this thread's row among its warp's, whose loop ends with the first of them
   // planes of 16 bytes a thread: [stage][piece][y, h (one or two), gate]
   const bool has_y = P.y != nullptr, has_g = P.gate_kind == kGateRow && P.gate_stride != 0;
   const int planes = HP + (has_y ? 1 : 0) + (has_g ? 1 : 0);
@@ -193,19 +196,21 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads, WARP_ROW ? 8 : N
         if (has_y) bring16(base + plane(stage, i, HP) * 16, static_cast<const T*>(P.y) + r * P.y_stride + v * kVec);
         if (has_g) bring16(base + plane(stage, i, planes - 1) * 16, static_cast<const T*>(P.gate) + r * P.gate_stride + v * kVec);
       }
-      // two planes of a thread: a warp's copies in order of their addresses, 512 bytes at a time (its own 32 a thread would fetch
-      // every sector twice)
-      if constexpr (HP == 2) {
-        const int lane = threadIdx.x & 31;
+    }
+    // two planes of a thread: a warp's copies in order of their addresses, 512 bytes at a time (its own 32 a thread would fetch
+    // every sector twice)
+    if (HP == 2 && (LANE_ROWS > 1 || r < P.rows)) {
+      const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+      for (int i = 0; i < N; ++i)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int c = q * 32 + lane, other = (c >> 1) - lane, v = t + other + i * step;
-            if (v < P.vecs)
-              bring16(base + (plane(stage, i, c & 1) + other) * 16, static_cast<const H*>(P.h) + r * P.h_stride + v * kVec + (c & 1) * 4);
-          }
-      }
+        for (int q = 0; q < 2; ++q) {
+          const int c = q * 32 + lane, other = (c >> 1) - lane;
+          const int v = (LANE_ROWS > 1 ? (c >> 1) % PER : t + other) + i * step;
+          const int64_t ro = r + (LANE_ROWS > 1 ? (c >> 1) / PER - nth : 0);
+          if (v < P.vecs && (LANE_ROWS == 1 || ro < P.rows))
+            bring16(base + (plane(stage, i, c & 1) + other) * 16, static_cast<const H*>(P.h) + ro * P.h_stride + v * kVec + (c & 1) * 4);
+        }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -220,7 +225,8 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads, WARP_ROW ? 8 : N
   }
   // sums use two places in turn: one is written again only behind the other's barrier, when all have read it
   int place = 0, stage = 0;
-  for (; row < P.rows; row += rows_at_once) {
+  for (; row - nth < P.rows; row += rows_at_once) {
+    const int vecs = LANE_ROWS > 1 && row >= P.rows ? 0 : P.vecs;
     brought(P.stages - 1);
     if constexpr (HP == 2) __syncwarp();
     uint64_t z[N][kPairs], u[N][kPairs];  // h' and the block's output; of pieces past the row's end: zeros
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads, WARP_ROW ? 8 : N
     if (has_y) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (t + i * step < P.vecs) unpack<T>(held[plane(stage, i, HP)], u[i]);
+        if (t + i * step < vecs) unpack<T>(held[plane(stage, i, HP)], u[i]);
         else u[i][0] = u[i][1] = u[i][2] = u[i][3] = 0;
       }
       if (P.post_eps >= 0.f) {
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads, WARP_ROW ? 8 : N
 #pragma unroll
           for (int e = 0; e < kPairs; ++e) sum2 = fma2(u[i][e], u[i][e], sum2);
         unpair(sum2, lo, hi);
-        factor *= rsqrtf(fmaf(row_sum<WARP_ROW>(lo + hi, s_sum[place]), P.inv_dim, P.post_eps));
+        factor *= rsqrtf(fmaf(row_sum<LANES>(lo + hi, s_sum[place]), P.inv_dim, P.post_eps));
         place ^= 1;
       }
     }
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads, WARP_ROW ? 8 : N
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int v = t + i * step;
-      if (v >= P.vecs) continue;
+      if (v >= vecs) continue;
       Raw<H>::get(held[plane(stage, i, 0)], held[plane(stage, i, HP - 1)], z[i]);
       if (has_y) {
         uint64_t w[kPairs];
@@ -277,16 +283,16 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads, WARP_ROW ? 8 : N
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int v = t + i * step;
-      if (v < P.vecs && P.h_out) Raw<H>::store(static_cast<H*>(P.h_out) + row * P.h_out_stride + v * kVec, z[i], P.wide);
+      if (v < vecs && P.h_out) Raw<H>::store(static_cast<H*>(P.h_out) + row * P.h_out_stride + v * kVec, z[i], P.wide);
     }
     if (!P.x_out) continue;
     unpair(sum2, lo, hi);
-    const uint64_t r = both(rsqrtf(fmaf(row_sum<WARP_ROW>(lo + hi, s_sum[place]), P.inv_dim, P.eps)));
+    const uint64_t r = both(rsqrtf(fmaf(row_sum<LANES>(lo + hi, s_sum[place]), P.inv_dim, P.eps)));
     place ^= 1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int v = t + i * step;
-      if (v >= P.vecs) continue;
+      if (v >= vecs) continue;
 #pragma unroll
       for (int e = 0; e < kPairs; ++e) z[i][e] = mul2(z[i][e], r);
       if (P.norm) {
@@ -303,30 +309,39 @@ __global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads, WARP_ROW ? 8 : N
 
 constexpr int kSmem = 200 * 1024;  // of rows on their way, of an SM
 
-template <typename T, typename H, bool WARP_ROW, int N>
+template <typename T, typename H, int LANES, int N>
 cudaError_t launch_of(ResidualParams p, int threads, int device, cudaStream_t s) {
   static std::atomic<bool> done[64];
   if (device >= 64 || !done[device].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(residual_kernel<T, H, WARP_ROW, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(residual_kernel<T, H, LANES, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (device < 64) done[device].store(true, std::memory_order_release);
   }
   const int planes = sizeof(H) / 2 + (p.y ? 1 : 0) + (p.gate_kind == kGateRow && p.gate_stride ? 1 : 0);
   const int bytes = threads * N * planes * 16;  // of a stage
-  const int64_t blocks = WARP_ROW ? (p.rows + threads / 32 - 1) / (threads / 32) : p.rows;
+  const int at_once = LANES ? threads / (LANES ? LANES : 1) : 1;  // rows of a block
+  const int64_t blocks = (p.rows + at_once - 1) / at_once;
   const int sms = sm_count(device), resident = std::min(std::max(1024 / threads, 1), kSmem / bytes);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(std::max(sms, 1)) * resident));
   p.stages = std::min<int64_t>(std::min(kSmem / (resident * bytes), 3), (blocks + grid - 1) / grid);
-  return launch_pdl(residual_kernel<T, H, WARP_ROW, N>, dim3(grid), dim3(threads), p.stages * bytes, s, p);
+  return launch_pdl(residual_kernel<T, H, LANES, N>, dim3(grid), dim3(threads), p.stages * bytes, s, p);
 }
 
 template <typename T, typename H>
 cudaError_t launch_residual(const ResidualParams& p, int device, cudaStream_t s) {
-  // a warp holds rows of up to 512 elements; else as few threads as hold the row two pieces each, or four
-  if (p.vecs <= 32) return launch_of<T, H, true, 1>(p, 128, device, s);
-  if (p.vecs <= 64) return launch_of<T, H, true, 2>(p, 128, device, s);
-  if (p.vecs <= 1024) return launch_of<T, H, false, 2>(p, ((p.vecs + 1) / 2 + 31) / 32 * 32, device, s);
-  return launch_of<T, H, false, 4>(p, 512, device, s);
+  // A warp holds rows of up to 512 elements, or several shorter ones (67108864 elements with a gate per element, d = 64: a row to a warp
+  // 405 us, four 127; d = 120: 223, two 129); else a block does, two pieces to a thread, but one where two would leave more idle (d = 520:
+  // 195 us, 176; d = 768: 137, 125; with more than four warps the other way round, d = 2056: 139, 154), and three or four of long rows
+  // (d = 12288: three 137 us, four 143).
+  if (p.vecs <= 8) return launch_of<T, H, 8, 1>(p, 128, device, s);
+  if (p.vecs <= 16) return launch_of<T, H, 16, 1>(p, 128, device, s);
+  if (p.vecs <= 32) return launch_of<T, H, 32, 1>(p, 128, device, s);
+  if (p.vecs <= 64) return launch_of<T, H, 32, 2>(p, 128, device, s);
+  auto threads = [&](int n) { return ((p.vecs + n - 1) / n + 31) / 32 * 32; };
+  if (p.vecs <= 128 && threads(1) < 2 * threads(2)) return launch_of<T, H, 0, 1>(p, threads(1), device, s);
+  if (p.vecs <= 1024) return launch_of<T, H, 0, 2>(p, threads(2), device, s);
+  if (p.vecs <= 1536) return launch_of<T, H, 0, 3>(p, threads(3), device, s);
+  return launch_of<T, H, 0, 4>(p, 512, device, s);
 }
 
 }  // namespace
