@@ -133,7 +133,7 @@ cudaError_t launch_cross(const AttendParams& p, bool many, int device, cudaStrea
     const cudaError_t e = launch_rows<T, kDense, D>(p, device, s);
     if (e != cudaSuccess || p.row_ctas == 1 || p.row_whole) return e;
     const int jobs = (p.row_ctas - 1) * (p.item_rows / 32) * (D / 32);
-    return launch_pdl(join_rows<T, kDense, D>, dim3(std::min(jobs, 4 * p.row_ctas)), dim3(kWarps * 32), 0, s, p);  // (4 an SM are resident)
+    return launch_pdl(join_rows<T, kDense, D>, dim3(std::min(jobs, 3 * p.row_ctas)), dim3(kWarps * 32), 0, s, p);  // (3 an SM are resident)
   }
   const cudaError_t e =
       p.rows > 8 ? launch_attend<T, kDense, D, true, false>(p, device, s) : launch_attend<T, kDense, D, false, false>(p, device, s);

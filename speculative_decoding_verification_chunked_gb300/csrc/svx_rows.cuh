@@ -309,14 +309,17 @@ __device__ __forceinline__ int build_row_plan(const AttendParams& P, RowPlan& s,
   return total;
 }
 
-// The T tiles over the CTAs, as Split, but a single tile is enough for a CTA (5 tiles of an item: 9.4 us; two or four tiles to a CTA 9.9
-// and 11.5).
+// The T tiles over the CTAs, as Split.  Fewer CTAs have more to do, and leave the join fewer pieces: with up to 8 tiles each is a CTA's
+// (5 tiles of an item: 9.4 us; two or four to a CTA 9.9 and 11.5), else at least two (8 items of 16: single 15.7 us, two 13.9, four 14.6;
+// one of 32: 13.6, 12.6, 14.5), or four of long items (one of 128: 26.3, 19.6, 17.7; two of 79, d = 64: 28.0, 21.3, 17.0), until there
+// are three to each of all CTAs (8 items of 63: at least four 23.8 us, all CTAs 21.6).
 struct RowSplit {
   uint32_t used, q, r, total;
   float per_used;
   __device__ __forceinline__ RowSplit(const AttendParams& P, int T) {
     total = T;
-    used = min(total, static_cast<uint32_t>(P.row_ctas));
+    const uint32_t ctas = P.row_ctas, least = total <= 8 ? 1 : total <= 40 ? min(P.row_least, 2) : P.row_least;
+    used = total >= 3 * ctas ? ctas : min((total + least - 1) / least, ctas);
     q = used ? total / used : 0;
     r = total - q * used;
     per_used = __frcp_rn(static_cast<float>(used));
@@ -1022,10 +1025,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
 
 // Merges the pieces of the items that more than one CTA worked on, each of which crosses a boundary between CTAs first.  A job: such an
 // item, 32 of its rows and 32 dimensions; a CTA takes every nth.  A thread: a row (its lane) and four dimensions (its warp);
-// four pieces are fetched at a time with their states, and merged as they come.
+// eight pieces are fetched at a time with their states, and merged as they come (20 rows x 65536 keys of one item, 152 pieces: four at a
+// time and four CTAs an SM 52 us, 45; 8 items of 20 pieces 36.0 and 35.4).
 template <typename T, int SRC, int D>
-__global__ void __launch_bounds__(kWarps * 32, 4) join_rows(const __grid_constant__ AttendParams P) {
-  constexpr int AT_ONCE = 4, PARTS = D / 32;
+__global__ void __launch_bounds__(kWarps * 32, 3) join_rows(const __grid_constant__ AttendParams P) {
+  constexpr int AT_ONCE = 8, PARTS = D / 32;
   static_assert(kMaxCtas <= kWarps * 32, "a boundary for each thread");
   struct Item {
     int16_t b, pieces;
@@ -1104,7 +1108,8 @@ constexpr int kJoinTiles = 8, kJoinTilesLarge = 14;
 
 struct RowSizes {
   int32_t item_rows, ctas;
-  bool whole;  // no item is split over CTAs
+  int32_t least;  // tiles of a CTA (RowSplit)
+  bool whole;     // no item is split over CTAs
   size_t rows_o, rows_ml, total;
 };
 
@@ -1119,6 +1124,7 @@ inline void size_rows(RowSizes* z, int64_t items, int64_t per, int item_rows, in
   z->item_rows = item_rows;
   most = std::min(most, kMaxCtas);
   z->whole = may_whole && (items + most - 1) / most * per <= tiles / most + (item_rows * head_dim > 2 * kRowTile * 64 ? kJoinTilesLarge : kJoinTiles);
+  z->least = z->whole ? 1 : per >= 64 ? 4 : 2;
   z->ctas = static_cast<int32_t>(tiles ? std::min<int64_t>(most, tiles) : most);  // (without tiles: for the rows that have no keys)
   z->rows_o = up256(at);
   if (z->whole) {  // no pieces
@@ -1134,6 +1140,7 @@ inline void place_rows(AttendParams& p, const RowSizes& z, char* ws) {
   p.rows_ml = reinterpret_cast<float2*>(ws + z.rows_ml);
   p.item_rows = z.item_rows;
   p.row_ctas = z.ctas;
+  p.row_least = z.least;
   p.row_whole = z.whole;
   p.group_inverse = 1.f / static_cast<float>(p.group);
 }

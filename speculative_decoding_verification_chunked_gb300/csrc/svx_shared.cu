@@ -221,7 +221,8 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
                       static_cast<long long>(own + far), ct);
   const int64_t chunks = own + (out->many ? 0 : far);
   // With many rows the SMs are shared out over the two kernels by their work, so that they end together: a CTA of attend_kernel brings in
-  // some 45 GB/s of short sequences; a tile of rows_kernel takes 1.4 us with two row tiles, 1.0 with one.  (By the bounds known here: lengths
+  // some 45 GB/s of short sequences, and begins and ends an item in 0.18 us (84 requests of one slot each, 8 KV heads: 43 us without that
+  // term, 30); a tile of rows_kernel takes 1.4 us with two row tiles, 1.0 with one.  (By the bounds known here: lengths
   // may be shorter.)
   int own_ctas = sms;
   if (out->many) {
@@ -229,9 +230,9 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
     // d = 128: 64 and 60)
     const int item_rows = item_rows_for((all_rows + used - 1) / used);
     const int64_t items = c->n_kv_heads * (all_rows / item_rows + used), per = (max_prefix + kKeyTile - 1) / kKeyTile;
-    const double own_us = static_cast<double>(n_req) * c->n_kv_heads * max_len * c->head_dim * 4 / 45e3;
+    const double own_us = static_cast<double>(n_req) * c->n_kv_heads * max_len * c->head_dim * 4 / 45e3 + 0.18 * n_req * c->n_kv_heads * z.blocks;
     const double far_us = static_cast<double>(items) * per * (item_rows > kRowTile ? 1.4 : 1.0);
-    own_ctas = std::min(std::max(static_cast<int>(sms * own_us / (own_us + far_us) + 0.5), 4), sms - 4);
+    own_ctas = std::min(std::max(static_cast<int>(sms * own_us / (own_us + far_us) + 0.5), 8), sms - 4);
     // Where a prefix's rows are several items, as many CTAs as make the items' halves whole: then the CTAs of a KV head's items go
     // through the same keys at a time, and find them in L2 (256 requests behind 65536 slots, 32 such items: 107 CTAs 251 us, 112 233).
     const int64_t blocks = (all_rows + used * item_rows - 1) / (used * item_rows), half = c->n_kv_heads * used * blocks / 2;
