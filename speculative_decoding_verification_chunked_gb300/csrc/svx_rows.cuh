@@ -1103,8 +1103,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) join_rows(const __grid_constan
 
 // What splitting items over CTAs costs, their pieces written, read and joined, in tiles of a CTA: more where its pieces are 256 KiB
 // each.  (128 items of 16 tiles, two row tiles, d = 128: whole 31 us, split 46; 256 of 32: 95 and 103; d = 64, 256 of 12: 40 and 47;
-// 64 of 12: 21.8 and 21.4; 32 of 64 tiles: 89 and 39.)
-constexpr int kJoinTiles = 8, kJoinTilesLarge = 14;
+// 64 of 12: 21.8 and 21.4; 32 of 64 tiles: 89 and 39; one row tile, d = 128: 40 of 8: 16.6 and 17.8, 32 of 8: 16.5 and 15.1.)
+constexpr int kJoinTiles = 8, kJoinTilesLarge = 14, kJoinTilesOne = 6;
 
 struct RowSizes {
   int32_t item_rows, ctas;
@@ -1123,7 +1123,8 @@ inline void size_rows(RowSizes* z, int64_t items, int64_t per, int item_rows, in
   const int64_t tiles = items * per;
   z->item_rows = item_rows;
   most = std::min(most, kMaxCtas);
-  z->whole = may_whole && (items + most - 1) / most * per <= tiles / most + (item_rows * head_dim > 2 * kRowTile * 64 ? kJoinTilesLarge : kJoinTiles);
+  const int join = item_rows == kRowTile ? kJoinTilesOne : head_dim == 128 ? kJoinTilesLarge : kJoinTiles;
+  z->whole = may_whole && (items + most - 1) / most * per <= tiles / most + join;
   z->least = z->whole ? 1 : per >= 64 ? 4 : 2;
   z->ctas = static_cast<int32_t>(tiles ? std::min<int64_t>(most, tiles) : most);  // (without tiles: for the rows that have no keys)
   z->rows_o = up256(at);
