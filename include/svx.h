@@ -722,7 +722,7 @@ svx_status svx_cross_attn(const svx_cross* c, void* workspace, int64_t workspace
 #define SVX_GATE_SCALAR 1
 #define SVX_GATE_CHANNEL 2
 #define SVX_GATE_ELEMENT 3
-/* svx_residual.act: what the gate goes through. */
+/* svx_residual.act: what the gate goes through (SVX_ACT_NONE where there is none). */
 #define SVX_ACT_NONE 0
 #define SVX_ACT_TANH 1
 #define SVX_ACT_SIGMOID 2

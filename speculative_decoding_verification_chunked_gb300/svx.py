@@ -863,7 +863,7 @@ _ACTS = {None: 0, "tanh": 1, "sigmoid": 2}
 
 
 def residual_norm(h, y=None, h_out=None, x_out=None, norm=None, eps: float = 1e-6, post_norm=None,
-                  post_eps: Optional[float] = None, gate=None, act: Optional[str] = None, alpha: float = 1.0,
+                  post_eps: Optional[float] = None, gate=..., act: Optional[str] = None, alpha: float = 1.0,
                   beta: float = 1.0, stream=None):
     """svx_residual_norm: the residual stream between two blocks.
 
@@ -873,13 +873,18 @@ def residual_norm(h, y=None, h_out=None, x_out=None, norm=None, eps: float = 1e-
     y (the block's output) and x_out (the next block's input): device bf16 or fp16 [..., dim]; h and h_out (the residual stream): of that
     type or fp32, the same shape.  Rows dense, evenly spaced over the leading dimensions; dim a multiple of 8 up to 16384.
     norm, post_norm: [dim] of y's type, or None: ones.  post_eps None: no norm after the block.  gate: [1], [dim] or of y's
-    shape, y's type; act: None, "tanh" or "sigmoid" of it.  y None: no block, x_out is the norm of alpha h.  h_out or
-    x_out may be None; h_out may be h and x_out may be y."""
+    shape, y's type; act: None, "tanh" or "sigmoid" of it.  gate None: no gate, and act, whichever it is, has nothing to work on (a layer
+    whose gate is optional passes both); act where no gate is passed at all is refused.  y None: no block, x_out is the norm of
+    alpha h.  h_out or x_out may be None; h_out may be h and x_out may be y."""
     if stream is not None:
         with _on_stream(stream, h.get_device()):
             return residual_norm(h, y, h_out, x_out, norm, eps, post_norm, post_eps, gate, act, alpha, beta)
     if act not in _ACTS:
         raise SvxError(ERR_INVALID_ARG, f"act: {act!r}, expected None, 'tanh' or 'sigmoid'")
+    if gate is None:
+        act = None
+    elif gate is ...:
+        gate = None
     (_native_module or _native()).residual_norm(h, y, h_out, x_out, norm, eps, post_norm, post_eps, gate, _ACTS[act], alpha, beta)
 
 
