@@ -357,8 +357,7 @@ def run(s):
         s["svx"].cross_attn(s["q"], s["k"], s["v"], s["o"], s["lse"], lens=s["lens"], mask=s["mask"])
         return {"o": s["o"], "lse": s["lse"]}
     s["svx"].residual_norm(s["h"], s["y"], s["h_out"], s["x"], norm=s["norm"], eps=EPS, post_norm=s["post_norm"],
-                           post_eps=EPS if c["post"] else None, gate=s["gate"],
-                           act=None if s["gate"] is None or c["act"] == "none" else c["act"],
+                           post_eps=EPS if c["post"] else None, gate=s["gate"], act=None if c["act"] == "none" else c["act"],
                            alpha=c["alpha"], beta=c["beta"])
     return {"h": s["h_out"], "x": s["x"]}
 
