@@ -433,8 +433,13 @@ PyObject* cross_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     rows_dense(v, "v");
     rows_dense(o, "o");
     if (o.sizes() != q.sizes()) refuse(SVX_ERR_INVALID_ARG, "o: " + describe(o) + ", expected q's shape");
-    if (v.sizes() != k.sizes() || v.strides() != k.strides())
-      refuse(SVX_ERR_INVALID_ARG, "v: " + describe(v) + ", expected k's shape and strides: " + describe(k));
+    bool alike = v.sizes() == k.sizes();
+    for (int64_t i = 0; alike && i < 3; ++i) alike = k.size(i) <= 1 || v.stride(i) == k.stride(i);  // (one entry: never stepped over)
+    if (!alike) {
+      std::ostringstream s;
+      s << "v: " << describe(v) << ", strides " << v.strides() << "; expected k's shape and strides: " << describe(k) << ", strides " << k.strides();
+      refuse(SVX_ERR_INVALID_ARG, s.str());
+    }
     if (k.size(0) != q.size(0) || k.size(3) != q.size(3))
       refuse(SVX_ERR_INVALID_ARG, "k: " + describe(k) + ", expected [requests, states, KV heads, head_dim] of q's requests and head_dim");
     c.n_req = static_cast<int32_t>(q.size(0));

@@ -847,7 +847,7 @@ def qk_norm_rope(q, k, v, pos, rope: Rope, q_out, k_out, v_out=None, q_norm=None
 def cross_attn(q, k, v, o, lse=None, lens=None, mask=None, scale: float = 0.0, status=None, workspace=None, stream=None):
     """svx_cross_attn: tokens of a decoder attend to an encoder's states, of another length and in no order.
 
-    q, o: device bf16 or fp16 [B][Hq][n][d]; k, v: [B][S][Hkv][d], equally strided; rows of d dense, the other dimensions in any
+    q, o: device bf16 or fp16 [B][Hq][n][d]; k, v: [B][S][Hkv][d], equally strided (but in dimensions of one entry); rows of d dense, the other dimensions in any
     order (transposed views of projections; all but o may be broadcast).  n from a single token up; S may be 0.  lse: fp32
     [B][Hq][n], or None.  lens: int32 [B], states of each request that count (None: all); mask: bool [B][S], False: a state that does
     not count; what such states hold is not used.  O = 0, LSE = -inf where none counts.  scale: 0 means 1/sqrt(d).  status: int32 [1]
