@@ -616,8 +616,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       auto look = [&](int t) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int key = (g.tile0 + t) * kKeyTile + u * 32 + lane;
-          page[u] = t < g.n && key < g.len ? __ldg(table + page_of(P.pages, static_cast<uint32_t>(key))) : 0;
+          const uint32_t key = static_cast<uint32_t>(g.tile0 + t) * kKeyTile + u * 32 + lane;  // (behind the last tile: up to 2^31 + 127)
+          page[u] = t < g.n && key < static_cast<uint32_t>(g.len) ? __ldg(table + page_of(P.pages, key)) : 0;
         }
       };
       if constexpr (SRC == kShared) look(0);
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       float m = kNegInf, l = 0.f;
       for (int i = 0; i < mine && ok; ++i, ++ns) {
         const int t0 = (g.tile0 + (two ? i : 2 * i + s)) * kKeyTile;
-        const bool all = (SRC != kDense || !P.mask) && t0 + kKeyTile <= g.len;
+        const bool all = (SRC != kDense || !P.mask) && t0 <= g.len - kKeyTile;  // (t0 + kKeyTile can be 2^31)
         Seen seen = {};
         if (!all) seen = keys_seen<SRC>(P, g, t0);
         if (!W.warp_wait(SFULL + 8u * s, ns & 1u)) {
