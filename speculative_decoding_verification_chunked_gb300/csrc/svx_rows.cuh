@@ -31,7 +31,8 @@
 // 16 heads of d = 64: 68 us, of which the bytes are 20).  There leaving out the chunks of 32 keys behind a length gained 0 to 4%, and
 // cost full tiles 3 to 5%; P beside S in tensor memory, so that S(i + 2) need not wait for P V(i), gained nothing at d = 64.
 //
-// Every wait is bounded (2 s of global time): one that gives up raises the status word and makes all roles stop, drain and leave.
+// Every wait is bounded (2 s of global time; that for a segment's last product with Q, which a segment of many keys takes longer to reach, 2 s
+// without a new tile): one that gives up raises the status word and makes all roles stop, drain and leave.
 #pragma once
 
 #include "svx_attend.cuh"
@@ -64,7 +65,7 @@ struct RowsCfg {
   static constexpr uint32_t OFF_ML = OFF_OUT + 8 * 2048;  // float2 [2][128]: the streams' states at a segment's end
   static constexpr int N_BAR = 2 * KST + 2 * VST + 2 * QST + 4 * 2 + 1;
   static constexpr uint32_t OFF_BAR = OFF_ML + 2 * kRowTile * 8;
-  static constexpr uint32_t OFF_MISC = OFF_BAR + N_BAR * 8;  // [0] TMEM base, [1] abort flag
+  static constexpr uint32_t OFF_MISC = OFF_BAR + N_BAR * 8;  // [0] TMEM base, [1] abort flag, [2] K tiles begun
   static constexpr uint32_t BYTES = OFF_MISC + 16;
   static constexpr uint32_t SMEM = BYTES + 1024;  // slack to align the base to 1024 bytes
   static constexpr uint32_t TMEM_COLS = 512;
@@ -419,7 +420,7 @@ __device__ __forceinline__ RowOut row_out(const AttendParams& P, const RowPlan& 
 }
 
 struct RowWaiter {
-  volatile uint32_t* abort;
+  volatile uint32_t* abort;  // [1]: K tiles begun
   int* status;
   __device__ __forceinline__ void give_up() {
     *abort = 1u;
@@ -427,6 +428,25 @@ struct RowWaiter {
   }
   // (a converged warp stays so: all lanes' results are the same)
   __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); }
+  // For Q's place, which is free once all of a segment's tiles have met it: the limit runs from the last tile begun.
+  __device__ __forceinline__ bool warp_wait_q(uint32_t bar, uint32_t parity) {
+    bool ok = bar_try(bar, parity);
+    uint64_t t0 = ok ? 0 : now_ns();
+    uint32_t tiles = abort[1];
+    for (uint32_t it = 1; !ok; ++it) {
+      ok = bar_try(bar, parity);
+      if (ok || (it & 63u) != 0) continue;
+      if (*abort) break;
+      if (abort[1] != tiles) {
+        tiles = abort[1];
+        t0 = now_ns();
+      } else if (now_ns() - t0 > kWaitLimit) {
+        give_up();
+        break;
+      }
+    }
+    return __all_sync(0xffffffffu, ok);
+  }
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
     if (bar_try(bar, parity)) return true;
     const uint64_t t0 = now_ns();
@@ -548,7 +568,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       bar_init(OEMPTY + 8u * i, 128);
     }
     bar_init(DRAIN, 1);
-    misc[1] = 0u;
+    misc[1] = misc[2] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -624,6 +644,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       for (int t = 0; t < g.n; ++t, ++i) {
         const int t0 = (g.tile0 + t) * kKeyTile;
         const int stage = i % stages;
+        if (!is_v && lane == 0) misc[2] = i;
         const uint32_t dst = ring + stage * C::TILE;
         const Seen seen = keys_seen<SRC>(P, g, t0);
         const bool all = (seen.w[0] & seen.w[1] & seen.w[2] & seen.w[3]) == 0xffffffffu;
@@ -721,7 +742,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       const uint32_t full = QFULL + 8u * buf;
       uint32_t dst = base + C::OFF_Q + buf * (QT * C::Q_TILE);
       if (P.q_box) {
-        if (seg >= C::QST && !W.warp_wait(QEMPTY + 8u * buf, (seg / C::QST - 1) & 1u)) break;
+        if (seg >= C::QST && !W.warp_wait_q(QEMPTY + 8u * buf, (seg / C::QST - 1) & 1u)) break;
         const int boxes = (QT == 2 && g.rows > kRowTile ? 2 : 1) * (D / 64);
         if (lane == 0) arrive_expecting(full, boxes * kHalf);
         __syncwarp();
@@ -739,7 +760,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       int64_t off[QT * 4];
 #pragma unroll
       for (int u = 0; u < QT * 4; ++u) off[u] = u * 32 + lane < g.rows ? row_q<SRC, D>(P, plan, g, u * 32 + lane) : -1;
-      if (seg >= C::QST && !W.warp_wait(QEMPTY + 8u * buf, (seg / C::QST - 1) & 1u)) break;
+      if (seg >= C::QST && !W.warp_wait_q(QEMPTY + 8u * buf, (seg / C::QST - 1) & 1u)) break;
 #pragma unroll
       for (int u = 0; u < QT * 4; ++u) {
         if (QT == 2 && u >= 4 && g.rows <= kRowTile) break;
