@@ -979,7 +979,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         const int c0 = two ? 0 : s * (D / 2), c1 = two ? D : c0 + D / 2;
         RowOut at{0, 0};
         if (mine_too) at = row_out<SRC, D>(P, plan, g, r);
-        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int c = c0; c < c1; c += 32) {
           float o[32];
@@ -1028,7 +1028,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         if (mine_too && (two || s == 0)) {
           if (!whole) P.rows_ml[static_cast<int64_t>(slot) * P.item_rows + r] = make_float2(m, l);
           else if (SRC == kShared) P.state_ml[at.lse] = make_float2(m, l);
-          else if (P.lse) P.lse[at.lse] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
+          else if (P.lse) P.lse[at.lse] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
         }
         tc_before();
       }
