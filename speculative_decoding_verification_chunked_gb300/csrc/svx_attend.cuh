@@ -92,6 +92,8 @@ struct AttendParams {
   // of rows_kernel (svx_rows.cuh)
   float4* rows_o;               // [row_ctas][2][D / 4][item_rows]: states of items that more than one CTA works on
   float2* rows_ml;              // [row_ctas][2][item_rows]
+  float4* row_sums;             // [row_ctas][2 streams][D / 4][128 rows]: of long segments (rows_kernel's kSumTiles)
+  float* row_refs;              // [row_ctas][2][128]: what they are relative to
   int32_t item_rows, row_ctas, row_least;
   int32_t row_whole;            // items are not split over CTAs
   float group_inverse;          // 1 / group

@@ -23,6 +23,10 @@
 // O is then as exact as with fp32 weights.  Where there are more than 128 rows to the same keys (of prefixes: on average) the products
 // bound the time, and P is rounded once: a weight is off by up to 2^-8 (bf16) or 2^-11 (fp16) of itself.
 //
+// Long sums.  The tensor cores drop from each product what lies some 26 bits below the sum that it joins: where V is positive, O lost 2^-27 of
+// itself a key (0.08% of 131072 keys in one segment, 2.6% of 4 million, half of 2^27).  So every kSumTiles tiles a stream's O goes to memory,
+// where it is added up in fp32, and begins anew: the loss is that of 32768 keys, 2^-12, half of what rounding O to fp16 may take.
+//
 // What bounds it.  Two row tiles, d = 128: the products; 8192 x 16384 tokens of 32 heads 1204 us = 1827 TFLOP/s, 95% of the measured cuBLAS
 // rate.  d = 64: half the products to the same softmax, whose own steps decide (2 x 2048 x 4096 tokens of 16 heads: the tensor
 // pipe busy for 39%, the exponentials' for 39%, 43% of the issue slots).  One row tile: the bytes of K and V (16 samples behind 32768
@@ -48,6 +52,7 @@ constexpr int kRowTile = 128;
 constexpr uint32_t kHalf = kKeyTile * 128;      // bytes of 64 dimensions of 128 rows (an operand's swizzle atoms: 8 rows of 128 bytes)
 constexpr uint64_t kWaitLimit = 2000000000ull;
 constexpr int kRowThreads = 384;
+constexpr int kSumTiles = 256;  // that a stream adds up in tensor memory (a power of two)
 
 // QT: row tiles of an item, 1 or 2.
 template <int D, int QT>
@@ -504,6 +509,47 @@ __device__ __noinline__ void scale_columns(uint32_t at, int n, float f) {
     tmem_write32(at + c, v);
   }
 }
+// A stream's O of this thread's row, in tensor memory, and what it had before that is in memory: a column's quad every kRowTile, relative to
+// 2^ref.  Moves O there (first: there was nothing), or brings it back on top of O.  (Out of line, addresses and all.)
+template <int D>
+__device__ __noinline__ void put_sums(uint32_t at, float4* sums, float* ref, float m, bool first) {
+  const int stream = blockIdx.x * 2 + threadIdx.x / kRowTile, row = threadIdx.x % kRowTile;
+  sums += static_cast<int64_t>(stream) * (D / 4) * kRowTile + row;
+  ref += stream * kRowTile + row;
+  const float f = first || m == kNegInf ? 0.f : ex2(*ref - m);  // (no key so far: zeros)
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tmem_read32<0>(at + c, o);
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      float4* const to = sums + (c + k) / 4 * kRowTile;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!first) x = *to;
+      *to = make_float4(fmaf(x.x, f, o[k]), fmaf(x.y, f, o[k + 1]), fmaf(x.z, f, o[k + 2]), fmaf(x.w, f, o[k + 3]));
+    }
+  }
+  *ref = m;
+}
+template <int D>
+__device__ __noinline__ void take_sums(uint32_t at, const float4* sums, const float* ref, float m) {
+  const int stream = blockIdx.x * 2 + threadIdx.x / kRowTile, row = threadIdx.x % kRowTile;
+  sums += static_cast<int64_t>(stream) * (D / 4) * kRowTile + row;
+  ref += stream * kRowTile + row;
+  const float f = m == kNegInf ? 0.f : ex2(*ref - m);
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tmem_read32<0>(at + c, o);
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float4 x = sums[(c + k) / 4 * kRowTile];
+      o[k] = fmaf(x.x, f, o[k]), o[k + 1] = fmaf(x.y, f, o[k + 1]), o[k + 2] = fmaf(x.z, f, o[k + 2]), o[k + 3] = fmaf(x.w, f, o[k + 3]);
+    }
+    tmem_write32(at + c, o);
+  }
+  tmem_written();
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -821,7 +867,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         const uint32_t a = tmem + s * 128, d = tmem + C::O_COL + s * D;
         const uint32_t b = desc_of(base + C::OFF_V, kHalf) + vt * (C::TILE >> 4);
 #pragma unroll
-        for (int k = 0; k < kKeyTile / 16; ++k) mma_ts(one, d, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 2048) >> 4), idesc_o, u > 1 || k > 0);
+        for (int k = 0; k < kKeyTile / 16; ++k)
+          mma_ts(one, d, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 2048) >> 4), idesc_o, (u >> 1) % kSumTiles != 0 || k > 0);
         if constexpr (QT == 1) {
 #pragma unroll
           for (int k = 0; k < kKeyTile / 16; ++k) mma_ts(one, d, a + (k >> 1) * 32 + 16 + (k & 1) * 8, b + ((k * 2048) >> 4), idesc_o, true);
@@ -874,6 +921,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
         }
         if (busy) {
           tc_after();
+          if (i % kSumTiles == 0 && i > 0) put_sums<D>(tmem + lanes + C::O_COL + s * D, P.row_sums, P.row_refs, m, i == kSumTiles);  // (O holds all up to i - 1)
           const bool some = !all && (seen.w[0] & seen.w[1] & seen.w[2] & seen.w[3]) != ~0u;
           if (QT == 1 && some) hide_keys(at_s, seen);
           const uint64_t scale2 = pair(P.scale, P.scale);
@@ -951,6 +999,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       const bool whole = g.tile0 == 0 && g.first + g.n == g.end;
       const int slot = blockIdx.x * 2 + (g.tile0 == 0 ? 1 : 0);
       const bool other = !two && steps > 1;  // the same rows' other half
+      if (mine > kSumTiles && ok) {
+        ok = W.warp_wait(OFULL + 8u * s, no[s] & 1u);
+        if (ok && busy) {
+          tc_after();
+          take_sums<D>(tmem + lanes + C::O_COL + s * D, P.row_sums, P.row_refs, m);
+          tc_before();
+        }
+      }
       if (!two) {
         if (mine > 0) s_ml[s * kRowTile + row] = make_float2(m, l);
         ok = softmax_sync(ok);
@@ -1131,7 +1187,7 @@ struct RowSizes {
   int32_t item_rows, ctas;
   int32_t least;  // tiles of a CTA (RowSplit)
   bool whole;     // no item is split over CTAs
-  size_t rows_o, rows_ml, total;
+  size_t rows_o, rows_ml, sums, refs, total;
 };
 
 // Rows of an item where the rows with the same keys are at most `rows`.
@@ -1148,18 +1204,18 @@ inline void size_rows(RowSizes* z, int64_t items, int64_t per, int item_rows, in
   z->whole = may_whole && (items + most - 1) / most * per <= tiles / most + join;
   z->least = z->whole ? 1 : per >= 64 ? 4 : 2;
   z->ctas = static_cast<int32_t>(tiles ? std::min<int64_t>(most, tiles) : most);  // (without tiles: for the rows that have no keys)
+  const size_t rows = static_cast<size_t>(z->ctas) * 2 * z->item_rows, sums = per > kSumTiles ? static_cast<size_t>(z->ctas) * 2 * kRowTile : 0;
   z->rows_o = up256(at);
-  if (z->whole) {  // no pieces
-    z->rows_ml = z->rows_o;
-    z->total = z->rows_o + 256;
-    return;
-  }
-  z->rows_ml = z->rows_o + static_cast<size_t>(z->ctas) * 2 * z->item_rows * head_dim * 4;
-  z->total = z->rows_ml + up256(static_cast<size_t>(z->ctas) * 2 * z->item_rows * 8);
+  z->rows_ml = z->rows_o + (z->whole ? 0 : rows * head_dim * 4);  // (whole items leave no pieces)
+  z->sums = z->rows_ml + (z->whole ? 0 : up256(rows * 8));
+  z->refs = z->sums + sums * head_dim * 4;
+  z->total = std::max(z->refs + sums * 4, z->rows_o + 256);
 }
 inline void place_rows(AttendParams& p, const RowSizes& z, char* ws) {
   p.rows_o = reinterpret_cast<float4*>(ws + z.rows_o);
   p.rows_ml = reinterpret_cast<float2*>(ws + z.rows_ml);
+  p.row_sums = reinterpret_cast<float4*>(ws + z.sums);
+  p.row_refs = reinterpret_cast<float*>(ws + z.refs);
   p.item_rows = z.item_rows;
   p.row_ctas = z.ctas;
   p.row_least = z.least;

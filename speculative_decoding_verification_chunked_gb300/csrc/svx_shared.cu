@@ -250,6 +250,8 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
   if (out->many) {
     out->rz.rows_o += z.total;
     out->rz.rows_ml += z.total;
+    out->rz.sums += z.total;
+    out->rz.refs += z.total;
     z.total += out->rz.total;
   }
   return SVX_OK;
