@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     constexpr int PIECES = D / 8, RPI = 32 / PIECES;  // a row's pieces of 16 bytes; rows that a warp copies at a time
     const int piece = lane % PIECES, r0 = lane / PIECES;
     const CUtensorMap* const map = is_v ? &P.v_map : &P.k_map;
-    const bool maps = !kBoundsChecked && P.box > 0;
+    const bool maps = P.box > 0;
     const int box = maps ? P.box : kKeyTile;
     if (maps && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
     int i = 0;
@@ -702,30 +702,36 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
           boxes = boxes && __all_sync(0xffffffffu, static_cast<uint32_t>(page[0]) < n && static_cast<uint32_t>(page[1]) < n &&
                                                        static_cast<uint32_t>(page[2]) < n && static_cast<uint32_t>(page[3]) < n);
         }
-        if (boxes) {  // a tile whose keys all count: in boxes, one or more a lane
-          const int runs = kKeyTile / box;
-          // lane l: half l / runs of the dimensions, run l % runs
-          const int run = lane % runs, key = run * box;
-          int w = g.b * P.page_step, z = t0;
+        // in boxes, one or more a lane.  Lane l: half l / runs of the dimensions, run l % runs
+        const int runs = kKeyTile / box, half = lane / runs, key = lane % runs * box;
+        int w = g.b * P.page_step, z = t0;
+        if (boxes) {
           if constexpr (SRC == kShared) {
             const int32_t p01 = __shfl_sync(0xffffffffu, page[0], key & 31), p1 = __shfl_sync(0xffffffffu, page[1], key & 31),
                           p2 = __shfl_sync(0xffffffffu, page[2], key & 31), p3 = __shfl_sync(0xffffffffu, page[3], key & 31);
             w = key < 64 ? (key < 32 ? p01 : p1) : key < 96 ? p2 : p3;
             z = t0 + key - page_of(P.pages, static_cast<uint32_t>(t0 + key)) * P.pages.page_size;
-            look(t + 1);
           }
+          if constexpr (kBoundsChecked) {  // (its first and last row: where one is outside, row by row, which finds it again and reports it)
+            const T* const from = pool + w * P.pages.page_stride + g.h * P.pages.head_stride + z * P.pages.tok_stride;
+            const bool in = in_bounds(from, D, pool, P.pages.extent, nullptr, kSitePool) &&
+                            in_bounds(from + (box - 1) * P.pages.tok_stride, D, pool, P.pages.extent, nullptr, kSitePool);
+            boxes = __all_sync(0xffffffffu, in || half >= D / 64);
+          }
+        }
+        if (boxes) {
+          if constexpr (SRC == kShared) look(t + 1);
           if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
             ok = false;
             break;
           }
           if (lane == 0) arrive_expecting(full + 8u * stage, C::TILE);
           __syncwarp();
-          const int half = lane / runs;
           if (half < D / 64) bring_box(dst + half * kHalf + key * 128, map, half * 64, g.h * P.head_step, z, w, full + 8u * stage);
           if (lane != 0) bar_arrive(full + 8u * stage);
           continue;
         }
-        if constexpr (SRC == kDense && !kBoundsChecked) {  // rows a stride apart
+        if constexpr (SRC == kDense) {  // rows a stride apart
           const T* from = pool + g.b * P.pages.page_stride + g.h * P.pages.head_stride + (t0 + r0) * P.pages.tok_stride + piece * 8;
           if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
             ok = false;
@@ -736,7 +742,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
 #pragma unroll 8
             for (int j = 0; j < 32 / RPI; ++j, from += RPI * P.pages.tok_stride) {
               const int in32 = j * RPI + r0, r = u * 32 + in32;
-              const bool is = seen.w[u] >> in32 & 1u;
+              const bool is = (seen.w[u] >> in32 & 1u) != 0 && in_bounds(from, 8, pool, P.pages.extent, P.pages.status, kSitePool);
               copy16(dst + (piece >> 3) * kHalf + r * 128 + (((piece & 7) ^ (r & 7)) << 4), is ? from : pool, is ? 16 : 0);
             }
         } else {
@@ -746,16 +752,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
             off[u] = -1;
             const int key = t0 + u * 32 + lane;
             if (!(seen.w[u] >> lane & 1u)) continue;
-            if constexpr (SRC == kShared) {
-              off[u] = slot_offset(P.pages, page[u], key - page_of(P.pages, static_cast<uint32_t>(key)) * P.pages.page_size);
-              if (off[u] < 0) atomicOr(P.pages.status, kErrInput);
-            } else {
-              off[u] = g.b * P.pages.page_stride + key * P.pages.tok_stride;
-            }
+            off[u] = slot_offset(P.pages, page[u], key - page_of(P.pages, static_cast<uint32_t>(key)) * P.pages.page_size);
+            if (off[u] < 0) atomicOr(P.pages.status, kErrInput);
             if (off[u] >= 0) off[u] += g.h * P.pages.head_stride;
             if (off[u] >= 0 && !in_bounds(pool + off[u], D, pool, P.pages.extent, P.pages.status, kSitePool)) off[u] = -1;
           }
-          if constexpr (SRC == kShared) look(t + 1);
+          look(t + 1);
           if (i >= stages && !W.warp_wait(empty + 8u * stage, (i / stages - 1) & 1u)) {
             ok = false;
             break;
