@@ -675,6 +675,11 @@ svx_status svx_paged_evict(const svx_pages* cache, int32_t n_req, const int32_t*
  * 1: 2^18, 2: 2^19) of the status word; in libsvx.so nothing changes. */
 svx_status svx_debug_clip_paged(int32_t buffer, int64_t elements);
 
+/* Test hook: until it is called again with 0, a wait in every CTA of this thread's svx_cross_attn and svx_paged_decode_shared calls of
+ * many rows runs out after a millisecond, as one does after two seconds in which nothing moves: bit 1 of the status word, and NaN in the
+ * rows that these CTAs had to do. */
+svx_status svx_debug_expire_rows(int32_t on);
+
 /* ---- attention to an encoder's states -------------------------------------------------------- */
 
 /* n_tok tokens of each of n_req requests against n_states states of each.  Row (b, h, j) of q is at b * q_req + h * q_head + j * q_tok
@@ -689,7 +694,8 @@ typedef struct {
   float* lse;              /* device [n_req][n_q_heads][n_tok], or NULL */
   const int32_t* len;      /* device [n_req]: only the first len[b] states of a request count, 0..n_states; NULL: all */
   const uint8_t* mask;     /* device, state t of request b at b * mask_req + t: 0: it does not count; NULL: all do */
-  int32_t* status;         /* device status word (as in svx_pages), or NULL; also raised if a bounded wait of the kernel gave up */
+  int32_t* status;         /* device status word (as in svx_pages), or NULL; also raised if a bounded wait of the kernel
+                            * gave up, which leaves NaN in the rows that wait was for */
   int64_t q_req, q_head, q_tok;
   int64_t kv_req, kv_head, kv_state;
   int64_t o_req, o_head, o_tok;

@@ -96,6 +96,7 @@ struct AttendParams {
   float* row_refs;              // [row_ctas][2][128]: what they are relative to
   int32_t item_rows, row_ctas, row_least;
   int32_t row_whole;            // items are not split over CTAs
+  int32_t expire;               // test hook: a wait is made to run out
   float group_inverse;          // 1 / group
 };
 

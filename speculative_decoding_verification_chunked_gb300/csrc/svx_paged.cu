@@ -99,7 +99,10 @@ svx_status paged_view(const svx_pages* c, int32_t n_req, PageView* out) {
 
 namespace {
 thread_local int64_t t_clip[kClips] = {-1, -1, -1};
+thread_local bool t_expire = false;
 }
+
+bool expire_waits() { return t_expire; }
 
 int64_t clipped(PagedBuffer kind, int64_t extent) {
   return t_clip[kind] >= 0 && t_clip[kind] < extent ? t_clip[kind] : extent;
@@ -169,6 +172,11 @@ static uint64_t turn_fraction(double f) {
 extern "C" svx_status svx_debug_clip_paged(int32_t buffer, int64_t elements) {
   if (buffer < 0 || buffer >= svx::kClips) return svx::paged_fail(SVX_ERR_INVALID_ARG, "buffer must be 0, 1 or 2");
   svx::t_clip[buffer] = elements < 0 ? -1 : elements;
+  return SVX_OK;
+}
+
+extern "C" svx_status svx_debug_expire_rows(int32_t on) {
+  svx::t_expire = on != 0;
   return SVX_OK;
 }
 

@@ -78,6 +78,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // svx_debug_clip_paged: the most elements that this thread's calls describe a buffer of a kind as holding.
 enum PagedBuffer : int { kClipInputs = 0, kClipOutputs = 1, kClipPool = 2, kClips = 3 };
 int64_t clipped(PagedBuffer kind, int64_t extent);
+// svx_debug_expire_rows: whether this thread's calls let a wait of rows_kernel run out.
+bool expire_waits();
 
 // Host side, shared by the entry points (svx_paged.cu).
 svx_status paged_fail(svx_status st, const char* fmt, ...);

@@ -36,7 +36,8 @@
 // cost full tiles 3 to 5%; P beside S in tensor memory, so that S(i + 2) need not wait for P V(i), gained nothing at d = 64.
 //
 // Every wait is bounded (2 s of global time; that for a segment's last product with Q, which a segment of many keys takes longer to reach, 2 s
-// without a new tile): one that gives up raises the status word and makes all roles stop, drain and leave.
+// without a new tile): one that gives up raises the status word and makes all roles stop, drain and leave; the rows that the CTA had to do become
+// NaN, since there may be no status word.
 #pragma once
 
 #include "svx_attend.cuh"
@@ -50,7 +51,7 @@ namespace {
 
 constexpr int kRowTile = 128;
 constexpr uint32_t kHalf = kKeyTile * 128;      // bytes of 64 dimensions of 128 rows (an operand's swizzle atoms: 8 rows of 128 bytes)
-constexpr uint64_t kWaitLimit = 2000000000ull;
+constexpr uint64_t kWaitLimit = 2000000000ull;  // ns
 constexpr int kRowThreads = 384;
 constexpr int kSumTiles = 256;  // that a stream adds up in tensor memory (a power of two)
 
@@ -476,6 +477,15 @@ struct RowWaiter {
       }
   }
 };
+
+// The test hook: a wait on a barrier on which nothing arrives before the products have ended, for a millisecond.
+__device__ __noinline__ bool run_out(RowWaiter w, uint32_t bar) {
+  const uint64_t t0 = now_ns();
+  while (now_ns() - t0 < 1000000ull)
+    if (bar_try(bar, 0u)) return true;  // (a CTA without work)
+  w.give_up();
+  return false;
+}
 
 // Which keys of a tile count, bit r % 32 of word r / 32; a warp's lanes together.
 struct Seen {
@@ -904,7 +914,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
     float2* const s_ml = reinterpret_cast<float2*>(gbase + C::OFF_ML);
     uint4* const out = reinterpret_cast<uint4*>(gbase + C::OFF_OUT) + warp * 128;
     uint32_t ns = 0, no[2] = {0, 0};  // S's of this stream, and ends of both, so far
-    bool ok = true;  // (once a wait has given up, all that follows is left out, but for the barriers of all softmax threads)
+    bool ok = !P.expire || run_out(W, DRAIN);  // (once a wait has given up, all that follows is left out, but for the barriers of all softmax threads)
     for (int x = x0; x < x1;) {
       const RowSeg g = row_seg<SRC>(P, plan, x, x1);
       const bool two = QT == 2 && g.rows > kRowTile;
@@ -1020,7 +1030,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
       }
       ++no[0];
       if (two || other) ++no[1];
-      if (ok && busy) {
+      if (busy) {
         tc_after();
         // two row blocks: all of this stream's columns; one: half of the columns, of both streams
         float f0 = 1.f, f1 = 0.f;
@@ -1032,6 +1042,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const __grid_const
           f1 = ex2(b.x + less);
           l = a.y * f0 + b.y * f1;
         }
+        if (!ok) l = f0 = __int_as_float(0x7fffffff);  // a wait gave up: whatever is in O, the row becomes NaN, here or where it is joined
         const bool mine_too = row < my_rows;
         const int r = two ? s * kRowTile + row : row;
         const int c0 = two ? 0 : s * (D / 2), c1 = two ? D : c0 + D / 2;
@@ -1222,6 +1233,7 @@ inline void place_rows(AttendParams& p, const RowSizes& z, char* ws) {
   p.row_ctas = z.ctas;
   p.row_least = z.least;
   p.row_whole = z.whole;
+  p.expire = expire_waits();
   p.group_inverse = 1.f / static_cast<float>(p.group);
 }
 

@@ -229,6 +229,7 @@ _SIGS = {
     "svx_cross_attn": (ctypes.c_int, [ctypes.POINTER(Cross), _P, ctypes.c_int64, _P]),
     "svx_residual_norm": (ctypes.c_int, [ctypes.POINTER(Residual), _P]),
     "svx_debug_clip_paged": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64]),
+    "svx_debug_expire_rows": (ctypes.c_int, [ctypes.c_int32]),
     "svx_version": (ctypes.c_char_p, []),
     "svx_abi_sizes": (ctypes.c_int32, [ctypes.POINTER(ctypes.c_int64), ctypes.c_int32]),
 }
@@ -851,7 +852,8 @@ def cross_attn(q, k, v, o, lse=None, lens=None, mask=None, scale: float = 0.0, s
     order (transposed views of projections; all but o may be broadcast).  n from a single token up; S may be 0.  lse: fp32
     [B][Hq][n], or None.  lens: int32 [B], states of each request that count (None: all); mask: bool [B][S], False: a state that does
     not count; what such states hold is not used.  O = 0, LSE = -inf where none counts.  scale: 0 means 1/sqrt(d).  status: int32 [1]
-    that becomes non-zero if a length leaves [0, S], or None.  Several samples of one encoded input: their rows as tokens
+    that becomes non-zero if a length leaves [0, S] or a bounded wait in the kernel gave up, or None (a wait that gave up leaves NaN in
+    its rows in any case).  Several samples of one encoded input: their rows as tokens
     (q viewed as [B][Hq][samples * n][d]), so that its states are read once for all of them."""
     if stream is not None:
         with _on_stream(stream, q.get_device()):
