@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
     const int pieces = c1 - c0 + 1;
     if (pieces == 1 && !weigh) continue;
     const int rows = item_rows(P, plan, b, blk);
-    const int64_t row0 = static_cast<int64_t>(b) * P.n_q + h * P.group + blk * kRowsMax;  // (with scores)
+    const int64_t row0 = static_cast<int64_t>(b) * P.n_q + h * P.group + blk * kRowsMax;  // (kPaged)
     // piece c lies in slot 0 of its CTA, but the first in slot 1 if the item begins in that CTA's range
     const int64_t slot0 = static_cast<int64_t>(c0 * 2 + (split.begin(c0) <= first ? 1 : 0)) * kRowsMax;
     auto slot = [&](int c) { return c == 0 ? slot0 : static_cast<int64_t>(c0 + c) * 2 * kRowsMax; };
@@ -990,7 +990,9 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
         }
         if (i < outs && part == 0) {
           const int r = i / (D / 4);
-          write_row<T>(P, place<SRC, D>(P, plan, b, h, blk, r), (i - r * (D / 4)) * 4, s_ml[r].x, s_ml[r].y, o);
+          // (worked out anew from b, h and blk here: 5 requests of 28 / 4 heads 11.7 us, of 48 / 4 16.5; from row0 11.1 and 14.9)
+          const RowOut at = SRC == kPaged ? RowOut{(row0 + r) * D, row0 + r} : place<SRC, D>(P, plan, b, h, blk, r);
+          write_row<T>(P, at, (i - r * (D / 4)) * 4, s_ml[r].x, s_ml[r].y, o);
         }
         if (share > 1 || i + kWarps * 32 - tid >= outs) break;  // the same for all threads
         i += kWarps * 32;
