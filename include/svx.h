@@ -636,10 +636,18 @@ svx_status svx_paged_decode_shared_workspace(const svx_pages* cache, int32_t n_r
                                              const svx_prefixes* prefixes, int64_t max_len, int64_t* bytes);
 
 /* svx_paged_decode for requests that share prefixes: request b attends to the slots of its prefix and then to its own slots
- * [0, len[b]) of cache->table (either may be none; with neither O = 0, LSE = -inf).  A prefix's K and V are read once for all its
+ * [0, len[b]) of cache->table (either may be none; with neither O = 0, LSE = -inf).  A prefix's K and V are read once for many of its
  * requests, not once for each.  q, len, max_len, scale, o, lse and what K, V hold: as svx_paged_decode (a value that is not finite
  * spoils the rows that read it).  first, like lengths and page ids, is checked on the device.  Outputs and workspace must not overlap
- * inputs, the pools or one another. */
+ * inputs, the pools or one another.  There are no accumulated weights: requests whose slots svx_paged_evict is to choose by weight need
+ * svx_paged_decode.
+ * Speed hangs on what the host knows.  max_len and prefixes->max_len decide how the SMs are shared out between prefixes and own slots: give
+ * bounds near the lengths (256 requests behind 65536 slots with up to 512 of their own: 230 us; bounds of 2048 own slots 360, of 8192
+ * 1350, of 65536 5300).  n_prefix decides the kernel, by the rows that n_req * n_q_heads / n_kv_heads leave to each on average: with
+ * more than 16 a prefix is read once for 128 or 256 rows, else once for 16 (that batch in a call for 16 prefixes of which one has requests
+ * 440 us, for 64 2230).
+ * Precision: with up to 128 rows to a prefix on average, softmax weights enter the product with V to 2^-15 of themselves; with more they are
+ * rounded once, to half a step of the type (2^-8 of themselves with bf16, 2^-11 with fp16). */
 svx_status svx_paged_decode_shared(const svx_pages* cache, int32_t n_req, int32_t n_q_heads, const void* q,
                                    const svx_prefixes* prefixes, const int32_t* len, int64_t max_len, float scale, void* o,
                                    float* lse, void* workspace, int64_t workspace_bytes, void* stream);
@@ -702,7 +710,7 @@ typedef struct {
   int64_t mask_req;
   int32_t n_req;           /* 1 .. 256 */
   int32_t n_tok;           /* >= 1; times n_q_heads / n_kv_heads at most 1048560 */
-  int32_t n_states;        /* >= 0 */
+  int32_t n_states;        /* 0 .. 2^31 - 257; n_req * n_kv_heads * (rows of 16) * (chunks of 4096 / (2 head_dim) states) below 2^31 */
   int32_t n_q_heads, n_kv_heads, head_dim; /* head_dim 64 or 128; n_q_heads a multiple of n_kv_heads, at most 4096 */
   int32_t dtype;           /* SVX_BF16 or SVX_FP16 */
   int32_t device;
@@ -715,7 +723,10 @@ svx_status svx_cross_attn_workspace(const svx_cross* c, int64_t* bytes);
 
 /* O = softmax(q K^T scale) V over the states that count, LSE = natural log of the softmax denominator; O = 0 and LSE = -inf where
  * none does.  Query head h reads KV head h / (n_q_heads / n_kv_heads).  States that count must be finite, as in svx_paged_decode; what
- * the others hold is not used, whatever it is.  Outputs and workspace must not overlap inputs or one another (a strided buffer
+ * the others hold is not used, whatever it is.  Precision: as svx_paged_decode_shared, by the rows (tokens times query heads) of a KV
+ * head.  With many rows the work of a call whose items fill the SMs is laid out by n_states, not by the lengths: where one request is
+ * much longer than the others its rows are few SMs' work (19 requests of 64 tokens, 32 / 8 heads, one of 16384 states among 100: 173 us, all
+ * of 16384 204).  Outputs and workspace must not overlap inputs or one another (a strided buffer
  * counts from its first element to its last).  workspace: device, 256-byte aligned; contents need no set-up.
  * Enqueued on `stream` (cudaStream_t) of `device`; allocates and keeps nothing, so it may be captured (after one eager call).  Calls
  * whose GPU work overlaps need workspaces and outputs of their own. */
@@ -760,7 +771,8 @@ typedef struct {
 /* Between two blocks of a layer, row by row:
  *   u = y, or y * post_norm / sqrt(mean(y^2) + post_eps);   h_out = alpha h + beta act(gate) u;
  *   x_out = h_out * norm / sqrt(mean(h_out^2) + eps)   (of h_out before its rounding)
- * all in fp32, rounded once.  Mean squares have to be within fp32's range.  h_out may be h and x_out may be y (same stride);
+ * all in fp32, rounded once; tanh and the sigmoid within 2^-17 of themselves.  The sums of a row's squares have to be within fp32's
+ * range.  h_out may be h and x_out may be y (same stride);
  * otherwise outputs must not overlap inputs or one another (a strided buffer counts from its first element to its last).
  * Enqueued on `stream` (cudaStream_t) of `device`; allocates and keeps nothing. */
 svx_status svx_residual_norm(const svx_residual* in, void* stream);

@@ -1193,7 +1193,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) join_rows(const __grid_constan
 
 // What splitting items over CTAs costs, their pieces written, read and joined, in tiles of a CTA: more where its pieces are 256 KiB
 // each.  (128 items of 16 tiles, two row tiles, d = 128: whole 31 us, split 46; 256 of 32: 95 and 103; d = 64, 256 of 12: 40 and 47;
-// 64 of 12: 21.8 and 21.4; 32 of 64 tiles: 89 and 39; one row tile, d = 128: 40 of 8: 16.6 and 17.8, 32 of 8: 16.5 and 15.1.)
+// 64 of 12: 21.8 and 21.4; 32 of 64 tiles: 89 and 39; one row tile, d = 128: 40 of 8: 16.6 and 17.8, 32 of 8: 16.5 and 15.1.)  By the most
+// tiles of an item that the host knows of: of 152 items of up to 128 tiles, 8 of 128 and the others of one tile take 173 us, all of 128 204.
 constexpr int kJoinTiles = 8, kJoinTilesLarge = 14, kJoinTilesOne = 6;
 
 struct RowSizes {

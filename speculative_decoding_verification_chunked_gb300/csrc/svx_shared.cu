@@ -214,7 +214,9 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
   const int64_t own = static_cast<int64_t>(n_req) * c->n_kv_heads * z.blocks * ((max_len + ct - 1) / ct);
   const int64_t far = c->n_kv_heads * (all_rows / kRowsMax + used) * ((max_prefix + ct - 1) / ct);
   // By the rows to a prefix, on average (32 heads, 8 KV heads, one prefix of 16384 slots: 16 rows 24.3 us by attend_kernel alone, 24.9 with
-  // rows_kernel; 32 rows 34 and 26; 64 rows and 32768 slots 87 and 48; eight prefixes of 4096 slots with 8 rows each 38 and 43).
+  // rows_kernel; 32 rows 34 and 26; 64 rows and 32768 slots 87 and 48; eight prefixes of 4096 slots with 8 rows each 38 and 43).  `first` is
+  // on the device, so prefixes without requests count too (256 requests of one prompt in a call for 1 prefix 230 us, for 16 440, for 64,
+  // where attend_kernel takes them, 2230).
   out->many = all_rows > static_cast<int64_t>(kRowsMax) * f->n_prefix;
   if (own + far > 0x7fffffff)
     return paged_fail(SVX_ERR_UNSUPPORTED, "heads times lengths are too large (%lld chunks of %d slots, at most 2^31 - 1)",
@@ -222,8 +224,9 @@ svx_status shared_sizes(const svx_pages* c, int32_t n_req, int32_t n_q, const sv
   const int64_t chunks = own + (out->many ? 0 : far);
   // With many rows the SMs are shared out over the two kernels by their work, so that they end together: a CTA of attend_kernel brings in
   // some 45 GB/s of short sequences, and begins and ends an item in 0.18 us (84 requests of one slot each, 8 KV heads: 43 us without that
-  // term, 30); a tile of rows_kernel takes 1.4 us with two row tiles, 1.0 with one.  (By the bounds known here: lengths
-  // may be shorter.)
+  // term, 30); a tile of rows_kernel takes 1.4 us with two row tiles, 1.0 with one.  By the bounds known here: where lengths are
+  // far below them, the kernel that has the work has few CTAs (256 requests of up to 512 slots behind 65536: bounds of 512 own slots 230
+  // us, of 2048 360, of 8192 1350, of 65536 5300; 16 of them behind 32768: 45, 59, 119, 544; prefix bounds 4 times too wide 670 and 61).
   int own_ctas = sms;
   if (out->many) {
     // (of a prefix, on average; 8 of 16 requests' 64 rows, 4096 slots, d = 64: in items of 128 rows 39 us, of 256 44; 16 such of 2048 slots,

@@ -854,7 +854,8 @@ def cross_attn(q, k, v, o, lse=None, lens=None, mask=None, scale: float = 0.0, s
     not count; what such states hold is not used.  O = 0, LSE = -inf where none counts.  scale: 0 means 1/sqrt(d).  status: int32 [1]
     that becomes non-zero if a length leaves [0, S] or a bounded wait in the kernel gave up, or None (a wait that gave up leaves NaN in
     its rows in any case).  Several samples of one encoded input: their rows as tokens
-    (q viewed as [B][Hq][samples * n][d]), so that its states are read once for all of them."""
+    (q viewed as [B][Hq][samples * n][d]), so that its states are read once for all of them.  With more than 128 rows (tokens times query
+    heads of a KV head) softmax weights are rounded to q's type in the product with V."""
     if stream is not None:
         with _on_stream(stream, q.get_device()):
             return cross_attn(q, k, v, o, lse, lens, mask, scale, status, workspace)
@@ -965,7 +966,9 @@ class PagedCache:
         prefix_table: int32 [P][max_prefix_pages], prefix_lens: int32 [P]; first: int32 [P + 1]: requests [first[p], first[p + 1]) have
         prefix p (neighbours in the batch; those outside [first[0], first[P]) have none).  table, lens: the requests' own slots,
         behind the prefix (lens may be 0).  q, o: [B][Hq][1][d]; lse: fp32 [B][Hq][1].  max_prefix, max_len: bounds on the lengths
-        known on the host (0: what the tables hold)."""
+        known on the host (0: what the tables hold).  Give them where tables have room: the SMs are shared out by them, and bounds of 4, 16
+        and 128 times the lengths make a large batch 1.6, 6 and 23 times slower; so do prefixes without requests, where there are many.
+        No accumulated weights: slots that `evict` is to choose by weight need `decode`."""
         if stream is not None:
             with _on_stream(stream, self.device):
                 return self.decode_shared(q, prefix_table, prefix_lens, first, table, lens, o, lse, max_prefix, max_len, scale, workspace)
