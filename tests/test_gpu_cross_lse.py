@@ -16,11 +16,11 @@ def svx():
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("t", [torch.bfloat16, torch.float16], ids=str)
 def test_the_same_sum_has_the_same_logarithm(svx, t, d):
-    """1 to 512 states with a score of 0: sums of weights are the numbers of states (times a power of two), exact, so that LSE is the rounding
+    """1 to 512 of 2048 states, with a score of 0: sums of weights are the numbers of states (times a power of two), exact, so that LSE is the rounding
     of one and the same number, within log2f's ulp of log2(sum) times ln 2, and O = V = 1."""
     for base in (0, 256):
         lens = torch.arange(base + 1, base + 257, dtype=torch.int32, device="cuda")
-        k = torch.ones((1, base + 256, 1, d), dtype=t, device="cuda").expand(256, -1, 1, d)
+        k = torch.ones((1, 2048, 1, d), dtype=t, device="cuda").expand(256, -1, 1, d)
         seen = {}
         for rows in (10, 20, 200):  # one block of 16 rows, one row tile, two
             q = torch.zeros((256, 1, rows, d), dtype=t, device="cuda")

@@ -30,7 +30,7 @@ class Expire:
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("b, n, states", [(3, 40, 300), (1, 40, 20000), (3, 300, 300), (1, 700, 9000), (160, 20, 128)])
+@pytest.mark.parametrize("b, n, states", [(3, 40, 1500), (1, 40, 20000), (3, 300, 1500), (1, 700, 9000), (160, 20, 1300)])
 def test_states(svx, b, n, states, d):
     """Items that are split over CTAs and items that are not, of one row tile and of two."""
     g = torch.Generator(device="cuda").manual_seed(n)
